@@ -58,6 +58,7 @@ typedef enum lrs_status {
 
 #define LRS_DTYPE_FP16 0
 #define LRS_DTYPE_BF16 1
+#define LRS_DTYPE_FP32 2 /* row operators only (segmented_row_topk and below), not the row sorts */
 
 /* Key types of radix_sort_keys_typed / radix_sort_pairs_typed. */
 #define LRS_KEY_U32 0
@@ -229,6 +230,29 @@ int segmented_row_sort(const uint16_t *vals_in, uint16_t *vals_out, int64_t *idx
                        void *workspace, size_t workspace_bytes, void *stream, const lrs_options *opts);
 
 /*
+ * The first k columns of segmented_row_sort without the sort: the k largest
+ * (descending nonzero) or smallest elements of every row, in order, with the
+ * int64 column each came from.  Elements are ordered by the same
+ * order-preserving map of their bit patterns as the row sorts use, over all 16
+ * or 32 bits, and equal patterns by column: ties go to the lowest column, -0
+ * is below +0 and NaNs lie beyond the infinities by pattern.
+ *   x         rows of n elements, row r starting at element r * row_stride
+ *             (row_stride >= 0: rows may lie apart, or, being read only, overlap)
+ *   vals_out  [rows][k] patterns of x's type     idx_out  [rows][k] int64
+ *   dtype: LRS_DTYPE_FP16, LRS_DTYPE_BF16 or LRS_DTYPE_FP32
+ *   0 <= k <= n, k <= LRS_MAX_TOPK; n <= LRS_MAX_ROW_LEN; rows * n < 2^40;
+ *   rows == 0 or k == 0 is a no-op.
+ * Calls on fewer than 256 long rows share each row among workgroups and need
+ * segmented_row_topk_workspace_size bytes; others need none (the size is 0 and
+ * workspace may be NULL).  Only opts->timer is used (kind 4).
+ */
+#define LRS_MAX_TOPK 1024
+size_t segmented_row_topk_workspace_size(int64_t rows, int64_t n, int64_t k, int dtype, const lrs_options *opts);
+int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_t *idx_out, int64_t rows, int64_t n,
+                       int64_t k, int dtype, int descending, void *workspace, size_t workspace_bytes, void *stream,
+                       const lrs_options *opts);
+
+/*
  * The per-pass digit counts of radix_sort_keys' first kernel: all passes'
  * histograms from one read of the keys (FlagTree PR #1084, step 2 "Before":
  * one kernel counts every pass).  hist_out[p * 2^b + d] = number of keys
@@ -277,7 +301,7 @@ int radix_sort_pairs_no_alloc(const uint32_t *keys_in, const uint32_t *vals_in, 
  * that).  radix_sort_timer_read waits for the events and reports, per kernel
  * kind (0 = workspace clear, 1 = digit histogram and the reduce-then-scan
  * count and scan, 2 = sweep/scatter pass, 3 = copy probe, 4 = whole-row
- * resident sort), the summed milliseconds and the number of launches in the
+ * resident sort and the kernels of the row operators), the summed milliseconds and the number of launches in the
  * two 5-entry arrays (either may be NULL), then empties the timer.  At most
  * 65536 launches are recorded between reads.  radix_sort_timer_destroy frees
  * the timer and its events (NULL is a no-op); no call may still be recording

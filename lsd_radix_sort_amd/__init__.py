@@ -33,6 +33,7 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "lsd_radix_sort.h")
 LRS_OK = 0
 LRS_DTYPE_FP16 = 0
 LRS_DTYPE_BF16 = 1
+LRS_DTYPE_FP32 = 2
 LRS_KEY_U32 = 0
 LRS_KEY_I32 = 1
 LRS_KEY_F32 = 2
@@ -105,6 +106,8 @@ def load_library():
         "radix_sort_timer_destroy": ([P], None),
         "radix_sort_timer_trace_tiles": ([P, P, u64], c_int),
         "radix_sort_timer_trace_used": ([P, P], c_int),
+        "segmented_row_topk_workspace_size": ([i64, i64, i64, c_int, O], szt),
+        "segmented_row_topk": ([P, i64, P, P, i64, i64, i64, c_int, c_int, P, szt, P, O], c_int),
         "radix_sort_status_string": ([c_int], ctypes.c_char_p),
     }
     for name, (args, res) in sigs.items():
@@ -536,3 +539,6 @@ def copy_probe(src: torch.Tensor, dst: torch.Tensor, options: SortOptions | None
     if not dst.is_contiguous() or dst.numel() * dst.element_size() < nbytes:
         _bad("dst must be contiguous and at least as large as src")
     _check(lib.radix_sort_copy_probe(_ptr(src), _ptr(dst), nbytes, _stream(src), _opt(options)), "copy_probe")
+
+
+from .row_ops import segmented_row_topk, segmented_row_topk_workspace_size  # noqa: E402

@@ -930,7 +930,7 @@ const char *radix_sort_status_string(int status) {
         case LRS_ERR_SIZE: return "element count or shape beyond the supported limit";
         case LRS_ERR_ALIASING: return "an output overlaps an input, another output or the workspace";
         case LRS_ERR_WORKSPACE_TOO_SMALL: return "workspace smaller than the *_workspace_size() figure";
-        case LRS_ERR_DTYPE: return "dtype must be LRS_DTYPE_FP16 or LRS_DTYPE_BF16";
+        case LRS_ERR_DTYPE: return "dtype or key type not one the call takes";
         case LRS_ERR_HIP: return "the HIP runtime rejected a launch";
         case LRS_ERR_ALIGNMENT: return "a pointer is not aligned as required";
         case LRS_ERR_OPTION: return "an lrs_options field has an invalid value";

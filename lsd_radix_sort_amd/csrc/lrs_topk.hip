@@ -1,0 +1,340 @@
+// lrs_topk.hip -- the first k columns of a row sort without the sort (gfx950).
+//
+// Each element becomes one 64-bit word, order image above, complemented column
+// below, so the wanted elements are the k largest words, no two words are
+// alike, and ties go to the lowest column whatever order the words arrive in.
+// One workgroup reads its row once, 16 bytes a lane.  The k-th largest of the
+// first chunk's per-load maxima bounds the row's k-th largest from below; only
+// elements at or above the bound enter a buffer in LDS, and when the buffer is
+// nearly full its k largest stay and the least of them becomes the bound.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/lsd_radix_sort.h"
+#include "lrs_host.h"
+#include "lrs_rows.h"
+
+namespace lrs {
+namespace {
+
+constexpr int kTopBlock = 256;
+constexpr int kTopVecs = 8;       // 16-byte loads a thread has in flight
+constexpr int kTopBuffer = 4096;  // words in LDS: k at most 1024 and one load of every thread, twice over
+
+struct TopArgs {
+    const void *x;
+    uint64_t stride;      // elements from one row to the next
+    uint64_t rows;
+    uint32_t n;           // elements in a row
+    uint32_t k;
+    uint32_t splits;      // workgroups that share one row
+    uint32_t split_len;   // elements each of them reads
+    uint32_t flip;        // 0, or all ones for the smallest first
+    void *values;         // patterns
+    int64_t *indices;
+    uint64_t *words;      // splits > 1: [rows][splits][k], 0 where a split has fewer
+};
+
+// Order image of a pattern, the wanted elements largest (signed).
+__device__ inline int image16(uint32_t pattern, uint32_t flip) {
+    const int v = static_cast<int16_t>(pattern);
+    return static_cast<int16_t>((v ^ ((v >> 15) & 0x7FFF)) ^ static_cast<int>(flip));
+}
+__device__ inline int image32(uint32_t pattern, uint32_t flip) {
+    const int v = static_cast<int>(pattern);
+    return (v ^ ((v >> 31) & 0x7FFFFFFF)) ^ static_cast<int>(flip);
+}
+template <int W> __device__ inline int image(uint32_t pattern, uint32_t flip) {
+    return W == 2 ? image16(pattern, flip) : image32(pattern, flip);
+}
+// The map is its own inverse.
+template <int W> __device__ inline uint32_t pattern_of(int img, uint32_t flip) {
+    const int v = img ^ static_cast<int>(flip);
+    if (W == 2) return static_cast<uint32_t>(v ^ ((v >> 15) & 0x7FFF)) & 0xFFFFu;
+    return static_cast<uint32_t>(v ^ ((v >> 31) & 0x7FFFFFFF));
+}
+__device__ inline uint64_t word_of(int img, uint32_t column) {
+    return (static_cast<uint64_t>(static_cast<uint32_t>(img) ^ 0x80000000u) << 32) | (0xFFFFFFFFu - column);
+}
+__device__ inline int image_of(uint64_t word) { return static_cast<int>(static_cast<uint32_t>(word >> 32) ^ 0x80000000u); }
+__device__ inline uint32_t column_of(uint64_t word) { return 0xFFFFFFFFu - static_cast<uint32_t>(word); }
+
+// Sorts buf[0, count) descending; the words from count to the next power of
+// two are cleared (a real word is never 0).  Barriers before and after.
+__device__ void sort_words(uint64_t *buf, uint32_t count) {
+    uint32_t m = 2;
+    while (m < count) m <<= 1;
+    __syncthreads();
+    for (uint32_t i = count + threadIdx.x; i < m; i += kTopBlock) buf[i] = 0;
+    __syncthreads();
+    for (uint32_t size = 2; size <= m; size <<= 1)
+        for (uint32_t d = size >> 1; d > 0; d >>= 1) {
+            for (uint32_t t = threadIdx.x; t < m / 2; t += kTopBlock) {
+                const uint32_t i = 2 * t - (t & (d - 1)), j = i + d;
+                const uint64_t a = buf[i], b = buf[j];
+                const bool down = (i & size) == 0;
+                if ((a < b) == down) {
+                    buf[i] = b;
+                    buf[j] = a;
+                }
+            }
+            __syncthreads();
+        }
+}
+
+template <int W> __device__ void write_row(const TopArgs &a, const uint64_t *buf, uint64_t row, uint32_t k) {
+    for (uint32_t j = threadIdx.x; j < k; j += kTopBlock) {
+        const uint64_t w = buf[j];
+        const uint64_t at = row * a.k + j;
+        if (W == 2)
+            static_cast<uint16_t *>(a.values)[at] = static_cast<uint16_t>(pattern_of<2>(image_of(w), a.flip));
+        else
+            static_cast<uint32_t *>(a.values)[at] = pattern_of<4>(image_of(w), a.flip);
+        a.indices[at] = column_of(w);
+    }
+}
+
+template <int W>
+__global__ __launch_bounds__(kTopBlock) void topk_kernel(TopArgs a) {
+    constexpr int kVec = 16 / W;
+    constexpr uint32_t kStep = kTopBlock * kVec;        // elements of one load of every thread
+    constexpr uint32_t kChunk = kStep * kTopVecs;
+    __shared__ uint64_t buf[kTopBuffer];
+    __shared__ uint32_t count;
+    __shared__ uint32_t sums[2][kTopBlock / kLanes];
+    using Stored = typename Row<W == 2 ? kRowF16 : kRowF32>::Stored;
+
+    for (uint64_t task = blockIdx.x; task < a.rows * a.splits; task += gridDim.x) {
+        const uint64_t row = task / a.splits;
+        const uint32_t split = static_cast<uint32_t>(task % a.splits);
+        const uint32_t first = split * a.split_len;
+        const uint32_t len = min(a.split_len, a.n - first);
+        const Stored *x = static_cast<const Stored *>(a.x) + row * a.stride + first;
+        const uint32_t vecs = len / kVec;
+        const uint32_t want = min(a.k, len);
+        // elements whose image is below `bound` cannot be among the k
+        int bound = INT32_MIN;
+        bool closed = false;  // nothing that comes later can be among the k either
+        __syncthreads();      // the last task's readers of buf are done
+        if (threadIdx.x == 0) count = 0;
+        __syncthreads();
+
+        // keep the k largest words; later elements with the k-th one's image
+        // come after it, so from now on only larger images enter
+        auto shrink = [&]() {
+            sort_words(buf, count);
+            const int img = image_of(buf[want - 1]);
+            __syncthreads();
+            if (threadIdx.x == 0) count = want;
+            closed = img == INT32_MAX;
+            bound = closed ? img : img + 1;
+            __syncthreads();
+        };
+        auto add = [&](int img, uint32_t at) {
+            if (img >= bound && !closed) {
+                const uint32_t slot = atomicAdd(&count, 1u);
+                if (slot < kTopBuffer) buf[slot] = word_of(img, first + at);
+            }
+        };
+        auto add_vec = [&](u32x4 v, uint32_t vec) {
+            for (int e = 0; e < kVec; ++e) {
+                const uint32_t pat = W == 2 ? (v[e / 2] >> (16 * (e & 1))) & 0xFFFFu : v[e % 4];
+                add(image<W>(pat, a.flip), vec * kVec + e);
+            }
+        };
+
+        for (uint32_t base = 0; base < vecs; base += kChunk / kVec) {
+            u32x4 v[kTopVecs];
+            int top[kTopVecs];
+            for (int u = 0; u < kTopVecs; ++u) {
+                const uint32_t vec = base + u * kTopBlock + threadIdx.x;
+                if (vec < vecs) v[u] = load16(x + static_cast<uint64_t>(vec) * kVec);
+            }
+            for (int u = 0; u < kTopVecs; ++u) {
+                const uint32_t vec = base + u * kTopBlock + threadIdx.x;
+                int m = INT32_MIN;
+                for (int e = 0; e < kVec; ++e) {
+                    const uint32_t pat = W == 2 ? (v[u][e / 2] >> (16 * (e & 1))) & 0xFFFFu : v[u][e % 4];
+                    m = max(m, image<W>(pat, a.flip));
+                }
+                top[u] = vec < vecs ? m : INT32_MIN;
+            }
+            if (base == 0 && min(vecs, kChunk / kVec) >= want) {
+                // the largest image that at least `want` loads reach, to within
+                // the search's early end
+                int lo = INT32_MIN, hi = INT32_MAX;
+                if (W == 2) lo = -32768, hi = 32767;
+                uint32_t round = 0;
+                while (lo < hi) {
+                    const int mid = static_cast<int>((static_cast<int64_t>(lo) + hi + 1) >> 1);
+                    uint32_t c = 0;
+                    for (int u = 0; u < kTopVecs; ++u) {
+                        const bool in = base + u * kTopBlock + threadIdx.x < vecs;
+                        c += __popcll(__ballot(in && top[u] >= mid));
+                    }
+                    uint32_t *s = sums[round++ & 1];
+                    if (threadIdx.x % kLanes == 0) s[threadIdx.x / kLanes] = c;
+                    __syncthreads();
+                    c = 0;
+                    for (int w = 0; w < kTopBlock / kLanes; ++w) c += s[w];
+                    if (c >= want) {
+                        lo = mid;
+                        if (c <= want + want / 4) break;
+                    } else {
+                        hi = mid - 1;
+                    }
+                }
+                bound = lo;
+            }
+            const uint32_t before = count;
+            __syncthreads();
+            for (int u = 0; u < kTopVecs; ++u) {
+                const uint32_t vec = base + u * kTopBlock + threadIdx.x;
+                if (vec < vecs && top[u] >= bound) add_vec(v[u], vec);
+            }
+            __syncthreads();
+            if (count > kTopBuffer) {
+                // too many at once: one load of every thread at a time
+                __syncthreads();
+                if (threadIdx.x == 0) count = before;
+                __syncthreads();
+                for (int u = 0; u < kTopVecs; ++u) {
+                    const uint32_t held = count;
+                    __syncthreads();  // every thread has read it before one adds
+                    if (held + kStep > kTopBuffer) shrink();
+                    const uint32_t vec = base + u * kTopBlock + threadIdx.x;
+                    if (vec < vecs && top[u] >= bound) add_vec(v[u], vec);
+                    __syncthreads();
+                }
+            }
+            if (count > kTopBuffer / 2) shrink();
+        }
+        __syncthreads();
+        // the elements after the last whole load
+        const uint32_t tail = vecs * kVec + threadIdx.x;
+        if (tail < len) add(image<W>(x[tail], a.flip), tail);
+        __syncthreads();
+        const uint32_t c = count;
+        sort_words(buf, c);
+        if (a.splits == 1) {
+            write_row<W>(a, buf, row, a.k);
+        } else {
+            uint64_t *out = a.words + task * a.k;
+            for (uint32_t j = threadIdx.x; j < a.k; j += kTopBlock) out[j] = j < want ? buf[j] : 0;
+        }
+    }
+}
+
+// The k largest of a row's splits * k words.
+template <int W>
+__global__ __launch_bounds__(kTopBlock) void topk_merge_kernel(TopArgs a) {
+    __shared__ uint64_t buf[kTopBuffer];
+    for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const uint32_t total = a.splits * a.k;  // at most kTopBuffer
+        const uint64_t *in = a.words + row * total;
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < total; i += kTopBlock) buf[i] = in[i];
+        sort_words(buf, total);
+        write_row<W>(a, buf, row, a.k);
+    }
+}
+
+// How many workgroups share a row: enough that few rows still occupy the GPU,
+// each with a piece worth a workgroup, and no more words than one merges.
+uint32_t topk_splits(uint64_t rows, uint64_t n, uint64_t k) {
+    if (rows == 0 || rows >= 256) return 1;
+    const uint64_t piece = std::max<uint64_t>(4096, 8 * k);
+    uint64_t s = std::min<uint64_t>((512 + rows - 1) / rows, n / piece);
+    s = std::min<uint64_t>(s, kTopBuffer / k);
+    return static_cast<uint32_t>(std::max<uint64_t>(1, s));
+}
+
+int check_topk(int64_t rows, int64_t n, int64_t k, int64_t stride, int dtype) {
+    if (dtype != LRS_DTYPE_FP16 && dtype != LRS_DTYPE_BF16 && dtype != LRS_DTYPE_FP32) return LRS_ERR_DTYPE;
+    if (rows < 0 || n < 0 || k < 0 || stride < 0) return LRS_ERR_SIZE;
+    if (static_cast<uint64_t>(n) > LRS_MAX_ROW_LEN || k > n || k > LRS_MAX_TOPK) return LRS_ERR_SIZE;
+    if (n > 0 && static_cast<uint64_t>(rows) >= (uint64_t(1) << 40) / static_cast<uint64_t>(n)) return LRS_ERR_SIZE;
+    if (stride > 0 && static_cast<uint64_t>(rows) >= (uint64_t(1) << 48) / static_cast<uint64_t>(stride)) return LRS_ERR_SIZE;
+    return LRS_OK;
+}
+
+uint64_t topk_bytes(uint64_t rows, uint64_t n, uint64_t k) {
+    if (rows == 0 || k == 0) return 0;
+    const uint64_t s = topk_splits(rows, n, k);
+    return s > 1 ? rows * s * k * sizeof(uint64_t) : 0;
+}
+
+}  // namespace
+}  // namespace lrs
+
+using namespace lrs;
+
+extern "C" {
+
+size_t segmented_row_topk_workspace_size(int64_t rows, int64_t n, int64_t k, int dtype, const lrs_options *opts) {
+    if (!options_ok(opts) || check_topk(rows, n, k, n, dtype) != LRS_OK) return 0;
+    return static_cast<size_t>(topk_bytes(rows, n, k));
+}
+
+int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_t *idx_out, int64_t rows, int64_t n,
+                       int64_t k, int dtype, int descending, void *workspace, size_t workspace_bytes, void *stream,
+                       const lrs_options *opts) try {
+    Ctx c;
+    if (!make_ctx(stream, opts, c)) return LRS_ERR_OPTION;
+    const int st = check_topk(rows, n, k, row_stride, dtype);
+    if (st != LRS_OK) return st;
+    if (rows == 0 || k == 0) return LRS_OK;
+    const uint64_t R = rows, N = n, K = k, size = dtype == LRS_DTYPE_FP32 ? 4 : 2;
+    const uint64_t need = topk_bytes(R, N, K);
+    if (!x || !vals_out || !idx_out || (need && !workspace)) return LRS_ERR_NULL_POINTER;
+    if (misaligned(x, size) || misaligned(vals_out, size) || misaligned(idx_out, 8) ||
+        (need && misaligned(workspace, 256)))
+        return LRS_ERR_ALIGNMENT;
+    if (workspace_bytes < need) return LRS_ERR_WORKSPACE_TOO_SMALL;
+    const uint64_t xb = ((R - 1) * static_cast<uint64_t>(row_stride) + N) * size, vb = R * K * size, ib = R * K * 8;
+    if (overlaps(vals_out, vb, x, xb) || overlaps(idx_out, ib, x, xb) || overlaps(vals_out, vb, idx_out, ib) ||
+        overlaps(workspace, need, x, xb) || overlaps(workspace, need, vals_out, vb) ||
+        overlaps(workspace, need, idx_out, ib))
+        return LRS_ERR_ALIASING;
+
+    c.elems = R * N;
+    TopArgs a{};
+    a.x = x;
+    a.stride = static_cast<uint64_t>(row_stride);
+    a.rows = R;
+    a.n = static_cast<uint32_t>(N);
+    a.k = static_cast<uint32_t>(K);
+    a.splits = topk_splits(R, N, K);
+    // whole 16-byte loads to a split
+    a.split_len = static_cast<uint32_t>(((N + a.splits - 1) / a.splits + 7) / 8 * 8);
+    a.splits = static_cast<uint32_t>((N + a.split_len - 1) / a.split_len);
+    a.flip = descending ? 0u : ~0u;
+    a.values = vals_out;
+    a.indices = idx_out;
+    a.words = static_cast<uint64_t *>(workspace);
+    const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(R * a.splits, 1u << 20)));
+    {
+        TimedLaunch t(4, c);
+        if (size == 2)
+            launch_on(topk_kernel<2>, grid, dim3(kTopBlock), t.L, a);
+        else
+            launch_on(topk_kernel<4>, grid, dim3(kTopBlock), t.L, a);
+        if (hipGetLastError() != hipSuccess) return LRS_ERR_HIP;
+    }
+    if (a.splits > 1) {
+        TimedLaunch t(4, c);
+        const dim3 merge(static_cast<uint32_t>(R));
+        if (size == 2)
+            launch_on(topk_merge_kernel<2>, merge, dim3(kTopBlock), t.L, a);
+        else
+            launch_on(topk_merge_kernel<4>, merge, dim3(kTopBlock), t.L, a);
+        if (hipGetLastError() != hipSuccess) return LRS_ERR_HIP;
+    }
+    return LRS_OK;
+} catch (...) {
+    return LRS_ERR_HIP;
+}
+
+}  // extern "C"
