@@ -253,6 +253,96 @@ int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_
                        const lrs_options *opts);
 
 /*
+ * Distillation from a teacher's top logits.  Row r of the student's logits s
+ * has n columns, and the teacher's top k logits t with their columns i come as
+ * segmented_row_topk (or a sliced row sort) returns them.  Slot j counts when
+ * 0 <= i_j < n and t_j > -inf (other slots are unused: shorter lists are padded
+ * with column -1).  With z = s / temperature, p = softmax(z) over all columns:
+ *   without teacher_lse  q = softmax of t / temperature over the counted slots;
+ *   with teacher_lse     q_j = exp(t_j / temperature - teacher_lse[r]), and the
+ *       tail, all columns not counted, has q0 = max(0, 1 - sum q) against the
+ *       student's mass p0 there (q0 = 0 where no column is left, or where the
+ *       student has none there and q0 <= 2^-20, the rounding of teacher_lse);
+ *   row_loss = sum_j q_j (log q_j - log p_{i_j}) + q0 (log q0 - log p0), 0 log 0 = 0;
+ *   loss     = sum_r w_r row_loss_r, w = row_weights, or 1 / rows if NULL.
+ * A row of weight 0 has row_loss and gradient 0 whatever it holds, and so has a
+ * row with no counted slot (with a tail: up to rounding).  Where the student
+ * gives no mass to what the teacher does, the row's loss is +inf.  NaN and +inf
+ * logits give NaN.  A column listed more than once has the sum of its slots' q.
+ *   loss      [1] f32          row_loss  [rows] f32, or NULL
+ *   grad      d loss / d logits in the logits' type, row r at r * grad_stride
+ *             (grad_stride >= n), times *loss_grad in the backward (NULL: 1)
+ *   row_stats [rows][k + 2] f32, written by the forward for the backward of the
+ *             same inputs (its contents are the library's)
+ * topk_distill_step is forward and backward in one call with loss_grad 1, for
+ * programs that know the loss is what they differentiate.  The teacher's
+ * tensors are constants: they get no gradient.
+ * 1 <= k <= LRS_MAX_TOPK (also more than n); n <= LRS_MAX_ROW_LEN;
+ * rows * n < 2^40; temperature finite and above 0 (else LRS_ERR_OPTION);
+ * rows == 0 gives loss 0.  Results do not depend on the order in which
+ * workgroups run.  Only opts->timer is used (kind 4).
+ */
+typedef struct lrs_distill {
+    const void *logits;           /* rows x n, row r at element r * row_stride */
+    int64_t row_stride;
+    const void *teacher_values;   /* rows x k, row r at element r * teacher_stride */
+    int64_t teacher_stride;
+    const void *teacher_indices;  /* rows x k int32 or int64, row r at element r * index_stride */
+    int64_t index_stride;
+    const float *teacher_lse;     /* [rows] log-sum-exp of the teacher's whole row / temperature, or NULL */
+    const float *row_weights;     /* [rows], or NULL */
+    int64_t rows, n, k;
+    int dtype;                    /* of the logits and the gradient: LRS_DTYPE_* */
+    int teacher_dtype;            /* LRS_DTYPE_* */
+    int index_bytes;              /* 4 or 8 */
+    float temperature;
+} lrs_distill;
+
+size_t topk_distill_workspace_size(int64_t rows, int64_t n, int64_t k, int dtype, const lrs_options *opts);
+int topk_distill_forward(const lrs_distill *in, float *loss, float *row_loss, float *row_stats, void *workspace,
+                         size_t workspace_bytes, void *stream, const lrs_options *opts);
+int topk_distill_backward(const lrs_distill *in, const float *row_stats, const float *loss_grad, void *grad,
+                          int64_t grad_stride, void *stream, const lrs_options *opts);
+int topk_distill_step(const lrs_distill *in, float *loss, float *row_loss, void *grad, int64_t grad_stride,
+                      void *workspace, size_t workspace_bytes, void *stream, const lrs_options *opts);
+
+/*
+ * How often each expert was chosen: counts_out[e] = number of slots equal to e
+ * in the rows x k matrix of expert ids (int32 or int64, row r at element
+ * r * index_stride), over the rows whose row_mask byte is not 0 (NULL: all).
+ * Ids outside [0, experts) are dropped slots and count for nothing.
+ * rows_counted, if not NULL, receives the number of such rows.
+ * 1 <= experts <= LRS_MAX_EXPERTS; rows * k < 2^31.
+ */
+#define LRS_MAX_EXPERTS 4096
+int expert_counts(const void *indices, int64_t index_stride, int index_bytes, const uint8_t *row_mask,
+                  int32_t *counts_out, int32_t *rows_counted, int64_t rows, int64_t k, int64_t experts, void *stream,
+                  const lrs_options *opts);
+
+/*
+ * The load balance loss of rows x experts router logits x, given the counts c
+ * (of these rows, or summed over ranks): f_e = experts * c_e / sum c (0 if the
+ * sum is 0), b_r = sum_e f_e p_re and z_r = log sum_e exp x_re,
+ *   loss = mean over the counted rows of  balance_weight b_r + z_weight z_r^2,
+ * 0 if no row counts.  p is the softmax of the row (LRS_SCORE_SOFTMAX) or its
+ * sigmoids divided by their sum (LRS_SCORE_SIGMOID; z_weight must then be 0).
+ * The counts are constants of the gradient.  Rows not counted and rows that are
+ * all -inf (experts masked out) add 0 and have gradient 0.
+ *   loss      [1] f32, or NULL: gradient only
+ *   grad      d loss / d x in x's type, row r at r * grad_stride, times
+ *             *loss_grad (NULL: 1), or NULL: loss only
+ *   rows_counted  as expert_counts gives it; needed with row_mask, else may be
+ *             NULL (all rows)
+ */
+#define LRS_SCORE_SOFTMAX 0
+#define LRS_SCORE_SIGMOID 1
+size_t expert_balance_workspace_size(int64_t rows, int64_t experts, const lrs_options *opts);
+int expert_balance(const void *logits, int64_t row_stride, const int32_t *counts, const int32_t *rows_counted,
+                   const uint8_t *row_mask, int64_t rows, int64_t experts, int dtype, int score, float balance_weight,
+                   float z_weight, float *loss, const float *loss_grad, void *grad, int64_t grad_stride, void *workspace,
+                   size_t workspace_bytes, void *stream, const lrs_options *opts);
+
+/*
  * The per-pass digit counts of radix_sort_keys' first kernel: all passes'
  * histograms from one read of the keys (FlagTree PR #1084, step 2 "Before":
  * one kernel counts every pass).  hist_out[p * 2^b + d] = number of keys

@@ -87,6 +87,7 @@ def load_library():
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m lsd_radix_sort_amd.build`")
     lib = ctypes.CDLL(LIB_PATH)
     P, u64, i64, c_int, szt = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+    F = ctypes.c_float
     O = ctypes.POINTER(_Options)
     sigs = {
         "radix_sort_workspace_size": ([u64, c_int, c_int, c_int, c_int, O], szt),
@@ -108,6 +109,13 @@ def load_library():
         "radix_sort_timer_trace_used": ([P, P], c_int),
         "segmented_row_topk_workspace_size": ([i64, i64, i64, c_int, O], szt),
         "segmented_row_topk": ([P, i64, P, P, i64, i64, i64, c_int, c_int, P, szt, P, O], c_int),
+        "topk_distill_workspace_size": ([i64, i64, i64, c_int, O], szt),
+        "topk_distill_forward": ([P, P, P, P, P, szt, P, O], c_int),
+        "topk_distill_backward": ([P, P, P, P, i64, P, O], c_int),
+        "topk_distill_step": ([P, P, P, P, i64, P, szt, P, O], c_int),
+        "expert_counts": ([P, i64, c_int, P, P, P, i64, i64, i64, P, O], c_int),
+        "expert_balance_workspace_size": ([i64, i64, O], szt),
+        "expert_balance": ([P, i64, P, P, P, i64, i64, c_int, c_int, F, F, P, P, P, i64, P, szt, P, O], c_int),
         "radix_sort_status_string": ([c_int], ctypes.c_char_p),
     }
     for name, (args, res) in sigs.items():
@@ -541,4 +549,7 @@ def copy_probe(src: torch.Tensor, dst: torch.Tensor, options: SortOptions | None
     _check(lib.radix_sort_copy_probe(_ptr(src), _ptr(dst), nbytes, _stream(src), _opt(options)), "copy_probe")
 
 
-from .row_ops import segmented_row_topk, segmented_row_topk_workspace_size  # noqa: E402
+from .row_ops import (  # noqa: E402
+    expert_balance_backward, expert_balance_forward, expert_balance_loss, expert_balance_step,
+    expert_balance_workspace_size, expert_counts, segmented_row_topk, segmented_row_topk_workspace_size,
+    topk_distill_backward, topk_distill_forward, topk_distill_loss, topk_distill_step, topk_distill_workspace_size)

@@ -1,0 +1,533 @@
+// lrs_distill.hip -- distillation from a teacher's top logits (gfx950).
+//
+// With z = s / T, p = softmax(z) over a row of student logits s and q the
+// teacher's mass on its top columns S (and q0 on all others, the tail, when its
+// whole log-sum-exp is known), the row's loss is
+//   sum_j q_j (log q_j - log p_j) + q0 (log q0 - log p0),
+// and its gradient in z is A p_v - q_v on S and A p_v - q0 p_v / p0 elsewhere
+// (A = all the teacher's mass: 1, or 0 in a row without any).  A row needs one
+// pass for its sum of exponentials and, for the gradient, a second one.
+//
+// Sums over a row are in 32 bits a thread (a few hundred terms) and in 64 bits
+// from there on, as is everything there is once a row or a slot: the terms of
+// a loss nearly cancel, and 1 - sum q loses a small tail in 32 bits.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/lsd_radix_sort.h"
+#include "lrs_host.h"
+#include "lrs_rows.h"
+
+namespace lrs {
+namespace {
+
+constexpr int kDisBlock = 256;
+constexpr float kLog2e = 1.44269504088896340736f;
+// Columns whose membership in S one workgroup holds as a bitmap at a time.
+constexpr uint32_t kMapColumns = 65536;
+
+struct DisArgs {
+    const void *logits;
+    uint64_t stride;
+    uint64_t rows;
+    uint32_t n, k;
+    const void *tv;       // teacher's top logits
+    uint64_t tv_stride;
+    int tv_type;
+    const void *ti;       // their columns
+    uint64_t ti_stride;
+    int ti_bytes;
+    const float *tlse;    // the teacher's log-sum-exp by row, or null: no tail
+    const float *weights; // by row, or null: 1 / rows
+    float inv_t;
+    uint32_t splits, split_len;
+    float2 *partial;      // [rows][splits]: largest logit and sum of exponentials of the tail (of all, without one)
+    float *stats;         // [rows][k + 2]
+    float *row_loss;
+    float *loss;
+    const float *loss_grad;
+    void *grad;
+    uint64_t grad_stride;
+};
+
+__device__ inline int64_t column_at(const DisArgs &a, uint64_t row, uint32_t j) {
+    const uint64_t at = row * a.ti_stride + j;
+    return a.ti_bytes == 8 ? static_cast<const int64_t *>(a.ti)[at] : static_cast<const int32_t *>(a.ti)[at];
+}
+__device__ inline float teacher_at(const DisArgs &a, uint64_t row, uint32_t j) {
+    const uint64_t at = row * a.tv_stride + j;
+    if (a.tv_type == kRowF32) return static_cast<const float *>(a.tv)[at];
+    const uint16_t v = static_cast<const uint16_t *>(a.tv)[at];
+    return a.tv_type == kRowBF16 ? Row<kRowBF16>::value(v) : Row<kRowF16>::value(v);
+}
+__device__ inline float weight_at(const DisArgs &a, uint64_t row) {
+    return a.weights ? a.weights[row] : 1.0f / static_cast<float>(a.rows);
+}
+
+// Joins two (largest, sum of exponentials below it) pairs; c = log2(e) / T.
+__device__ inline void join(float &m, float &z, float m2, float z2, float c) {
+    const float hi = fmaxf(m, m2);
+    if (hi == -INFINITY) {
+        z += z2;  // both sums are 0 (or NaN, which stays)
+        return;
+    }
+    z = z * exp2f((m - hi) * c) + z2 * exp2f((m2 - hi) * c);
+    m = hi;
+}
+
+// One workgroup: the largest logit and the sum of exponentials of a piece of a row.
+template <int T, bool TAIL>
+__global__ __launch_bounds__(kDisBlock) void distill_sum_kernel(DisArgs a) {
+    constexpr int kVec = Row<T>::kVec;
+    __shared__ uint32_t map[TAIL ? kMapColumns / 32 : 1];
+    __shared__ float wm[kDisBlock / kLanes], wz[kDisBlock / kLanes];
+    const float c = kLog2e * a.inv_t;
+    using Stored = typename Row<T>::Stored;
+    for (uint64_t task = blockIdx.x; task < a.rows * a.splits; task += gridDim.x) {
+        const uint64_t row = task / a.splits;
+        const uint32_t first = static_cast<uint32_t>(task % a.splits) * a.split_len;
+        const uint32_t last = min(a.n, first + a.split_len);
+        const Stored *x = static_cast<const Stored *>(a.logits) + row * a.stride;
+        float m = -INFINITY, z = 0.f;
+        if (weight_at(a, row) != 0.f) {
+            for (uint32_t lo = first; lo < last; lo += kMapColumns) {
+                const uint32_t hi = min(last, lo + kMapColumns);
+                if (TAIL) {
+                    __syncthreads();
+                    for (uint32_t i = threadIdx.x; i < kMapColumns / 32; i += kDisBlock) map[i] = 0;
+                    __syncthreads();
+                    for (uint32_t j = threadIdx.x; j < a.k; j += kDisBlock) {
+                        const int64_t col = column_at(a, row, j);
+                        if (col >= lo && col < hi && teacher_at(a, row, j) > -INFINITY)
+                            atomicOr(&map[(col - lo) / 32], 1u << ((col - lo) % 32));
+                    }
+                    __syncthreads();
+                }
+                const uint32_t vecs = (hi - lo) / kVec;
+                auto take = [&](float f) {
+                    if (f > m) {
+                        z = m == -INFINITY ? z : z * exp2f((m - f) * c);
+                        m = f;
+                    }
+                    if (f != -INFINITY) z += exp2f((f - m) * c);
+                };
+                for (uint32_t v = threadIdx.x; v < vecs; v += kDisBlock) {
+                    float f[kVec];
+                    unpack16<T>(load16(x + lo + static_cast<uint64_t>(v) * kVec), f);
+                    const uint32_t bits = TAIL ? map[v * kVec / 32] >> (v * kVec % 32) : 0;
+                    for (int e = 0; e < kVec; ++e)
+                        if (!TAIL || !((bits >> e) & 1)) take(f[e]);
+                }
+                const uint32_t t = vecs * kVec + threadIdx.x;
+                if (t < hi - lo && (!TAIL || !((map[t / 32] >> (t % 32)) & 1))) take(Row<T>::value(x[lo + t]));
+            }
+        }
+        for (int d = kLanes / 2; d > 0; d >>= 1) join(m, z, __shfl_xor(m, d), __shfl_xor(z, d), c);
+        __syncthreads();
+        if (threadIdx.x % kLanes == 0) {
+            wm[threadIdx.x / kLanes] = m;
+            wz[threadIdx.x / kLanes] = z;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kDisBlock / kLanes; ++w) join(m, z, wm[w], wz[w], c);
+            a.partial[task] = make_float2(m, z);
+        }
+    }
+}
+
+// One wave a row: the teacher's masses, the loss, and what the gradient needs:
+// stats[0] a reference logit, stats[1] the factor of exp(z - reference) off S,
+// stats[2 + j] the gradient at slot j's column, all before weight / T.
+template <int T>
+__global__ __launch_bounds__(kLanes) void distill_row_kernel(DisArgs a) {
+    __shared__ double q[LRS_MAX_TOPK];
+    __shared__ int32_t col[LRS_MAX_TOPK];
+    using Stored = typename Row<T>::Stored;
+    const int lane = threadIdx.x;
+    const double inv_t = a.inv_t;
+    for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        float *stats = a.stats + row * (a.k + 2);
+        if (weight_at(a, row) == 0.f) {
+            for (uint32_t j = lane; j < a.k + 2; j += kLanes) stats[j] = 0.f;
+            if (lane == 0 && a.row_loss) a.row_loss[row] = 0.f;
+            continue;
+        }
+        const Stored *x = static_cast<const Stored *>(a.logits) + row * a.stride;
+        const bool tail = a.tlse != nullptr;
+        // the row's sums
+        float m = -INFINITY;
+        for (uint32_t s = lane; s < a.splits; s += kLanes) m = fmaxf(m, a.partial[row * a.splits + s].x);
+        m = wave_max(m);
+        double z = 0;
+        for (uint32_t s = lane; s < a.splits; s += kLanes) {
+            const float2 p = a.partial[row * a.splits + s];
+            z += p.x == -INFINITY ? p.y : p.y * exp((static_cast<double>(p.x) - m) * inv_t);
+        }
+        z = wave_sum(z);
+        // the counted slots
+        __syncthreads();
+        float tm = -INFINITY;
+        for (uint32_t j = lane; j < a.k; j += kLanes) {
+            const int64_t at = column_at(a, row, j);
+            const float t = teacher_at(a, row, j);
+            const bool counts = at >= 0 && at < a.n && t > -INFINITY;
+            col[j] = counts ? static_cast<int32_t>(at) : -1;
+            if (counts) tm = fmaxf(tm, t);
+        }
+        tm = wave_max(tm);
+        __syncthreads();
+        const double ref = tail ? a.tlse[row] : tm * inv_t;
+        double sum = 0;
+        uint32_t distinct = 0;
+        float sm = -INFINITY;  // the largest student logit on S
+        for (uint32_t j = lane; j < a.k; j += kLanes) {
+            const bool counts = col[j] >= 0;
+            const double e = counts ? exp(teacher_at(a, row, j) * inv_t - ref) : 0;
+            q[j] = e;
+            sum += e;
+            bool again = false;
+            for (uint32_t i = 0; i < j; ++i) again |= col[i] == col[j];
+            distinct += counts && !again;
+            if (counts) sm = fmaxf(sm, Row<T>::value(x[col[j]]));
+        }
+        sum = wave_sum(sum);
+        distinct = wave_sum(distinct);
+        sm = wave_max(sm);
+        double scale = 1, q0 = 0, mass = sum;
+        if (tail) {
+            q0 = fmax(0.0, 1.0 - sum);
+            if (distinct == a.n || (m == -INFINITY && q0 <= 0x1p-20)) q0 = 0;
+        } else {
+            scale = sum > 0 ? 1 / sum : 0;
+            mass = sum > 0 ? 1 : 0;
+        }
+        // log-sum-exp of the whole row: the tail's and S's (without a tail z covers the row)
+        float top = m;
+        double whole = z;
+        if (tail) {
+            top = fmaxf(m, sm);
+            double on = 0;
+            for (uint32_t j = lane; j < a.k; j += kLanes) {
+                bool again = false;
+                for (uint32_t i = 0; i < j; ++i) again |= col[i] == col[j];
+                if (col[j] < 0 || again) continue;
+                const float s = Row<T>::value(x[col[j]]);
+                if (s != -INFINITY) on += exp((static_cast<double>(s) - top) * inv_t);
+            }
+            whole = wave_sum(on) + (m == -INFINITY ? z : z * exp((static_cast<double>(m) - top) * inv_t));
+        }
+        const double lse = top == -INFINITY ? -INFINITY : top * inv_t + log(whole);
+        const double lse0 = m == -INFINITY ? -INFINITY : m * inv_t + log(z);
+        const double a_mass = mass + q0;
+        double loss = 0;
+        __syncthreads();
+        for (uint32_t j = lane; j < a.k; j += kLanes) {
+            float g = 0;
+            if (col[j] >= 0) {
+                const double s = Row<T>::value(x[col[j]]);
+                const double qj = q[j] * scale;
+                if (qj > 0) loss += s == -INFINITY ? INFINITY : qj * (log(qj) - (s * inv_t - lse));
+                double all = 0;  // what the teacher puts on this column, if it is there more than once
+                for (uint32_t i = 0; i < a.k; ++i)
+                    if (col[i] == col[j]) all += q[i] * scale;
+                const double p = s == -INFINITY ? 0 : exp(s * inv_t - lse);
+                g = static_cast<float>(a_mass * p - all);
+            }
+            stats[2 + j] = g;
+        }
+        loss = wave_sum(loss);
+        if (lane == 0) {
+            if (q0 > 0) loss += m == -INFINITY ? INFINITY : q0 * (log(q0) - (lse0 - lse));
+            if (a.row_loss) a.row_loss[row] = static_cast<float>(loss);
+            stats[0] = m == -INFINITY ? 0.f : m;
+            double f = 0;
+            if (m != -INFINITY) {
+                f = a_mass * exp(m * inv_t - lse);
+                if (q0 > 0) f -= q0 / z;
+            }
+            stats[1] = static_cast<float>(f);
+        }
+    }
+}
+
+// The weighted sum of the row losses, in a fixed order.
+__global__ __launch_bounds__(1024) void distill_loss_kernel(DisArgs a) {
+    __shared__ double part[1024 / kLanes];
+    double s = 0;
+    for (uint64_t r = threadIdx.x; r < a.rows; r += 1024) {
+        const float w = weight_at(a, r);
+        if (w != 0.f) s += static_cast<double>(w) * a.row_loss[r];
+    }
+    s = wave_sum(s);
+    if (threadIdx.x % kLanes == 0) part[threadIdx.x / kLanes] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = 0;
+        for (int w = 0; w < 1024 / kLanes; ++w) s += part[w];
+        *a.loss = static_cast<float>(s);
+    }
+}
+
+// One workgroup: the gradient of a piece of a row.
+template <int T>
+__global__ __launch_bounds__(kDisBlock) void distill_grad_kernel(DisArgs a) {
+    constexpr int kVec = Row<T>::kVec;
+    using Stored = typename Row<T>::Stored;
+    const float c = kLog2e * a.inv_t;
+    const float up = a.loss_grad ? *a.loss_grad : 1.f;
+    for (uint64_t task = blockIdx.x; task < a.rows * a.splits; task += gridDim.x) {
+        const uint64_t row = task / a.splits;
+        const uint32_t first = static_cast<uint32_t>(task % a.splits) * a.split_len;
+        const uint32_t len = min(a.n - first, a.split_len);
+        const Stored *x = static_cast<const Stored *>(a.logits) + row * a.stride + first;
+        Stored *g = static_cast<Stored *>(a.grad) + row * a.grad_stride + first;
+        const float *stats = a.stats + row * (a.k + 2);
+        const float w = weight_at(a, row);
+        const uint32_t vecs = len / kVec;
+        if (w == 0.f) {  // whatever its logits hold
+            for (uint32_t v = threadIdx.x; v < vecs; v += kDisBlock) store16(g + static_cast<uint64_t>(v) * kVec, u32x4{0, 0, 0, 0});
+            const uint32_t t = vecs * kVec + threadIdx.x;
+            if (t < len) g[t] = 0;
+            continue;
+        }
+        const float m = stats[0], scale = up * w * a.inv_t, f = stats[1] * scale;
+        for (uint32_t v = threadIdx.x; v < vecs; v += kDisBlock) {
+            float e[kVec];
+            unpack16<T>(load16(x + static_cast<uint64_t>(v) * kVec), e);
+            for (int i = 0; i < kVec; ++i) e[i] = exp2f((e[i] - m) * c) * f;
+            store16(g + static_cast<uint64_t>(v) * kVec, pack16<T>(e));
+        }
+        const uint32_t t = vecs * kVec + threadIdx.x;
+        if (t < len) g[t] = Row<T>::pattern(exp2f((Row<T>::value(x[t]) - m) * c) * f);
+        // the teacher's columns over what was written there
+        __syncthreads();
+        for (uint32_t j = threadIdx.x; j < a.k; j += kDisBlock) {
+            const int64_t at = column_at(a, row, j) - first;
+            if (at >= 0 && at < len && teacher_at(a, row, j) > -INFINITY) g[at] = Row<T>::pattern(stats[2 + j] * scale);
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+}  // namespace lrs
+
+namespace lrs {
+namespace {
+
+// How many workgroups share a row: enough that few rows still fill the GPU,
+// each with a piece worth a workgroup.
+void distill_split(uint64_t rows, uint64_t n, uint32_t &splits, uint32_t &len) {
+    uint64_t s = 1;
+    if (rows < 2048) s = std::min<uint64_t>((2048 + rows - 1) / std::max<uint64_t>(rows, 1), n / 8192);
+    s = std::max<uint64_t>(1, s);
+    const uint64_t l = std::max<uint64_t>(8, ((n + s - 1) / s + 7) / 8 * 8);
+    len = static_cast<uint32_t>(l);
+    splits = static_cast<uint32_t>(std::max<uint64_t>(1, (n + l - 1) / l));
+}
+
+int check_sizes(int64_t rows, int64_t n, int64_t k, int dtype) {
+    if (!row_type_ok(dtype)) return LRS_ERR_DTYPE;
+    if (rows < 0 || n < 0 || k < 1 || k > LRS_MAX_TOPK || static_cast<uint64_t>(n) > LRS_MAX_ROW_LEN) return LRS_ERR_SIZE;
+    if (static_cast<uint64_t>(rows) >= (uint64_t(1) << 40) / std::max<uint64_t>(1, static_cast<uint64_t>(n)))
+        return LRS_ERR_SIZE;
+    return LRS_OK;
+}
+struct DisSpace {
+    uint64_t partial = 0, stats = 0, row_loss = 0, total = 0;
+};
+DisSpace distill_space(uint64_t rows, uint64_t n, uint64_t k) {
+    DisSpace w;
+    if (rows == 0) return w;
+    uint32_t splits, len;
+    distill_split(rows, n, splits, len);
+    auto place = [&](uint64_t bytes) {
+        const uint64_t at = w.total;
+        w.total += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    w.partial = place(rows * splits * sizeof(float2));
+    w.stats = place(rows * (k + 2) * sizeof(float));
+    w.row_loss = place(rows * sizeof(float));
+    return w;
+}
+
+// Everything the three calls check of the inputs; fills the arguments.
+int distill_inputs(const lrs_distill *d, DisArgs &a) {
+    if (d == nullptr) return LRS_ERR_NULL_POINTER;
+    const int st = check_sizes(d->rows, d->n, d->k, d->dtype);
+    if (st != LRS_OK) return st;
+    if (!row_type_ok(d->teacher_dtype) || (d->index_bytes != 4 && d->index_bytes != 8)) return LRS_ERR_DTYPE;
+    if (!stride_ok(d->row_stride, d->rows) || !stride_ok(d->teacher_stride, d->rows) || !stride_ok(d->index_stride, d->rows))
+        return LRS_ERR_SIZE;
+    if (!(d->temperature > 0.f) || !std::isfinite(d->temperature) || !std::isfinite(1.f / d->temperature))
+        return LRS_ERR_OPTION;
+    if (d->rows > 0 && ((d->n > 0 && !d->logits) || !d->teacher_values || !d->teacher_indices))
+        return LRS_ERR_NULL_POINTER;
+    if (misaligned(d->logits, row_type_size(d->dtype)) || misaligned(d->teacher_values, row_type_size(d->teacher_dtype)) ||
+        misaligned(d->teacher_indices, d->index_bytes) || misaligned(d->teacher_lse, 4) || misaligned(d->row_weights, 4))
+        return LRS_ERR_ALIGNMENT;
+    a.logits = d->logits;
+    a.stride = d->row_stride;
+    a.rows = d->rows;
+    a.n = static_cast<uint32_t>(d->n);
+    a.k = static_cast<uint32_t>(d->k);
+    a.tv = d->teacher_values;
+    a.tv_stride = d->teacher_stride;
+    a.tv_type = d->teacher_dtype;
+    a.ti = d->teacher_indices;
+    a.ti_stride = d->index_stride;
+    a.ti_bytes = d->index_bytes;
+    a.tlse = d->teacher_lse;
+    a.weights = d->row_weights;
+    a.inv_t = 1.f / d->temperature;
+    distill_split(a.rows, a.n, a.splits, a.split_len);
+    return LRS_OK;
+}
+
+// Whether [p, p + bytes) touches any input.
+bool hits_input(const lrs_distill *d, const void *p, uint64_t bytes) {
+    const uint64_t r = d->rows, k = d->k;
+    return overlaps(p, bytes, d->logits, span(r, d->row_stride, d->n, row_type_size(d->dtype))) ||
+           overlaps(p, bytes, d->teacher_values, span(r, d->teacher_stride, k, row_type_size(d->teacher_dtype))) ||
+           overlaps(p, bytes, d->teacher_indices, span(r, d->index_stride, k, d->index_bytes)) ||
+           overlaps(p, bytes, d->teacher_lse, d->teacher_lse ? 4 * r : 0) ||
+           overlaps(p, bytes, d->row_weights, d->row_weights ? 4 * r : 0);
+}
+
+constexpr uint64_t kMaxGrid = 1u << 20;
+
+template <int T> void distill_launch_sums(const DisArgs &a, const Ctx &c) {
+    const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(a.rows * a.splits, kMaxGrid)));
+    {
+        TimedLaunch t(4, c);
+        if (a.tlse != nullptr)
+            launch_on(distill_sum_kernel<T, true>, grid, dim3(kDisBlock), t.L, a);
+        else
+            launch_on(distill_sum_kernel<T, false>, grid, dim3(kDisBlock), t.L, a);
+    }
+    TimedLaunch t(4, c);
+    launch_on(distill_row_kernel<T>, dim3(static_cast<uint32_t>(std::min<uint64_t>(a.rows, kMaxGrid))), dim3(kLanes), t.L, a);
+}
+
+template <int T> void distill_launch_grad(const DisArgs &a, const Ctx &c) {
+    TimedLaunch t(4, c);
+    launch_on(distill_grad_kernel<T>, dim3(static_cast<uint32_t>(std::min<uint64_t>(a.rows * a.splits, kMaxGrid))),
+              dim3(kDisBlock), t.L, a);
+}
+
+int distill_forward(const DisArgs &a, int dtype, const Ctx &c) {
+    if (a.rows > 0) {
+        if (dtype == LRS_DTYPE_FP16) distill_launch_sums<kRowF16>(a, c);
+        else if (dtype == LRS_DTYPE_BF16) distill_launch_sums<kRowBF16>(a, c);
+        else distill_launch_sums<kRowF32>(a, c);
+        if (hipGetLastError() != hipSuccess) return LRS_ERR_HIP;
+    }
+    TimedLaunch t(4, c);
+    launch_on(distill_loss_kernel, dim3(1), dim3(1024), t.L, a);
+    return hipGetLastError() == hipSuccess ? LRS_OK : LRS_ERR_HIP;
+}
+
+int distill_backward(const DisArgs &a, int dtype, const Ctx &c) {
+    if (a.rows == 0 || a.n == 0) return LRS_OK;
+    if (dtype == LRS_DTYPE_FP16) distill_launch_grad<kRowF16>(a, c);
+    else if (dtype == LRS_DTYPE_BF16) distill_launch_grad<kRowBF16>(a, c);
+    else distill_launch_grad<kRowF32>(a, c);
+    return hipGetLastError() == hipSuccess ? LRS_OK : LRS_ERR_HIP;
+}
+
+// Forward with or without a gradient.
+int distill_run(const lrs_distill *d, float *loss, float *row_loss, float *stats, void *grad, int64_t grad_stride,
+                bool step, void *workspace, size_t workspace_bytes, void *stream, const lrs_options *opts) {
+    Ctx c;
+    if (!make_ctx(stream, opts, c)) return LRS_ERR_OPTION;
+    DisArgs a{};
+    const int st = distill_inputs(d, a);
+    if (st != LRS_OK) return st;
+    if (step && (!stride_ok(grad_stride, d->rows) || (d->rows > 1 && grad_stride < d->n))) return LRS_ERR_SIZE;
+    const DisSpace w = distill_space(a.rows, a.n, a.k);
+    if (!loss || (w.total && !workspace) || (step && a.rows && a.n && !grad)) return LRS_ERR_NULL_POINTER;
+    const uint64_t size = row_type_size(d->dtype);
+    if (misaligned(loss, 4) || misaligned(row_loss, 4) || misaligned(stats, 4) || misaligned(grad, size) ||
+        (w.total && misaligned(workspace, 256)))
+        return LRS_ERR_ALIGNMENT;
+    if (workspace_bytes < w.total) return LRS_ERR_WORKSPACE_TOO_SMALL;
+    const uint64_t lb = row_loss ? 4 * a.rows : 0, sb = stats ? 4 * a.rows * (a.k + 2) : 0;
+    const uint64_t gb = step ? span(a.rows, grad_stride, a.n, size) : 0;
+    const void *out[] = {loss, row_loss, stats, grad, workspace};
+    const uint64_t bytes[] = {4, lb, sb, gb, w.total};
+    for (int i = 0; i < 5; ++i) {
+        if (bytes[i] == 0) continue;
+        if (hits_input(d, out[i], bytes[i])) return LRS_ERR_ALIASING;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(out[i], bytes[i], out[j], bytes[j])) return LRS_ERR_ALIASING;
+    }
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.partial = reinterpret_cast<float2 *>(ws + w.partial);
+    a.stats = stats ? stats : reinterpret_cast<float *>(ws + w.stats);
+    a.row_loss = row_loss ? row_loss : reinterpret_cast<float *>(ws + w.row_loss);
+    a.loss = loss;
+    a.grad = grad;
+    a.grad_stride = static_cast<uint64_t>(grad_stride);
+    c.elems = a.rows * a.n;
+    const int fs = distill_forward(a, d->dtype, c);
+    return fs != LRS_OK || !step ? fs : distill_backward(a, d->dtype, c);
+}
+
+}  // namespace
+}  // namespace lrs
+
+using namespace lrs;
+
+extern "C" {
+
+size_t topk_distill_workspace_size(int64_t rows, int64_t n, int64_t k, int dtype, const lrs_options *opts) {
+    if (!options_ok(opts) || check_sizes(rows, n, k, dtype) != LRS_OK) return 0;
+    return static_cast<size_t>(distill_space(rows, n, k).total);
+}
+
+int topk_distill_forward(const lrs_distill *in, float *loss, float *row_loss, float *row_stats, void *workspace,
+                         size_t workspace_bytes, void *stream, const lrs_options *opts) try {
+    return distill_run(in, loss, row_loss, row_stats, nullptr, 0, false, workspace, workspace_bytes, stream, opts);
+} catch (...) {
+    return LRS_ERR_HIP;
+}
+
+int topk_distill_step(const lrs_distill *in, float *loss, float *row_loss, void *grad, int64_t grad_stride,
+                      void *workspace, size_t workspace_bytes, void *stream, const lrs_options *opts) try {
+    return distill_run(in, loss, row_loss, nullptr, grad, grad_stride, true, workspace, workspace_bytes, stream, opts);
+} catch (...) {
+    return LRS_ERR_HIP;
+}
+
+int topk_distill_backward(const lrs_distill *in, const float *row_stats, const float *loss_grad, void *grad,
+                          int64_t grad_stride, void *stream, const lrs_options *opts) try {
+    Ctx c;
+    if (!make_ctx(stream, opts, c)) return LRS_ERR_OPTION;
+    DisArgs a{};
+    const int st = distill_inputs(in, a);
+    if (st != LRS_OK) return st;
+    if (!stride_ok(grad_stride, in->rows) || (in->rows > 1 && grad_stride < in->n)) return LRS_ERR_SIZE;
+    if (a.rows == 0 || a.n == 0) return LRS_OK;
+    if (!row_stats || !grad) return LRS_ERR_NULL_POINTER;
+    const uint64_t size = row_type_size(in->dtype);
+    if (misaligned(row_stats, 4) || misaligned(loss_grad, 4) || misaligned(grad, size)) return LRS_ERR_ALIGNMENT;
+    const uint64_t gb = span(a.rows, grad_stride, a.n, size);
+    if (hits_input(in, grad, gb) || overlaps(grad, gb, row_stats, 4 * a.rows * (a.k + 2)) ||
+        overlaps(grad, gb, loss_grad, loss_grad ? 4 : 0))
+        return LRS_ERR_ALIASING;
+    a.stats = const_cast<float *>(row_stats);
+    a.loss_grad = loss_grad;
+    a.grad = grad;
+    a.grad_stride = static_cast<uint64_t>(grad_stride);
+    c.elems = a.rows * a.n;
+    return distill_backward(a, in->dtype, c);
+} catch (...) {
+    return LRS_ERR_HIP;
+}
+
+}  // extern "C"

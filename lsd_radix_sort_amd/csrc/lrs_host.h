@@ -82,6 +82,20 @@ inline bool overlaps(const void *a, uint64_t na, const void *b, uint64_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// The row operators' matrices: element types, strides in elements (0: every
+// row the same), and the bytes from the first element to past the last.
+inline bool row_type_ok(int dtype) {
+    return dtype == LRS_DTYPE_FP16 || dtype == LRS_DTYPE_BF16 || dtype == LRS_DTYPE_FP32;
+}
+inline uint64_t row_type_size(int dtype) { return dtype == LRS_DTYPE_FP32 ? 4 : 2; }
+inline bool stride_ok(int64_t stride, int64_t rows) {
+    return stride >= 0 &&
+           (stride == 0 || static_cast<uint64_t>(rows) < (uint64_t(1) << 48) / static_cast<uint64_t>(stride));
+}
+inline uint64_t span(uint64_t rows, uint64_t stride, uint64_t n, uint64_t size) {
+    return rows == 0 || n == 0 ? 0 : ((rows - 1) * stride + n) * size;
+}
+
 // One launch, timed into a timer slot when the call has a timer.  For calls
 // over many elements the dispatch itself stamps the slot's events, so nothing
 // is enqueued between dependent kernels.  Calls over at most kHostPacedMax

@@ -71,7 +71,10 @@ template <> struct Row<kRowF32> {
 // The kVec elements of a 16-byte word as floats, and back.
 template <int T> __device__ inline void unpack16(u32x4 v, float (&f)[Row<T>::kVec]) {
     if constexpr (T == kRowF32) {
-        for (int i = 0; i < 4; ++i) f[i] = __builtin_bit_cast(float, v[i]);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = v[i];  // a bit cast of v[i] itself reads element 0 here
+            f[i] = __builtin_bit_cast(float, w);
+        }
     } else {
         for (int i = 0; i < 4; ++i) Row<T>::unpack(v[i], f[2 * i], f[2 * i + 1]);
     }

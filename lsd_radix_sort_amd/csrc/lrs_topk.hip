@@ -252,11 +252,10 @@ uint32_t topk_splits(uint64_t rows, uint64_t n, uint64_t k) {
 }
 
 int check_topk(int64_t rows, int64_t n, int64_t k, int64_t stride, int dtype) {
-    if (dtype != LRS_DTYPE_FP16 && dtype != LRS_DTYPE_BF16 && dtype != LRS_DTYPE_FP32) return LRS_ERR_DTYPE;
-    if (rows < 0 || n < 0 || k < 0 || stride < 0) return LRS_ERR_SIZE;
+    if (!row_type_ok(dtype)) return LRS_ERR_DTYPE;
+    if (rows < 0 || n < 0 || k < 0 || !stride_ok(stride, rows)) return LRS_ERR_SIZE;
     if (static_cast<uint64_t>(n) > LRS_MAX_ROW_LEN || k > n || k > LRS_MAX_TOPK) return LRS_ERR_SIZE;
     if (n > 0 && static_cast<uint64_t>(rows) >= (uint64_t(1) << 40) / static_cast<uint64_t>(n)) return LRS_ERR_SIZE;
-    if (stride > 0 && static_cast<uint64_t>(rows) >= (uint64_t(1) << 48) / static_cast<uint64_t>(stride)) return LRS_ERR_SIZE;
     return LRS_OK;
 }
 
@@ -286,14 +285,14 @@ int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_
     const int st = check_topk(rows, n, k, row_stride, dtype);
     if (st != LRS_OK) return st;
     if (rows == 0 || k == 0) return LRS_OK;
-    const uint64_t R = rows, N = n, K = k, size = dtype == LRS_DTYPE_FP32 ? 4 : 2;
+    const uint64_t R = rows, N = n, K = k, size = row_type_size(dtype);
     const uint64_t need = topk_bytes(R, N, K);
     if (!x || !vals_out || !idx_out || (need && !workspace)) return LRS_ERR_NULL_POINTER;
     if (misaligned(x, size) || misaligned(vals_out, size) || misaligned(idx_out, 8) ||
         (need && misaligned(workspace, 256)))
         return LRS_ERR_ALIGNMENT;
     if (workspace_bytes < need) return LRS_ERR_WORKSPACE_TOO_SMALL;
-    const uint64_t xb = ((R - 1) * static_cast<uint64_t>(row_stride) + N) * size, vb = R * K * size, ib = R * K * 8;
+    const uint64_t xb = span(R, row_stride, N, size), vb = R * K * size, ib = R * K * 8;
     if (overlaps(vals_out, vb, x, xb) || overlaps(idx_out, ib, x, xb) || overlaps(vals_out, vb, idx_out, ib) ||
         overlaps(workspace, need, x, xb) || overlaps(workspace, need, vals_out, vb) ||
         overlaps(workspace, need, idx_out, ib))

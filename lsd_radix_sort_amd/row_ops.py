@@ -1,13 +1,20 @@
 """Operators on the head of a sorted row and on counts of small keys.
 
     segmented_row_topk(x, k, descending=True)
+    topk_distill_forward / _backward / _step(logits, teacher_values, teacher_indices, ...)
+    expert_counts(indices, experts)
+    expert_balance_forward / _backward / _step(logits, indices, ...)
 
-The entry points of the C ABI under the same names (include/lsd_radix_sort.h),
-with the checks, streams, outputs and errors of the package's sorts.  Matrices
-may have any row stride (a slice of a wider buffer); the elements of a row are
-contiguous.
+The entry points of the C ABI (include/lsd_radix_sort.h), with the checks,
+streams, outputs and errors of the package's sorts.  Matrices may have any row
+stride (a slice of a wider buffer); the elements of a row are contiguous.
+topk_distill_loss and expert_balance_loss are the same losses for programs that
+differentiate through torch autograd; the `_step` calls return loss and
+gradient at once, without it.
 """
 from __future__ import annotations
+
+import ctypes
 
 import torch
 
@@ -59,3 +66,296 @@ def segmented_row_topk(x: torch.Tensor, k: int, descending: bool = True, values_
                                        rows, n, k, dtype, int(descending), _lrs._ptr(workspace), need,
                                        _lrs._stream(x), opt), "segmented_row_topk")
     return values_out, indices_out
+
+
+# -------------------------------------------- distillation from top logits
+
+class _Distill(ctypes.Structure):
+    # mirrors struct lrs_distill
+    _fields_ = [("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("teacher_values", ctypes.c_void_p), ("teacher_stride", ctypes.c_int64),
+                ("teacher_indices", ctypes.c_void_p), ("index_stride", ctypes.c_int64),
+                ("teacher_lse", ctypes.c_void_p), ("row_weights", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("teacher_dtype", ctypes.c_int), ("index_bytes", ctypes.c_int),
+                ("temperature", ctypes.c_float)]
+
+
+def _by_row(t, name: str, rows: int, device) -> int | None:
+    if t is None:
+        return None
+    _lrs._same_device(t, name, device)
+    if t.dtype != torch.float32 or t.shape != (rows,) or not t.is_contiguous():
+        _lrs._bad(f"{name} must be a contiguous float32 tensor of shape ({rows},)")
+    return t.data_ptr()
+
+
+def _ids(t, name: str, rows: int, device) -> int:
+    """Check a rows x k integer matrix; returns its element size."""
+    _lrs._same_device(t, name, device)
+    if t.dtype not in (torch.int32, torch.int64):
+        _lrs._bad(f"{name} must be int32 or int64, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows:
+        _lrs._bad(f"{name} must be a 2-D tensor of {rows} rows")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        _lrs._bad(f"{name} must have contiguous rows (stride 1 along the last dimension)")
+    return t.element_size()
+
+
+def _distill_inputs(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights) -> _Distill:
+    dtype = _matrix(logits, "logits")
+    rows, n = logits.shape
+    device = logits.device
+    teacher_dtype = _matrix(teacher_values, "teacher_values")
+    _lrs._same_device(teacher_values, "teacher_values", device)
+    index_bytes = _ids(teacher_indices, "teacher_indices", rows, device)
+    if teacher_values.shape != teacher_indices.shape:
+        _lrs._bad(f"teacher_values {tuple(teacher_values.shape)} and teacher_indices {tuple(teacher_indices.shape)} differ")
+    return _Distill(logits.data_ptr(), logits.stride(0), teacher_values.data_ptr(), teacher_values.stride(0),
+                    teacher_indices.data_ptr(), teacher_indices.stride(0),
+                    _by_row(teacher_lse, "teacher_lse", rows, device),
+                    _by_row(row_weights, "row_weights", rows, device), rows, n, teacher_values.shape[1], dtype,
+                    teacher_dtype, index_bytes, temperature)
+
+
+def _grad_out(t, like: torch.Tensor) -> torch.Tensor:
+    """A gradient like the logits: new and contiguous, or the caller's with contiguous rows."""
+    if t is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    _lrs._same_device(t, "grad_out", like.device)
+    if t.dtype != like.dtype or t.shape != like.shape or (t.shape[1] > 1 and t.stride(1) != 1):
+        _lrs._bad(f"grad_out must be a {like.dtype} tensor of shape {tuple(like.shape)} with contiguous rows")
+    return t
+
+
+def _scale(t, device) -> int | None:
+    """The upstream gradient of a scalar loss."""
+    if t is None:
+        return None
+    _lrs._same_device(t, "loss_grad", device)
+    if t.dtype != torch.float32 or t.numel() != 1:
+        _lrs._bad("loss_grad must be one float32 number")
+    return t.data_ptr()
+
+
+def topk_distill_workspace_size(rows: int, n: int, k: int, dtype: torch.dtype = torch.bfloat16,
+                                options: "_lrs.SortOptions | None" = None) -> int:
+    return int(_lrs.load_library().topk_distill_workspace_size(rows, n, k, _DTYPES[dtype], _lrs._opt(options)))
+
+
+def _distill_workspace(lib, workspace, d: _Distill, opt, device) -> torch.Tensor:
+    return _lrs._workspace(workspace, lib.topk_distill_workspace_size(d.rows, d.n, d.k, d.dtype, opt), device)
+
+
+def topk_distill_forward(logits: torch.Tensor, teacher_values: torch.Tensor, teacher_indices: torch.Tensor,
+                         temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
+                         row_weights: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         options: "_lrs.SortOptions | None" = None):
+    """KL divergence of a student's rows of logits from a teacher's top logits.
+
+    teacher_values, teacher_indices: [rows, k], the teacher's top logits and their columns (slots with a
+    column outside the row, such as -1, are unused).  With teacher_lse ([rows] float32, the log-sum-exp of
+    the teacher's whole row over the temperature) the rest of the teacher's mass counts against the rest of
+    the student's; without it the teacher's top logits are renormalised.  row_weights: [rows] float32, default
+    1 / rows; a row of weight 0 is left out.  Returns (loss, row_loss [rows], row_stats for the backward)."""
+    lib = _lrs.load_library()
+    d = _distill_inputs(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights)
+    opt = _lrs._opt(options)
+    workspace = _distill_workspace(lib, workspace, d, opt, logits.device)
+    loss = torch.empty((), dtype=torch.float32, device=logits.device)
+    row_loss = torch.empty(d.rows, dtype=torch.float32, device=logits.device)
+    stats = torch.empty((d.rows, d.k + 2), dtype=torch.float32, device=logits.device)
+    _lrs._check(lib.topk_distill_forward(ctypes.byref(d), loss.data_ptr(), row_loss.data_ptr(), stats.data_ptr(),
+                                         workspace.data_ptr(), workspace.numel(), _lrs._stream(logits), opt),
+                "topk_distill_forward")
+    return loss, row_loss, stats
+
+
+def topk_distill_backward(logits: torch.Tensor, teacher_values: torch.Tensor, teacher_indices: torch.Tensor,
+                          row_stats: torch.Tensor, temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
+                          row_weights: torch.Tensor | None = None, loss_grad: torch.Tensor | None = None,
+                          grad_out: torch.Tensor | None = None, options: "_lrs.SortOptions | None" = None):
+    """The gradient of topk_distill_forward's loss in the logits, times loss_grad, from the same inputs
+    and the row_stats that the forward returned."""
+    lib = _lrs.load_library()
+    d = _distill_inputs(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights)
+    _lrs.check_output(row_stats, "row_stats", logits.device, 4, (d.rows, d.k + 2))
+    grad_out = _grad_out(grad_out, logits)
+    _lrs._check(lib.topk_distill_backward(ctypes.byref(d), row_stats.data_ptr(), _scale(loss_grad, logits.device),
+                                          grad_out.data_ptr(), grad_out.stride(0), _lrs._stream(logits),
+                                          _lrs._opt(options)), "topk_distill_backward")
+    return grad_out
+
+
+def topk_distill_step(logits: torch.Tensor, teacher_values: torch.Tensor, teacher_indices: torch.Tensor,
+                      temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
+                      row_weights: torch.Tensor | None = None, grad_out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, options: "_lrs.SortOptions | None" = None):
+    """topk_distill_forward and its gradient in one call: returns (loss, row_loss, grad)."""
+    lib = _lrs.load_library()
+    d = _distill_inputs(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights)
+    opt = _lrs._opt(options)
+    workspace = _distill_workspace(lib, workspace, d, opt, logits.device)
+    loss = torch.empty((), dtype=torch.float32, device=logits.device)
+    row_loss = torch.empty(d.rows, dtype=torch.float32, device=logits.device)
+    grad_out = _grad_out(grad_out, logits)
+    _lrs._check(lib.topk_distill_step(ctypes.byref(d), loss.data_ptr(), row_loss.data_ptr(), grad_out.data_ptr(),
+                                      grad_out.stride(0), workspace.data_ptr(), workspace.numel(),
+                                      _lrs._stream(logits), opt), "topk_distill_step")
+    return loss, row_loss, grad_out
+
+
+class _DistillLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, values, indices, temperature, lse, weights):
+        loss, _, stats = topk_distill_forward(logits, values, indices, temperature, lse, weights)
+        ctx.save_for_backward(logits, values, indices, stats, lse, weights)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, loss_grad):
+        logits, values, indices, stats, lse, weights = ctx.saved_tensors
+        grad = topk_distill_backward(logits, values, indices, stats, ctx.temperature, lse, weights, loss_grad)
+        return grad, None, None, None, None, None
+
+
+def topk_distill_loss(logits: torch.Tensor, teacher_values: torch.Tensor, teacher_indices: torch.Tensor,
+                      temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
+                      row_weights: torch.Tensor | None = None) -> torch.Tensor:
+    """topk_distill_forward's loss, differentiable in the logits (the teacher and the weights are constants)."""
+    return _DistillLoss.apply(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights)
+
+
+# ------------------------------------------ expert counts and balance loss
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _mask(t, rows: int, device) -> int | None:
+    if t is None:
+        return None
+    _lrs._same_device(t, "row_mask", device)
+    if t.dtype not in (torch.bool, torch.uint8) or t.shape != (rows,) or not t.is_contiguous():
+        _lrs._bad(f"row_mask must be a contiguous bool or uint8 tensor of shape ({rows},)")
+    return t.data_ptr()
+
+
+def expert_counts(indices: torch.Tensor, experts: int, row_mask: torch.Tensor | None = None,
+                  options: "_lrs.SortOptions | None" = None):
+    """How often each expert occurs in a [tokens, k] matrix of expert ids, over the tokens whose row_mask is
+    set; ids outside [0, experts) are dropped slots.  Returns (counts int32 [experts], rows_counted int32 [1])."""
+    lib = _lrs.load_library()
+    if not isinstance(indices, torch.Tensor) or not indices.is_cuda:
+        _lrs._bad("indices must be a GPU tensor")
+    index_bytes = _ids(indices, "indices", indices.shape[0] if indices.dim() else 0, indices.device)
+    rows, k = indices.shape
+    both = torch.empty(experts + 1, dtype=torch.int32, device=indices.device)
+    at = both.data_ptr()
+    _lrs._check(lib.expert_counts(indices.data_ptr(), indices.stride(0), index_bytes,
+                                  _mask(row_mask, rows, indices.device), at, at + 4 * experts, rows, k, experts,
+                                  _lrs._stream(indices), _lrs._opt(options)), "expert_counts")
+    return both[:experts], both[experts:]
+
+
+def expert_balance_workspace_size(rows: int, experts: int, options: "_lrs.SortOptions | None" = None) -> int:
+    return int(_lrs.load_library().expert_balance_workspace_size(rows, experts, _lrs._opt(options)))
+
+
+def _balance(logits, counts, rows_counted, balance_weight, z_weight, score, row_mask, want_loss, loss_grad, want_grad,
+             grad_out, workspace, options):
+    lib = _lrs.load_library()
+    dtype = _matrix(logits, "logits")
+    rows, experts = logits.shape
+    device = logits.device
+    if score not in _SCORES:
+        _lrs._bad(f"score must be one of {sorted(_SCORES)}")
+    for t, name, size in ((counts, "counts", experts), (rows_counted, "rows_counted", 1)):
+        if t is None and size == 1:
+            continue
+        _lrs._same_device(t, name, device)
+        if t.dtype != torch.int32 or t.shape != (size,) or not t.is_contiguous():
+            _lrs._bad(f"{name} must be a contiguous int32 tensor of shape ({size},)")
+    opt = _lrs._opt(options)
+    loss, grad, nbytes, ws = None, None, 0, None
+    if want_loss:
+        loss = torch.empty((), dtype=torch.float32, device=device)
+        workspace = _lrs._workspace(workspace, lib.expert_balance_workspace_size(rows, experts, opt), device)
+        ws, nbytes = workspace.data_ptr(), workspace.numel()
+    if want_grad:
+        grad = _grad_out(grad_out, logits)
+    _lrs._check(lib.expert_balance(logits.data_ptr(), logits.stride(0), counts.data_ptr(), _lrs._ptr(rows_counted),
+                                   _mask(row_mask, rows, device), rows, experts, dtype, _SCORES[score],
+                                   balance_weight, z_weight, _lrs._ptr(loss), _scale(loss_grad, device),
+                                   _lrs._ptr(grad), 0 if grad is None else grad.stride(0), ws, nbytes,
+                                   _lrs._stream(logits), opt), "expert_balance")
+    return loss, grad
+
+
+def _router_counts(logits, indices, row_mask, counts, options):
+    """Counts of these tokens, and the given (all ranks') counts in their place."""
+    _matrix(logits, "logits")
+    _ids(indices, "indices", logits.shape[0], logits.device)
+    mine, kept = expert_counts(indices, logits.shape[1], row_mask, options)
+    return (mine if counts is None else counts), kept
+
+
+def expert_balance_forward(logits: torch.Tensor, indices: torch.Tensor, balance_weight: float = 1.0,
+                           z_weight: float = 0.0, score: str = "softmax", row_mask: torch.Tensor | None = None,
+                           counts: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                           options: "_lrs.SortOptions | None" = None):
+    """The load balance loss of [tokens, experts] router logits whose tokens chose `indices` [tokens, k].
+
+    loss = mean over the tokens of row_mask of balance_weight * sum_e f_e p_e + z_weight * logsumexp^2, with
+    f_e = experts * counts_e / sum(counts) and p the softmax (or normalised sigmoid) of the token's logits.
+    counts: int32 [experts] to use in place of these tokens' own, such as their sum over ranks.
+    Returns (loss, counts, rows_counted)."""
+    counts, kept = _router_counts(logits, indices, row_mask, counts, options)
+    loss, _ = _balance(logits, counts, kept, balance_weight, z_weight, score, row_mask, True, None, False, None,
+                       workspace, options)
+    return loss, counts, kept
+
+
+def expert_balance_backward(logits: torch.Tensor, counts: torch.Tensor, rows_counted: torch.Tensor | None = None,
+                            balance_weight: float = 1.0, z_weight: float = 0.0, score: str = "softmax",
+                            row_mask: torch.Tensor | None = None, loss_grad: torch.Tensor | None = None,
+                            grad_out: torch.Tensor | None = None, options: "_lrs.SortOptions | None" = None):
+    """The gradient of expert_balance_forward's loss in the logits, times loss_grad."""
+    return _balance(logits, counts, rows_counted, balance_weight, z_weight, score, row_mask, False, loss_grad, True,
+                    grad_out, None, options)[1]
+
+
+def expert_balance_step(logits: torch.Tensor, indices: torch.Tensor, balance_weight: float = 1.0,
+                        z_weight: float = 0.0, score: str = "softmax", row_mask: torch.Tensor | None = None,
+                        counts: torch.Tensor | None = None, grad_out: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, options: "_lrs.SortOptions | None" = None):
+    """expert_balance_forward and its gradient from one read of the logits: returns (loss, counts, grad)."""
+    counts, kept = _router_counts(logits, indices, row_mask, counts, options)
+    loss, grad = _balance(logits, counts, kept, balance_weight, z_weight, score, row_mask, True, None, True, grad_out,
+                          workspace, options)
+    return loss, counts, grad
+
+
+class _BalanceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, indices, balance_weight, z_weight, score, row_mask, counts):
+        loss, counts, kept = expert_balance_forward(logits, indices, balance_weight, z_weight, score, row_mask, counts)
+        ctx.save_for_backward(logits, counts, kept, row_mask)
+        ctx.how = (balance_weight, z_weight, score)
+        ctx.mark_non_differentiable(counts)
+        return loss, counts
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, loss_grad, _):
+        logits, counts, kept, row_mask = ctx.saved_tensors
+        grad = expert_balance_backward(logits, counts, kept, *ctx.how, row_mask, loss_grad)
+        return grad, None, None, None, None, None, None
+
+
+def expert_balance_loss(logits: torch.Tensor, indices: torch.Tensor, balance_weight: float = 1.0,
+                        z_weight: float = 0.0, score: str = "softmax", row_mask: torch.Tensor | None = None,
+                        counts: torch.Tensor | None = None):
+    """expert_balance_forward's loss, differentiable in the logits, and the counts: (loss, counts)."""
+    return _BalanceLoss.apply(logits, indices, balance_weight, z_weight, score, row_mask, counts)
