@@ -227,6 +227,296 @@ __global__ __launch_bounds__(kTopBlock) void topk_kernel(TopArgs a) {
     }
 }
 
+// ---- short rows -----------------------------------------------------------
+//
+// Rows of at most 64 elements: an element a lane, 64 / P rows a wave (P the
+// power of two at or above n), sorted by a bitonic network across the P lanes.
+// A 16-bit image and the column fit one 32-bit word.
+template <int W> struct ShortWord;
+template <> struct ShortWord<2> {
+    using T = uint32_t;
+    __device__ static T make(int img, uint32_t column) {
+        return (static_cast<uint32_t>(img + 32768) << 16) | (0xFFFFu - column);
+    }
+    __device__ static int img(T w) { return static_cast<int>(w >> 16) - 32768; }
+    __device__ static uint32_t column(T w) { return 0xFFFFu - (w & 0xFFFFu); }
+    __device__ static T lane(T w, int l) { return __builtin_amdgcn_readlane(w, l); }
+};
+template <> struct ShortWord<4> {
+    using T = uint64_t;
+    __device__ static T make(int img, uint32_t column) { return word_of(img, column); }
+    __device__ static int img(T w) { return image_of(w); }
+    __device__ static uint32_t column(T w) { return column_of(w); }
+    __device__ static T lane(T w, int l) {
+        const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(w >> 32), l);
+        const uint32_t low = __builtin_amdgcn_readlane(static_cast<uint32_t>(w), l);
+        return (static_cast<uint64_t>(hi) << 32) | low;
+    }
+};
+
+// The word of lane ^ D.
+template <int D> __device__ inline uint32_t swap_lanes(uint32_t v) {
+    if constexpr (D < 32) return __builtin_amdgcn_ds_swizzle(v, (D << 10) | 0x1F);
+    else return __shfl_xor(v, D);
+}
+template <int D> __device__ inline uint64_t swap_lanes(uint64_t v) {
+    return (static_cast<uint64_t>(swap_lanes<D>(static_cast<uint32_t>(v >> 32))) << 32) |
+           swap_lanes<D>(static_cast<uint32_t>(v));
+}
+template <int SIZE, int D, typename T> __device__ inline void lane_merge(T &w, int lane) {
+    if constexpr (D > 0) {
+        const T o = swap_lanes<D>(w);
+        const bool keep_larger = ((lane & SIZE) == 0) == ((lane & D) == 0);
+        w = keep_larger == (w < o) ? o : w;
+        lane_merge<SIZE, D / 2>(w, lane);
+    }
+}
+// Sorts the words of every P lanes, the largest in the lowest lane.
+template <int P, int SIZE = 2, typename T> __device__ inline void lane_sort(T &w, int lane) {
+    if constexpr (SIZE <= P) {
+        lane_merge<SIZE, SIZE / 2>(w, SIZE == P ? lane & (P - 1) : lane);
+        lane_sort<P, 2 * SIZE>(w, lane);
+    }
+}
+
+template <int W> __device__ inline void write_short(const TopArgs &a, typename ShortWord<W>::T w, uint64_t at) {
+    using Word = ShortWord<W>;
+    if (W == 2)
+        static_cast<uint16_t *>(a.values)[at] = static_cast<uint16_t>(pattern_of<2>(Word::img(w), a.flip));
+    else
+        static_cast<uint32_t *>(a.values)[at] = pattern_of<4>(Word::img(w), a.flip);
+    a.indices[at] = Word::column(w);
+}
+
+template <int W, int P>
+__global__ __launch_bounds__(kTopBlock) void topk_lanes_kernel(TopArgs a) {
+    using Word = ShortWord<W>;
+    using Stored = typename Row<W == 2 ? kRowF16 : kRowF32>::Stored;
+    const int lane = threadIdx.x % kLanes, j = lane % P;
+    constexpr uint64_t kRows = kTopBlock / P;
+    for (uint64_t base = blockIdx.x * kRows; base < a.rows; base += gridDim.x * kRows) {
+        const uint64_t row = base + threadIdx.x / P;
+        typename Word::T w = 0;  // below every element's
+        if (row < a.rows && j < static_cast<int>(a.n))
+            w = Word::make(image<W>(static_cast<const Stored *>(a.x)[row * a.stride + j], a.flip), j);
+        lane_sort<P>(w, lane);
+        if (row < a.rows && j < static_cast<int>(a.k)) write_short<W>(a, w, row * a.k + j);
+    }
+}
+
+// The largest of the wave's values, in every lane.
+__device__ inline int wave_max_int(int v) {
+    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x111, 0xF, 0xF, false));  // row_shr 1, 2, 4, 8
+    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x112, 0xF, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x114, 0xF, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x118, 0xF, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x142, 0xF, 0xF, false));  // row_bcast 15, 31
+    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x143, 0xF, 0xF, false));
+    return __builtin_amdgcn_readlane(v, kLanes - 1);
+}
+// The largest of each 16 lanes' values, in all of them.
+__device__ inline int row16_max(int v) {
+    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x128, 0xF, 0xF, false));  // row_ror 8, 4, 2, 1
+    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x124, 0xF, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x122, 0xF, 0xF, false));
+    return max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x121, 0xF, 0xF, false));
+}
+__device__ inline uint32_t lanes_below(uint64_t mask) {
+    return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                     __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
+}
+
+// E consecutive elements of a row as images, INT32_MIN past its end.
+template <int W, int E> __device__ inline void load_images(const typename Row<W == 2 ? kRowF16 : kRowF32>::Stored *x,
+                                                           uint32_t at, uint32_t n, uint32_t flip, int (&img)[E]) {
+    constexpr int kVec = 16 / W;
+#pragma unroll
+    for (int q = 0; q < E / kVec; ++q) {
+        const uint32_t first = at + q * kVec;
+        u32x4 v{};
+        if (first + kVec <= n) {
+            v = load16(x + first);
+        } else if (first < n) {
+            for (int e = 0; e < kVec; ++e) {
+                const uint32_t pat = first + e < n ? x[first + e] : 0;
+                if (W == 2) v[e / 2] |= pat << (16 * (e & 1));
+                else v[e % 4] = pat;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            const uint32_t pat = W == 2 ? (v[e / 2] >> (16 * (e & 1))) & 0xFFFFu : v[e % 4];
+            img[q * kVec + e] = first + e < n ? image<W>(pat, flip) : INT32_MIN;
+        }
+    }
+}
+
+// Rows of at most 16 * E elements and small k: 16 lanes a row, E consecutive
+// elements a lane, sorted within the lane.  k times the 16 lanes' heads give
+// the next largest, the lowest lane's where they are equal, and that lane
+// moves on.
+template <int W, int E>
+__global__ __launch_bounds__(kTopBlock) void topk_heads_kernel(TopArgs a) {
+    using Stored = typename Row<W == 2 ? kRowF16 : kRowF32>::Stored;
+    const int j = threadIdx.x % 16;
+    constexpr uint64_t kRows = kTopBlock / 16;
+    const uint32_t n = a.n, at = j * E;
+    for (uint64_t base = blockIdx.x * kRows; base < a.rows; base += gridDim.x * kRows) {
+        const uint64_t row = base + threadIdx.x / 16;
+        int img[E];
+        uint32_t order = 0;  // the places of the sorted elements within the lane, 4 bits each
+        load_images<W, E>(static_cast<const Stored *>(a.x) + min(row, a.rows - 1) * a.stride, at, n, a.flip, img);
+        int pos[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) pos[e] = e;
+        // neighbours change places until none is out of order, so equal ones keep theirs
+#pragma unroll
+        for (int r = 0; r < E; ++r)
+#pragma unroll
+            for (int e = r & 1; e + 1 < E; e += 2) {
+                const bool up = img[e] < img[e + 1];
+                const int x = img[e], p = pos[e];
+                img[e] = up ? img[e + 1] : x;
+                img[e + 1] = up ? x : img[e + 1];
+                pos[e] = up ? pos[e + 1] : p;
+                pos[e + 1] = up ? p : pos[e + 1];
+            }
+#pragma unroll
+        for (int e = 0; e < E; ++e) order |= static_cast<uint32_t>(pos[e]) << (4 * e);
+        uint32_t left = at >= n ? 0 : min(n - at, static_cast<uint32_t>(E));
+        int mine = 0, column = 0;
+        for (uint32_t r = 0; r < a.k; ++r) {
+            const int top = row16_max(img[0]);
+            // an element past the row's end has the lowest image; a real one of that image is still left
+            const int first = ~row16_max(img[0] == top && left > 0 ? ~j : INT32_MIN);
+            const bool here = first == j;
+            // the column from the lane that holds it, to the lane that writes it
+            const int c = row16_max(here ? static_cast<int>(at + (order & 15u)) : -1);
+            if (j == static_cast<int>(r)) {
+                mine = top;
+                column = c;
+            }
+            if (here) {
+#pragma unroll
+                for (int e = 0; e + 1 < E; ++e) img[e] = img[e + 1];
+                img[E - 1] = INT32_MIN;
+                order >>= 4;
+                --left;
+            }
+        }
+        if (row < a.rows && j < static_cast<int>(a.k)) {
+            const uint64_t out = row * a.k + j;
+            if (W == 2)
+                static_cast<uint16_t *>(a.values)[out] = static_cast<uint16_t>(pattern_of<2>(mine, a.flip));
+            else
+                static_cast<uint32_t *>(a.values)[out] = pattern_of<4>(mine, a.flip);
+            a.indices[out] = column;
+        }
+    }
+}
+
+// Rows of at most 64 * V loads and k <= 64: a wave a row, held in registers.
+// A bisection over the lanes' largest images, and over all where that leaves
+// too many, finds a bound that at least k and at most 64 elements reach; those
+// move to a lane each and count the words above theirs, which is their place.
+template <int W, int V>
+__global__ __launch_bounds__(kTopBlock) void topk_wave_kernel(TopArgs a) {
+    constexpr int kVec = 16 / W;
+    constexpr int kLowest = W == 2 ? -32768 : INT32_MIN;
+    using Word = ShortWord<W>;
+    using Stored = typename Row<W == 2 ? kRowF16 : kRowF32>::Stored;
+    __shared__ typename Word::T held[kTopBlock / kLanes][kLanes];
+    const int lane = threadIdx.x % kLanes, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+    constexpr uint64_t kRows = kTopBlock / kLanes;
+    const uint32_t n = a.n, k = a.k;
+    const uint32_t lanes = min(static_cast<uint32_t>(kLanes), (n + kVec - 1) / kVec);  // that hold elements
+    const uint32_t enough = min(max(16u, 2 * k), static_cast<uint32_t>(kLanes));
+    for (uint64_t row = blockIdx.x * kRows + wave; row < a.rows; row += gridDim.x * kRows) {
+        const Stored *x = static_cast<const Stored *>(a.x) + row * a.stride;
+        int img[V][kVec];
+        int most = INT32_MIN;
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            load_images<W, kVec>(x, (u * kLanes + lane) * kVec, n, a.flip, img[u]);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) most = max(most, img[u][e]);
+        }
+        auto reach = [&](int bound) {
+            uint32_t c = 0;
+#pragma unroll
+            for (int u = 0; u < V; ++u)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) c += __popcll(__ballot(img[u][e] >= bound));
+            return bound == INT32_MIN ? n : c;
+        };
+        // at least k elements reach lo, and fewer than k anything above hi
+        int hi = wave_max_int(most), lo = kLowest;
+        uint32_t c = n;
+        if (lanes >= k) {
+            lo = ~wave_max_int(lane < static_cast<int>(lanes) ? ~most : INT32_MIN);
+            uint32_t reached = lanes;
+            int top = hi;
+            while (reached > k + k / 4 && lo < top) {
+                const int mid = (lo | top) - ((lo ^ top) >> 1);
+                const uint32_t m = __popcll(__ballot(most >= mid));
+                reached = m >= k ? m : reached;
+                lo = m >= k ? mid : lo;
+                top = m >= k ? top : mid - 1;
+            }
+            c = reach(lo);
+        }
+        while (c > enough && lo < hi) {
+            const int mid = (lo | hi) - ((lo ^ hi) >> 1);
+            const uint32_t m = reach(mid);
+            c = m >= k ? m : c;
+            lo = m >= k ? mid : lo;
+            hi = m >= k ? hi : mid - 1;
+        }
+        // more than 64 left: their images are equal but for fewer than k above
+        const bool ties = c > kLanes;
+        uint32_t count = 0;
+        if (!ties || lo < INT32_MAX) {
+            const int bound = ties ? lo + 1 : lo;
+#pragma unroll
+            for (int u = 0; u < V; ++u)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const uint32_t at = (u * kLanes + lane) * kVec + e;
+                    const bool in = at < n && img[u][e] >= bound;
+                    const uint64_t mask = __ballot(in);
+                    if (mask == 0) continue;
+                    if (in) held[wave][count + lanes_below(mask)] = Word::make(img[u][e], at);
+                    count += __popcll(mask);
+                }
+        }
+        if (ties) {  // the first of the equal ones, one after the other
+            int next = -1;
+            while (count < k) {
+                int first = INT32_MIN;  // the complement of the lowest column after `next`
+#pragma unroll
+                for (int u = 0; u < V; ++u)
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) {
+                        const int at = (u * kLanes + lane) * kVec + e;
+                        if (at < static_cast<int>(n) && at > next && img[u][e] == lo) first = max(first, ~at);
+                    }
+                next = ~wave_max_int(first);
+                if (lane == 0) held[wave][count] = Word::make(lo, next);
+                ++count;
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const typename Word::T w = lane < static_cast<int>(count) ? held[wave][lane] : 0;
+        __builtin_amdgcn_wave_barrier();
+        uint32_t place = 0;
+        for (uint32_t j = 0; j < count; j += 4)  // the words of lanes past the last are 0
+#pragma unroll
+            for (int i = 0; i < 4; ++i) place += Word::lane(w, j + i) > w;
+        if (lane < static_cast<int>(count) && place < k) write_short<W>(a, w, row * k + place);
+    }
+}
+
 // The k largest of a row's splits * k words.
 template <int W>
 __global__ __launch_bounds__(kTopBlock) void topk_merge_kernel(TopArgs a) {
@@ -239,6 +529,33 @@ __global__ __launch_bounds__(kTopBlock) void topk_merge_kernel(TopArgs a) {
         sort_words(buf, total);
         write_row<W>(a, buf, row, a.k);
     }
+}
+
+// Rows that one wave, or part of one, sorts in registers.
+constexpr uint64_t kWaveVecs = 8;  // 16-byte loads a lane at most
+bool topk_short(uint64_t n, uint64_t k, uint64_t size) {
+    return n <= kLanes || (k <= kLanes && n <= kLanes * kWaveVecs * 16 / size);
+}
+
+template <int W> void launch_short(const TopArgs &a, const Launch &L) {
+    const auto grid = [&](uint64_t rows_each) {
+        return dim3(static_cast<uint32_t>(std::min<uint64_t>((a.rows + rows_each - 1) / rows_each, 1u << 20)));
+    };
+    const dim3 block(kTopBlock);
+    if (a.n <= 8) return launch_on(topk_lanes_kernel<W, 8>, grid(kTopBlock / 8), block, L, a);
+    if (a.n <= 16) return launch_on(topk_lanes_kernel<W, 16>, grid(kTopBlock / 16), block, L, a);
+    if (a.n <= 128 && a.k <= 16) {
+        if (W == 4 && a.n <= 64) return launch_on(topk_heads_kernel<W, 16 / W>, grid(kTopBlock / 16), block, L, a);
+        return launch_on(topk_heads_kernel<W, 8>, grid(kTopBlock / 16), block, L, a);
+    }
+    if (a.n <= 32) return launch_on(topk_lanes_kernel<W, 32>, grid(kTopBlock / 32), block, L, a);
+    if (a.n <= 64) return launch_on(topk_lanes_kernel<W, 64>, grid(kTopBlock / 64), block, L, a);
+    const uint64_t vecs = (a.n + kLanes * 16 / W - 1) / (kLanes * 16 / W);
+    const dim3 waves = grid(kTopBlock / kLanes);
+    if (vecs <= 1) return launch_on(topk_wave_kernel<W, 1>, waves, block, L, a);
+    if (vecs <= 2) return launch_on(topk_wave_kernel<W, 2>, waves, block, L, a);
+    if (vecs <= 4) return launch_on(topk_wave_kernel<W, 4>, waves, block, L, a);
+    launch_on(topk_wave_kernel<W, 8>, waves, block, L, a);
 }
 
 // How many workgroups share a row: enough that few rows still occupy the GPU,
@@ -259,8 +576,8 @@ int check_topk(int64_t rows, int64_t n, int64_t k, int64_t stride, int dtype) {
     return LRS_OK;
 }
 
-uint64_t topk_bytes(uint64_t rows, uint64_t n, uint64_t k) {
-    if (rows == 0 || k == 0) return 0;
+uint64_t topk_bytes(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
+    if (rows == 0 || k == 0 || topk_short(n, k, size)) return 0;
     const uint64_t s = topk_splits(rows, n, k);
     return s > 1 ? rows * s * k * sizeof(uint64_t) : 0;
 }
@@ -274,7 +591,7 @@ extern "C" {
 
 size_t segmented_row_topk_workspace_size(int64_t rows, int64_t n, int64_t k, int dtype, const lrs_options *opts) {
     if (!options_ok(opts) || check_topk(rows, n, k, n, dtype) != LRS_OK) return 0;
-    return static_cast<size_t>(topk_bytes(rows, n, k));
+    return static_cast<size_t>(topk_bytes(rows, n, k, row_type_size(dtype)));
 }
 
 int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_t *idx_out, int64_t rows, int64_t n,
@@ -286,7 +603,7 @@ int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_
     if (st != LRS_OK) return st;
     if (rows == 0 || k == 0) return LRS_OK;
     const uint64_t R = rows, N = n, K = k, size = row_type_size(dtype);
-    const uint64_t need = topk_bytes(R, N, K);
+    const uint64_t need = topk_bytes(R, N, K, size);
     if (!x || !vals_out || !idx_out || (need && !workspace)) return LRS_ERR_NULL_POINTER;
     if (misaligned(x, size) || misaligned(vals_out, size) || misaligned(idx_out, 8) ||
         (need && misaligned(workspace, 256)))
@@ -313,6 +630,14 @@ int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_
     a.values = vals_out;
     a.indices = idx_out;
     a.words = static_cast<uint64_t *>(workspace);
+    if (topk_short(N, K, size)) {
+        TimedLaunch t(4, c);
+        if (size == 2)
+            launch_short<2>(a, t.L);
+        else
+            launch_short<4>(a, t.L);
+        return hipGetLastError() == hipSuccess ? LRS_OK : LRS_ERR_HIP;
+    }
     const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(R * a.splits, 1u << 20)));
     {
         TimedLaunch t(4, c);

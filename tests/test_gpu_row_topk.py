@@ -181,3 +181,17 @@ def test_graph_replay():
             g.replay()
             ev, ei = lrs.segmented_row_topk(x, k)
             assert torch.equal(i, ei) and torch.equal(v, ev)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("kind", ["normal", "equal", "masked", "patterns", "falling"])
+@pytest.mark.parametrize("rows,n,k", [
+    (1, 9, 9), (131, 16, 5), (77, 17, 17), (500, 31, 3), (5, 33, 33), (9, 63, 63), (6, 64, 64), (3, 65, 64), (5, 66, 65),
+    (1000, 129, 1), (33, 512, 64), (8, 1023, 40), (7, 1025, 64), (5, 2048, 64), (5, 2047, 2), (3, 2049, 64), (4, 4095, 33),
+    (4, 4096, 64), (2, 4097, 64)])
+def test_short_rows(dtype, kind, rows, n, k):
+    """Rows held by one wave or part of one, at the edges of each form."""
+    log(f"topk {dtype} {kind} {rows}x{n} k={k}")
+    bits = make_bits(kind, rows, n, dtype, 300 + n)
+    check(bits, dtype, k, True)
+    check(bits, dtype, k, False, pad=3, offset=1)
