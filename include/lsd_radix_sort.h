@@ -272,7 +272,7 @@ int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_
  *   loss      [1] f32          row_loss  [rows] f32, or NULL
  *   grad      d loss / d logits in the logits' type, row r at r * grad_stride
  *             (grad_stride >= n), times *loss_grad in the backward (NULL: 1)
- *   row_stats [rows][k + 2] f32, written by the forward for the backward of the
+ *   row_stats [rows][k + 3] f32, written by the forward for the backward of the
  *             same inputs (its contents are the library's)
  * topk_distill_step is forward and backward in one call with loss_grad 1, for
  * programs that know the loss is what they differentiate.  The teacher's

@@ -23,11 +23,15 @@ struct Launch {
 #define LRS_PLAIN_UNTIMED 1
 #endif
 template <typename Kernel, typename... Args>
-inline void launch_on(Kernel kernel, dim3 grid, dim3 block, const Launch &L, Args... args) {
+inline void launch_lds(Kernel kernel, dim3 grid, dim3 block, uint32_t lds_bytes, const Launch &L, Args... args) {
     if (LRS_PLAIN_UNTIMED && L.start == nullptr && L.stop == nullptr)
-        hipLaunchKernelGGL(kernel, grid, block, 0, L.s, args...);
+        hipLaunchKernelGGL(kernel, grid, block, lds_bytes, L.s, args...);
     else
-        hipExtLaunchKernelGGL(kernel, grid, block, 0, L.s, L.start, L.stop, 0, args...);
+        hipExtLaunchKernelGGL(kernel, grid, block, lds_bytes, L.s, L.start, L.stop, 0, args...);
+}
+template <typename Kernel, typename... Args>
+inline void launch_on(Kernel kernel, dim3 grid, dim3 block, const Launch &L, Args... args) {
+    launch_lds(kernel, grid, block, 0, L, args...);
 }
 
 }  // namespace lrs

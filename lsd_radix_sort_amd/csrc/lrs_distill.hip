@@ -33,6 +33,7 @@ struct DisArgs {
     const void *logits;
     uint64_t stride;
     uint64_t rows;
+    uint64_t first_row;   // of this launch
     uint32_t n, k;
     const void *tv;       // teacher's top logits
     uint64_t tv_stride;
@@ -45,7 +46,7 @@ struct DisArgs {
     float inv_t;
     uint32_t splits, split_len;
     float2 *partial;      // [rows][splits]: largest logit and sum of exponentials of the tail (of all, without one)
-    float *stats;         // [rows][k + 2]
+    float *stats;         // [rows][k + kStats]
     float *row_loss;
     float *loss;
     const float *loss_grad;
@@ -139,9 +140,21 @@ __global__ __launch_bounds__(kDisBlock) void distill_sum_kernel(DisArgs a) {
     }
 }
 
-// One wave a row: the teacher's masses, the loss, and what the gradient needs:
-// stats[0] a reference logit, stats[1] the factor of exp(z - reference) off S,
-// stats[2 + j] the gradient at slot j's column, all before weight / T.
+// Whether x c of a row with this largest logit may pass what 32 bits hold.
+__device__ inline bool huge_logit(float m, float c) { return fabsf(m) < INFINITY && !(fabsf(m * c) < 0x1p100f); }
+
+// What a row's gradient needs: off S it is f 2^((x - b) c - r) with b, r and f
+// the first three stats (r whole and b 0, or b the largest logit and r 0 where
+// that is huge), at slot j's column stats[3 + j], all before weight / T.
+constexpr uint32_t kStats = 3;
+__device__ inline void write_stats(float *stats, double reference, float c, double f) {
+    const bool huge = fabs(reference) < INFINITY && !(fabs(reference) < 0x1p100);
+    stats[0] = huge ? static_cast<float>(reference / c) : 0.f;
+    stats[1] = huge ? 0.f : static_cast<float>(reference);
+    stats[2] = static_cast<float>(f);
+}
+
+// One wave a row: the teacher's masses, the loss and the stats.
 template <int T>
 __global__ __launch_bounds__(kLanes) void distill_row_kernel(DisArgs a) {
     __shared__ double q[LRS_MAX_TOPK];
@@ -150,9 +163,9 @@ __global__ __launch_bounds__(kLanes) void distill_row_kernel(DisArgs a) {
     const int lane = threadIdx.x;
     const double inv_t = a.inv_t;
     for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        float *stats = a.stats + row * (a.k + 2);
+        float *stats = a.stats + row * (a.k + kStats);
         if (weight_at(a, row) == 0.f) {
-            for (uint32_t j = lane; j < a.k + 2; j += kLanes) stats[j] = 0.f;
+            for (uint32_t j = lane; j < a.k + kStats; j += kLanes) stats[j] = 0.f;
             if (lane == 0 && a.row_loss) a.row_loss[row] = 0.f;
             continue;
         }
@@ -220,8 +233,9 @@ __global__ __launch_bounds__(kLanes) void distill_row_kernel(DisArgs a) {
             }
             whole = wave_sum(on) + (m == -INFINITY ? z : z * exp((static_cast<double>(m) - top) * inv_t));
         }
-        const double lse = top == -INFINITY ? -INFINITY : top * inv_t + log(whole);
-        const double lse0 = m == -INFINITY ? -INFINITY : m * inv_t + log(z);
+        // relative to `top`, which may be huge
+        const double lse = top == -INFINITY ? -INFINITY : log(whole);
+        const double lse0 = m == -INFINITY ? -INFINITY : (static_cast<double>(m) - top) * inv_t + log(z);
         const double a_mass = mass + q0;
         double loss = 0;
         __syncthreads();
@@ -230,26 +244,30 @@ __global__ __launch_bounds__(kLanes) void distill_row_kernel(DisArgs a) {
             if (col[j] >= 0) {
                 const double s = Row<T>::value(x[col[j]]);
                 const double qj = q[j] * scale;
-                if (qj > 0) loss += s == -INFINITY ? INFINITY : qj * (log(qj) - (s * inv_t - lse));
+                if (qj > 0) loss += s == -INFINITY ? INFINITY : qj * (log(qj) - ((s - top) * inv_t - lse));
                 double all = 0;  // what the teacher puts on this column, if it is there more than once
                 for (uint32_t i = 0; i < a.k; ++i)
                     if (col[i] == col[j]) all += q[i] * scale;
-                const double p = s == -INFINITY ? 0 : exp(s * inv_t - lse);
+                const double p = s == -INFINITY ? 0 : exp((s - top) * inv_t - lse);
                 g = static_cast<float>(a_mass * p - all);
             }
-            stats[2 + j] = g;
+            stats[kStats + j] = g;
         }
         loss = wave_sum(loss);
         if (lane == 0) {
             if (q0 > 0) loss += m == -INFINITY ? INFINITY : q0 * (log(q0) - (lse0 - lse));
             if (a.row_loss) a.row_loss[row] = static_cast<float>(loss);
-            stats[0] = m == -INFINITY ? 0.f : m;
+            // 2^((x - b) c - r) in place of exp((x - m) / T)
+            const float c = kLog2e * a.inv_t;
+            const double exact = static_cast<double>(m) * c;
+            const double r = m == -INFINITY ? 0 : huge_logit(m, c) ? exact : rintf(m * c);
             double f = 0;
             if (m != -INFINITY) {
-                f = a_mass * exp(m * inv_t - lse);
+                f = a_mass * exp((static_cast<double>(m) - top) * inv_t - lse);
                 if (q0 > 0) f -= q0 / z;
+                f *= exp2(r - exact);
             }
-            stats[1] = static_cast<float>(f);
+            write_stats(stats, r, c, f);
         }
     }
 }
@@ -285,7 +303,7 @@ __global__ __launch_bounds__(kDisBlock) void distill_grad_kernel(DisArgs a) {
         const uint32_t len = min(a.n - first, a.split_len);
         const Stored *x = static_cast<const Stored *>(a.logits) + row * a.stride + first;
         Stored *g = static_cast<Stored *>(a.grad) + row * a.grad_stride + first;
-        const float *stats = a.stats + row * (a.k + 2);
+        const float *stats = a.stats + row * (a.k + kStats);
         const float w = weight_at(a, row);
         const uint32_t vecs = len / kVec;
         if (w == 0.f) {  // whatever its logits hold
@@ -294,30 +312,313 @@ __global__ __launch_bounds__(kDisBlock) void distill_grad_kernel(DisArgs a) {
             if (t < len) g[t] = 0;
             continue;
         }
-        const float m = stats[0], scale = up * w * a.inv_t, f = stats[1] * scale;
+        const float b = stats[0], r = stats[1], scale = up * w * a.inv_t, f = stats[2] * scale;
         for (uint32_t v = threadIdx.x; v < vecs; v += kDisBlock) {
             float e[kVec];
             unpack16<T>(load16(x + static_cast<uint64_t>(v) * kVec), e);
-            for (int i = 0; i < kVec; ++i) e[i] = exp2f((e[i] - m) * c) * f;
+            for (int i = 0; i < kVec; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(e[i] - b, c, -r)) * f;
             store16(g + static_cast<uint64_t>(v) * kVec, pack16<T>(e));
         }
         const uint32_t t = vecs * kVec + threadIdx.x;
-        if (t < len) g[t] = Row<T>::pattern(exp2f((Row<T>::value(x[t]) - m) * c) * f);
+        if (t < len) g[t] = Row<T>::pattern(__builtin_amdgcn_exp2f(fmaf(Row<T>::value(x[t]) - b, c, -r)) * f);
         // the teacher's columns over what was written there
         __syncthreads();
         for (uint32_t j = threadIdx.x; j < a.k; j += kDisBlock) {
             const int64_t at = column_at(a, row, j) - first;
-            if (at >= 0 && at < len && teacher_at(a, row, j) > -INFINITY) g[at] = Row<T>::pattern(stats[2 + j] * scale);
+            if (at >= 0 && at < len && teacher_at(a, row, j) > -INFINITY) g[at] = Row<T>::pattern(stats[kStats + j] * scale);
         }
         __syncthreads();
     }
 }
 
-}  // namespace
-}  // namespace lrs
+// ---- a whole row in one workgroup's registers ------------------------------
 
-namespace lrs {
-namespace {
+// 2^d of a 64-bit d, to 32 bits.
+__device__ inline double power_of_two(double d) {
+    const double i = rint(d);
+    return ldexp(static_cast<double>(__builtin_amdgcn_exp2f(static_cast<float>(d - i))),
+                 static_cast<int>(fmax(fmin(i, 2000.0), -2000.0)));
+}
+
+// LDS of a held row: what is known of the k slots, the partial sums and the
+// bitmap of the columns in S (last).
+struct HeldLds {
+    static constexpr uint32_t kFixed = 512;
+    __host__ __device__ static uint32_t slots(uint32_t k) { return (k + 1) / 2 * 2; }
+    __host__ __device__ static uint32_t map(uint32_t k) { return kFixed + slots(k) * 20; }
+    __host__ __device__ static uint32_t bytes(uint32_t k, uint32_t n) { return map(k) + (n + 31) / 32 * 4; }
+};
+
+// One workgroup of B threads a row, V loads of 16 bytes a thread held in
+// registers from the one read to the gradient.  Exponents are in units of
+// log 2 with c = log2(e) / T rounded to 32 bits, everywhere the same c, and
+// references to them are whole numbers R: the sums of 2^(x c - R) of two waves
+// join exactly, and log2 sum 2^(x c) = R + log2(sum).
+template <int T, int B, int V>
+__global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
+    constexpr int kVec = Row<T>::kVec;
+    constexpr int kWaves = B / kLanes;
+    using Stored = typename Row<T>::Stored;
+    extern __shared__ __align__(16) uint8_t lds[];
+    double *wz = reinterpret_cast<double *>(lds);                  // by wave
+    double *wr = reinterpret_cast<double *>(lds + 128);
+    double *out = reinterpret_cast<double *>(lds + 256);           // the row's reference, the factor
+    uint32_t *again = reinterpret_cast<uint32_t *>(lds + 272);     // a column is there more than once
+    const uint32_t slots = HeldLds::slots(a.k);
+    double *q = reinterpret_cast<double *>(lds + HeldLds::kFixed);
+    int32_t *col = reinterpret_cast<int32_t *>(q + slots);
+    float *sl = reinterpret_cast<float *>(col + slots);            // the student's logit, then the slot's gradient
+    float *tl = sl + slots;
+    uint32_t *map = reinterpret_cast<uint32_t *>(lds + HeldLds::map(a.k));
+    const uint32_t tid = threadIdx.x;
+    const int lane = tid % kLanes, wave = tid / kLanes;
+    const uint32_t n = a.n, k = a.k, vecs = n / kVec, rest = vecs * kVec + tid;
+    const float c = kLog2e * a.inv_t;
+    const bool tail = a.tlse != nullptr;
+    const uint32_t none = T == kRowF16 ? 0xFC00FC00u : T == kRowBF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+
+    const uint64_t row = a.first_row + blockIdx.x;
+    const Stored *x = static_cast<const Stored *>(a.logits) + row * a.stride;
+    Stored *g = static_cast<Stored *>(a.grad) + row * a.grad_stride;
+    float *stats = a.stats ? a.stats + row * (k + kStats) : nullptr;
+    const float weight = weight_at(a, row);
+    if (weight == 0.f) {  // whatever its logits hold
+        if (stats)
+            for (uint32_t j = tid; j < k + kStats; j += B) stats[j] = 0.f;
+        if (tid == 0) a.row_loss[row] = 0.f;
+        if (a.grad) {
+            for (uint32_t v = tid; v < vecs; v += B) store16(g + static_cast<uint64_t>(v) * kVec, u32x4{0, 0, 0, 0});
+            if (rest < n) g[rest] = 0;
+        }
+        return;
+    }
+    // the first slot of every thread, then the row
+    int64_t at = tid < k ? column_at(a, row, tid) : -1;
+    float t = tid < k ? teacher_at(a, row, tid) : 0.f;
+    u32x4 v[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        v[u] = u32x4{none, none, none, none};
+        if (u * B + tid < vecs) v[u] = load16(x + static_cast<uint64_t>(u * B + tid) * kVec);
+    }
+    float over = rest < n ? Row<T>::value(x[rest]) : -INFINITY;
+    for (uint32_t i = tid; i < (n + 31) / 32; i += B) map[i] = 0;
+    if (tid == 0) *again = 0;
+    __syncthreads();
+    Stored raw = 0;
+#pragma unroll 1
+    for (uint32_t j = tid; j < k; j += B) {
+        if (j != tid) {
+            at = column_at(a, row, j);
+            t = teacher_at(a, row, j);
+        }
+        const bool counts = at >= 0 && at < n && t > -INFINITY;
+        col[j] = counts ? static_cast<int32_t>(at) : -1;
+        tl[j] = t;
+        if (counts) {
+            const uint32_t bit = 1u << (at % 32);
+            if (atomicOr(&map[at / 32], bit) & bit) *again = 1;
+            if (j == tid) raw = x[at];
+        }
+    }
+    __syncthreads();
+    // the teacher's masses, while the row is on its way
+    double sum = 0, known = 0;
+    uint32_t distinct = 0;
+    if (wave == 0) {
+        float tm = -INFINITY;
+#pragma unroll 1
+        for (uint32_t j = lane; j < k; j += kLanes)
+            if (col[j] >= 0) tm = fmaxf(tm, tl[j]);
+        tm = wave_max(tm);
+        known = tail ? a.tlse[row] : tm == -INFINITY ? 0.0 : static_cast<double>(tm) * a.inv_t;
+#pragma unroll 1
+        for (uint32_t j = lane; j < k; j += kLanes) {
+            const double e = col[j] >= 0 ? exp(static_cast<double>(tl[j]) * a.inv_t - known) : 0;
+            q[j] = e;
+            sum += e;
+            bool first = col[j] >= 0;
+            if (*again)
+#pragma unroll 1
+                for (uint32_t i = 0; i < j; ++i) first &= col[i] != col[j];
+            distinct += first;
+        }
+        sum = wave_sum(sum);
+        distinct = wave_sum(distinct);
+    }
+    if (tail) {  // S does not count in the sum
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const uint32_t e0 = (u * B + tid) * kVec;
+            if (e0 < n) {
+                const uint32_t bits = (map[e0 / 32] >> (e0 % 32)) & ((1u << kVec) - 1);
+                if (bits) {
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e)
+                        if ((bits >> e) & 1) {
+                            if (T == kRowF32) v[u][e % 4] = none;
+                            else v[u][e / 2] = e & 1 ? (v[u][e / 2] & 0xFFFFu) | (none & 0xFFFF0000u)
+                                                     : (v[u][e / 2] & 0xFFFF0000u) | (none & 0xFFFFu);
+                        }
+                }
+            }
+        }
+        if (rest < n && ((map[rest / 32] >> (rest % 32)) & 1)) over = -INFINITY;
+    }
+    float m = over;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        float f[kVec];
+        unpack16<T>(v[u], f);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) m = f[e] > m ? f[e] : m;
+    }
+    // each pass unpacks the held words anew: their floats would take twice the registers
+    const auto anew = [&]() {
+#pragma unroll
+        for (int u = 0; u < V; ++u) asm volatile("" : "+v"(v[u]));
+    };
+    anew();
+    m = wave_max(m);
+    float r = m == -INFINITY ? 0.f : rintf(m * c);
+    // logits as large as the type's lowest value: all but the largest have no
+    // share, and x c need not be finite
+    const bool huge = huge_logit(m, c);
+    if (huge) {
+        r = 0.f;
+        const auto only = [&](float f) { return f == m ? 0.f : f != f ? f : -INFINITY; };
+        for (int u = 0; u < V; ++u) {
+            float f[kVec];
+            unpack16<T>(v[u], f);
+            for (int e = 0; e < kVec; ++e) f[e] = only(f[e]);
+            v[u] = pack16<T>(f);
+        }
+        over = only(over);
+        anew();
+    }
+    const double reference = m == -INFINITY ? -INFINITY : huge ? static_cast<double>(m) * c : r;
+    float part = __builtin_amdgcn_exp2f(fmaf(over, c, -r));
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        float f[kVec];
+        unpack16<T>(v[u], f);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) part += __builtin_amdgcn_exp2f(fmaf(f[e], c, -r));
+    }
+    anew();
+    const double z_wave = wave_sum(static_cast<double>(part));
+    if (lane == 0) {
+        wz[wave] = z_wave;
+        wr[wave] = reference;
+    }
+#pragma unroll 1
+    for (uint32_t j = tid; j < k; j += B)
+        sl[j] = col[j] < 0 ? -INFINITY : Row<T>::value(j == tid ? raw : x[col[j]]);
+    __syncthreads();
+    if (wave == 0) {
+        // the row's sum (off S where there is a tail)
+        double R = lane < kWaves ? wr[lane] : -INFINITY;
+        double z = lane < kWaves ? wz[lane] : 0;
+        const double mine = R;
+        R = wave_max(R);
+        const bool empty = R == -INFINITY;
+        if (mine != -INFINITY) z = ldexp(z, static_cast<int>(fmax(mine - R, -4000.0)));
+        z = wave_sum(z);
+        double scale = 1, q0 = 0, mass = sum;
+        if (tail) {
+            q0 = fmax(0.0, 1.0 - sum);
+            if (distinct == n || (empty && q0 <= 0x1p-20)) q0 = 0;
+        } else {
+            scale = sum > 0 ? 1 / sum : 0;
+            mass = sum > 0 ? 1 : 0;
+        }
+        // the whole row's
+        double whole_r = empty ? 0.0 : R;
+        double whole = z;
+        if (tail) {
+            float sm = -INFINITY;
+#pragma unroll 1
+            for (uint32_t j = lane; j < k; j += kLanes) sm = fmaxf(sm, sl[j]);
+            sm = wave_max(sm);
+            if (sm != -INFINITY) whole_r = fmax(empty ? -INFINITY : R, rint(static_cast<double>(sm) * c));
+            double on = 0;
+#pragma unroll 1
+            for (uint32_t j = lane; j < k; j += kLanes) {
+                bool first = col[j] >= 0 && sl[j] != -INFINITY;
+                if (first && *again)
+#pragma unroll 1
+                    for (uint32_t i = 0; i < j; ++i) first &= col[i] != col[j];
+                if (first) on += power_of_two(static_cast<double>(sl[j]) * c - whole_r);
+            }
+            on = wave_sum(on);
+            whole = on + (empty ? z : ldexp(z, static_cast<int>(fmax(R - whole_r, -4000.0))));
+        }
+        // the logarithms, a lane each
+        const double of = lane == 0 ? whole : lane == 1 ? z : lane == 2 ? q0 : sum;
+        const double logs = log2(of);
+        // log-sum-exps stay apart from their references, which may be huge
+        const double lse = __shfl(logs, 0), lse0 = __shfl(logs, 1) + ((empty ? 0.0 : R) - whole_r);
+        const double log_q0 = __shfl(logs, 2), log_sum = tail ? 0 : __shfl(logs, 3);
+        const double a_mass = mass + q0;
+        constexpr double kLn2 = 0.693147180559945309417;
+        double loss = 0;
+#pragma unroll 1
+        for (uint32_t j = lane; j < k; j += kLanes) {
+            double grad = 0;
+            if (col[j] >= 0) {
+                const double qj = q[j] * scale, arg = static_cast<double>(sl[j]) * c - whole_r - lse;
+                const bool zero = sl[j] == -INFINITY;
+                if (qj > 0)
+                    loss += zero ? INFINITY
+                                 : qj * (static_cast<double>(tl[j]) * a.inv_t - known - (log_sum + arg) * kLn2);
+                double all = q[j];  // what the teacher puts on this column, if it is there more than once
+                if (*again) {
+                    all = 0;
+#pragma unroll 1
+                    for (uint32_t i = 0; i < k; ++i)
+                        if (col[i] == col[j]) all += q[i];
+                }
+                grad = (zero ? 0 : a_mass * power_of_two(arg)) - all * scale;
+            }
+            const float gj = static_cast<float>(grad);
+            if (stats) stats[kStats + j] = gj;
+            sl[j] = gj;
+        }
+        loss = wave_sum(loss);
+        if (lane == 0) {
+            if (q0 > 0) loss += empty ? INFINITY : q0 * (log_q0 - (lse0 - lse)) * kLn2;
+            a.row_loss[row] = static_cast<float>(loss);
+            double f = 0;
+            if (!empty) {
+                f = a_mass * ldexp(1.0, static_cast<int>(fmax(R - whole_r, -4000.0))) / whole;
+                if (q0 > 0) f -= q0 / z;
+            }
+            out[0] = empty ? 0.0 : R;
+            out[1] = f;
+            if (stats) write_stats(stats, out[0], c, f);
+        }
+    }
+    if (!a.grad) return;
+    __syncthreads();
+    const float scale = weight * a.inv_t, f = static_cast<float>(out[1]) * scale;
+    r = m == -INFINITY ? 0.f : !huge ? static_cast<float>(out[0]) : reference == out[0] ? 0.f : INFINITY;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        if (u * B + tid < vecs) {
+            float e[kVec];
+            unpack16<T>(v[u], e);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(e[i], c, -r)) * f;
+            store16(g + static_cast<uint64_t>(u * B + tid) * kVec, pack16<T>(e));
+        }
+    }
+    if (rest < n) g[rest] = Row<T>::pattern(__builtin_amdgcn_exp2f(fmaf(over, c, -r)) * f);
+    // the teacher's columns over what was written there
+    __syncthreads();
+#pragma unroll 1
+    for (uint32_t j = tid; j < k; j += B)
+        if (col[j] >= 0) g[col[j]] = Row<T>::pattern(sl[j] * scale);
+}
 
 // How many workgroups share a row: enough that few rows still fill the GPU,
 // each with a piece worth a workgroup.
@@ -340,7 +641,8 @@ int check_sizes(int64_t rows, int64_t n, int64_t k, int dtype) {
 struct DisSpace {
     uint64_t partial = 0, stats = 0, row_loss = 0, total = 0;
 };
-DisSpace distill_space(uint64_t rows, uint64_t n, uint64_t k) {
+bool distill_held(uint64_t n, uint64_t size);
+DisSpace distill_space(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
     DisSpace w;
     if (rows == 0) return w;
     uint32_t splits, len;
@@ -350,8 +652,10 @@ DisSpace distill_space(uint64_t rows, uint64_t n, uint64_t k) {
         w.total += (bytes + 255) / 256 * 256;
         return at;
     };
-    w.partial = place(rows * splits * sizeof(float2));
-    w.stats = place(rows * (k + 2) * sizeof(float));
+    if (!distill_held(n, size)) {
+        w.partial = place(rows * splits * sizeof(float2));
+        w.stats = place(rows * (k + kStats) * sizeof(float));
+    }
     w.row_loss = place(rows * sizeof(float));
     return w;
 }
@@ -420,8 +724,44 @@ template <int T> void distill_launch_grad(const DisArgs &a, const Ctx &c) {
               dim3(kDisBlock), t.L, a);
 }
 
+// Rows of at most 256 KB are held in registers: by workgroups of 1024 threads
+// where there are no more rows than CUs, by the fewest threads that hold one
+// where several workgroups share a CU.
+constexpr uint64_t kHeldBytes = 1024 * 16 * 16;
+bool distill_held(uint64_t n, uint64_t size) { return n * size <= kHeldBytes; }
+
+template <int T> void distill_launch_held(const DisArgs &a, uint32_t rows, const Ctx &c) {
+    TimedLaunch t(4, c);
+    const dim3 grid(rows);
+    const uint32_t lds = HeldLds::bytes(a.k, a.n);
+    const uint64_t vecs = a.n / Row<T>::kVec;
+    const auto go = [&](auto kernel, int block) { launch_lds(kernel, grid, dim3(block), lds, t.L, a); };
+    if (a.rows <= 256) {
+        if (vecs <= 1024 * 2) return go(distill_held_kernel<T, 1024, 2>, 1024);
+        if (vecs <= 1024 * 4) return go(distill_held_kernel<T, 1024, 4>, 1024);
+        if (vecs <= 1024 * 8) return go(distill_held_kernel<T, 1024, 8>, 1024);
+        return go(distill_held_kernel<T, 1024, 16>, 1024);
+    }
+    if (vecs <= 256 * 2) return go(distill_held_kernel<T, 256, 2>, 256);
+    if (vecs <= 256 * 4) return go(distill_held_kernel<T, 256, 4>, 256);
+    if (vecs <= 256 * 8) return go(distill_held_kernel<T, 256, 8>, 256);
+    if (vecs <= 256 * 16) return go(distill_held_kernel<T, 256, 16>, 256);
+    if (vecs <= 512 * 16) return go(distill_held_kernel<T, 512, 16>, 512);
+    go(distill_held_kernel<T, 1024, 16>, 1024);
+}
+
+// The loss and what a gradient needs; with a.grad and held rows the gradient too.
 int distill_forward(const DisArgs &a, int dtype, const Ctx &c) {
-    if (a.rows > 0) {
+    if (a.rows > 0 && distill_held(a.n, row_type_size(dtype))) {
+        DisArgs part = a;
+        for (; part.first_row < a.rows; part.first_row += kMaxGrid) {
+            const uint32_t rows = static_cast<uint32_t>(std::min<uint64_t>(a.rows - part.first_row, kMaxGrid));
+            if (dtype == LRS_DTYPE_FP16) distill_launch_held<kRowF16>(part, rows, c);
+            else if (dtype == LRS_DTYPE_BF16) distill_launch_held<kRowBF16>(part, rows, c);
+            else distill_launch_held<kRowF32>(part, rows, c);
+            if (hipGetLastError() != hipSuccess) return LRS_ERR_HIP;
+        }
+    } else if (a.rows > 0) {
         if (dtype == LRS_DTYPE_FP16) distill_launch_sums<kRowF16>(a, c);
         else if (dtype == LRS_DTYPE_BF16) distill_launch_sums<kRowBF16>(a, c);
         else distill_launch_sums<kRowF32>(a, c);
@@ -449,14 +789,14 @@ int distill_run(const lrs_distill *d, float *loss, float *row_loss, float *stats
     const int st = distill_inputs(d, a);
     if (st != LRS_OK) return st;
     if (step && (!stride_ok(grad_stride, d->rows) || (d->rows > 1 && grad_stride < d->n))) return LRS_ERR_SIZE;
-    const DisSpace w = distill_space(a.rows, a.n, a.k);
+    const DisSpace w = distill_space(a.rows, a.n, a.k, row_type_size(d->dtype));
     if (!loss || (w.total && !workspace) || (step && a.rows && a.n && !grad)) return LRS_ERR_NULL_POINTER;
     const uint64_t size = row_type_size(d->dtype);
     if (misaligned(loss, 4) || misaligned(row_loss, 4) || misaligned(stats, 4) || misaligned(grad, size) ||
         (w.total && misaligned(workspace, 256)))
         return LRS_ERR_ALIGNMENT;
     if (workspace_bytes < w.total) return LRS_ERR_WORKSPACE_TOO_SMALL;
-    const uint64_t lb = row_loss ? 4 * a.rows : 0, sb = stats ? 4 * a.rows * (a.k + 2) : 0;
+    const uint64_t lb = row_loss ? 4 * a.rows : 0, sb = stats ? 4 * a.rows * (a.k + kStats) : 0;
     const uint64_t gb = step ? span(a.rows, grad_stride, a.n, size) : 0;
     const void *out[] = {loss, row_loss, stats, grad, workspace};
     const uint64_t bytes[] = {4, lb, sb, gb, w.total};
@@ -468,14 +808,15 @@ int distill_run(const lrs_distill *d, float *loss, float *row_loss, float *stats
     }
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.partial = reinterpret_cast<float2 *>(ws + w.partial);
-    a.stats = stats ? stats : reinterpret_cast<float *>(ws + w.stats);
+    const bool held = distill_held(a.n, size);
+    a.stats = stats || held ? stats : reinterpret_cast<float *>(ws + w.stats);
     a.row_loss = row_loss ? row_loss : reinterpret_cast<float *>(ws + w.row_loss);
     a.loss = loss;
     a.grad = grad;
     a.grad_stride = static_cast<uint64_t>(grad_stride);
     c.elems = a.rows * a.n;
     const int fs = distill_forward(a, d->dtype, c);
-    return fs != LRS_OK || !step ? fs : distill_backward(a, d->dtype, c);
+    return fs != LRS_OK || !step || held ? fs : distill_backward(a, d->dtype, c);
 }
 
 }  // namespace
@@ -487,7 +828,7 @@ extern "C" {
 
 size_t topk_distill_workspace_size(int64_t rows, int64_t n, int64_t k, int dtype, const lrs_options *opts) {
     if (!options_ok(opts) || check_sizes(rows, n, k, dtype) != LRS_OK) return 0;
-    return static_cast<size_t>(distill_space(rows, n, k).total);
+    return static_cast<size_t>(distill_space(rows, n, k, row_type_size(dtype)).total);
 }
 
 int topk_distill_forward(const lrs_distill *in, float *loss, float *row_loss, float *row_stats, void *workspace,
@@ -517,7 +858,7 @@ int topk_distill_backward(const lrs_distill *in, const float *row_stats, const f
     const uint64_t size = row_type_size(in->dtype);
     if (misaligned(row_stats, 4) || misaligned(loss_grad, 4) || misaligned(grad, size)) return LRS_ERR_ALIGNMENT;
     const uint64_t gb = span(a.rows, grad_stride, a.n, size);
-    if (hits_input(in, grad, gb) || overlaps(grad, gb, row_stats, 4 * a.rows * (a.k + 2)) ||
+    if (hits_input(in, grad, gb) || overlaps(grad, gb, row_stats, 4 * a.rows * (a.k + kStats)) ||
         overlaps(grad, gb, loss_grad, loss_grad ? 4 : 0))
         return LRS_ERR_ALIASING;
     a.stats = const_cast<float *>(row_stats);

@@ -97,5 +97,9 @@ __device__ inline float wave_max(float v) {
     for (int d = kLanes / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
     return v;
 }
+__device__ inline double wave_max(double v) {
+    for (int d = kLanes / 2; d > 0; d >>= 1) v = fmax(v, __shfl_xor(v, d));
+    return v;
+}
 
 }  // namespace lrs

@@ -164,7 +164,7 @@ def topk_distill_forward(logits: torch.Tensor, teacher_values: torch.Tensor, tea
     workspace = _distill_workspace(lib, workspace, d, opt, logits.device)
     loss = torch.empty((), dtype=torch.float32, device=logits.device)
     row_loss = torch.empty(d.rows, dtype=torch.float32, device=logits.device)
-    stats = torch.empty((d.rows, d.k + 2), dtype=torch.float32, device=logits.device)
+    stats = torch.empty((d.rows, d.k + 3), dtype=torch.float32, device=logits.device)
     _lrs._check(lib.topk_distill_forward(ctypes.byref(d), loss.data_ptr(), row_loss.data_ptr(), stats.data_ptr(),
                                          workspace.data_ptr(), workspace.numel(), _lrs._stream(logits), opt),
                 "topk_distill_forward")
@@ -179,7 +179,7 @@ def topk_distill_backward(logits: torch.Tensor, teacher_values: torch.Tensor, te
     and the row_stats that the forward returned."""
     lib = _lrs.load_library()
     d = _distill_inputs(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights)
-    _lrs.check_output(row_stats, "row_stats", logits.device, 4, (d.rows, d.k + 2))
+    _lrs.check_output(row_stats, "row_stats", logits.device, 4, (d.rows, d.k + 3))
     grad_out = _grad_out(grad_out, logits)
     _lrs._check(lib.topk_distill_backward(ctypes.byref(d), row_stats.data_ptr(), _scale(loss_grad, logits.device),
                                           grad_out.data_ptr(), grad_out.stride(0), _lrs._stream(logits),

@@ -341,3 +341,58 @@ def test_no_rows():
     loss, row_loss, grad = lrs.topk_distill_step(e, torch.empty(0, 3, device="cuda"),
                                                  torch.empty(0, 3, dtype=torch.int64, device="cuda"))
     assert float(loss) == 0 and row_loss.numel() == 0 and grad.shape == (0, 100)
+
+
+def check_shifted(s, t, i, temperature, tlse):
+    """check for logits so large that 64 bits lose log n beside them: the formulas of the rows less their largest."""
+    rows, n = s.shape
+    dtype = {v: k for k, v in DTYPES.items()}[s.dtype]
+    wr = torch.full((rows,), 1.0 / rows)
+    top = s.double().max(1, keepdim=True)[0]
+    loss, grad, terms, z = reference(s.double() - top, t, i, temperature, tlse, wr)
+    args = (s.cuda(), t.cuda(), i.cuda())
+    gl = None if tlse is None else tlse.cuda()
+    _, row_loss, stats = lrs.topk_distill_forward(*args, temperature, gl)
+    back = lrs.topk_distill_backward(*args, stats, temperature, gl)
+    _, row_loss2, step = lrs.topk_distill_step(*args, temperature, gl)
+    tol = (n / 256 + 64) * ULP
+    fine = torch.isfinite(loss)
+    for got in (row_loss.cpu().double(), row_loss2.cpu().double()):
+        assert torch.equal(torch.isinf(got), ~fine) and not torch.isnan(got).any()
+        assert bool(((got - loss)[fine].abs() <= tol + 2 * ULP * loss[fine].abs()).all())
+    # what is far below the row's largest has no share at all
+    spread = torch.where(z < -1000, torch.zeros_like(z), z).abs()
+    lim = terms * (tol + 4 * ULP * (spread + 1)) + half_step(dtype, grad)
+    for name, got in (("backward", back), ("step", step)):
+        off = (got.cpu().double() - grad).abs()
+        assert bool((off <= lim).all()), f"{name}: gradient off by {(off - lim).max()} over its bound"
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("temperature", [1.0, 0.5, 3.0])
+@pytest.mark.parametrize("n,k", [(50, 4), (9001, 30), (70_001, 5)])
+def test_lowest_values_as_masks(dtype, tail, temperature, n, k):
+    """Masks of the type's lowest value: some columns, all but S, a whole row, all but one column."""
+    log(f"lowest {dtype} tail={tail} T={temperature} n={n}")
+    s, t, i, tlse = make(6, n, k, dtype, 700, tail, temperature)
+    low = torch.finfo(s.dtype).min
+    off = [next(j for j in range(n // 2, n) if j not in set(i[r].tolist())) for r in range(6)]
+    # a column of S under such a mask is left out where others are not: its loss would pass 32 bits
+    s[0, ::3] = low
+    s[0, i[0]] = 1.0
+    s[1] = low
+    s[2] = low
+    s[2, i[2]] = 1.5
+    s[2, off[2]] = 0.5
+    s[3] = low
+    s[3, i[3]] = -9.0
+    s[3, off[3]] = -2.0
+    s[4, :n // 2] = -math.inf
+    s[4, n // 2:] = low
+    s[4, i[4, 0]] = low
+    check_shifted(s, t, i, temperature, tlse)
+    s[5] = torch.finfo(s.dtype).max / 2
+    s[5, ::2] = torch.finfo(s.dtype).max / 4
+    s[5, i[5]] = torch.finfo(s.dtype).max / 2
+    check_shifted(s, t, i, temperature, tlse)
