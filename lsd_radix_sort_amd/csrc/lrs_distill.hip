@@ -340,6 +340,39 @@ __device__ inline double power_of_two(double d) {
                  static_cast<int>(fmax(fmin(i, 2000.0), -2000.0)));
 }
 
+// 2^d to about 44 bits: the series of exp on |y| <= ln 2 / 2, cut after
+// y^11 / 11!.  Its coefficients go through scalar registers, made where they
+// are used: in a loop that holds a row they would otherwise be kept in 22
+// vector registers throughout.
+__device__ inline double scalar(double v) {
+    asm volatile("" : "+s"(v));
+    return v;
+}
+constexpr double kLn2 = 0.693147180559945309417;
+__device__ inline double exp2_64(double d) {
+    const double i = rint(d), y = (d - i) * scalar(kLn2);
+    double p = scalar(1.0 / 39916800);
+    p = fma(p, y, scalar(1.0 / 3628800));
+    p = fma(p, y, scalar(1.0 / 362880));
+    p = fma(p, y, scalar(1.0 / 40320));
+    p = fma(p, y, scalar(1.0 / 5040));
+    p = fma(p, y, scalar(1.0 / 720));
+    p = fma(p, y, scalar(1.0 / 120));
+    p = fma(p, y, scalar(1.0 / 24));
+    p = fma(p, y, scalar(1.0 / 6));
+    p = fma(p, y, 0.5);
+    p = fma(p, y, 1.0);
+    p = fma(p, y, 1.0);
+    return ldexp(p, static_cast<int>(fmax(fmin(i, 2000.0), -2000.0)));
+}
+// log2 of a number in the range of 32 bits: the hardware's, and the rest from
+// log(1 + e) = e - e^2 / 2 at e = v 2^-that - 1, below 2^-20.
+__device__ inline double log2_64(double v) {
+    const double y = __builtin_amdgcn_logf(static_cast<float>(v));
+    const double e = v * exp2_64(-y) - 1.0;
+    return y + fma(e * e, -0.5, e) * scalar(1.0 / kLn2);
+}
+
 // LDS of a held row: what is known of the k slots, the partial sums and the
 // bitmap of the columns in S (last).
 struct HeldLds {
@@ -350,7 +383,8 @@ struct HeldLds {
 };
 
 // One workgroup of B threads a row, V loads of 16 bytes a thread held in
-// registers from the one read to the gradient.  Exponents are in units of
+// registers from the one read to the gradient, both past the caches' usual
+// order (nontemporal): nothing of them is read again.  Exponents are in units of
 // log 2 with c = log2(e) / T rounded to 32 bits, everywhere the same c, and
 // references to them are whole numbers R: the sums of 2^(x c - R) of two waves
 // join exactly, and log2 sum 2^(x c) = R + log2(sum).
@@ -363,21 +397,24 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
     double *wz = reinterpret_cast<double *>(lds);                  // by wave
     double *wr = reinterpret_cast<double *>(lds + 128);
     double *out = reinterpret_cast<double *>(lds + 256);           // the row's reference, the factor
-    uint32_t *again = reinterpret_cast<uint32_t *>(lds + 272);     // a column is there more than once
+    double *teacher = reinterpret_cast<double *>(lds + 272);       // its reference, its mass on S
+    uint32_t *again = reinterpret_cast<uint32_t *>(lds + 288);     // a column is there more than once
+    uint32_t *columns = again + 1;                                 // distinct ones
     const uint32_t slots = HeldLds::slots(a.k);
     double *q = reinterpret_cast<double *>(lds + HeldLds::kFixed);
     int32_t *col = reinterpret_cast<int32_t *>(q + slots);
     float *sl = reinterpret_cast<float *>(col + slots);            // the student's logit, then the slot's gradient
     float *tl = sl + slots;
     uint32_t *map = reinterpret_cast<uint32_t *>(lds + HeldLds::map(a.k));
-    const uint32_t tid = threadIdx.x;
-    const int lane = tid % kLanes, wave = tid / kLanes;
-    const uint32_t n = a.n, k = a.k, vecs = n / kVec, rest = vecs * kVec + tid;
+    const uint32_t tid = threadIdx.x, vecs = a.n / kVec;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kLanes);
+    const uint32_t n = a.n, k = a.k, rest = vecs * kVec + tid;
     const float c = kLog2e * a.inv_t;
     const bool tail = a.tlse != nullptr;
     const uint32_t none = T == kRowF16 ? 0xFC00FC00u : T == kRowBF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
 
-    const uint64_t row = a.first_row + blockIdx.x;
+    const int lane = tid % kLanes;
+    const uint64_t row = a.first_row + xcd_chunk(blockIdx.x, gridDim.x);
     const Stored *x = static_cast<const Stored *>(a.logits) + row * a.stride;
     Stored *g = static_cast<Stored *>(a.grad) + row * a.grad_stride;
     float *stats = a.stats ? a.stats + row * (k + kStats) : nullptr;
@@ -387,21 +424,31 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
             for (uint32_t j = tid; j < k + kStats; j += B) stats[j] = 0.f;
         if (tid == 0) a.row_loss[row] = 0.f;
         if (a.grad) {
-            for (uint32_t v = tid; v < vecs; v += B) store16(g + static_cast<uint64_t>(v) * kVec, u32x4{0, 0, 0, 0});
+            for (uint32_t v = tid; v < vecs; v += B) store16_once(g + static_cast<uint64_t>(v) * kVec, u32x4{0, 0, 0, 0});
             if (rest < n) g[rest] = 0;
         }
         return;
     }
-    // the first slot of every thread, then the row
+    // the first slot of every thread, then the row: a scalar base, one offset for all
     int64_t at = tid < k ? column_at(a, row, tid) : -1;
     float t = tid < k ? teacher_at(a, row, tid) : 0.f;
+    const auto below = [&](uint32_t count, int u) { return static_cast<int>(tid) < static_cast<int>(count) - u * B; };
     u32x4 v[V];
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-        v[u] = u32x4{none, none, none, none};
-        if (u * B + tid < vecs) v[u] = load16(x + static_cast<uint64_t>(u * B + tid) * kVec);
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(x + u * B * kVec) + tid * 16;
+        if ((u + 1) * B <= vecs) {
+            v[u] = load16_once(p);
+        } else {
+            v[u] = u32x4{none, none, none, none};
+            if (below(vecs, u)) v[u] = load16_once(p);
+        }
     }
     float over = rest < n ? Row<T>::value(x[rest]) : -INFINITY;
+    float r = 0.f, factor = 1.f, m = 0.f;
+    uint32_t sign = 0;
+    bool huge = false;
+    double reference = 0;
     for (uint32_t i = tid; i < (n + 31) / 32; i += B) map[i] = 0;
     if (tid == 0) *again = 0;
     __syncthreads();
@@ -423,18 +470,18 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
     }
     __syncthreads();
     // the teacher's masses, while the row is on its way
-    double sum = 0, known = 0;
-    uint32_t distinct = 0;
     if (wave == 0) {
+        double sum = 0;
+        uint32_t distinct = 0;
         float tm = -INFINITY;
 #pragma unroll 1
         for (uint32_t j = lane; j < k; j += kLanes)
             if (col[j] >= 0) tm = fmaxf(tm, tl[j]);
         tm = wave_max(tm);
-        known = tail ? a.tlse[row] : tm == -INFINITY ? 0.0 : static_cast<double>(tm) * a.inv_t;
+        const double known = tail ? a.tlse[row] : tm == -INFINITY ? 0.0 : static_cast<double>(tm) * a.inv_t;
 #pragma unroll 1
         for (uint32_t j = lane; j < k; j += kLanes) {
-            const double e = col[j] >= 0 ? exp(static_cast<double>(tl[j]) * a.inv_t - known) : 0;
+            const double e = col[j] >= 0 ? exp2_64((static_cast<double>(tl[j]) * a.inv_t - known) * scalar(1.0 / kLn2)) : 0;
             q[j] = e;
             sum += e;
             bool first = col[j] >= 0;
@@ -445,13 +492,17 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
         }
         sum = wave_sum(sum);
         distinct = wave_sum(distinct);
+        if (lane == 0) {
+            teacher[0] = known;
+            teacher[1] = sum;
+            *columns = distinct;
+        }
     }
     if (tail) {  // S does not count in the sum
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            const uint32_t e0 = (u * B + tid) * kVec;
-            if (e0 < n) {
-                const uint32_t bits = (map[e0 / 32] >> (e0 % 32)) & ((1u << kVec) - 1);
+            if (below(vecs, u)) {
+                const uint32_t bits = (map[u * (B * kVec / 32) + tid * kVec / 32] >> (tid * kVec % 32)) & ((1u << kVec) - 1);
                 if (bits) {
 #pragma unroll
                     for (int e = 0; e < kVec; ++e)
@@ -465,48 +516,54 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
         }
         if (rest < n && ((map[rest / 32] >> (rest % 32)) & 1)) over = -INFINITY;
     }
-    float m = over;
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
-        float f[kVec];
-        unpack16<T>(v[u], f);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) m = f[e] > m ? f[e] : m;
-    }
     // each pass unpacks the held words anew: their floats would take twice the registers
     const auto anew = [&]() {
 #pragma unroll
         for (int u = 0; u < V; ++u) asm volatile("" : "+v"(v[u]));
     };
-    anew();
-    m = wave_max(m);
-    float r = m == -INFINITY ? 0.f : rintf(m * c);
-    // logits as large as the type's lowest value: all but the largest have no
-    // share, and x c need not be finite
-    const bool huge = huge_logit(m, c);
-    if (huge) {
-        r = 0.f;
-        const auto only = [&](float f) { return f == m ? 0.f : f != f ? f : -INFINITY; };
-        for (int u = 0; u < V; ++u) {
-            float f[kVec];
-            unpack16<T>(v[u], f);
-            for (int e = 0; e < kVec; ++e) f[e] = only(f[e]);
-            v[u] = pack16<T>(f);
-        }
-        over = only(over);
-        anew();
-    }
-    const double reference = m == -INFINITY ? -INFINITY : huge ? static_cast<double>(m) * c : r;
-    float part = __builtin_amdgcn_exp2f(fmaf(over, c, -r));
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
+    const auto larger = [&](float m, int u) {
         float f[kVec];
         unpack16<T>(v[u], f);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) part += __builtin_amdgcn_exp2f(fmaf(f[e], c, -r));
+        for (int e = 0; e < kVec; ++e) m = f[e] > m ? f[e] : m;
+        return m;
+    };
+    const auto sum_of = [&](auto term) {
+        float part = term(over);
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            float f[kVec];
+            unpack16<T>(v[u], f);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) part += term(f[e]);
+        }
+        return wave_sum(static_cast<double>(part));
+    };
+    const auto power = [&](float x) { return __builtin_amdgcn_exp2f(fmaf(x, c, -r)); };
+    // A sum needs a reference near its largest term, not at it: first one from
+    // the first load of each lane, and if the sum then leaves its range, the
+    // largest of all.
+    m = wave_max(larger(over, 0));
+    r = m == -INFINITY || huge_logit(m, c) ? 0.f : rintf(m * c);
+    anew();
+    double z_wave = sum_of(power);
+    anew();
+    reference = r;
+    if (!(z_wave >= 0x1p-20 && z_wave <= 0x1p40)) {
+        m = over;
+#pragma unroll
+        for (int u = 0; u < V; ++u) m = larger(m, u);
+        m = wave_max(m);
+        huge = huge_logit(m, c);
+        r = m == -INFINITY || huge ? 0.f : rintf(m * c);
+        reference = m == -INFINITY ? -INFINITY : huge ? static_cast<double>(m) * c : r;
     }
     anew();
-    const double z_wave = wave_sum(static_cast<double>(part));
+    // logits as large as the type's lowest value: all but the largest have no
+    // share, and x c need not be finite
+    if (huge) z_wave = sum_of([&](float x) { return x == m ? 1.f : x != x ? x : 0.f; });
+    else if (!(z_wave >= 0x1p-20 && z_wave <= 0x1p40)) z_wave = sum_of(power);
+    anew();
     if (lane == 0) {
         wz[wave] = z_wave;
         wr[wave] = reference;
@@ -519,7 +576,7 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
         // the row's sum (off S where there is a tail)
         double R = lane < kWaves ? wr[lane] : -INFINITY;
         double z = lane < kWaves ? wz[lane] : 0;
-        const double mine = R;
+        const double mine = R, known = teacher[0], sum = teacher[1];
         R = wave_max(R);
         const bool empty = R == -INFINITY;
         if (mine != -INFINITY) z = ldexp(z, static_cast<int>(fmax(mine - R, -4000.0)));
@@ -527,7 +584,7 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
         double scale = 1, q0 = 0, mass = sum;
         if (tail) {
             q0 = fmax(0.0, 1.0 - sum);
-            if (distinct == n || (empty && q0 <= 0x1p-20)) q0 = 0;
+            if (*columns == n || (empty && q0 <= 0x1p-20)) q0 = 0;
         } else {
             scale = sum > 0 ? 1 / sum : 0;
             mass = sum > 0 ? 1 : 0;
@@ -555,12 +612,11 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
         }
         // the logarithms, a lane each
         const double of = lane == 0 ? whole : lane == 1 ? z : lane == 2 ? q0 : sum;
-        const double logs = log2(of);
+        const double logs = log2_64(of);
         // log-sum-exps stay apart from their references, which may be huge
         const double lse = __shfl(logs, 0), lse0 = __shfl(logs, 1) + ((empty ? 0.0 : R) - whole_r);
         const double log_q0 = __shfl(logs, 2), log_sum = tail ? 0 : __shfl(logs, 3);
         const double a_mass = mass + q0;
-        constexpr double kLn2 = 0.693147180559945309417;
         double loss = 0;
 #pragma unroll 1
         for (uint32_t j = lane; j < k; j += kLanes) {
@@ -601,18 +657,41 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
     if (!a.grad) return;
     __syncthreads();
     const float scale = weight * a.inv_t, f = static_cast<float>(out[1]) * scale;
-    r = m == -INFINITY ? 0.f : !huge ? static_cast<float>(out[0]) : reference == out[0] ? 0.f : INFINITY;
+    r = reference == -INFINITY ? 0.f : static_cast<float>(out[0]);
+    if (huge) r = reference == out[0] ? 0.f : INFINITY;
+    // 16-bit gradients: the factor joins the exponent, where that keeps it to
+    // 2^-19, and its sign the result
+    const float joint = r - __builtin_amdgcn_logf(fabsf(f));
+    if (T != kRowF32 && fabsf(joint) < 64.f) {
+        r = joint;
+        sign = f < 0.f ? 0x80008000u : 0u;
+    } else {
+        factor = f;
+    }
+    const auto only = [&](float x) { return x == m ? 0.f : x != x ? x : -INFINITY; };
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-        if (u * B + tid < vecs) {
+        if (below(vecs, u)) {
             float e[kVec];
             unpack16<T>(v[u], e);
+            if (huge) {
+                for (int i = 0; i < kVec; ++i) e[i] = only(e[i]);
+            }
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(e[i], c, -r)) * f;
-            store16(g + static_cast<uint64_t>(u * B + tid) * kVec, pack16<T>(e));
+            for (int i = 0; i < kVec; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(e[i], c, -r));
+            if (factor != 1.f) {
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) e[i] *= factor;
+            }
+            u32x4 w = pack16<T>(e);
+            if (T != kRowF32) w ^= sign;
+            store16_once(reinterpret_cast<uint8_t *>(g + u * B * kVec) + tid * 16, w);
         }
     }
-    if (rest < n) g[rest] = Row<T>::pattern(__builtin_amdgcn_exp2f(fmaf(over, c, -r)) * f);
+    if (rest < n) {
+        const float e = __builtin_amdgcn_exp2f(fmaf(huge ? only(over) : over, c, -r));
+        g[rest] = Row<T>::pattern(e * factor) ^ static_cast<Stored>(sign);
+    }
     // the teacher's columns over what was written there
     __syncthreads();
 #pragma unroll 1
@@ -732,10 +811,11 @@ bool distill_held(uint64_t n, uint64_t size) { return n * size <= kHeldBytes; }
 
 template <int T> void distill_launch_held(const DisArgs &a, uint32_t rows, const Ctx &c) {
     TimedLaunch t(4, c);
-    const dim3 grid(rows);
     const uint32_t lds = HeldLds::bytes(a.k, a.n);
     const uint64_t vecs = a.n / Row<T>::kVec;
-    const auto go = [&](auto kernel, int block) { launch_lds(kernel, grid, dim3(block), lds, t.L, a); };
+    const auto go = [&](auto kernel, int block) {
+        launch_lds(kernel, dim3(rows), dim3(block), lds, t.L, a);
+    };
     if (a.rows <= 256) {
         if (vecs <= 1024 * 2) return go(distill_held_kernel<T, 1024, 2>, 1024);
         if (vecs <= 1024 * 4) return go(distill_held_kernel<T, 1024, 4>, 1024);

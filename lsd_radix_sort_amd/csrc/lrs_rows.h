@@ -24,6 +24,21 @@ typedef u32x4 u32x4_align2 __attribute__((aligned(2)));
 __device__ inline u32x4 load16(const void *p) { return *static_cast<const u32x4_align2 *>(p); }
 __device__ inline void store16(void *p, u32x4 v) { *static_cast<u32x4_align2 *>(p) = v; }
 
+// For what is read or written once: the same, without keeping it in the caches.
+__device__ inline u32x4 load16_once(const void *p) {
+    return __builtin_nontemporal_load(static_cast<const u32x4_align2 *>(p));
+}
+__device__ inline void store16_once(void *p, u32x4 v) {
+    __builtin_nontemporal_store(v, static_cast<u32x4_align2 *>(p));
+}
+
+// The task of a workgroup where each XCD takes a contiguous share of them
+// (workgroups go to the 8 XCDs in turn).
+__device__ inline uint32_t xcd_chunk(uint32_t block, uint32_t blocks) {
+    const uint32_t xcd = block % 8, share = blocks / 8, more = blocks % 8;
+    return xcd * share + min(xcd, more) + block / 8;
+}
+
 template <int T> struct Row;
 
 template <> struct Row<kRowF16> {
@@ -89,17 +104,51 @@ template <int T> __device__ inline u32x4 pack16(const float (&f)[Row<T>::kVec]) 
     return v;
 }
 
+// The lanes' values moved by a DPP control; lanes without a source, and rows of
+// 16 lanes outside ROWS, get `none`.
+template <int CONTROL, int ROWS = 0xF, typename V> __device__ inline V moved(V v, V none) {
+    static_assert(sizeof(V) == 4 || sizeof(V) == 8);
+    if constexpr (sizeof(V) == 4) {
+        return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v),
+                                                                 CONTROL, ROWS, 0xF, false));
+    } else {
+        typedef int pair __attribute__((ext_vector_type(2)));
+        const pair p = __builtin_bit_cast(pair, v), o = __builtin_bit_cast(pair, none);
+        const pair r = {__builtin_amdgcn_update_dpp(o.x, p.x, CONTROL, ROWS, 0xF, false),
+                        __builtin_amdgcn_update_dpp(o.y, p.y, CONTROL, ROWS, 0xF, false)};
+        return __builtin_bit_cast(V, r);
+    }
+}
+template <typename V> __device__ inline V last_lane(V v) {
+    if constexpr (sizeof(V) == 4) {
+        return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), kLanes - 1));
+    } else {
+        typedef int pair __attribute__((ext_vector_type(2)));
+        const pair p = __builtin_bit_cast(pair, v);
+        const pair r = {__builtin_amdgcn_readlane(p.x, kLanes - 1), __builtin_amdgcn_readlane(p.y, kLanes - 1)};
+        return __builtin_bit_cast(V, r);
+    }
+}
+// Joins the values of a whole wave, every lane active, in a fixed order: within
+// rows of 16 lanes (row_shr 1, 2, 4, 8), then across them (row_bcast 15, 31).
+// The result is the same in every lane, in scalar registers.
+template <typename V, typename F> __device__ inline V wave_join(V v, V none, F join) {
+    v = join(v, moved<0x111>(v, none));
+    v = join(v, moved<0x112>(v, none));
+    v = join(v, moved<0x114>(v, none));
+    v = join(v, moved<0x118>(v, none));
+    v = join(v, moved<0x142, 0xA>(v, none));
+    v = join(v, moved<0x143, 0xC>(v, none));
+    return last_lane(v);
+}
 template <typename V> __device__ inline V wave_sum(V v) {
-    for (int d = kLanes / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
-    return v;
+    return wave_join(v, V(0), [](V a, V b) { return a + b; });
 }
 __device__ inline float wave_max(float v) {
-    for (int d = kLanes / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+    return wave_join(v, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ inline double wave_max(double v) {
-    for (int d = kLanes / 2; d > 0; d >>= 1) v = fmax(v, __shfl_xor(v, d));
-    return v;
+    return wave_join(v, static_cast<double>(-INFINITY), [](double a, double b) { return fmax(a, b); });
 }
 
 }  // namespace lrs
