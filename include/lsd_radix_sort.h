@@ -343,6 +343,18 @@ int expert_balance(const void *logits, int64_t row_stride, const int32_t *counts
                    size_t workspace_bytes, void *stream, const lrs_options *opts);
 
 /*
+ * expert_counts and expert_balance on its counts in one call, for a step that
+ * needs no other rank's counts: counts_out [experts], rows_counted [1] (or
+ * NULL), loss and, unless it is NULL, the gradient with loss_grad 1.
+ */
+size_t expert_balance_step_workspace_size(int64_t rows, int64_t k, int64_t experts, const lrs_options *opts);
+int expert_balance_step(const void *logits, int64_t row_stride, const void *indices, int64_t index_stride, int index_bytes,
+                        const uint8_t *row_mask, int64_t rows, int64_t k, int64_t experts, int dtype, int score,
+                        float balance_weight, float z_weight, int32_t *counts_out, int32_t *rows_counted, float *loss,
+                        void *grad, int64_t grad_stride, void *workspace, size_t workspace_bytes, void *stream,
+                        const lrs_options *opts);
+
+/*
  * The per-pass digit counts of radix_sort_keys' first kernel: all passes'
  * histograms from one read of the keys (FlagTree PR #1084, step 2 "Before":
  * one kernel counts every pass).  hist_out[p * 2^b + d] = number of keys

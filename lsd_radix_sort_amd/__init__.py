@@ -116,6 +116,9 @@ def load_library():
         "expert_counts": ([P, i64, c_int, P, P, P, i64, i64, i64, P, O], c_int),
         "expert_balance_workspace_size": ([i64, i64, O], szt),
         "expert_balance": ([P, i64, P, P, P, i64, i64, c_int, c_int, F, F, P, P, P, i64, P, szt, P, O], c_int),
+        "expert_balance_step_workspace_size": ([i64, i64, i64, O], szt),
+        "expert_balance_step": ([P, i64, P, i64, c_int, P, i64, i64, i64, c_int, c_int, F, F, P, P, P, P, i64, P, szt, P, O],
+                                c_int),
         "radix_sort_status_string": ([c_int], ctypes.c_char_p),
     }
     for name, (args, res) in sigs.items():
@@ -551,5 +554,5 @@ def copy_probe(src: torch.Tensor, dst: torch.Tensor, options: SortOptions | None
 
 from .row_ops import (  # noqa: E402
     expert_balance_backward, expert_balance_forward, expert_balance_loss, expert_balance_step,
-    expert_balance_workspace_size, expert_counts, segmented_row_topk, segmented_row_topk_workspace_size,
+    expert_balance_step_workspace_size, expert_balance_workspace_size, expert_counts, segmented_row_topk, segmented_row_topk_workspace_size,
     topk_distill_backward, topk_distill_forward, topk_distill_loss, topk_distill_step, topk_distill_workspace_size)

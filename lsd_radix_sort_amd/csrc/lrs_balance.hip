@@ -70,16 +70,81 @@ __global__ __launch_bounds__(kBalBlock) void count_kernel(CountArgs a) {
     }
 }
 
+// The counts of a whole call by several workgroups: each its own share of the
+// ids, [blocks][experts + 1], the counted rows of its share last.  No order and
+// no clearing is needed; whoever uses the counts adds the shares.
+constexpr int kShareBlock = 1024;
+constexpr uint32_t kShareIds = 8;  // a thread has in flight
+
+struct IdArgs {
+    const void *idx;
+    int idx_bytes;
+    uint64_t stride;
+    const uint8_t *mask;
+    uint32_t rows, k, experts;
+};
+__device__ inline int64_t id_at(const IdArgs &a, uint64_t at) {
+    return a.idx_bytes == 8 ? static_cast<const int64_t *>(a.idx)[at] : static_cast<const int32_t *>(a.idx)[at];
+}
+// Adds ids [first, last) of the rows x k matrix, and the rows [row0, row1) that
+// count, to a histogram in LDS (experts + 1 cells, cleared by the caller).
+template <int B> __device__ void count_ids(const IdArgs &a, uint32_t first, uint32_t last, uint32_t row0, uint32_t row1,
+                                           int32_t *hist) {
+    const bool dense = a.stride == a.k && !a.mask;
+    for (uint32_t base = first + threadIdx.x; base < last; base += B * kShareIds) {
+        int64_t id[kShareIds];
+#pragma unroll
+        for (uint32_t u = 0; u < kShareIds; ++u) {
+            const uint32_t i = base + u * B;
+            id[u] = -1;
+            if (i < last && base <= 0xFFFFFFFFu - u * B) {
+                const uint32_t row = dense ? 0 : i / a.k;
+                if (dense || !a.mask || a.mask[row])
+                    id[u] = id_at(a, dense ? i : static_cast<uint64_t>(row) * a.stride + (i - row * a.k));
+            }
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < kShareIds; ++u)
+            if (id[u] >= 0 && id[u] < a.experts) atomicAdd(&hist[id[u]], 1);
+    }
+    int32_t kept = 0;
+    for (uint32_t r = row0 + threadIdx.x; r < row1; r += B) kept += !a.mask || a.mask[r];
+    kept = wave_sum(kept);
+    if (threadIdx.x % kLanes == 0 && kept) atomicAdd(&hist[a.experts], kept);
+}
+
+__global__ __launch_bounds__(kShareBlock) void count_share_kernel(IdArgs a, int32_t *shares, uint32_t *ticket) {
+    __shared__ int32_t hist[LRS_MAX_EXPERTS + 1];
+    for (uint32_t e = threadIdx.x; e <= a.experts; e += kShareBlock) hist[e] = 0;
+    __syncthreads();
+    const uint32_t total = a.rows * a.k, blocks = gridDim.x, b = blockIdx.x;
+    const uint64_t t = total, r = a.rows;
+    count_ids<kShareBlock>(a, static_cast<uint32_t>(t * b / blocks), static_cast<uint32_t>(t * (b + 1) / blocks),
+                           static_cast<uint32_t>(r * b / blocks), static_cast<uint32_t>(r * (b + 1) / blocks), hist);
+    __syncthreads();
+    for (uint32_t e = threadIdx.x; e <= a.experts; e += kShareBlock)
+        shares[static_cast<uint64_t>(b) * (a.experts + 1) + e] = hist[e];
+    if (b == 0 && threadIdx.x == 0) *ticket = 0;
+}
+
 struct BalArgs {
     const void *x;
     uint64_t stride;
     uint64_t rows;
     uint32_t experts;
+    uint32_t lanes;           // that share a row
     const uint8_t *mask;
+    // the counts: given, or as shares, or (neither) counted from `ids` by the one workgroup there is
     const int32_t *counts;
     const int32_t *kept;
+    const int32_t *shares;
+    uint32_t share_count;
+    IdArgs ids;
+    int32_t *counts_out;      // with shares or ids
+    int32_t *kept_out;
     float alpha, beta;
-    double *partial;  // by workgroup
+    double *partial;          // by workgroup
+    uint32_t *ticket;         // workgroups that are done; null: another kernel adds the partial sums
     uint32_t blocks;
     float *loss;
     const float *loss_grad;
@@ -87,80 +152,188 @@ struct BalArgs {
     uint64_t grad_stride;
 };
 
-// One wave a row.
-template <int T, bool SIG, bool LOSS, bool GRAD>
+__device__ inline float mean_of(double sum, int32_t kept) { return kept > 0 ? static_cast<float>(sum / kept) : 0.f; }
+
+// A row's elements in the registers of `lanes` neighbours, V loads of 16 bytes
+// each, from its one read to the gradient; 64 / lanes rows a wave at a time.
+// Bound by memory where rows are many: a row of 256 bf16 takes 32 lanes, some
+// 13 instructions an element, a third of the time that its bytes take.
+template <int T, bool SIG, int V>
 __global__ __launch_bounds__(kBalBlock) void balance_kernel(BalArgs a) {
+    constexpr int kVec = Row<T>::kVec;
     using Stored = typename Row<T>::Stored;
-    __shared__ float load[LRS_MAX_EXPERTS];
+    __shared__ int32_t hist[LRS_MAX_EXPERTS + 1];
     __shared__ double part[kBalWaves];
-    __shared__ int64_t total;
-    const int lane = threadIdx.x % kLanes, wave = threadIdx.x / kLanes;
-    if (wave == 0) {
-        int64_t s = 0;
-        for (uint32_t e = lane; e < a.experts; e += kLanes) s += a.counts[e];
-        s = wave_sum(s);
-        if (lane == 0) total = s;
+    __shared__ int64_t sums[kBalWaves];
+    __shared__ uint32_t arrived;
+    const uint32_t tid = threadIdx.x, E = a.experts;
+    const int lane = tid % kLanes, wave = tid / kLanes;
+    const uint32_t sub = lane % a.lanes;
+
+    // the first rows are on their way while the counts are added up
+    const uint64_t step = static_cast<uint64_t>(gridDim.x) * (kBalBlock / a.lanes);
+    uint64_t row = static_cast<uint64_t>(blockIdx.x) * (kBalBlock / a.lanes) + tid / a.lanes;
+    const uint32_t none = T == kRowF16 ? 0xFC00FC00u : T == kRowBF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+    u32x4 v[V];
+    bool counted = false;
+    const auto load_row = [&](uint64_t r) {
+        counted = r < a.rows && (!a.mask || a.mask[r]);
+        const Stored *x = static_cast<const Stored *>(a.x) + r * a.stride;
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const uint32_t at = (u * a.lanes + sub) * kVec;
+            v[u] = u32x4{none, none, none, none};
+            if (!counted || at >= E) continue;
+            if (at + kVec <= E) {
+                v[u] = load16_once(x + at);
+            } else {
+                float f[kVec];
+                for (int e = 0; e < kVec; ++e) f[e] = at + e < E ? Row<T>::value(x[at + e]) : -INFINITY;
+                v[u] = pack16<T>(f);
+            }
+        }
+    };
+    load_row(row);
+
+    if (a.counts) {
+        for (uint32_t e = tid; e < E; e += kBalBlock) hist[e] = a.counts[e];
+        if (tid == 0) hist[E] = a.kept ? *a.kept : static_cast<int32_t>(a.rows);
+    } else if (a.shares) {
+        for (uint32_t e = tid; e <= E; e += kBalBlock) {
+            int32_t c = 0;
+#pragma unroll 8
+            for (uint32_t b = 0; b < a.share_count; ++b) c += a.shares[static_cast<uint64_t>(b) * (E + 1) + e];
+            hist[e] = c;
+        }
+    } else {
+        for (uint32_t e = tid; e <= E; e += kBalBlock) hist[e] = 0;
+        __syncthreads();
+        count_ids<kBalBlock>(a.ids, 0, a.ids.rows * a.ids.k, 0, a.ids.rows, hist);
     }
     __syncthreads();
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kBalBlock)
-        load[e] = total > 0 ? static_cast<float>(static_cast<double>(a.counts[e]) * a.experts / total) : 0.f;
+    int64_t total = 0;
+    for (uint32_t e = tid; e < E; e += kBalBlock) total += hist[e];
+    total = wave_sum(total);
+    if (lane == 0) sums[wave] = total;
+    if (!a.counts && blockIdx.x == 0) {
+        for (uint32_t e = tid; e < E; e += kBalBlock) a.counts_out[e] = hist[e];
+        if (tid == 0 && a.kept_out) *a.kept_out = hist[E];
+    }
     __syncthreads();
-    const int32_t kept = a.kept ? *a.kept : static_cast<int32_t>(a.rows);
-    const float inv = kept > 0 ? 1.f / kept : 0.f;
-    const float up = (GRAD && a.loss_grad ? *a.loss_grad : 1.f) * inv;
-    double loss = 0;
-    for (uint64_t row = static_cast<uint64_t>(blockIdx.x) * kBalWaves + wave; row < a.rows;
-         row += static_cast<uint64_t>(gridDim.x) * kBalWaves) {
-        const Stored *x = static_cast<const Stored *>(a.x) + row * a.stride;
-        Stored *g = static_cast<Stored *>(a.grad) + row * a.grad_stride;
-        const bool counted = !a.mask || a.mask[row];
-        if (!counted) {
-            if (GRAD)
-                for (uint32_t e = lane; e < a.experts; e += kLanes) g[e] = 0;
-            continue;
+    total = 0;
+    for (int w = 0; w < kBalWaves; ++w) total += sums[w];
+    const int32_t kept = hist[E];
+    // this lane's columns stay the same from row to row
+    float load[V][kVec];
+    const double per = total > 0 ? static_cast<double>(E) / static_cast<double>(total) : 0;
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            const uint32_t at = (u * a.lanes + sub) * kVec + e;
+            load[u][e] = at < E ? static_cast<float>(hist[at] * per) : 0.f;
         }
-        float m = 0;
+    const float inv = kept > 0 ? 1.f / kept : 0.f;
+    const float up = (a.loss_grad ? *a.loss_grad : 1.f) * inv;
+    const auto plus = [](float p, float q) { return p + q; };
+    double loss = 0;
+    // every group of a wave makes the same number of turns
+    for (uint64_t base = row - tid / a.lanes; base < a.rows; base += step, row += step) {
+        const bool mine = counted;
+        float w[V][kVec];
+#pragma unroll
+        for (int u = 0; u < V; ++u) unpack16<T>(v[u], w[u]);
+        if (base + step < a.rows) load_row(row + step);
+        float m = -INFINITY;
         if (!SIG) {
-            m = -INFINITY;
-            for (uint32_t e = lane; e < a.experts; e += kLanes) m = fmaxf(m, Row<T>::value(x[e]));
-            m = wave_max(m);
+#pragma unroll
+            for (int u = 0; u < V; ++u)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) m = w[u][e] > m ? w[u][e] : m;
+            m = group_join(m, a.lanes, [](float p, float q) { return fmaxf(p, q); });
+            if (m == -INFINITY) m = 0.f;
         }
         float s = 0, b = 0;
-        for (uint32_t e = lane; e < a.experts; e += kLanes) {
-            const float v = Row<T>::value(x[e]);
-            const float w = SIG ? 1.f / (1.f + exp2f(-v * kLog2e)) : v == -INFINITY ? 0.f : exp2f((v - m) * kLog2e);
-            s += w;
-            b += w * load[e];
-        }
-        s = wave_sum(s);
-        b = wave_sum(b);
+        float slope[SIG ? V : 1][kVec];  // sigmoid times 1 - sigmoid, without the cancellation
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                if (SIG) {
+                    const float t = __builtin_amdgcn_exp2f(-w[u][e] * kLog2e), g = __builtin_amdgcn_rcpf(1.f + t);
+                    w[u][e] = g;
+                    slope[SIG ? u : 0][e] = g == 0.f ? 0.f : g * (g * t);
+                } else {
+                    w[u][e] = __builtin_amdgcn_exp2f((w[u][e] - m) * kLog2e);
+                }
+                s += w[u][e];
+                b += w[u][e] * load[u][e];
+            }
+        s = group_join(s, a.lanes, plus);
+        b = group_join(b, a.lanes, plus);
         const bool empty = s == 0.f;
         const float r = empty ? 0.f : 1.f / s;
         b *= r;
-        const float z = SIG || empty ? 0.f : m + log2f(s) * kLn2;
-        if (LOSS) loss += static_cast<double>(a.alpha * b + a.beta * z * z);
-        if (GRAD)
-            for (uint32_t e = lane; e < a.experts; e += kLanes) {
-                const float v = Row<T>::value(x[e]);
-                float d;
-                if (SIG) {
-                    const float t = exp2f(-v * kLog2e), w = 1.f / (1.f + t);
-                    // 1 - sigmoid(v) without the cancellation: sigmoid(-v)
-                    d = w == 0.f ? 0.f : w * r * (1.f / (1.f + exp2f(v * kLog2e))) * a.alpha * (load[e] - b);
+        const float z = SIG || empty ? 0.f : m + __builtin_amdgcn_logf(s) * kLn2;
+        if (mine && sub == 0) loss += static_cast<double>(a.alpha * b + a.beta * z * z);
+        if (a.grad && row < a.rows) {
+            Stored *g = static_cast<Stored *>(a.grad) + row * a.grad_stride;
+            const float p = mine ? a.alpha * r * up : 0.f;
+            const float q = mine ? 2.f * a.beta * z * r * up : 0.f;
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                const uint32_t at = (u * a.lanes + sub) * kVec;
+                if (at >= E) continue;
+                float d[kVec];
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    d[e] = (SIG ? slope[SIG ? u : 0][e] : w[u][e]) * fmaf(p, load[u][e] - b, q);
+                const u32x4 out = mine ? pack16<T>(d) : u32x4{0, 0, 0, 0};
+                if (at + kVec <= E) {
+                    store16_once(g + at, out);
                 } else {
-                    const float p = v == -INFINITY ? 0.f : exp2f((v - m) * kLog2e) * r;
-                    d = p * (a.alpha * (load[e] - b) + 2.f * a.beta * z);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e)
+                        if (at + e < E) g[at + e] = mine ? Row<T>::pattern(d[e]) : 0;
                 }
-                g[e] = Row<T>::pattern(d * up);
             }
-    }
-    if (LOSS) {
-        if (lane == 0) part[wave] = loss;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < kBalWaves; ++w) loss += part[w];
-            a.partial[blockIdx.x] = loss;
         }
+    }
+    if (!a.loss) return;
+    loss = wave_sum(loss);
+    if (lane == 0) part[wave] = loss;
+    __syncthreads();
+    if (tid == 0) {
+        loss = 0;
+        for (int w = 0; w < kBalWaves; ++w) loss += part[w];
+        if (gridDim.x == 1) {
+            *a.loss = mean_of(loss, kept);
+        } else if (!a.ticket) {
+            a.partial[blockIdx.x] = loss;
+        } else {
+            // the exchange has come back before the ticket is taken, so the
+            // last workgroup finds every sum at the memory all XCDs share
+            unsigned long long was = __hip_atomic_exchange(reinterpret_cast<unsigned long long *>(a.partial + blockIdx.x),
+                                                           __builtin_bit_cast(unsigned long long, loss), __ATOMIC_RELAXED,
+                                                           __HIP_MEMORY_SCOPE_AGENT);
+            asm volatile("" : "+v"(was)::"memory");
+            arrived = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+    if (gridDim.x == 1 || !a.ticket) return;
+    __syncthreads();
+    if (arrived != gridDim.x - 1) return;
+    loss = 0;
+    for (uint32_t i = tid; i < gridDim.x; i += kBalBlock)
+        loss += __builtin_bit_cast(double, __hip_atomic_load(reinterpret_cast<unsigned long long *>(a.partial + i),
+                                                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    loss = wave_sum(loss);
+    if (lane == 0) part[wave] = loss;
+    __syncthreads();
+    if (tid == 0) {
+        loss = 0;
+        for (int w = 0; w < kBalWaves; ++w) loss += part[w];
+        *a.loss = mean_of(loss, kept);
     }
 }
 
@@ -175,26 +348,92 @@ __global__ __launch_bounds__(kBalBlock) void balance_loss_kernel(BalArgs a) {
     if (threadIdx.x == 0) {
         s = 0;
         for (int w = 0; w < kBalWaves; ++w) s += part[w];
-        const int32_t kept = a.kept ? *a.kept : static_cast<int32_t>(a.rows);
-        *a.loss = kept > 0 ? static_cast<float>(s / kept) : 0.f;
+        *a.loss = mean_of(s, a.kept ? *a.kept : static_cast<int32_t>(a.rows));
     }
 }
 
-constexpr uint64_t kBalMaxBlocks = 2048;
-uint32_t balance_blocks(uint64_t rows) {
-    return static_cast<uint32_t>(std::min<uint64_t>(kBalMaxBlocks, (rows + kBalWaves - 1) / kBalWaves));
+// How a row is laid over lanes: the fewest places for its 16-byte words with at
+// most 4 a lane (or as many as 64 lanes need), and of those the fewest lanes,
+// whose sums take the fewest steps.
+void balance_layout(uint64_t vecs, uint32_t &lanes, uint32_t &per_lane) {
+    uint64_t best = ~uint64_t(0);
+    lanes = 64;
+    per_lane = 1;
+    while (lanes * per_lane < vecs) per_lane *= 2;
+    if (vecs > 256) return;
+    for (uint32_t l = 1; l <= 64; l *= 2)
+        for (uint32_t p = 1; p <= 4; ++p)
+            if (l * p >= vecs && l * p < best) {
+                best = l * p;
+                lanes = l;
+                per_lane = p;
+            }
 }
 
-template <int T, bool SIG> void balance_launch(const BalArgs &a, const Ctx &c) {
-    TimedLaunch t(4, c);
-    const dim3 grid(a.blocks), block(kBalBlock);
-    if (a.loss && a.grad) launch_on(balance_kernel<T, SIG, true, true>, grid, block, t.L, a);
-    else if (a.loss) launch_on(balance_kernel<T, SIG, true, false>, grid, block, t.L, a);
-    else launch_on(balance_kernel<T, SIG, false, true>, grid, block, t.L, a);
+constexpr uint64_t kBalMaxBlocks = 1024;
+uint32_t balance_blocks(uint64_t rows, uint64_t experts, uint64_t size) {
+    uint32_t lanes, per_lane;
+    balance_layout((experts * size + 15) / 16, lanes, per_lane);
+    const uint64_t each = kBalBlock / lanes;
+    return static_cast<uint32_t>(std::min<uint64_t>(kBalMaxBlocks, (rows + each - 1) / each));
 }
-template <int T> void balance_launch(const BalArgs &a, int score, const Ctx &c) {
-    if (score == LRS_SCORE_SIGMOID) balance_launch<T, true>(a, c);
-    else balance_launch<T, false>(a, c);
+
+template <int T, bool SIG> void balance_launch(const BalArgs &a, uint32_t per_lane, const Launch &L) {
+    const dim3 grid(a.blocks), block(kBalBlock);
+    switch (per_lane) {
+    case 1: return launch_on(balance_kernel<T, SIG, 1>, grid, block, L, a);
+    case 2: return launch_on(balance_kernel<T, SIG, 2>, grid, block, L, a);
+    case 3: return launch_on(balance_kernel<T, SIG, 3>, grid, block, L, a);
+    case 4: return launch_on(balance_kernel<T, SIG, 4>, grid, block, L, a);
+    case 8: return launch_on(balance_kernel<T, SIG, 8>, grid, block, L, a);
+    default:
+        if constexpr (T == kRowF32) launch_on(balance_kernel<T, SIG, 16>, grid, block, L, a);  // 16-bit rows need 8 at most
+    }
+}
+int balance_launch(BalArgs a, int dtype, int score, const Ctx &c) {
+    uint32_t per_lane;
+    balance_layout((a.experts * row_type_size(dtype) + 15) / 16, a.lanes, per_lane);
+    TimedLaunch t(4, c);
+    const bool sig = score == LRS_SCORE_SIGMOID;
+    if (dtype == LRS_DTYPE_FP16) sig ? balance_launch<kRowF16, true>(a, per_lane, t.L) : balance_launch<kRowF16, false>(a, per_lane, t.L);
+    else if (dtype == LRS_DTYPE_BF16) sig ? balance_launch<kRowBF16, true>(a, per_lane, t.L) : balance_launch<kRowBF16, false>(a, per_lane, t.L);
+    else sig ? balance_launch<kRowF32, true>(a, per_lane, t.L) : balance_launch<kRowF32, false>(a, per_lane, t.L);
+    return hipGetLastError() == hipSuccess ? LRS_OK : LRS_ERR_HIP;
+}
+
+// One workgroup counts and takes the rows where both are little work.
+constexpr uint64_t kAloneIds = 4096, kAloneElems = 32768;
+uint32_t count_shares(uint64_t ids) {
+    return static_cast<uint32_t>(std::min<uint64_t>(64, std::max<uint64_t>(1, ids / (kShareBlock * kShareIds))));
+}
+struct BalSpace {
+    uint64_t partial = 0, ticket = 0, shares = 0, total = 0;
+};
+BalSpace balance_space(uint64_t rows, uint64_t k, uint64_t experts) {
+    BalSpace w;
+    w.ticket = kBalMaxBlocks * sizeof(double);
+    w.shares = w.ticket + 256;
+    w.total = w.shares + count_shares(rows * k) * (experts + 1) * sizeof(int32_t);
+    return w;
+}
+
+int check_ids(int64_t index_stride, int index_bytes, int64_t rows, int64_t k, int64_t experts) {
+    if (index_bytes != 4 && index_bytes != 8) return LRS_ERR_DTYPE;
+    if (rows < 0 || k < 0 || experts < 1 || experts > LRS_MAX_EXPERTS || !stride_ok(index_stride, rows) ||
+        rows > INT32_MAX || (k > 0 && rows > INT32_MAX / k))
+        return LRS_ERR_SIZE;
+    return LRS_OK;
+}
+int check_balance(int64_t row_stride, int64_t rows, int64_t experts, int dtype, int score, float balance_weight,
+                  float z_weight, const void *grad, int64_t grad_stride) {
+    if (!row_type_ok(dtype)) return LRS_ERR_DTYPE;
+    if ((score != LRS_SCORE_SOFTMAX && score != LRS_SCORE_SIGMOID) || !std::isfinite(balance_weight) ||
+        !std::isfinite(z_weight) || (score == LRS_SCORE_SIGMOID && z_weight != 0.f))
+        return LRS_ERR_OPTION;
+    if (rows < 0 || rows > INT32_MAX || experts < 1 || experts > LRS_MAX_EXPERTS || !stride_ok(row_stride, rows) ||
+        (grad && (!stride_ok(grad_stride, rows) || (rows > 1 && grad_stride < experts))))
+        return LRS_ERR_SIZE;
+    return LRS_OK;
 }
 
 }  // namespace
@@ -209,10 +448,8 @@ int expert_counts(const void *indices, int64_t index_stride, int index_bytes, co
                   const lrs_options *opts) try {
     Ctx c;
     if (!make_ctx(stream, opts, c)) return LRS_ERR_OPTION;
-    if (index_bytes != 4 && index_bytes != 8) return LRS_ERR_DTYPE;
-    if (rows < 0 || k < 0 || experts < 1 || experts > LRS_MAX_EXPERTS || !stride_ok(index_stride, rows) ||
-        rows > INT32_MAX || (k > 0 && rows > INT32_MAX / k))
-        return LRS_ERR_SIZE;
+    const int st = check_ids(index_stride, index_bytes, rows, k, experts);
+    if (st != LRS_OK) return st;
     const bool some = rows > 0 && k > 0;
     if (!counts_out || (some && !indices)) return LRS_ERR_NULL_POINTER;
     if (misaligned(indices, index_bytes) || misaligned(counts_out, 4) || misaligned(rows_counted, 4)) return LRS_ERR_ALIGNMENT;
@@ -241,7 +478,7 @@ int expert_counts(const void *indices, int64_t index_stride, int index_bytes, co
 
 size_t expert_balance_workspace_size(int64_t rows, int64_t experts, const lrs_options *opts) {
     if (!options_ok(opts) || rows < 1 || rows > INT32_MAX || experts < 1 || experts > LRS_MAX_EXPERTS) return 0;
-    return balance_blocks(rows) * sizeof(double);
+    return kBalMaxBlocks * sizeof(double);
 }
 
 int expert_balance(const void *logits, int64_t row_stride, const int32_t *counts, const int32_t *rows_counted,
@@ -250,13 +487,8 @@ int expert_balance(const void *logits, int64_t row_stride, const int32_t *counts
                    size_t workspace_bytes, void *stream, const lrs_options *opts) try {
     Ctx c;
     if (!make_ctx(stream, opts, c)) return LRS_ERR_OPTION;
-    if (!row_type_ok(dtype)) return LRS_ERR_DTYPE;
-    if ((score != LRS_SCORE_SOFTMAX && score != LRS_SCORE_SIGMOID) || !std::isfinite(balance_weight) ||
-        !std::isfinite(z_weight) || (score == LRS_SCORE_SIGMOID && z_weight != 0.f))
-        return LRS_ERR_OPTION;
-    if (rows < 0 || rows > INT32_MAX || experts < 1 || experts > LRS_MAX_EXPERTS || !stride_ok(row_stride, rows) ||
-        (grad && (!stride_ok(grad_stride, rows) || (rows > 1 && grad_stride < experts))))
-        return LRS_ERR_SIZE;
+    const int st = check_balance(row_stride, rows, experts, dtype, score, balance_weight, z_weight, grad, grad_stride);
+    if (st != LRS_OK) return st;
     const uint64_t size = row_type_size(dtype);
     const uint64_t need = loss ? expert_balance_workspace_size(rows, experts, nullptr) : 0;
     if ((!loss && !grad && rows > 0) || !counts || (rows > 0 && !logits) || (need && !workspace) || (row_mask && !rows_counted))
@@ -285,24 +517,91 @@ int expert_balance(const void *logits, int64_t row_stride, const int32_t *counts
     a.alpha = balance_weight;
     a.beta = z_weight;
     a.partial = static_cast<double *>(workspace);
-    a.blocks = balance_blocks(a.rows);
     a.loss = loss;
     a.loss_grad = loss_grad;
     a.grad = grad;
     a.grad_stride = static_cast<uint64_t>(grad_stride);
     c.elems = a.rows * a.experts;
     if (rows > 0) {
-        if (dtype == LRS_DTYPE_FP16) balance_launch<kRowF16>(a, score, c);
-        else if (dtype == LRS_DTYPE_BF16) balance_launch<kRowBF16>(a, score, c);
-        else balance_launch<kRowF32>(a, score, c);
-        if (hipGetLastError() != hipSuccess) return LRS_ERR_HIP;
+        a.blocks = balance_blocks(a.rows, a.experts, size);
+        const int launched = balance_launch(a, dtype, score, c);
+        if (launched != LRS_OK) return launched;
     }
-    if (loss) {
+    if (loss && a.blocks != 1) {
         TimedLaunch t(4, c);
         launch_on(balance_loss_kernel, dim3(1), dim3(kBalBlock), t.L, a);
         if (hipGetLastError() != hipSuccess) return LRS_ERR_HIP;
     }
     return LRS_OK;
+} catch (...) {
+    return LRS_ERR_HIP;
+}
+
+size_t expert_balance_step_workspace_size(int64_t rows, int64_t k, int64_t experts, const lrs_options *opts) {
+    if (!options_ok(opts) || check_ids(0, 8, rows, k, experts) != LRS_OK) return 0;
+    return static_cast<size_t>(balance_space(rows, k, experts).total);
+}
+
+int expert_balance_step(const void *logits, int64_t row_stride, const void *indices, int64_t index_stride, int index_bytes,
+                        const uint8_t *row_mask, int64_t rows, int64_t k, int64_t experts, int dtype, int score,
+                        float balance_weight, float z_weight, int32_t *counts_out, int32_t *rows_counted, float *loss,
+                        void *grad, int64_t grad_stride, void *workspace, size_t workspace_bytes, void *stream,
+                        const lrs_options *opts) try {
+    Ctx c;
+    if (!make_ctx(stream, opts, c)) return LRS_ERR_OPTION;
+    int st = check_ids(index_stride, index_bytes, rows, k, experts);
+    if (st != LRS_OK) return st;
+    st = check_balance(row_stride, rows, experts, dtype, score, balance_weight, z_weight, grad, grad_stride);
+    if (st != LRS_OK) return st;
+    const uint64_t R = rows, K = k, E = experts, size = row_type_size(dtype);
+    const bool some = R > 0 && K > 0;
+    const BalSpace w = balance_space(R, K, E);
+    if ((R > 0 && !logits) || (some && !indices) || !counts_out || !loss || !workspace) return LRS_ERR_NULL_POINTER;
+    if (misaligned(logits, size) || misaligned(grad, size) || misaligned(indices, index_bytes) ||
+        misaligned(counts_out, 4) || misaligned(rows_counted, 4) || misaligned(loss, 4) || misaligned(workspace, 256))
+        return LRS_ERR_ALIGNMENT;
+    if (workspace_bytes < w.total) return LRS_ERR_WORKSPACE_TOO_SMALL;
+    const void *in[] = {logits, indices, row_mask};
+    const uint64_t inb[] = {span(R, row_stride, E, size), some ? span(R, index_stride, K, index_bytes) : 0, row_mask ? R : 0};
+    const void *out[] = {grad, loss, counts_out, rows_counted, workspace};
+    const uint64_t outb[] = {grad ? span(R, grad_stride, E, size) : 0, 4, 4 * E, rows_counted ? 4u : 0u, w.total};
+    for (int i = 0; i < 5; ++i) {
+        for (int j = 0; j < 3; ++j)
+            if (overlaps(out[i], outb[i], in[j], inb[j])) return LRS_ERR_ALIASING;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(out[i], outb[i], out[j], outb[j])) return LRS_ERR_ALIASING;
+    }
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    BalArgs a{};
+    a.x = logits;
+    a.stride = static_cast<uint64_t>(row_stride);
+    a.rows = R;
+    a.experts = static_cast<uint32_t>(E);
+    a.mask = row_mask;
+    a.ids = IdArgs{indices, index_bytes, static_cast<uint64_t>(index_stride), row_mask, static_cast<uint32_t>(R),
+                   static_cast<uint32_t>(K), static_cast<uint32_t>(E)};
+    a.counts_out = counts_out;
+    a.kept_out = rows_counted;
+    a.alpha = balance_weight;
+    a.beta = z_weight;
+    a.partial = reinterpret_cast<double *>(ws);
+    a.loss = loss;
+    a.grad = grad;
+    a.grad_stride = static_cast<uint64_t>(grad_stride);
+    c.elems = R * E;
+    if (R * K <= kAloneIds && R * E <= kAloneElems) {
+        a.blocks = 1;
+    } else {
+        a.blocks = balance_blocks(R, E, size);
+        a.ticket = reinterpret_cast<uint32_t *>(ws + w.ticket);
+        a.shares = reinterpret_cast<int32_t *>(ws + w.shares);
+        a.share_count = count_shares(R * K);
+        TimedLaunch t(4, c);
+        launch_on(count_share_kernel, dim3(a.share_count), dim3(kShareBlock), t.L, a.ids, const_cast<int32_t *>(a.shares),
+                  a.ticket);
+        if (hipGetLastError() != hipSuccess) return LRS_ERR_HIP;
+    }
+    return balance_launch(a, dtype, score, c);
 } catch (...) {
     return LRS_ERR_HIP;
 }

@@ -720,8 +720,7 @@ int check_sizes(int64_t rows, int64_t n, int64_t k, int dtype) {
 struct DisSpace {
     uint64_t partial = 0, stats = 0, row_loss = 0, total = 0;
 };
-bool distill_held(uint64_t n, uint64_t size);
-DisSpace distill_space(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
+DisSpace distill_space(uint64_t rows, uint64_t n, uint64_t k) {
     DisSpace w;
     if (rows == 0) return w;
     uint32_t splits, len;
@@ -731,10 +730,9 @@ DisSpace distill_space(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
         w.total += (bytes + 255) / 256 * 256;
         return at;
     };
-    if (!distill_held(n, size)) {
-        w.partial = place(rows * splits * sizeof(float2));
-        w.stats = place(rows * (k + kStats) * sizeof(float));
-    }
+    // the same whichever form the rows take
+    w.partial = place(rows * splits * sizeof(float2));
+    w.stats = place(rows * (k + kStats) * sizeof(float));
     w.row_loss = place(rows * sizeof(float));
     return w;
 }
@@ -869,7 +867,7 @@ int distill_run(const lrs_distill *d, float *loss, float *row_loss, float *stats
     const int st = distill_inputs(d, a);
     if (st != LRS_OK) return st;
     if (step && (!stride_ok(grad_stride, d->rows) || (d->rows > 1 && grad_stride < d->n))) return LRS_ERR_SIZE;
-    const DisSpace w = distill_space(a.rows, a.n, a.k, row_type_size(d->dtype));
+    const DisSpace w = distill_space(a.rows, a.n, a.k);
     if (!loss || (w.total && !workspace) || (step && a.rows && a.n && !grad)) return LRS_ERR_NULL_POINTER;
     const uint64_t size = row_type_size(d->dtype);
     if (misaligned(loss, 4) || misaligned(row_loss, 4) || misaligned(stats, 4) || misaligned(grad, size) ||
@@ -908,7 +906,7 @@ extern "C" {
 
 size_t topk_distill_workspace_size(int64_t rows, int64_t n, int64_t k, int dtype, const lrs_options *opts) {
     if (!options_ok(opts) || check_sizes(rows, n, k, dtype) != LRS_OK) return 0;
-    return static_cast<size_t>(distill_space(rows, n, k, row_type_size(dtype)).total);
+    return static_cast<size_t>(distill_space(rows, n, k).total);
 }
 
 int topk_distill_forward(const lrs_distill *in, float *loss, float *row_loss, float *row_stats, void *workspace,

@@ -141,6 +141,18 @@ template <typename V, typename F> __device__ inline V wave_join(V v, V none, F j
     v = join(v, moved<0x143, 0xC>(v, none));
     return last_lane(v);
 }
+// The same for every `lanes` neighbours of a wave (a power of two), the result in
+// each of them: quads, eights and sixteens by quad_perm, row_half_mirror and
+// row_mirror, then across rows.
+template <typename V, typename F> __device__ inline V group_join(V v, uint32_t lanes, F join) {
+    if (lanes > 1) v = join(v, moved<0xB1>(v, v));
+    if (lanes > 2) v = join(v, moved<0x4E>(v, v));
+    if (lanes > 4) v = join(v, moved<0x141>(v, v));
+    if (lanes > 8) v = join(v, moved<0x140>(v, v));
+    if (lanes > 16) v = join(v, __shfl_xor(v, 16));
+    if (lanes > 32) v = join(v, __shfl_xor(v, 32));
+    return v;
+}
 template <typename V> __device__ inline V wave_sum(V v) {
     return wave_join(v, V(0), [](V a, V b) { return a + b; });
 }

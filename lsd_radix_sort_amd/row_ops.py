@@ -293,12 +293,41 @@ def _balance(logits, counts, rows_counted, balance_weight, z_weight, score, row_
     return loss, grad
 
 
-def _router_counts(logits, indices, row_mask, counts, options):
-    """Counts of these tokens, and the given (all ranks') counts in their place."""
-    _matrix(logits, "logits")
-    _ids(indices, "indices", logits.shape[0], logits.device)
-    mine, kept = expert_counts(indices, logits.shape[1], row_mask, options)
-    return (mine if counts is None else counts), kept
+def expert_balance_step_workspace_size(rows: int, k: int, experts: int,
+                                       options: "_lrs.SortOptions | None" = None) -> int:
+    """Workspace bytes of expert_balance_forward and _step on these tokens' own counts."""
+    return int(_lrs.load_library().expert_balance_step_workspace_size(rows, k, experts, _lrs._opt(options)))
+
+
+def _step(logits, indices, balance_weight, z_weight, score, row_mask, counts, want_kept, want_grad, grad_out, workspace,
+          options):
+    """Loss, counts, rows counted (if wanted) and gradient (if wanted), on these tokens' counts or the given ones."""
+    lib = _lrs.load_library()
+    dtype = _matrix(logits, "logits")
+    rows, experts = logits.shape
+    device = logits.device
+    index_bytes = _ids(indices, "indices", rows, device)
+    if counts is not None:
+        _, kept = expert_counts(indices, experts, row_mask, options)
+        loss, grad = _balance(logits, counts, kept, balance_weight, z_weight, score, row_mask, True, None, want_grad,
+                              grad_out, workspace, options)
+        return loss, counts, kept, grad
+    if score not in _SCORES:
+        _lrs._bad(f"score must be one of {sorted(_SCORES)}")
+    opt = _lrs._opt(options)
+    k = indices.shape[1]
+    need = lib.expert_balance_step_workspace_size(rows, k, experts, opt)
+    workspace = _lrs._workspace(workspace, need, device)
+    counts = torch.empty(experts, dtype=torch.int32, device=device)
+    kept = torch.empty(1, dtype=torch.int32, device=device) if want_kept else None
+    loss = torch.empty((), dtype=torch.float32, device=device)
+    grad = _grad_out(grad_out, logits) if want_grad else None
+    _lrs._check(lib.expert_balance_step(logits.data_ptr(), logits.stride(0), indices.data_ptr(), indices.stride(0),
+                                        index_bytes, _mask(row_mask, rows, device), rows, k, experts, dtype,
+                                        _SCORES[score], balance_weight, z_weight, counts.data_ptr(), _lrs._ptr(kept),
+                                        loss.data_ptr(), _lrs._ptr(grad), 0 if grad is None else grad.stride(0),
+                                        workspace.data_ptr(), need, _lrs._stream(logits), opt), "expert_balance_step")
+    return loss, counts, kept, grad
 
 
 def expert_balance_forward(logits: torch.Tensor, indices: torch.Tensor, balance_weight: float = 1.0,
@@ -311,10 +340,8 @@ def expert_balance_forward(logits: torch.Tensor, indices: torch.Tensor, balance_
     f_e = experts * counts_e / sum(counts) and p the softmax (or normalised sigmoid) of the token's logits.
     counts: int32 [experts] to use in place of these tokens' own, such as their sum over ranks.
     Returns (loss, counts, rows_counted)."""
-    counts, kept = _router_counts(logits, indices, row_mask, counts, options)
-    loss, _ = _balance(logits, counts, kept, balance_weight, z_weight, score, row_mask, True, None, False, None,
-                       workspace, options)
-    return loss, counts, kept
+    return _step(logits, indices, balance_weight, z_weight, score, row_mask, counts, True, False, None, workspace,
+                 options)[:3]
 
 
 def expert_balance_backward(logits: torch.Tensor, counts: torch.Tensor, rows_counted: torch.Tensor | None = None,
@@ -331,9 +358,8 @@ def expert_balance_step(logits: torch.Tensor, indices: torch.Tensor, balance_wei
                         counts: torch.Tensor | None = None, grad_out: torch.Tensor | None = None,
                         workspace: torch.Tensor | None = None, options: "_lrs.SortOptions | None" = None):
     """expert_balance_forward and its gradient from one read of the logits: returns (loss, counts, grad)."""
-    counts, kept = _router_counts(logits, indices, row_mask, counts, options)
-    loss, grad = _balance(logits, counts, kept, balance_weight, z_weight, score, row_mask, True, None, True, grad_out,
-                          workspace, options)
+    loss, counts, _, grad = _step(logits, indices, balance_weight, z_weight, score, row_mask, counts, False, True,
+                                  grad_out, workspace, options)
     return loss, counts, grad
 
 

@@ -146,3 +146,28 @@ def test_expert_refusals():
     assert bal(g=x) == 5 and bal(g=c) == 5 and bal(loss=x) == 5 and bal(ws=x) == 5 and bal(g=loss) == 5 and bal(ws=g) == 5
     assert lib.expert_balance_workspace_size(10, 64, None) > 0
     assert lib.expert_balance_workspace_size(0, 64, None) == 0 and lib.expert_balance_workspace_size(10, 4097, None) == 0
+
+
+@no_gpu
+def test_balance_step_refusals():
+    lib = lrs.load_library()
+    i, m, c, n, x, loss, g, ws = A[:8]
+
+    def step(x=x, xs=64, i=i, istride=4, nb=8, m=m, rows=10, k=4, e=64, dtype=1, score=0, a=1.0, z=0.0, c=c, n=n, loss=loss,
+             g=g, gs=64, ws=ws, wb=BIG, opts=None):
+        return lib.expert_balance_step(x, xs, i, istride, nb, m, rows, k, e, dtype, score, a, z, c, n, loss, g, gs, ws, wb,
+                                       None, opts)
+    assert step(nb=2) == 7 and step(dtype=3) == 7
+    assert step(score=2) == 10 and step(score=1, z=0.1) == 10 and step(a=float("inf")) == 10 and step(z=float("nan")) == 10
+    assert step(opts=ctypes.byref(lrs._Options(7, 0, 0, 0, None))) == 10
+    assert step(rows=-1) == 4 and step(k=-1) == 4 and step(e=0) == 4 and step(e=4097) == 4 and step(rows=1 << 30) == 4
+    assert step(xs=-1) == 4 and step(istride=-1) == 4 and step(gs=63) == 4 and step(gs=-1) == 4
+    assert step(x=None) == 1 and step(i=None) == 1 and step(c=None) == 1 and step(loss=None) == 1 and step(ws=None) == 1
+    assert step(wb=lib.expert_balance_step_workspace_size(10, 4, 64, None) - 1) == 6
+    assert step(x=ctypes.c_void_p(0x50000001)) == 9 and step(i=ctypes.c_void_p(0x10000004)) == 9
+    assert step(c=ctypes.c_void_p(0x30000002)) == 9 and step(ws=ctypes.c_void_p(0x80000008)) == 9
+    assert step(g=x) == 5 and step(g=i) == 5 and step(g=m) == 5 and step(loss=i) == 5 and step(c=i) == 5 and step(n=c) == 5
+    assert step(ws=x) == 5 and step(ws=g) == 5 and step(loss=c) == 5
+    size = lib.expert_balance_step_workspace_size
+    assert size(-1, 4, 64, None) == 0 and size(10, 4, 4097, None) == 0 and size(0, 0, 1, None) > 0
+    assert size(1 << 20, 8, 4096, None) >= 64 * 4097 * 4
