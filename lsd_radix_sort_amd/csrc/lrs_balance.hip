@@ -156,23 +156,21 @@ __device__ inline float mean_of(double sum, int32_t kept) { return kept > 0 ? st
 
 // A row's elements in the registers of `lanes` neighbours, V loads of 16 bytes
 // each, from its one read to the gradient; 64 / lanes rows a wave at a time.
-// Bound by memory where rows are many: a row of 256 bf16 takes 32 lanes, some
-// 13 instructions an element, a third of the time that its bytes take.
-template <int T, bool SIG, int V>
-__global__ __launch_bounds__(kBalBlock) void balance_kernel(BalArgs a) {
+template <int T, bool SIG, int V, int B>
+__global__ __launch_bounds__(B) void balance_kernel(BalArgs a) {
     constexpr int kVec = Row<T>::kVec;
     using Stored = typename Row<T>::Stored;
     __shared__ int32_t hist[LRS_MAX_EXPERTS + 1];
-    __shared__ double part[kBalWaves];
-    __shared__ int64_t sums[kBalWaves];
+    __shared__ double part[(B / kLanes)];
+    __shared__ int64_t sums[(B / kLanes)];
     __shared__ uint32_t arrived;
     const uint32_t tid = threadIdx.x, E = a.experts;
     const int lane = tid % kLanes, wave = tid / kLanes;
     const uint32_t sub = lane % a.lanes;
 
     // the first rows are on their way while the counts are added up
-    const uint64_t step = static_cast<uint64_t>(gridDim.x) * (kBalBlock / a.lanes);
-    uint64_t row = static_cast<uint64_t>(blockIdx.x) * (kBalBlock / a.lanes) + tid / a.lanes;
+    const uint64_t step = static_cast<uint64_t>(gridDim.x) * (B / a.lanes);
+    uint64_t row = static_cast<uint64_t>(blockIdx.x) * (B / a.lanes) + tid / a.lanes;
     const uint32_t none = T == kRowF16 ? 0xFC00FC00u : T == kRowBF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
     u32x4 v[V];
     bool counted = false;
@@ -196,32 +194,45 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(BalArgs a) {
     load_row(row);
 
     if (a.counts) {
-        for (uint32_t e = tid; e < E; e += kBalBlock) hist[e] = a.counts[e];
+        for (uint32_t e = tid; e < E; e += B) hist[e] = a.counts[e];
         if (tid == 0) hist[E] = a.kept ? *a.kept : static_cast<int32_t>(a.rows);
     } else if (a.shares) {
-        for (uint32_t e = tid; e <= E; e += kBalBlock) {
+        // a thread a cell, or several where there are fewer cells
+        const uint32_t team = max(1u, B / (E + 1));
+        for (uint32_t e = tid; e <= E; e += B) hist[e] = 0;
+        __syncthreads();
+        for (uint32_t i = tid; i < team * (E + 1); i += B) {
+            const uint32_t e = i % (E + 1);
             int32_t c = 0;
-#pragma unroll 8
-            for (uint32_t b = 0; b < a.share_count; ++b) c += a.shares[static_cast<uint64_t>(b) * (E + 1) + e];
-            hist[e] = c;
+            for (uint32_t b = i / (E + 1); b < a.share_count; b += 8 * team) {
+                int32_t part[8];
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) {
+                    const uint32_t s = b + j * team;
+                    part[j] = s < a.share_count ? a.shares[s * (E + 1) + e] : 0;
+                }
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) c += part[j];
+            }
+            atomicAdd(&hist[e], c);
         }
     } else {
-        for (uint32_t e = tid; e <= E; e += kBalBlock) hist[e] = 0;
+        for (uint32_t e = tid; e <= E; e += B) hist[e] = 0;
         __syncthreads();
-        count_ids<kBalBlock>(a.ids, 0, a.ids.rows * a.ids.k, 0, a.ids.rows, hist);
+        count_ids<B>(a.ids, 0, a.ids.rows * a.ids.k, 0, a.ids.rows, hist);
     }
     __syncthreads();
     int64_t total = 0;
-    for (uint32_t e = tid; e < E; e += kBalBlock) total += hist[e];
+    for (uint32_t e = tid; e < E; e += B) total += hist[e];
     total = wave_sum(total);
     if (lane == 0) sums[wave] = total;
     if (!a.counts && blockIdx.x == 0) {
-        for (uint32_t e = tid; e < E; e += kBalBlock) a.counts_out[e] = hist[e];
+        for (uint32_t e = tid; e < E; e += B) a.counts_out[e] = hist[e];
         if (tid == 0 && a.kept_out) *a.kept_out = hist[E];
     }
     __syncthreads();
     total = 0;
-    for (int w = 0; w < kBalWaves; ++w) total += sums[w];
+    for (int w = 0; w < (B / kLanes); ++w) total += sums[w];
     const int32_t kept = hist[E];
     // this lane's columns stay the same from row to row
     float load[V][kVec];
@@ -305,7 +316,7 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(BalArgs a) {
     __syncthreads();
     if (tid == 0) {
         loss = 0;
-        for (int w = 0; w < kBalWaves; ++w) loss += part[w];
+        for (int w = 0; w < (B / kLanes); ++w) loss += part[w];
         if (gridDim.x == 1) {
             *a.loss = mean_of(loss, kept);
         } else if (!a.ticket) {
@@ -324,7 +335,7 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(BalArgs a) {
     __syncthreads();
     if (arrived != gridDim.x - 1) return;
     loss = 0;
-    for (uint32_t i = tid; i < gridDim.x; i += kBalBlock)
+    for (uint32_t i = tid; i < gridDim.x; i += B)
         loss += __builtin_bit_cast(double, __hip_atomic_load(reinterpret_cast<unsigned long long *>(a.partial + i),
                                                              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     loss = wave_sum(loss);
@@ -332,7 +343,7 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(BalArgs a) {
     __syncthreads();
     if (tid == 0) {
         loss = 0;
-        for (int w = 0; w < kBalWaves; ++w) loss += part[w];
+        for (int w = 0; w < (B / kLanes); ++w) loss += part[w];
         *a.loss = mean_of(loss, kept);
     }
 }
@@ -353,41 +364,44 @@ __global__ __launch_bounds__(kBalBlock) void balance_loss_kernel(BalArgs a) {
 }
 
 // How a row is laid over lanes: the fewest places for its 16-byte words with at
-// most 4 a lane (or as many as 64 lanes need), and of those the fewest lanes,
+// most 3 a lane (or as many as 64 lanes need), and of those the fewest lanes,
 // whose sums take the fewest steps.
 void balance_layout(uint64_t vecs, uint32_t &lanes, uint32_t &per_lane) {
     uint64_t best = ~uint64_t(0);
     lanes = 64;
-    per_lane = 1;
+    per_lane = 4;
     while (lanes * per_lane < vecs) per_lane *= 2;
-    if (vecs > 256) return;
     for (uint32_t l = 1; l <= 64; l *= 2)
-        for (uint32_t p = 1; p <= 4; ++p)
+        for (uint32_t p = 1; p <= 3; ++p)
             if (l * p >= vecs && l * p < best) {
                 best = l * p;
                 lanes = l;
                 per_lane = p;
             }
 }
-
+// Workgroups of 1024 threads, one a CU, as every one of them adds up the counts
+// first and takes the ticket last (65536 x 256 bf16: 25 us so, 29 us with 512
+// of 256 threads, 33 us with 1024 of them); rows of more than 3 loads a lane
+// need the registers of 256 threads.
+constexpr uint32_t balance_block(uint32_t per_lane) { return per_lane <= 3 ? 1024 : kBalBlock; }
 constexpr uint64_t kBalMaxBlocks = 1024;
 uint32_t balance_blocks(uint64_t rows, uint64_t experts, uint64_t size) {
     uint32_t lanes, per_lane;
     balance_layout((experts * size + 15) / 16, lanes, per_lane);
-    const uint64_t each = kBalBlock / lanes;
-    return static_cast<uint32_t>(std::min<uint64_t>(kBalMaxBlocks, (rows + each - 1) / each));
+    const uint64_t block = balance_block(per_lane), each = block / lanes;
+    return static_cast<uint32_t>(std::min<uint64_t>(256 * 1024 / block, (rows + each - 1) / each));
 }
 
 template <int T, bool SIG> void balance_launch(const BalArgs &a, uint32_t per_lane, const Launch &L) {
-    const dim3 grid(a.blocks), block(kBalBlock);
+    const auto go = [&](auto kernel) { launch_on(kernel, dim3(a.blocks), dim3(balance_block(per_lane)), L, a); };
     switch (per_lane) {
-    case 1: return launch_on(balance_kernel<T, SIG, 1>, grid, block, L, a);
-    case 2: return launch_on(balance_kernel<T, SIG, 2>, grid, block, L, a);
-    case 3: return launch_on(balance_kernel<T, SIG, 3>, grid, block, L, a);
-    case 4: return launch_on(balance_kernel<T, SIG, 4>, grid, block, L, a);
-    case 8: return launch_on(balance_kernel<T, SIG, 8>, grid, block, L, a);
+    case 1: return go(balance_kernel<T, SIG, 1, balance_block(1)>);
+    case 2: return go(balance_kernel<T, SIG, 2, balance_block(2)>);
+    case 3: return go(balance_kernel<T, SIG, 3, balance_block(3)>);
+    case 4: return go(balance_kernel<T, SIG, 4, balance_block(4)>);
+    case 8: return go(balance_kernel<T, SIG, 8, balance_block(8)>);
     default:
-        if constexpr (T == kRowF32) launch_on(balance_kernel<T, SIG, 16>, grid, block, L, a);  // 16-bit rows need 8 at most
+        if constexpr (T == kRowF32) go(balance_kernel<T, SIG, 16, balance_block(16)>);  // 16-bit rows need 8 at most
     }
 }
 int balance_launch(BalArgs a, int dtype, int score, const Ctx &c) {
