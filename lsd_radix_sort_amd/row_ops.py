@@ -147,6 +147,27 @@ def _distill_workspace(lib, workspace, d: _Distill, opt, device) -> torch.Tensor
     return _lrs._workspace(workspace, lib.topk_distill_workspace_size(d.rows, d.n, d.k, d.dtype, opt), device)
 
 
+def _distill_forward(d: _Distill, logits, row_loss, workspace, options):
+    lib = _lrs.load_library()
+    opt = _lrs._opt(options)
+    workspace = _distill_workspace(lib, workspace, d, opt, logits.device)
+    loss = torch.empty((), dtype=torch.float32, device=logits.device)
+    stats = torch.empty((d.rows, d.k + 3), dtype=torch.float32, device=logits.device)
+    _lrs._check(lib.topk_distill_forward(ctypes.byref(d), loss.data_ptr(), _lrs._ptr(row_loss), stats.data_ptr(),
+                                         workspace.data_ptr(), workspace.numel(), _lrs._stream(logits), opt),
+                "topk_distill_forward")
+    return loss, stats
+
+
+def _distill_backward(d: _Distill, logits, stats, loss_grad, grad_out, options):
+    lib = _lrs.load_library()
+    grad_out = _grad_out(grad_out, logits)
+    _lrs._check(lib.topk_distill_backward(ctypes.byref(d), stats.data_ptr(), _scale(loss_grad, logits.device),
+                                          grad_out.data_ptr(), grad_out.stride(0), _lrs._stream(logits),
+                                          _lrs._opt(options)), "topk_distill_backward")
+    return grad_out
+
+
 def topk_distill_forward(logits: torch.Tensor, teacher_values: torch.Tensor, teacher_indices: torch.Tensor,
                          temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
                          row_weights: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
@@ -158,16 +179,9 @@ def topk_distill_forward(logits: torch.Tensor, teacher_values: torch.Tensor, tea
     the teacher's whole row over the temperature) the rest of the teacher's mass counts against the rest of
     the student's; without it the teacher's top logits are renormalised.  row_weights: [rows] float32, default
     1 / rows; a row of weight 0 is left out.  Returns (loss, row_loss [rows], row_stats for the backward)."""
-    lib = _lrs.load_library()
     d = _distill_inputs(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights)
-    opt = _lrs._opt(options)
-    workspace = _distill_workspace(lib, workspace, d, opt, logits.device)
-    loss = torch.empty((), dtype=torch.float32, device=logits.device)
     row_loss = torch.empty(d.rows, dtype=torch.float32, device=logits.device)
-    stats = torch.empty((d.rows, d.k + 3), dtype=torch.float32, device=logits.device)
-    _lrs._check(lib.topk_distill_forward(ctypes.byref(d), loss.data_ptr(), row_loss.data_ptr(), stats.data_ptr(),
-                                         workspace.data_ptr(), workspace.numel(), _lrs._stream(logits), opt),
-                "topk_distill_forward")
+    loss, stats = _distill_forward(d, logits, row_loss, workspace, options)
     return loss, row_loss, stats
 
 
@@ -177,14 +191,9 @@ def topk_distill_backward(logits: torch.Tensor, teacher_values: torch.Tensor, te
                           grad_out: torch.Tensor | None = None, options: "_lrs.SortOptions | None" = None):
     """The gradient of topk_distill_forward's loss in the logits, times loss_grad, from the same inputs
     and the row_stats that the forward returned."""
-    lib = _lrs.load_library()
     d = _distill_inputs(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights)
     _lrs.check_output(row_stats, "row_stats", logits.device, 4, (d.rows, d.k + 3))
-    grad_out = _grad_out(grad_out, logits)
-    _lrs._check(lib.topk_distill_backward(ctypes.byref(d), row_stats.data_ptr(), _scale(loss_grad, logits.device),
-                                          grad_out.data_ptr(), grad_out.stride(0), _lrs._stream(logits),
-                                          _lrs._opt(options)), "topk_distill_backward")
-    return grad_out
+    return _distill_backward(d, logits, row_stats, loss_grad, grad_out, options)
 
 
 def topk_distill_step(logits: torch.Tensor, teacher_values: torch.Tensor, teacher_indices: torch.Tensor,
@@ -205,20 +214,36 @@ def topk_distill_step(logits: torch.Tensor, teacher_values: torch.Tensor, teache
     return loss, row_loss, grad_out
 
 
+def _once(gradient):
+    """`gradient` as the backward of a Function that cannot be differentiated again: the check for that is
+    made only where a graph of the backward is wanted."""
+    checked = torch.autograd.function.once_differentiable(gradient)
+
+    def backward(ctx, *grads):
+        return (checked if torch.is_grad_enabled() else gradient)(ctx, *grads)
+    return staticmethod(backward)
+
+
+def _distill_gradient(ctx, loss_grad):
+    logits, values, indices, stats, lse, weights = ctx.saved_tensors
+    d = ctx.inputs
+    # the forward's checked inputs serve again, unless a hook has moved what was saved
+    if (logits.data_ptr() != d.logits or values.data_ptr() != d.teacher_values or indices.data_ptr() != d.teacher_indices
+            or _lrs._ptr(lse) != d.teacher_lse or _lrs._ptr(weights) != d.row_weights):
+        d = _distill_inputs(logits, values, indices, d.temperature, lse, weights)
+    return _distill_backward(d, logits, stats, loss_grad, None, None), None, None, None, None, None
+
+
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, values, indices, temperature, lse, weights):
-        loss, _, stats = topk_distill_forward(logits, values, indices, temperature, lse, weights)
+        d = _distill_inputs(logits, values, indices, temperature, lse, weights)
+        loss, stats = _distill_forward(d, logits, None, None, None)
         ctx.save_for_backward(logits, values, indices, stats, lse, weights)
-        ctx.temperature = temperature
+        ctx.inputs = d
         return loss
 
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, loss_grad):
-        logits, values, indices, stats, lse, weights = ctx.saved_tensors
-        grad = topk_distill_backward(logits, values, indices, stats, ctx.temperature, lse, weights, loss_grad)
-        return grad, None, None, None, None, None
+    backward = _once(_distill_gradient)
 
 
 def topk_distill_loss(logits: torch.Tensor, teacher_values: torch.Tensor, teacher_indices: torch.Tensor,
@@ -363,6 +388,12 @@ def expert_balance_step(logits: torch.Tensor, indices: torch.Tensor, balance_wei
     return loss, counts, grad
 
 
+def _balance_gradient(ctx, loss_grad, _):
+    logits, counts, kept, row_mask = ctx.saved_tensors
+    grad = expert_balance_backward(logits, counts, kept, *ctx.how, row_mask, loss_grad)
+    return grad, None, None, None, None, None, None
+
+
 class _BalanceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, indices, balance_weight, z_weight, score, row_mask, counts):
@@ -372,12 +403,7 @@ class _BalanceLoss(torch.autograd.Function):
         ctx.mark_non_differentiable(counts)
         return loss, counts
 
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, loss_grad, _):
-        logits, counts, kept, row_mask = ctx.saved_tensors
-        grad = expert_balance_backward(logits, counts, kept, *ctx.how, row_mask, loss_grad)
-        return grad, None, None, None, None, None, None
+    backward = _once(_balance_gradient)
 
 
 def expert_balance_loss(logits: torch.Tensor, indices: torch.Tensor, balance_weight: float = 1.0,
