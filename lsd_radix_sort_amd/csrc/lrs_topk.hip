@@ -34,6 +34,7 @@ struct TopArgs {
     uint32_t flip;        // 0, or all ones for the smallest first
     void *values;         // patterns
     int64_t *indices;
+    uint64_t first_task;  // of this launch
     uint64_t *words;      // splits > 1: [rows][splits][k], 0 where a split has fewer
 };
 
@@ -63,15 +64,15 @@ __device__ inline uint32_t column_of(uint64_t word) { return 0xFFFFFFFFu - stati
 
 // Sorts buf[0, count) descending; the words from count to the next power of
 // two are cleared (a real word is never 0).  Barriers before and after.
-__device__ void sort_words(uint64_t *buf, uint32_t count) {
+template <int B> __device__ void sort_words(uint64_t *buf, uint32_t count) {
     uint32_t m = 2;
     while (m < count) m <<= 1;
     __syncthreads();
-    for (uint32_t i = count + threadIdx.x; i < m; i += kTopBlock) buf[i] = 0;
+    for (uint32_t i = count + threadIdx.x; i < m; i += B) buf[i] = 0;
     __syncthreads();
     for (uint32_t size = 2; size <= m; size <<= 1)
         for (uint32_t d = size >> 1; d > 0; d >>= 1) {
-            for (uint32_t t = threadIdx.x; t < m / 2; t += kTopBlock) {
+            for (uint32_t t = threadIdx.x; t < m / 2; t += B) {
                 const uint32_t i = 2 * t - (t & (d - 1)), j = i + d;
                 const uint64_t a = buf[i], b = buf[j];
                 const bool down = (i & size) == 0;
@@ -124,7 +125,7 @@ __global__ __launch_bounds__(kTopBlock) void topk_kernel(TopArgs a) {
         // keep the k largest words; later elements with the k-th one's image
         // come after it, so from now on only larger images enter
         auto shrink = [&]() {
-            sort_words(buf, count);
+            sort_words<kTopBlock>(buf, count);
             const int img = image_of(buf[want - 1]);
             __syncthreads();
             if (threadIdx.x == 0) count = want;
@@ -217,7 +218,7 @@ __global__ __launch_bounds__(kTopBlock) void topk_kernel(TopArgs a) {
         if (tail < len) add(image<W>(x[tail], a.flip), tail);
         __syncthreads();
         const uint32_t c = count;
-        sort_words(buf, c);
+        sort_words<kTopBlock>(buf, c);
         if (a.splits == 1) {
             write_row<W>(a, buf, row, a.k);
         } else {
@@ -321,33 +322,39 @@ __device__ inline int row16_max(int v) {
     v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x122, 0xF, 0xF, false));
     return max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x121, 0xF, 0xF, false));
 }
-__device__ inline uint32_t lanes_below(uint64_t mask) {
-    return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
-                                     __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
+// The sum over this lane and those below.
+__device__ inline uint32_t lanes_sum(uint32_t v) {
+    v += moved<0x111>(v, 0u);
+    v += moved<0x112>(v, 0u);
+    v += moved<0x114>(v, 0u);
+    v += moved<0x118>(v, 0u);
+    v += moved<0x142, 0xA>(v, 0u);
+    v += moved<0x143, 0xC>(v, 0u);
+    return v;
 }
 
 // E consecutive elements of a row as images, INT32_MIN past its end.
 template <int W, int E> __device__ inline void load_images(const typename Row<W == 2 ? kRowF16 : kRowF32>::Stored *x,
                                                            uint32_t at, uint32_t n, uint32_t flip, int (&img)[E]) {
     constexpr int kVec = 16 / W;
+    u32x4 v[E / kVec];
 #pragma unroll
     for (int q = 0; q < E / kVec; ++q) {
         const uint32_t first = at + q * kVec;
-        u32x4 v{};
-        if (first + kVec <= n) {
-            v = load16(x + first);
-        } else if (first < n) {
+        v[q] = u32x4{0, 0, 0, 0};
+        if (first + kVec <= n) v[q] = load16(x + first);
+        if (n % kVec != 0 && first < n && first + kVec > n)
             for (int e = 0; e < kVec; ++e) {
                 const uint32_t pat = first + e < n ? x[first + e] : 0;
-                if (W == 2) v[e / 2] |= pat << (16 * (e & 1));
-                else v[e % 4] = pat;
+                if (W == 2) v[q][e / 2] |= pat << (16 * (e & 1));
+                else v[q][e % 4] = pat;
             }
-        }
+    }
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            const uint32_t pat = W == 2 ? (v[e / 2] >> (16 * (e & 1))) & 0xFFFFu : v[e % 4];
-            img[q * kVec + e] = first + e < n ? image<W>(pat, flip) : INT32_MIN;
-        }
+    for (int i = 0; i < E; ++i) {
+        const int q = i / kVec, e = i % kVec;
+        const uint32_t pat = W == 2 ? (v[q][e / 2] >> (16 * (e & 1))) & 0xFFFFu : v[q][e % 4];
+        img[i] = at + i < n ? image<W>(pat, flip) : INT32_MIN;
     }
 }
 
@@ -416,9 +423,13 @@ __global__ __launch_bounds__(kTopBlock) void topk_heads_kernel(TopArgs a) {
 }
 
 // Rows of at most 64 * V loads and k <= 64: a wave a row, held in registers.
-// A bisection over the lanes' largest images, and over all where that leaves
-// too many, finds a bound that at least k and at most 64 elements reach; those
-// move to a lane each and count the words above theirs, which is their place.
+// Lanes' largest images are tried as a bound until one is reached by k to 2 k
+// lanes; the elements that reach it, at most 64, move to a lane each and count
+// the words above theirs, which is their place.  Where that leaves more than
+// 64, a bisection over the images of all finds the bound.  Bound by issue, not
+// memory: scalar steps count as much as vector ones, so the bound is looked
+// for among the lanes (9 scalar instructions a try) and places are summed by
+// lanes.
 template <int W, int V>
 __global__ __launch_bounds__(kTopBlock) void topk_wave_kernel(TopArgs a) {
     constexpr int kVec = 16 / W;
@@ -430,7 +441,6 @@ __global__ __launch_bounds__(kTopBlock) void topk_wave_kernel(TopArgs a) {
     constexpr uint64_t kRows = kTopBlock / kLanes;
     const uint32_t n = a.n, k = a.k;
     const uint32_t lanes = min(static_cast<uint32_t>(kLanes), (n + kVec - 1) / kVec);  // that hold elements
-    const uint32_t enough = min(max(16u, 2 * k), static_cast<uint32_t>(kLanes));
     for (uint64_t row = blockIdx.x * kRows + wave; row < a.rows; row += gridDim.x * kRows) {
         const Stored *x = static_cast<const Stored *>(a.x) + row * a.stride;
         int img[V][kVec];
@@ -441,53 +451,71 @@ __global__ __launch_bounds__(kTopBlock) void topk_wave_kernel(TopArgs a) {
 #pragma unroll
             for (int e = 0; e < kVec; ++e) most = max(most, img[u][e]);
         }
-        auto reach = [&](int bound) {
-            uint32_t c = 0;
-#pragma unroll
-            for (int u = 0; u < V; ++u)
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) c += __popcll(__ballot(img[u][e] >= bound));
-            return bound == INT32_MIN ? n : c;
-        };
-        // at least k elements reach lo, and fewer than k anything above hi
-        int hi = wave_max_int(most), lo = kLowest;
-        uint32_t c = n;
+        const auto column = [&](int u, int e) { return static_cast<uint32_t>((u * kLanes + lane) * kVec + e); };
+        int bound = kLowest;
         if (lanes >= k) {
-            lo = ~wave_max_int(lane < static_cast<int>(lanes) ? ~most : INT32_MIN);
-            uint32_t reached = lanes;
-            int top = hi;
-            while (reached > k + k / 4 && lo < top) {
-                const int mid = (lo | top) - ((lo ^ top) >> 1);
-                const uint32_t m = __popcll(__ballot(most >= mid));
-                reached = m >= k ? m : reached;
-                lo = m >= k ? mid : lo;
-                top = m >= k ? top : mid - 1;
+            uint64_t left = ~uint64_t(0) >> (kLanes - lanes);
+            while (left) {
+                const int pivot = __builtin_amdgcn_readlane(most, __builtin_ctzll(left));
+                const uint64_t reach = __ballot(most >= pivot);
+                const uint32_t c = __popcll(reach);
+                if (c < k) {
+                    left &= ~reach;
+                } else {
+                    bound = pivot;
+                    left &= c <= 2 * k ? 0 : __ballot(most > pivot);
+                }
             }
-            c = reach(lo);
         }
-        while (c > enough && lo < hi) {
-            const int mid = (lo | hi) - ((lo ^ hi) >> 1);
-            const uint32_t m = reach(mid);
-            c = m >= k ? m : c;
-            lo = m >= k ? mid : lo;
-            hi = m >= k ? hi : mid - 1;
-        }
-        // more than 64 left: their images are equal but for fewer than k above
-        const bool ties = c > kLanes;
-        uint32_t count = 0;
-        if (!ties || lo < INT32_MAX) {
-            const int bound = ties ? lo + 1 : lo;
+        // the elements that reach the bound: this lane's, and those of lanes below
+        uint32_t own, upto, count;
+        const auto add_up = [&]() {
+            own = 0;
 #pragma unroll
             for (int u = 0; u < V; ++u)
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const uint32_t at = (u * kLanes + lane) * kVec + e;
-                    const bool in = at < n && img[u][e] >= bound;
-                    const uint64_t mask = __ballot(in);
-                    if (mask == 0) continue;
-                    if (in) held[wave][count + lanes_below(mask)] = Word::make(img[u][e], at);
-                    count += __popcll(mask);
+                for (int e = 0; e < kVec; ++e) own += img[u][e] >= bound;
+            if (bound == INT32_MIN) {  // nor do the places past the row's end
+                own = 0;
+#pragma unroll
+                for (int u = 0; u < V; ++u) own += min(max(static_cast<int>(n - column(u, 0)), 0), kVec);
+            }
+            upto = lanes_sum(own);
+            count = __builtin_amdgcn_readlane(upto, kLanes - 1);
+        };
+        add_up();
+        bool ties = false;
+        int tied = 0;  // their image
+        if (count > kLanes) {
+            int lo = bound, hi = wave_max_int(most);  // fewer than k are above hi
+            while (count > kLanes && lo < hi) {
+                bound = (lo | hi) - ((lo ^ hi) >> 1);
+                add_up();
+                if (count >= k) lo = bound;
+                else hi = bound - 1;
+                if (count < k) count = kLanes + 1;
+            }
+            bound = lo;
+            add_up();
+            // more than 64 still: their images are equal but for fewer than k above
+            ties = count > kLanes;
+            if (ties) {
+                tied = lo;
+                count = 0;
+                if (lo < INT32_MAX) {
+                    bound = lo + 1;
+                    add_up();
                 }
+            }
+        }
+        if (own && count) {
+            uint32_t slot = upto - own;
+#pragma unroll
+            for (int u = 0; u < V; ++u)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    if (img[u][e] >= bound && (bound != INT32_MIN || column(u, e) < n))
+                        held[wave][slot++] = Word::make(img[u][e], column(u, e));
         }
         if (ties) {  // the first of the equal ones, one after the other
             int next = -1;
@@ -497,11 +525,11 @@ __global__ __launch_bounds__(kTopBlock) void topk_wave_kernel(TopArgs a) {
                 for (int u = 0; u < V; ++u)
 #pragma unroll
                     for (int e = 0; e < kVec; ++e) {
-                        const int at = (u * kLanes + lane) * kVec + e;
-                        if (at < static_cast<int>(n) && at > next && img[u][e] == lo) first = max(first, ~at);
+                        const int at = column(u, e);
+                        if (at < static_cast<int>(n) && at > next && img[u][e] == tied) first = max(first, ~at);
                     }
                 next = ~wave_max_int(first);
-                if (lane == 0) held[wave][count] = Word::make(lo, next);
+                if (lane == 0) held[wave][count] = Word::make(tied, next);
                 ++count;
             }
         }
@@ -517,24 +545,353 @@ __global__ __launch_bounds__(kTopBlock) void topk_wave_kernel(TopArgs a) {
     }
 }
 
-// The k largest of a row's splits * k words.
-template <int W>
-__global__ __launch_bounds__(kTopBlock) void topk_merge_kernel(TopArgs a) {
-    __shared__ uint64_t buf[kTopBuffer];
-    for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const uint32_t total = a.splits * a.k;  // at most kTopBuffer
-        const uint64_t *in = a.words + row * total;
-        __syncthreads();
-        for (uint32_t i = threadIdx.x; i < total; i += kTopBlock) buf[i] = in[i];
-        sort_words(buf, total);
-        write_row<W>(a, buf, row, a.k);
+// ---- a row, or a piece of one, in one workgroup's registers ------------------
+
+// Bins of images below the largest, 2^shift images a bin; whoever lies lower
+// is not counted.
+constexpr uint32_t kBins = 2048, kCoarse = 64, kFine = kBins / kCoarse;
+constexpr uint32_t kHeldWords = 2048;  // candidates in LDS
+constexpr uint32_t kRankWords = 128;   // so many are ranked by counting all the others
+
+struct Bins {
+    uint32_t coarse[kCoarse];
+    uint32_t fine[kBins];
+};
+template <int B> __device__ inline void clear_bins(Bins &h) {
+    if (threadIdx.x < kCoarse) h.coarse[threadIdx.x] = 0;
+    for (uint32_t i = threadIdx.x; i < kBins; i += B) h.fine[i] = 0;
+}
+__device__ inline void add_to_bins(Bins &h, int img, int top, uint32_t shift) {
+    const uint32_t bin = (static_cast<uint32_t>(top) - static_cast<uint32_t>(img)) >> shift;
+    if (bin < kBins) {
+        atomicAdd(&h.fine[bin], 1u);
+        atomicAdd(&h.coarse[bin / kFine], 1u);
+    }
+}
+// By a whole wave: the first bin up to which `want` were counted, kBins if fewer were.
+__device__ inline uint32_t bin_of(const Bins &h, uint32_t want) {
+    const uint32_t lane = threadIdx.x % kLanes;
+    const uint32_t c = h.coarse[lane], upto = lanes_sum(c);
+    const uint64_t enough = __ballot(upto >= want);
+    if (enough == 0) return kBins;
+    const int q = __builtin_ctzll(enough);
+    const uint32_t before = __builtin_amdgcn_readlane(upto - c, q);
+    const uint32_t f = lane < kFine ? h.fine[q * kFine + lane] : 0;
+    return q * kFine + __builtin_ctzll(__ballot(before + lanes_sum(f) >= want));
+}
+
+// Two images of 16 bits at once, the wanted elements largest.
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+__device__ inline i16x2 image_pair(uint32_t w, uint32_t flip) {
+    const i16x2 v = __builtin_bit_cast(i16x2, w);
+    const uint32_t sign = __builtin_bit_cast(uint32_t, static_cast<i16x2>(v >> 15));
+    return __builtin_bit_cast(i16x2, w ^ (sign & 0x7FFF7FFFu) ^ flip);
+}
+template <int W> __device__ inline int vec_max(u32x4 v, uint32_t flip) {
+    if constexpr (W == 2) {
+        const i16x2 m = __builtin_elementwise_max(
+            __builtin_elementwise_max(image_pair(v[0], flip), image_pair(v[1], flip)),
+            __builtin_elementwise_max(image_pair(v[2], flip), image_pair(v[3], flip)));
+        return max(static_cast<int>(m.x), static_cast<int>(m.y));
+    } else {
+        return max(max(image32(v[0], flip), image32(v[1], flip)), max(image32(v[2], flip), image32(v[3], flip)));
     }
 }
 
+// The sum over the workgroup of a count (two barriers).
+template <int B> __device__ inline uint32_t block_sum(uint32_t c, uint32_t *cells) {
+    c = wave_sum(c);
+    __syncthreads();
+    if (threadIdx.x % kLanes == 0) cells[threadIdx.x / kLanes] = c;
+    __syncthreads();
+    c = 0;
+    for (int w = 0; w < B / kLanes; ++w) c += cells[w];
+    return c;
+}
+
+// The candidates' places and their output, from buf[0, c), `want` of them wanted
+// (c <= CAP), no image above `top` or below `low`.  Few count the words above
+// theirs; more are dealt to bins in order first and count within their bin
+// (300 of 512 threads: 3 us by counting all).
+template <int W, int B, int CAP>
+__device__ void write_ranked(const TopArgs &a, uint64_t *buf, Bins &bins, uint32_t *cells, uint32_t c, uint32_t want, int top,
+                             int64_t low, uint64_t task, uint64_t row) {
+    const auto put = [&](uint64_t w, uint32_t place) {
+        if (a.splits == 1) {
+            const uint64_t at = row * a.k + place;
+            if (W == 2)
+                static_cast<uint16_t *>(a.values)[at] = static_cast<uint16_t>(pattern_of<2>(image_of(w), a.flip));
+            else
+                static_cast<uint32_t *>(a.values)[at] = pattern_of<4>(image_of(w), a.flip);
+            a.indices[at] = column_of(w);
+        } else {
+            a.words[task * a.k + place] = w;
+        }
+    };
+    const uint32_t tid = threadIdx.x;
+    if (c <= kRankWords) {
+        for (uint32_t i = tid; i < c; i += B) {
+            const uint64_t w = buf[i];
+            uint32_t place = 0;
+#pragma unroll 8
+            for (uint32_t j = 0; j < c; ++j) place += buf[j] > w;
+            if (place < want) put(w, place);
+        }
+    } else {
+        constexpr int kOwn = CAP / B, kShare = kBins / B;
+        clear_bins<B>(bins);
+        const uint32_t range = static_cast<uint32_t>(static_cast<int64_t>(top) - low);
+        const uint32_t shift = range < kBins ? 0 : 21 - __builtin_clz(range);
+        uint64_t w[kOwn];
+        uint32_t at[kOwn];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            w[i] = i * B + tid < c ? buf[i * B + tid] : 0;
+            if (w[i]) at[i] = atomicAdd(&bins.fine[(static_cast<uint32_t>(top) - static_cast<uint32_t>(image_of(w[i]))) >> shift], 1u);
+        }
+        __syncthreads();
+        uint32_t held[kShare], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kShare; ++i) sum += held[i] = bins.fine[tid * kShare + i];
+        const uint32_t upto = lanes_sum(sum);
+        if (tid % kLanes == kLanes - 1) cells[tid / kLanes] = upto;
+        __syncthreads();
+        uint32_t start = upto - sum;
+        for (uint32_t v = 0; v < tid / kLanes; ++v) start += cells[v];
+#pragma unroll
+        for (int i = 0; i < kShare; ++i) {
+            bins.fine[tid * kShare + i] = start;
+            start += held[i];
+        }
+        __syncthreads();
+        const auto bin_at = [&](uint64_t word) { return (static_cast<uint32_t>(top) - static_cast<uint32_t>(image_of(word))) >> shift; };
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i)
+            if (w[i]) buf[bins.fine[bin_at(w[i])] + at[i]] = w[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i)
+            if (w[i]) {
+                const uint32_t bin = bin_at(w[i]), from = bins.fine[bin], to = bin + 1 < kBins ? bins.fine[bin + 1] : c;
+                uint32_t place = from;
+                if (from < want)
+                    for (uint32_t j = from; j < to; ++j) place += buf[j] > w[i];
+                if (place < want) put(w[i], place);
+            }
+    }
+    if (a.splits > 1)
+        for (uint32_t j = want + tid; j < a.k; j += B) a.words[task * a.k + j] = 0;
+}
+
+// One workgroup of B threads a row (or a split of one), V loads of 16 bytes a
+// thread, all on their way at once.  A histogram below the largest image, of
+// the threads' largest images where k is at most half of them and of all
+// elements otherwise, gives a bound that at least k elements reach; they go to
+// LDS as words.  Where ties leave too many, the k-th image is found exactly and
+// the first of its columns fill up.
+template <int W, int B, int V>
+__global__ __launch_bounds__(B, 4) void topk_held_kernel(TopArgs a) {
+    constexpr int kVec = 16 / W;
+    using Stored = typename Row<W == 2 ? kRowF16 : kRowF32>::Stored;
+    __shared__ uint64_t buf[kHeldWords];
+    __shared__ Bins bins;
+    __shared__ int tops[B / kLanes];
+    __shared__ uint32_t cells[B / kLanes];
+    __shared__ uint32_t count;
+    const uint32_t tid = threadIdx.x;
+    const uint64_t task = a.first_task + xcd_chunk(blockIdx.x, gridDim.x);
+    const uint64_t row = task / a.splits;
+    const uint32_t first = static_cast<uint32_t>(task % a.splits) * a.split_len;
+    const uint32_t len = min(a.split_len, a.n - first), want = min(a.k, len);
+    const uint32_t vecs = len / kVec, rest = vecs * kVec + tid;
+    const Stored *x = static_cast<const Stored *>(a.x) + row * a.stride + first;
+
+    u32x4 v[V];
+    const auto below = [&](int u) { return static_cast<int>(tid) < static_cast<int>(vecs) - u * B; };
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        v[u] = u32x4{0, 0, 0, 0};
+        if (below(u)) v[u] = load16_once(reinterpret_cast<const uint8_t *>(x + u * B * kVec) + tid * 16);
+    }
+    const bool extra = rest < len;
+    const int over = extra ? image<W>(x[rest], a.flip) : INT32_MIN;
+    clear_bins<B>(bins);
+    if (tid == 0) count = 0;
+
+    int most[V], top = over;  // of each load, of all
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        most[u] = below(u) ? vec_max<W>(v[u], a.flip) : INT32_MIN;
+        top = max(top, most[u]);
+    }
+    const int mine = top;
+    const bool some = extra || below(0);
+    top = wave_max_int(top);
+    if (tid % kLanes == 0) tops[tid / kLanes] = top;
+    __syncthreads();
+    for (int w = 0; w < B / kLanes; ++w) top = max(top, tops[w]);
+
+    // f for every element of a load
+    const auto each = [&](u32x4 w, uint32_t at, auto f) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            const uint32_t pat = W == 2 ? (w[e / 2] >> (16 * (e & 1))) & 0xFFFFu : w[e % 4];
+            f(image<W>(pat, a.flip), at + e);
+        }
+    };
+    const auto place_of = [&](int u) { return (u * B + tid) * kVec; };
+    // each pass makes the images anew: kept, they would take twice the registers
+    const auto anew = [&]() {
+#pragma unroll
+        for (int u = 0; u < V; ++u) asm volatile("" : "+v"(v[u]));
+    };
+    anew();
+    const bool by_thread = 2 * want <= min(static_cast<uint32_t>(B), vecs);
+    uint32_t shift = W == 2 ? 0 : 13, bin;
+    for (;; shift += W == 2 ? 5 : 8) {  // at the second shift every image has a bin
+        if (by_thread) {
+            if (some) add_to_bins(bins, mine, top, shift);
+        } else {
+#pragma unroll
+            for (int u = 0; u < V; ++u)
+                if (below(u)) each(v[u], 0, [&](int img, uint32_t) { add_to_bins(bins, img, top, shift); });
+            if (extra) add_to_bins(bins, over, top, shift);
+        }
+        anew();
+        __syncthreads();
+        bin = bin_of(bins, want);
+        if (bin < kBins) break;
+        __syncthreads();
+        clear_bins<B>(bins);
+        __syncthreads();
+    }
+    const int64_t low = static_cast<int64_t>(top) - ((static_cast<int64_t>(bin + 1) << shift) - 1);
+    int bound = static_cast<int>(max(low, static_cast<int64_t>(W == 2 ? -32768 : INT32_MIN)));
+
+    const auto take = [&](int img, uint32_t at) {
+        if (img >= bound) {
+            const uint32_t slot = atomicAdd(&count, 1u);
+            if (slot < kHeldWords) buf[slot] = word_of(img, first + at);
+        }
+    };
+    if (mine >= bound && some) {
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+            if (most[u] >= bound && below(u)) each(v[u], place_of(u), take);
+        if (extra) take(over, rest);
+    }
+    __syncthreads();
+    uint32_t c = count;
+    if (c > kHeldWords) {  // rare: the row is read again
+        const auto again = [&](auto f) {
+            for (uint32_t i = tid; i < vecs; i += B) each(load16(x + i * kVec), i * kVec, f);
+            if (extra) f(over, rest);
+        };
+        // the k-th image: at least `want` reach lo, fewer pass hi
+        int lo = bound, hi = by_thread ? top : min(static_cast<int64_t>(top), low + (int64_t(1) << shift) - 1);
+        while (lo < hi) {
+            const int mid = (lo | hi) - ((lo ^ hi) >> 1);
+            uint32_t n = 0;
+            again([&](int img, uint32_t) { n += img >= mid; });
+            if (block_sum<B>(n, cells) >= want) lo = mid;
+            else hi = mid - 1;
+        }
+        __syncthreads();
+        if (tid == 0) count = 0;
+        __syncthreads();
+        if (lo < INT32_MAX) {
+            bound = lo + 1;
+            again(take);
+        }
+        bound = lo;
+        __syncthreads();
+        c = count;  // below `want`
+        // the first columns of image lo: stripe by stripe, in the order of threads
+        for (uint32_t base = 0; base <= vecs && c < want; base += B) {
+            const uint32_t i = base + tid;
+            // the elements after the last whole load are a stripe of their own threads' order
+            const bool in = i < vecs, last = base + B > vecs;
+            const u32x4 w = in ? load16(x + i * kVec) : u32x4{0, 0, 0, 0};
+            const auto fill = [&](bool on, auto elements) {
+                uint32_t here = 0;
+                if (on) elements([&](int img, uint32_t) { here += img == lo; });
+                const uint32_t upto = lanes_sum(here);
+                __syncthreads();
+                if (tid % kLanes == kLanes - 1) cells[tid / kLanes] = upto;
+                __syncthreads();
+                uint32_t at = c + upto - here, all = 0;
+                for (uint32_t w = 0; w < B / kLanes; ++w) {
+                    if (w < tid / kLanes) at += cells[w];
+                    all += cells[w];
+                }
+                if (on) elements([&](int img, uint32_t column) {
+                    if (img == lo) {
+                        if (at < want) buf[at] = word_of(lo, first + column);
+                        ++at;
+                    }
+                });
+                c = min(c + all, want);
+            };
+            fill(in, [&](auto f) { each(w, i * kVec, f); });
+            if (last) fill(extra, [&](auto f) { f(over, rest); });
+        }
+        __syncthreads();
+    }
+    write_ranked<W, B, kHeldWords>(a, buf, bins, cells, c, want, top, bound, task, row);
+}
+
+// The k largest of a row's splits * k words.
+constexpr int kMergeBlock = 1024;
+template <int W>
+__global__ __launch_bounds__(kMergeBlock) void topk_merge_kernel(TopArgs a) {
+    constexpr int B = kMergeBlock, V = kTopBuffer / B;
+    __shared__ uint64_t buf[kTopBuffer];
+    __shared__ Bins bins;
+    __shared__ int tops[B / kLanes];
+    __shared__ uint32_t cells[B / kLanes];
+    __shared__ uint32_t count;
+    const uint64_t row = blockIdx.x;
+    const uint32_t tid = threadIdx.x, total = a.splits * a.k;  // at most kTopBuffer
+    const uint64_t *in = a.words + row * total;
+    uint64_t w[V];
+    int top = INT32_MIN;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        w[u] = u * B + tid < total ? in[u * B + tid] : 0;
+        if (w[u]) top = max(top, image_of(w[u]));
+    }
+    clear_bins<B>(bins);
+    if (tid == 0) count = 0;
+    top = wave_max_int(top);
+    if (tid % kLanes == 0) tops[tid / kLanes] = top;
+    __syncthreads();
+    for (int i = 0; i < B / kLanes; ++i) top = max(top, tops[i]);
+    uint32_t shift = W == 2 ? 0 : 13, bin;
+    for (;; shift += W == 2 ? 5 : 8) {
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+            if (w[u]) add_to_bins(bins, image_of(w[u]), top, shift);
+        __syncthreads();
+        bin = bin_of(bins, a.k);
+        if (bin < kBins) break;
+        __syncthreads();
+        clear_bins<B>(bins);
+        __syncthreads();
+    }
+    const int64_t low = static_cast<int64_t>(top) - ((static_cast<int64_t>(bin + 1) << shift) - 1);
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+        if (w[u] && image_of(w[u]) >= low) buf[atomicAdd(&count, 1u)] = w[u];
+    __syncthreads();
+    a.splits = 1;  // what is written is the row
+    write_ranked<W, B, kTopBuffer>(a, buf, bins, cells, count, a.k, top, low, row, row);
+}
+
 // Rows that one wave, or part of one, sorts in registers.
-constexpr uint64_t kWaveVecs = 8;  // 16-byte loads a lane at most
-bool topk_short(uint64_t n, uint64_t k, uint64_t size) {
-    return n <= kLanes || (k <= kLanes && n <= kLanes * kWaveVecs * 16 / size);
+constexpr uint64_t kWaveElems = 1024;
+bool topk_short(uint64_t n, uint64_t k) {
+    return n <= kLanes || (k <= kLanes && n <= kWaveElems);
 }
 
 template <int W> void launch_short(const TopArgs &a, const Launch &L) {
@@ -554,18 +911,39 @@ template <int W> void launch_short(const TopArgs &a, const Launch &L) {
     const dim3 waves = grid(kTopBlock / kLanes);
     if (vecs <= 1) return launch_on(topk_wave_kernel<W, 1>, waves, block, L, a);
     if (vecs <= 2) return launch_on(topk_wave_kernel<W, 2>, waves, block, L, a);
-    if (vecs <= 4) return launch_on(topk_wave_kernel<W, 4>, waves, block, L, a);
-    launch_on(topk_wave_kernel<W, 8>, waves, block, L, a);
+    if constexpr (W == 4) launch_on(topk_wave_kernel<W, 4>, waves, block, L, a);
 }
 
-// How many workgroups share a row: enough that few rows still occupy the GPU,
-// each with a piece worth a workgroup, and no more words than one merges.
-uint32_t topk_splits(uint64_t rows, uint64_t n, uint64_t k) {
-    if (rows == 0 || rows >= 256) return 1;
-    const uint64_t piece = std::max<uint64_t>(4096, 8 * k);
-    uint64_t s = std::min<uint64_t>((512 + rows - 1) / rows, n / piece);
-    s = std::min<uint64_t>(s, kTopBuffer / k);
-    return static_cast<uint32_t>(std::max<uint64_t>(1, s));
+// Rows, or splits of rows, of at most 256 KB are held in registers.
+constexpr uint64_t kHeldBytes = 1024 * 16 * 16;
+
+// How many workgroups share a row: as many as leave each 256 KB at most, or, of
+// few long rows, 32 KB (1 x 131072 bf16: 10 us; 11 us in pieces of 64 KB or of 8 KB).  Their words have to fit
+// the merge; rows too long for that are streamed.
+uint32_t topk_splits(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
+    if (rows == 0) return 1;
+    const uint64_t most = kTopBuffer / k, least = (n * size + kHeldBytes - 1) / kHeldBytes;
+    const uint64_t few = rows <= 64 && n >= 32768 ? std::min<uint64_t>(256 / rows, n * size / 32768) : 1;
+    return static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(most, std::max<uint64_t>(least, few))));
+}
+
+// Threads by the rows there are: workgroups of 1024 where there are no more
+// than CUs, the fewest threads that hold a row where several share a CU.
+template <int W> void launch_held(TopArgs a, uint32_t tasks, const Launch &L) {
+    const uint64_t vecs = a.split_len / (16 / W);
+    const auto go = [&](auto kernel, int block) { launch_on(kernel, dim3(tasks), dim3(block), L, a); };
+    if (a.rows * a.splits <= 256) {
+        if (vecs <= 1024 * 2) return go(topk_held_kernel<W, 1024, 2>, 1024);
+        if (vecs <= 1024 * 4) return go(topk_held_kernel<W, 1024, 4>, 1024);
+        if (vecs <= 1024 * 8) return go(topk_held_kernel<W, 1024, 8>, 1024);
+        return go(topk_held_kernel<W, 1024, 16>, 1024);
+    }
+    if (vecs <= 256 * 2) return go(topk_held_kernel<W, 256, 2>, 256);
+    if (vecs <= 256 * 4) return go(topk_held_kernel<W, 256, 4>, 256);
+    if (vecs <= 256 * 8) return go(topk_held_kernel<W, 256, 8>, 256);
+    if (vecs <= 256 * 16) return go(topk_held_kernel<W, 256, 16>, 256);
+    if (vecs <= 512 * 16) return go(topk_held_kernel<W, 512, 16>, 512);
+    go(topk_held_kernel<W, 1024, 16>, 1024);
 }
 
 int check_topk(int64_t rows, int64_t n, int64_t k, int64_t stride, int dtype) {
@@ -577,8 +955,8 @@ int check_topk(int64_t rows, int64_t n, int64_t k, int64_t stride, int dtype) {
 }
 
 uint64_t topk_bytes(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
-    if (rows == 0 || k == 0 || topk_short(n, k, size)) return 0;
-    const uint64_t s = topk_splits(rows, n, k);
+    if (rows == 0 || k == 0 || topk_short(n, k)) return 0;
+    const uint64_t s = topk_splits(rows, n, k, size);
     return s > 1 ? rows * s * k * sizeof(uint64_t) : 0;
 }
 
@@ -622,7 +1000,7 @@ int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_
     a.rows = R;
     a.n = static_cast<uint32_t>(N);
     a.k = static_cast<uint32_t>(K);
-    a.splits = topk_splits(R, N, K);
+    a.splits = topk_splits(R, N, K, size);
     // whole 16-byte loads to a split
     a.split_len = static_cast<uint32_t>(((N + a.splits - 1) / a.splits + 7) / 8 * 8);
     a.splits = static_cast<uint32_t>((N + a.split_len - 1) / a.split_len);
@@ -630,7 +1008,7 @@ int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_
     a.values = vals_out;
     a.indices = idx_out;
     a.words = static_cast<uint64_t *>(workspace);
-    if (topk_short(N, K, size)) {
+    if (topk_short(N, K)) {
         TimedLaunch t(4, c);
         if (size == 2)
             launch_short<2>(a, t.L);
@@ -638,9 +1016,21 @@ int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_
             launch_short<4>(a, t.L);
         return hipGetLastError() == hipSuccess ? LRS_OK : LRS_ERR_HIP;
     }
-    const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(R * a.splits, 1u << 20)));
-    {
+    constexpr uint64_t kMaxGrid = 1u << 20;
+    const uint64_t tasks = R * a.splits;
+    if (a.split_len * size <= kHeldBytes) {
+        for (; a.first_task < tasks; a.first_task += kMaxGrid) {
+            TimedLaunch t(4, c);
+            const uint32_t now = static_cast<uint32_t>(std::min<uint64_t>(tasks - a.first_task, kMaxGrid));
+            if (size == 2)
+                launch_held<2>(a, now, t.L);
+            else
+                launch_held<4>(a, now, t.L);
+            if (hipGetLastError() != hipSuccess) return LRS_ERR_HIP;
+        }
+    } else {
         TimedLaunch t(4, c);
+        const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(tasks, kMaxGrid)));
         if (size == 2)
             launch_on(topk_kernel<2>, grid, dim3(kTopBlock), t.L, a);
         else
@@ -651,9 +1041,9 @@ int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_
         TimedLaunch t(4, c);
         const dim3 merge(static_cast<uint32_t>(R));
         if (size == 2)
-            launch_on(topk_merge_kernel<2>, merge, dim3(kTopBlock), t.L, a);
+            launch_on(topk_merge_kernel<2>, merge, dim3(kMergeBlock), t.L, a);
         else
-            launch_on(topk_merge_kernel<4>, merge, dim3(kTopBlock), t.L, a);
+            launch_on(topk_merge_kernel<4>, merge, dim3(kMergeBlock), t.L, a);
         if (hipGetLastError() != hipSuccess) return LRS_ERR_HIP;
     }
     return LRS_OK;
