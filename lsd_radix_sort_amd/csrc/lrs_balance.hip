@@ -161,6 +161,7 @@ __global__ __launch_bounds__(B) void balance_kernel(BalArgs a) {
     constexpr int kVec = Row<T>::kVec;
     using Stored = typename Row<T>::Stored;
     __shared__ int32_t hist[LRS_MAX_EXPERTS + 1];
+    __shared__ __align__(16) float shared_load[LRS_MAX_EXPERTS + 8];
     __shared__ double part[(B / kLanes)];
     __shared__ int64_t sums[(B / kLanes)];
     __shared__ uint32_t arrived;
@@ -173,18 +174,20 @@ __global__ __launch_bounds__(B) void balance_kernel(BalArgs a) {
     uint64_t row = static_cast<uint64_t>(blockIdx.x) * (B / a.lanes) + tid / a.lanes;
     const uint32_t none = T == kRowF16 ? 0xFC00FC00u : T == kRowBF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
     u32x4 v[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) v[u] = u32x4{none, none, none, none};
     bool counted = false;
+    // a place past the row's end keeps -inf; a row that does not count keeps
+    // what was there, and nothing comes of it
     const auto load_row = [&](uint64_t r) {
         counted = r < a.rows && (!a.mask || a.mask[r]);
+        if (!counted) return;
         const Stored *x = static_cast<const Stored *>(a.x) + r * a.stride;
 #pragma unroll
         for (int u = 0; u < V; ++u) {
             const uint32_t at = (u * a.lanes + sub) * kVec;
-            v[u] = u32x4{none, none, none, none};
-            if (!counted || at >= E) continue;
-            if (at + kVec <= E) {
-                v[u] = load16_once(x + at);
-            } else {
+            if (at + kVec <= E) v[u] = load16_once(x + at);
+            if (E % kVec != 0 && at < E && at + kVec > E) {
                 float f[kVec];
                 for (int e = 0; e < kVec; ++e) f[e] = at + e < E ? Row<T>::value(x[at + e]) : -INFINITY;
                 v[u] = pack16<T>(f);
@@ -234,19 +237,25 @@ __global__ __launch_bounds__(B) void balance_kernel(BalArgs a) {
     total = 0;
     for (int w = 0; w < (B / kLanes); ++w) total += sums[w];
     const int32_t kept = hist[E];
+    const double per = total > 0 ? static_cast<double>(E) / static_cast<double>(total) : 0;
+    for (uint32_t e = tid; e < E + kVec; e += B) shared_load[e] = e < E ? static_cast<float>(hist[e] * per) : 0.f;
+    __syncthreads();
     // this lane's columns stay the same from row to row
     float load[V][kVec];
-    const double per = total > 0 ? static_cast<double>(E) / static_cast<double>(total) : 0;
 #pragma unroll
-    for (int u = 0; u < V; ++u)
+    for (int u = 0; u < V; ++u) {
+        const uint32_t at = min((u * a.lanes + sub) * kVec, E / kVec * kVec);  // places past the row hold -inf
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            const uint32_t at = (u * a.lanes + sub) * kVec + e;
-            load[u][e] = at < E ? static_cast<float>(hist[at] * per) : 0.f;
+        for (int e = 0; e < kVec; e += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(shared_load + at + e);
+            load[u][e] = f.x;
+            load[u][e + 1] = f.y;
+            load[u][e + 2] = f.z;
+            load[u][e + 3] = f.w;
         }
+    }
     const float inv = kept > 0 ? 1.f / kept : 0.f;
     const float up = (a.loss_grad ? *a.loss_grad : 1.f) * inv;
-    const auto plus = [](float p, float q) { return p + q; };
     double loss = 0;
     // every group of a wave makes the same number of turns
     for (uint64_t base = row - tid / a.lanes; base < a.rows; base += step, row += step) {
@@ -255,42 +264,59 @@ __global__ __launch_bounds__(B) void balance_kernel(BalArgs a) {
 #pragma unroll
         for (int u = 0; u < V; ++u) unpack16<T>(v[u], w[u]);
         if (base + step < a.rows) load_row(row + step);
-        float m = -INFINITY;
+        // exponents of 2 relative to `ref`: x log2(e) - ref, x taken from `from`
+        // where a logit is so large that its product is not finite
+        float m = 0, ref = 0, from = 0;
         if (!SIG) {
+            m = w[0][0];
 #pragma unroll
             for (int u = 0; u < V; ++u)
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) m = w[u][e] > m ? w[u][e] : m;
-            m = group_join(m, a.lanes, [](float p, float q) { return fmaxf(p, q); });
+                for (int e = 0; e < kVec; e += 2) m = max3(m, w[u][e], w[u][e + 1]);
+            m = group_max(m, a.lanes);
             if (m == -INFINITY) m = 0.f;
+            if (__any(fabsf(m) > 0x1p120f)) {
+                from = m;
+#pragma unroll
+                for (int u = 0; u < V; ++u)
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) w[u][e] -= from;
+            }
+            ref = (m - from) * kLog2e;
         }
         float s = 0, b = 0;
         float slope[SIG ? V : 1][kVec];  // sigmoid times 1 - sigmoid, without the cancellation
+        const auto add = [&](int u, int e, float x) {
+            w[u][e] = x;
+            s += x;
+            b = fmaf(x, load[u][e], b);
+        };
+        if (SIG) {
 #pragma unroll
-        for (int u = 0; u < V; ++u)
+            for (int u = 0; u < V; ++u)
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                if (SIG) {
+                for (int e = 0; e < kVec; ++e) {
                     const float t = __builtin_amdgcn_exp2f(-w[u][e] * kLog2e), g = __builtin_amdgcn_rcpf(1.f + t);
-                    w[u][e] = g;
                     slope[SIG ? u : 0][e] = g == 0.f ? 0.f : g * (g * t);
-                } else {
-                    w[u][e] = __builtin_amdgcn_exp2f((w[u][e] - m) * kLog2e);
+                    add(u, e, g);
                 }
-                s += w[u][e];
-                b += w[u][e] * load[u][e];
-            }
-        s = group_join(s, a.lanes, plus);
-        b = group_join(b, a.lanes, plus);
+        } else {
+#pragma unroll
+            for (int u = 0; u < V; ++u)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) add(u, e, __builtin_amdgcn_exp2f(fmaf(w[u][e], kLog2e, -ref)));
+        }
+        const float2 sums = group_join(make_float2(s, b), a.lanes);
+        s = sums.x;
+        b = sums.y;
         const bool empty = s == 0.f;
-        const float r = empty ? 0.f : 1.f / s;
+        const float r = empty ? 0.f : __builtin_amdgcn_rcpf(s);
         b *= r;
-        const float z = SIG || empty ? 0.f : m + __builtin_amdgcn_logf(s) * kLn2;
+        const float z = SIG || empty ? 0.f : fmaf(ref + __builtin_amdgcn_logf(s), kLn2, from);
         if (mine && sub == 0) loss += static_cast<double>(a.alpha * b + a.beta * z * z);
         if (a.grad && row < a.rows) {
             Stored *g = static_cast<Stored *>(a.grad) + row * a.grad_stride;
-            const float p = mine ? a.alpha * r * up : 0.f;
-            const float q = mine ? 2.f * a.beta * z * r * up : 0.f;
+            const float p = a.alpha * r * up, q = fmaf(2.f * a.beta * z, r * up, -p * b);
 #pragma unroll
             for (int u = 0; u < V; ++u) {
                 const uint32_t at = (u * a.lanes + sub) * kVec;
@@ -298,7 +324,7 @@ __global__ __launch_bounds__(B) void balance_kernel(BalArgs a) {
                 float d[kVec];
 #pragma unroll
                 for (int e = 0; e < kVec; ++e)
-                    d[e] = (SIG ? slope[SIG ? u : 0][e] : w[u][e]) * fmaf(p, load[u][e] - b, q);
+                    d[e] = (SIG ? slope[SIG ? u : 0][e] : w[u][e]) * fmaf(p, load[u][e], q);
                 const u32x4 out = mine ? pack16<T>(d) : u32x4{0, 0, 0, 0};
                 if (at + kVec <= E) {
                     store16_once(g + at, out);

@@ -141,16 +141,39 @@ template <typename V, typename F> __device__ inline V wave_join(V v, V none, F j
     v = join(v, moved<0x143, 0xC>(v, none));
     return last_lane(v);
 }
-// The same for every `lanes` neighbours of a wave (a power of two), the result in
+// Sums and the largest of every `lanes` neighbours of a wave (a power of two), in
 // each of them: quads, eights and sixteens by quad_perm, row_half_mirror and
 // row_mirror, then across rows.
-template <typename V, typename F> __device__ inline V group_join(V v, uint32_t lanes, F join) {
-    if (lanes > 1) v = join(v, moved<0xB1>(v, v));
-    if (lanes > 2) v = join(v, moved<0x4E>(v, v));
-    if (lanes > 4) v = join(v, moved<0x141>(v, v));
-    if (lanes > 8) v = join(v, moved<0x140>(v, v));
-    if (lanes > 16) v = join(v, __shfl_xor(v, 16));
-    if (lanes > 32) v = join(v, __shfl_xor(v, 32));
+template <int CONTROL> __device__ inline float swapped(float v) {  // every lane has a source: joins with what uses it
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CONTROL, 0xF, 0xF, true));
+}
+// The largest of three, without the instructions that would quiet a signalling NaN first.
+__device__ inline float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ inline float2 group_join(float2 v, uint32_t lanes) {
+    const auto add = [&](float p, float q) {
+        v.x += p;
+        v.y += q;
+    };
+    if (lanes > 1) add(swapped<0xB1>(v.x), swapped<0xB1>(v.y));
+    if (lanes > 2) add(swapped<0x4E>(v.x), swapped<0x4E>(v.y));
+    if (lanes > 4) add(swapped<0x141>(v.x), swapped<0x141>(v.y));
+    if (lanes > 8) add(swapped<0x140>(v.x), swapped<0x140>(v.y));
+    if (lanes > 16) add(__shfl_xor(v.x, 16), __shfl_xor(v.y, 16));
+    if (lanes > 32) add(__shfl_xor(v.x, 32), __shfl_xor(v.y, 32));
+    return v;
+}
+__device__ inline float group_max(float v, uint32_t lanes) {
+    const auto join = [&](float p) { v = max3(v, p, p); };
+    if (lanes > 1) join(swapped<0xB1>(v));
+    if (lanes > 2) join(swapped<0x4E>(v));
+    if (lanes > 4) join(swapped<0x141>(v));
+    if (lanes > 8) join(swapped<0x140>(v));
+    if (lanes > 16) join(__shfl_xor(v, 16));
+    if (lanes > 32) join(__shfl_xor(v, 32));
     return v;
 }
 template <typename V> __device__ inline V wave_sum(V v) {
