@@ -350,6 +350,7 @@ __device__ inline double scalar(double v) {
 }
 constexpr double kLn2 = 0.693147180559945309417;
 __device__ inline double exp2_64(double d) {
+    d = d < -2000.0 ? -2000.0 : d;
     const double i = rint(d), y = (d - i) * scalar(kLn2);
     double p = scalar(1.0 / 39916800);
     p = fma(p, y, scalar(1.0 / 3628800));

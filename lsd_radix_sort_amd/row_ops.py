@@ -24,17 +24,21 @@ _DTYPES = {torch.float16: _lrs.LRS_DTYPE_FP16, torch.bfloat16: _lrs.LRS_DTYPE_BF
            torch.float32: _lrs.LRS_DTYPE_FP32}
 
 
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
 def _matrix(x, name: str) -> int:
     """Check a float matrix with contiguous rows; returns its LRS_DTYPE code."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         _lrs._bad(f"{name} must be a GPU tensor")
-    if x.dtype not in _DTYPES:
+    code = _DTYPES.get(x.dtype)
+    if code is None:
         _lrs._bad(f"{name} must be float16, bfloat16 or float32, got {x.dtype}")
     if x.dim() != 2:
         _lrs._bad(f"{name} must be a 2-D tensor")
-    if x.shape[1] > 1 and x.stride(1) != 1:
+    if x.stride(1) != 1 and x.size(1) > 1:
         _lrs._bad(f"{name} must have contiguous rows (stride 1 along the last dimension)")
-    return _DTYPES[x.dtype]
+    return code
 
 
 # ------------------------------------------------------------------- top k
@@ -85,7 +89,7 @@ def _by_row(t, name: str, rows: int, device) -> int | None:
     if t is None:
         return None
     _lrs._same_device(t, name, device)
-    if t.dtype != torch.float32 or t.shape != (rows,) or not t.is_contiguous():
+    if t.dtype is not torch.float32 or t.dim() != 1 or t.size(0) != rows or not t.is_contiguous():
         _lrs._bad(f"{name} must be a contiguous float32 tensor of shape ({rows},)")
     return t.data_ptr()
 
@@ -93,13 +97,14 @@ def _by_row(t, name: str, rows: int, device) -> int | None:
 def _ids(t, name: str, rows: int, device) -> int:
     """Check a rows x k integer matrix; returns its element size."""
     _lrs._same_device(t, name, device)
-    if t.dtype not in (torch.int32, torch.int64):
+    size = _ID_BYTES.get(t.dtype)
+    if size is None:
         _lrs._bad(f"{name} must be int32 or int64, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows:
+    if t.dim() != 2 or t.size(0) != rows:
         _lrs._bad(f"{name} must be a 2-D tensor of {rows} rows")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if t.stride(1) != 1 and t.size(1) > 1:
         _lrs._bad(f"{name} must have contiguous rows (stride 1 along the last dimension)")
-    return t.element_size()
+    return size
 
 
 def _distill_inputs(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights) -> _Distill:
@@ -109,19 +114,20 @@ def _distill_inputs(logits, teacher_values, teacher_indices, temperature, teache
     teacher_dtype = _matrix(teacher_values, "teacher_values")
     _lrs._same_device(teacher_values, "teacher_values", device)
     index_bytes = _ids(teacher_indices, "teacher_indices", rows, device)
-    if teacher_values.shape != teacher_indices.shape:
+    k = teacher_values.size(1)
+    if teacher_values.size(0) != rows or teacher_indices.size(1) != k:
         _lrs._bad(f"teacher_values {tuple(teacher_values.shape)} and teacher_indices {tuple(teacher_indices.shape)} differ")
     return _Distill(logits.data_ptr(), logits.stride(0), teacher_values.data_ptr(), teacher_values.stride(0),
                     teacher_indices.data_ptr(), teacher_indices.stride(0),
                     _by_row(teacher_lse, "teacher_lse", rows, device),
-                    _by_row(row_weights, "row_weights", rows, device), rows, n, teacher_values.shape[1], dtype,
+                    _by_row(row_weights, "row_weights", rows, device), rows, n, k, dtype,
                     teacher_dtype, index_bytes, temperature)
 
 
 def _grad_out(t, like: torch.Tensor) -> torch.Tensor:
     """A gradient like the logits: new and contiguous, or the caller's with contiguous rows."""
     if t is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
     _lrs._same_device(t, "grad_out", like.device)
     if t.dtype != like.dtype or t.shape != like.shape or (t.shape[1] > 1 and t.stride(1) != 1):
         _lrs._bad(f"grad_out must be a {like.dtype} tensor of shape {tuple(like.shape)} with contiguous rows")

@@ -396,3 +396,20 @@ def test_lowest_values_as_masks(dtype, tail, temperature, n, k):
     s[5, ::2] = torch.finfo(s.dtype).max / 4
     s[5, i[5]] = torch.finfo(s.dtype).max / 2
     check_shifted(s, t, i, temperature, tlse)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("n,k", [(40, 6), (20_003, 30), (140_001, 20)])
+def test_odd_teachers(dtype, n, k):
+    """Rows whose teacher has no mass on S, or all of it, unused slots anywhere, and weights of either sign."""
+    log(f"odd teachers {dtype} n={n} k={k}")
+    s, t, i, tlse = make(8, n, k, dtype, 800, True)
+    tlse[0] = math.inf
+    tlse[1] = torch.logsumexp(t[1].double(), 0).float()
+    t[2] = -math.inf
+    i[3, ::2] = -1
+    i[4, 1] = n
+    t[5, 0] = -math.inf
+    w = torch.tensor([0.5, -0.25, 1.0, 0.0, 2.0, -1.0, 1e-3, 0.125])
+    check(s, t, i, 1.0, tlse, w)
+    check(s, t, i, 1.0, None, w)
