@@ -917,14 +917,16 @@ template <int W> void launch_short(const TopArgs &a, const Launch &L) {
 // Rows, or splits of rows, of at most 256 KB are held in registers.
 constexpr uint64_t kHeldBytes = 1024 * 16 * 16;
 
-// How many workgroups share a row: as many as leave each 256 KB at most, or, of
-// few long rows, 32 KB (1 x 131072 bf16: 10 us; 11 us in pieces of 64 KB or of 8 KB).  Their words have to fit
-// the merge; rows too long for that are streamed.
+// How many workgroups share a row: one where it can be held (1 x 131072 bf16 in
+// pieces of 32 KB: 9.8 us on the GPU, 10.9 us whole, but a second launch costs
+// the host 3 us); else as many as leave each 256 KB, or, of few rows, 32 KB
+// (1 x 131072 fp32: 9.3 us, 12.9 us in two pieces).  Their words have to fit the
+// merge; rows too long for that are streamed.
 uint32_t topk_splits(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
-    if (rows == 0) return 1;
+    if (rows == 0 || n * size <= kHeldBytes) return 1;
     const uint64_t most = kTopBuffer / k, least = (n * size + kHeldBytes - 1) / kHeldBytes;
-    const uint64_t few = rows <= 64 && n >= 32768 ? std::min<uint64_t>(256 / rows, n * size / 32768) : 1;
-    return static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(most, std::max<uint64_t>(least, few))));
+    const uint64_t few = rows <= 64 ? std::min<uint64_t>(256 / rows, n * size / 32768) : 1;
+    return static_cast<uint32_t>(std::min<uint64_t>(most, std::max<uint64_t>(least, few)));
 }
 
 // Threads by the rows there are: workgroups of 1024 where there are no more

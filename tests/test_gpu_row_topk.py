@@ -143,10 +143,10 @@ def test_head_of_the_row_sort():
 
 
 def test_given_outputs_workspace_stream_and_timer():
-    bits = make_bits("normal", 3, 50_000, "bf16", 400)
+    bits = make_bits("normal", 3, 150_000, "bf16", 400)
     x = to_gpu(bits, "bf16")
-    need = lrs.segmented_row_topk_workspace_size(3, 50_000, 20, torch.bfloat16)
-    assert need > 0 and lrs.segmented_row_topk_workspace_size(256, 50_000, 20, torch.bfloat16) == 0
+    need = lrs.segmented_row_topk_workspace_size(3, 150_000, 20, torch.bfloat16)
+    assert need > 0 and lrs.segmented_row_topk_workspace_size(3, 50_000, 20, torch.bfloat16) == 0
     ws = torch.full((need,), 0xA5, dtype=torch.uint8, device="cuda")
     v = torch.empty(3, 20, dtype=torch.bfloat16, device="cuda")
     i = torch.empty(3, 20, dtype=torch.int64, device="cuda")
@@ -167,7 +167,7 @@ def test_given_outputs_workspace_stream_and_timer():
 
 
 def test_graph_replay():
-    for rows, n, k in ((2, 60_000, 30), (300, 200, 8)):
+    for rows, n, k in ((2, 60_000, 30), (2, 160_000, 30), (300, 200, 8)):
         x = torch.randn(rows, n, device="cuda").half()
         v, i = lrs.segmented_row_topk(x, k)
         ws = torch.empty(max(1, lrs.segmented_row_topk_workspace_size(rows, n, k, x.dtype)), dtype=torch.uint8,

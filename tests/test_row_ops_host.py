@@ -23,8 +23,8 @@ no_gpu = pytest.mark.skipif(_gpu_present(), reason="fake-pointer validation runs
 
 def test_topk_workspace_sizes():
     size = lrs.load_library().segmented_row_topk_workspace_size
-    assert size(1, 131072, 64, 1, None) >= 8 * 64 * 2
-    assert size(256, 131072, 64, 1, None) == 0       # enough rows: one workgroup each
+    assert size(1, 262144, 64, 1, None) >= 8 * 64 * 2
+    assert size(256, 131072, 64, 1, None) == 0       # one workgroup holds a row
     assert size(4, 1000, 10, 0, None) == 0           # too short to share
     assert size(0, 131072, 64, 1, None) == 0 and size(1, 131072, 0, 1, None) == 0
     assert size(1, 131072, 1025, 1, None) == 0       # k beyond the limit
@@ -44,13 +44,13 @@ def test_topk_refusals():
     assert st(k=5001) == 4 and st(k=1025) == 4 and st(n=1 << 30) == 4
     assert st(rows=1 << 30, n=2048) == 4 and st(rows=1 << 39, n=1, k=1, stride=1 << 20) == 4
     assert st(x=None) == 1 and st(v=None) == 1 and st(i=None) == 1
-    assert st(rows=1, n=100_000, ws=None) == 1 and st(rows=1, n=100_000, nb=8) == 6
+    assert st(rows=1, n=200_000, ws=None) == 1 and st(rows=1, n=200_000, nb=8) == 6
     assert st(x=ctypes.c_void_p(0x10000001)) == 9 and st(x=ctypes.c_void_p(0x10000002), dtype=2) == 9
     assert st(i=ctypes.c_void_p(0x30000004)) == 9
-    assert st(rows=1, n=100_000, ws=ctypes.c_void_p(0x40000010)) == 9
+    assert st(rows=1, n=200_000, ws=ctypes.c_void_p(0x40000010)) == 9
     assert st(v=x) == 5 and st(i=x) == 5 and st(v=i) == 5
     assert st(v=ctypes.c_void_p(0x10000000 + 2 * (3 * 5000 + 4990))) == 5
-    assert st(rows=1, n=100_000, ws=x) == 5
+    assert st(rows=1, n=200_000, ws=x) == 5
     assert st(opts=ctypes.byref(lrs._Options(7, 0, 0, 0, None))) == 10
     assert st(rows=0, x=None, v=None, i=None) == 0 and st(k=0, x=None, v=None, i=None) == 0
 
