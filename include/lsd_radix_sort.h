@@ -242,7 +242,7 @@ int segmented_row_sort(const uint16_t *vals_in, uint16_t *vals_out, int64_t *idx
  *   dtype: LRS_DTYPE_FP16, LRS_DTYPE_BF16 or LRS_DTYPE_FP32
  *   0 <= k <= n, k <= LRS_MAX_TOPK; n <= LRS_MAX_ROW_LEN; rows * n < 2^40;
  *   rows == 0 or k == 0 is a no-op.
- * Calls on fewer than 256 long rows share each row among workgroups and need
+ * Rows of more than 256 KB are shared among workgroups and need
  * segmented_row_topk_workspace_size bytes; others need none (the size is 0 and
  * workspace may be NULL).  Only opts->timer is used (kind 4).
  */

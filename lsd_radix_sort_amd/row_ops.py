@@ -11,6 +11,10 @@ stride (a slice of a wider buffer); the elements of a row are contiguous.
 topk_distill_loss and expert_balance_loss are the same losses for programs that
 differentiate through torch autograd; the `_step` calls return loss and
 gradient at once, without it.
+
+Calls that leave outputs and workspaces to the package go through a compiled
+binding (csrc/row_binding.cpp); it takes them only when every argument is in
+order, and the code here takes the others and names what is wrong with them.
 """
 from __future__ import annotations
 
@@ -19,6 +23,27 @@ import ctypes
 import torch
 
 import lsd_radix_sort_amd as _lrs
+
+_fast = None
+
+
+def _binding():
+    """The compiled binding of regular calls, bound to the loaded library's entry points."""
+    global _fast
+    if _fast is None:
+        lib = _lrs.load_library()
+        try:
+            from lsd_radix_sort_amd import _row_binding as fast
+        except ImportError as e:
+            raise ImportError("lsd_radix_sort_amd/_row_binding.so is missing or of another torch: build it with "
+                              "`python -m lsd_radix_sort_amd.build`") from e
+        names = ("segmented_row_topk_workspace_size", "segmented_row_topk", "topk_distill_workspace_size",
+                 "topk_distill_forward", "topk_distill_backward", "topk_distill_step",
+                 "expert_balance_step_workspace_size", "expert_balance_step", "expert_balance")
+        fast.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names})
+        _fast = fast
+    return _fast
+
 
 _DTYPES = {torch.float16: _lrs.LRS_DTYPE_FP16, torch.bfloat16: _lrs.LRS_DTYPE_BF16,
            torch.float32: _lrs.LRS_DTYPE_FP32}
@@ -54,6 +79,10 @@ def segmented_row_topk(x: torch.Tensor, k: int, descending: bool = True, values_
                        options: "_lrs.SortOptions | None" = None):
     """The k largest (or smallest) elements of every row of a 2-D fp16/bf16/fp32 GPU tensor, in order:
     the first k columns of a stable row sort.  Returns (values, int64 column indices)."""
+    if values_out is None and indices_out is None and workspace is None and options is None:
+        out = (_fast or _binding()).topk(x, int(k), bool(descending))
+        if out is not None:
+            return out
     lib = _lrs.load_library()
     dtype = _matrix(x, "x")
     rows, n = x.shape
@@ -185,6 +214,11 @@ def topk_distill_forward(logits: torch.Tensor, teacher_values: torch.Tensor, tea
     the teacher's whole row over the temperature) the rest of the teacher's mass counts against the rest of
     the student's; without it the teacher's top logits are renormalised.  row_weights: [rows] float32, default
     1 / rows; a row of weight 0 is left out.  Returns (loss, row_loss [rows], row_stats for the backward)."""
+    if workspace is None and options is None:
+        out = (_fast or _binding()).distill_forward(logits, teacher_values, teacher_indices, float(temperature), teacher_lse,
+                                                    row_weights)
+        if out is not None:
+            return out
     d = _distill_inputs(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights)
     row_loss = torch.empty(d.rows, dtype=torch.float32, device=logits.device)
     loss, stats = _distill_forward(d, logits, row_loss, workspace, options)
@@ -207,6 +241,11 @@ def topk_distill_step(logits: torch.Tensor, teacher_values: torch.Tensor, teache
                       row_weights: torch.Tensor | None = None, grad_out: torch.Tensor | None = None,
                       workspace: torch.Tensor | None = None, options: "_lrs.SortOptions | None" = None):
     """topk_distill_forward and its gradient in one call: returns (loss, row_loss, grad)."""
+    if grad_out is None and workspace is None and options is None:
+        out = (_fast or _binding()).distill_step(logits, teacher_values, teacher_indices, float(temperature), teacher_lse,
+                                                 row_weights)
+        if out is not None:
+            return out
     lib = _lrs.load_library()
     d = _distill_inputs(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights)
     opt = _lrs._opt(options)
@@ -255,7 +294,14 @@ class _DistillLoss(torch.autograd.Function):
 def topk_distill_loss(logits: torch.Tensor, teacher_values: torch.Tensor, teacher_indices: torch.Tensor,
                       temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
                       row_weights: torch.Tensor | None = None) -> torch.Tensor:
-    """topk_distill_forward's loss, differentiable in the logits (the teacher and the weights are constants)."""
+    """topk_distill_forward's loss, differentiable in the logits (the teacher and the weights are constants).
+
+    Inside a graph capture use topk_distill_step: a backward pass of torch's autograd may wait there for
+    streams of graphs that were built outside it."""
+    out = (_fast or _binding()).distill_loss(logits, teacher_values, teacher_indices, float(temperature), teacher_lse,
+                                             row_weights)
+    if out is not None:
+        return out
     return _DistillLoss.apply(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights)
 
 
@@ -333,6 +379,11 @@ def expert_balance_step_workspace_size(rows: int, k: int, experts: int,
 def _step(logits, indices, balance_weight, z_weight, score, row_mask, counts, want_kept, want_grad, grad_out, workspace,
           options):
     """Loss, counts, rows counted (if wanted) and gradient (if wanted), on these tokens' counts or the given ones."""
+    if counts is None and grad_out is None and workspace is None and options is None and score in _SCORES:
+        out = (_fast or _binding()).balance_step(logits, indices, float(balance_weight), float(z_weight), _SCORES[score],
+                                                 row_mask, want_kept, want_grad)
+        if out is not None:
+            return out
     lib = _lrs.load_library()
     dtype = _matrix(logits, "logits")
     rows, experts = logits.shape
@@ -415,5 +466,12 @@ class _BalanceLoss(torch.autograd.Function):
 def expert_balance_loss(logits: torch.Tensor, indices: torch.Tensor, balance_weight: float = 1.0,
                         z_weight: float = 0.0, score: str = "softmax", row_mask: torch.Tensor | None = None,
                         counts: torch.Tensor | None = None):
-    """expert_balance_forward's loss, differentiable in the logits, and the counts: (loss, counts)."""
+    """expert_balance_forward's loss, differentiable in the logits, and the counts: (loss, counts).
+
+    Inside a graph capture use expert_balance_step, as with topk_distill_loss."""
+    if counts is None and score in _SCORES:
+        out = (_fast or _binding()).balance_loss(logits, indices, float(balance_weight), float(z_weight), _SCORES[score],
+                                                 row_mask)
+        if out is not None:
+            return out
     return _BalanceLoss.apply(logits, indices, balance_weight, z_weight, score, row_mask, counts)
