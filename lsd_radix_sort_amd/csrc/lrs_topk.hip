@@ -684,14 +684,20 @@ __device__ void write_ranked(const TopArgs &a, uint64_t *buf, Bins &bins, uint32
         for (uint32_t j = want + tid; j < a.k; j += B) a.words[task * a.k + j] = 0;
 }
 
+// Whether the threads' largest elements give the bound: k of them at most half.
+constexpr int kBatch = 4;
+__host__ __device__ inline bool few_wanted(uint64_t want, uint64_t threads, uint64_t vecs) {
+    return 2 * want <= (threads < vecs ? threads : vecs);
+}
+
 // One workgroup of B threads a row (or a split of one), V loads of 16 bytes a
 // thread, all on their way at once.  A histogram below the largest image, of
 // the threads' largest images where k is at most half of them and of all
 // elements otherwise, gives a bound that at least k elements reach; they go to
 // LDS as words.  Where ties leave too many, the k-th image is found exactly and
 // the first of its columns fill up.
-template <int W, int B, int V>
-__global__ __launch_bounds__(B, 4) void topk_held_kernel(TopArgs a) {
+template <int W, int B, int V, bool HOLD>
+__global__ __launch_bounds__(B, HOLD ? 4 : 8) void topk_held_kernel(TopArgs a) {
     constexpr int kVec = 16 / W;
     using Stored = typename Row<W == 2 ? kRowF16 : kRowF32>::Stored;
     __shared__ uint64_t buf[kHeldWords];
@@ -707,23 +713,45 @@ __global__ __launch_bounds__(B, 4) void topk_held_kernel(TopArgs a) {
     const uint32_t vecs = len / kVec, rest = vecs * kVec + tid;
     const Stored *x = static_cast<const Stored *>(a.x) + row * a.stride + first;
 
-    u32x4 v[V];
+    u32x4 v[HOLD ? V : 1];
     const auto below = [&](int u) { return static_cast<int>(tid) < static_cast<int>(vecs) - u * B; };
+    const auto source = [&](int u) { return reinterpret_cast<const uint8_t *>(x + u * B * kVec) + tid * 16; };
+    if constexpr (HOLD) {
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-        v[u] = u32x4{0, 0, 0, 0};
-        if (below(u)) v[u] = load16_once(reinterpret_cast<const uint8_t *>(x + u * B * kVec) + tid * 16);
+        for (int u = 0; u < V; ++u) {
+            v[u] = u32x4{0, 0, 0, 0};
+            if (below(u)) v[u] = load16_once(source(u));
+        }
     }
     const bool extra = rest < len;
     const int over = extra ? image<W>(x[rest], a.flip) : INT32_MIN;
     clear_bins<B>(bins);
     if (tid == 0) count = 0;
 
-    int most[V], top = over;  // of each load, of all
+    // the largest of each load (not held: two 16-bit images to a word), of all
+    int most[HOLD || W == 4 ? V : V / 2], top = over;
+    if constexpr (HOLD) {
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-        most[u] = below(u) ? vec_max<W>(v[u], a.flip) : INT32_MIN;
-        top = max(top, most[u]);
+        for (int u = 0; u < V; ++u) {
+            most[u] = below(u) ? vec_max<W>(v[u], a.flip) : INT32_MIN;
+            top = max(top, most[u]);
+        }
+    } else {
+#pragma unroll
+        for (int b = 0; b < V; b += kBatch) {
+            u32x4 t[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (below(b + u)) t[u] = load16(source(b + u));
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int m = below(b + u) ? vec_max<W>(t[u], a.flip) : W == 2 ? -32768 : INT32_MIN;
+                top = max(top, below(b + u) ? m : top);
+                if (W == 4) most[b + u] = m;
+                else if (u % 2 == 0) most[(b + u) / 2] = m & 0xFFFF;
+                else most[(b + u) / 2] |= m << 16;
+            }
+        }
     }
     const int mine = top;
     const bool some = extra || below(0);
@@ -744,17 +772,17 @@ __global__ __launch_bounds__(B, 4) void topk_held_kernel(TopArgs a) {
     // each pass makes the images anew: kept, they would take twice the registers
     const auto anew = [&]() {
 #pragma unroll
-        for (int u = 0; u < V; ++u) asm volatile("" : "+v"(v[u]));
+        for (int u = 0; u < (HOLD ? V : 0); ++u) asm volatile("" : "+v"(v[u]));
     };
     anew();
-    const bool by_thread = 2 * want <= min(static_cast<uint32_t>(B), vecs);
+    const bool by_thread = !HOLD || few_wanted(want, B, vecs);
     uint32_t shift = W == 2 ? 0 : 13, bin;
     for (;; shift += W == 2 ? 5 : 8) {  // at the second shift every image has a bin
         if (by_thread) {
             if (some) add_to_bins(bins, mine, top, shift);
         } else {
 #pragma unroll
-            for (int u = 0; u < V; ++u)
+            for (int u = 0; u < (HOLD ? V : 0); ++u)
                 if (below(u)) each(v[u], 0, [&](int img, uint32_t) { add_to_bins(bins, img, top, shift); });
             if (extra) add_to_bins(bins, over, top, shift);
         }
@@ -776,9 +804,23 @@ __global__ __launch_bounds__(B, 4) void topk_held_kernel(TopArgs a) {
         }
     };
     if (mine >= bound && some) {
+        if constexpr (HOLD) {
 #pragma unroll
-        for (int u = 0; u < V; ++u)
-            if (most[u] >= bound && below(u)) each(v[u], place_of(u), take);
+            for (int u = 0; u < V; ++u)
+                if (most[u] >= bound && below(u)) each(v[u], place_of(u), take);
+        } else {
+            uint32_t hits = 0;  // loads that are read again: mostly one
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                const int m = W == 4 ? most[u] : u % 2 ? most[u / 2] >> 16 : static_cast<int16_t>(most[u / 2]);
+                hits |= static_cast<uint32_t>(m >= bound && below(u)) << u;
+            }
+            while (hits) {
+                const uint32_t at = (__builtin_ctz(hits) * B + tid) * kVec;
+                hits &= hits - 1;
+                each(load16(x + at), at, take);
+            }
+        }
         if (extra) take(over, rest);
     }
     __syncthreads();
@@ -935,17 +977,25 @@ template <int W> void launch_held(TopArgs a, uint32_t tasks, const Launch &L) {
     const uint64_t vecs = a.split_len / (16 / W);
     const auto go = [&](auto kernel, int block) { launch_on(kernel, dim3(tasks), dim3(block), L, a); };
     if (a.rows * a.splits <= 256) {
-        if (vecs <= 1024 * 2) return go(topk_held_kernel<W, 1024, 2>, 1024);
-        if (vecs <= 1024 * 4) return go(topk_held_kernel<W, 1024, 4>, 1024);
-        if (vecs <= 1024 * 8) return go(topk_held_kernel<W, 1024, 8>, 1024);
-        return go(topk_held_kernel<W, 1024, 16>, 1024);
+        if (vecs <= 1024 * 2) return go(topk_held_kernel<W, 1024, 2, true>, 1024);
+        if (vecs <= 1024 * 4) return go(topk_held_kernel<W, 1024, 4, true>, 1024);
+        if (vecs <= 1024 * 8) return go(topk_held_kernel<W, 1024, 8, true>, 1024);
+        return go(topk_held_kernel<W, 1024, 16, true>, 1024);
     }
-    if (vecs <= 256 * 2) return go(topk_held_kernel<W, 256, 2>, 256);
-    if (vecs <= 256 * 4) return go(topk_held_kernel<W, 256, 4>, 256);
-    if (vecs <= 256 * 8) return go(topk_held_kernel<W, 256, 8>, 256);
-    if (vecs <= 256 * 16) return go(topk_held_kernel<W, 256, 16>, 256);
-    if (vecs <= 512 * 16) return go(topk_held_kernel<W, 512, 16>, 512);
-    go(topk_held_kernel<W, 1024, 16>, 1024);
+    const uint64_t whole = std::min<uint64_t>(a.split_len, a.n - (a.splits - 1) * uint64_t(a.split_len)) / (16 / W);
+    if (vecs <= 256 * 2) return go(topk_held_kernel<W, 256, 2, true>, 256);
+    if (vecs <= 256 * 4) return go(topk_held_kernel<W, 256, 4, true>, 256);
+    if (vecs <= 256 * 8) return go(topk_held_kernel<W, 256, 8, true>, 256);
+    if (vecs <= 256 * 16) {
+        if (few_wanted(a.k, 256, whole)) return go(topk_held_kernel<W, 256, 16, false>, 256);
+        return go(topk_held_kernel<W, 256, 16, true>, 256);
+    }
+    if (vecs <= 512 * 16) {
+        if (few_wanted(a.k, 512, whole)) return go(topk_held_kernel<W, 512, 16, false>, 512);
+        return go(topk_held_kernel<W, 512, 16, true>, 512);
+    }
+    if (few_wanted(a.k, 1024, whole)) return go(topk_held_kernel<W, 1024, 16, false>, 1024);
+    go(topk_held_kernel<W, 1024, 16, true>, 1024);
 }
 
 int check_topk(int64_t rows, int64_t n, int64_t k, int64_t stride, int dtype) {
