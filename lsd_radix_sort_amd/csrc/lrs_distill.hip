@@ -389,8 +389,8 @@ struct HeldLds {
 // log 2 with c = log2(e) / T rounded to 32 bits, everywhere the same c, and
 // references to them are whole numbers R: the sums of 2^(x c - R) of two waves
 // join exactly, and log2 sum 2^(x c) = R + log2(sum).
-template <int T, int B, int V>
-__global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
+template <int T, int B, int V, bool GRAD>
+__global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a) {
     constexpr int kVec = Row<T>::kVec;
     constexpr int kWaves = B / kLanes;
     using Stored = typename Row<T>::Stored;
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
         if (stats)
             for (uint32_t j = tid; j < k + kStats; j += B) stats[j] = 0.f;
         if (tid == 0) a.row_loss[row] = 0.f;
-        if (a.grad) {
+        if (GRAD) {
             for (uint32_t v = tid; v < vecs; v += B) store16_once(g + static_cast<uint64_t>(v) * kVec, u32x4{0, 0, 0, 0});
             if (rest < n) g[rest] = 0;
         }
@@ -434,17 +434,18 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
     int64_t at = tid < k ? column_at(a, row, tid) : -1;
     float t = tid < k ? teacher_at(a, row, tid) : 0.f;
     const auto below = [&](uint32_t count, int u) { return static_cast<int>(tid) < static_cast<int>(count) - u * B; };
-    u32x4 v[V];
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
+    const auto load = [&](int u) {
         const uint8_t *p = reinterpret_cast<const uint8_t *>(x + u * B * kVec) + tid * 16;
-        if ((u + 1) * B <= vecs) {
-            v[u] = load16_once(p);
-        } else {
-            v[u] = u32x4{none, none, none, none};
-            if (below(vecs, u)) v[u] = load16_once(p);
-        }
-    }
+        u32x4 w{none, none, none, none};
+        if (below(vecs, u)) w = load16_once(p);
+        return w;
+    };
+    // with a gradient the whole row stays; else its first loads do, and others
+    // are read as they are used
+    constexpr int kKeep = GRAD || V <= 4 ? V : 4;
+    u32x4 v[kKeep];
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) v[u] = load(u);
     float over = rest < n ? Row<T>::value(x[rest]) : -INFINITY;
     float r = 0.f, factor = 1.f, m = 0.f;
     uint32_t sign = 0;
@@ -499,52 +500,71 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
             *columns = distinct;
         }
     }
-    if (tail) {  // S does not count in the sum
+    // S does not count in the sum of a tail
+    const auto without_s = [&](u32x4 &w, int u) {
+        if (below(vecs, u)) {
+            const uint32_t bits = (map[u * (B * kVec / 32) + tid * kVec / 32] >> (tid * kVec % 32)) & ((1u << kVec) - 1);
+            if (bits) {
 #pragma unroll
-        for (int u = 0; u < V; ++u) {
-            if (below(vecs, u)) {
-                const uint32_t bits = (map[u * (B * kVec / 32) + tid * kVec / 32] >> (tid * kVec % 32)) & ((1u << kVec) - 1);
-                if (bits) {
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e)
-                        if ((bits >> e) & 1) {
-                            if (T == kRowF32) v[u][e % 4] = none;
-                            else v[u][e / 2] = e & 1 ? (v[u][e / 2] & 0xFFFFu) | (none & 0xFFFF0000u)
-                                                     : (v[u][e / 2] & 0xFFFF0000u) | (none & 0xFFFFu);
-                        }
-                }
+                for (int e = 0; e < kVec; ++e)
+                    if ((bits >> e) & 1) {
+                        if (T == kRowF32) w[e % 4] = none;
+                        else w[e / 2] = e & 1 ? (w[e / 2] & 0xFFFFu) | (none & 0xFFFF0000u)
+                                              : (w[e / 2] & 0xFFFF0000u) | (none & 0xFFFFu);
+                    }
             }
         }
+    };
+    if (tail) {
+#pragma unroll
+        for (int u = 0; u < kKeep; ++u) without_s(v[u], u);
         if (rest < n && ((map[rest / 32] >> (rest % 32)) & 1)) over = -INFINITY;
     }
     // each pass unpacks the held words anew: their floats would take twice the registers
     const auto anew = [&]() {
 #pragma unroll
-        for (int u = 0; u < V; ++u) asm volatile("" : "+v"(v[u]));
+        for (int u = 0; u < kKeep; ++u) asm volatile("" : "+v"(v[u]));
     };
-    const auto larger = [&](float m, int u) {
+    const auto larger = [&](float m, u32x4 w) {
         float f[kVec];
-        unpack16<T>(v[u], f);
+        unpack16<T>(w, f);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) m = f[e] > m ? f[e] : m;
         return m;
     };
+    // f for every load of the row, four on their way at a time where it does not stay
+    const auto each = [&](auto f) {
+#pragma unroll
+        for (int u = 0; u < kKeep; ++u) f(v[u]);
+        if constexpr (kKeep < V) {
+#pragma unroll 1
+            for (int b = kKeep; b < V; b += kKeep) {
+                u32x4 t[kKeep];
+#pragma unroll
+                for (int u = 0; u < kKeep; ++u) t[u] = load(b + u);
+#pragma unroll
+                for (int u = 0; u < kKeep; ++u) {
+                    if (tail) without_s(t[u], b + u);
+                    f(t[u]);
+                }
+            }
+        }
+    };
     const auto sum_of = [&](auto term) {
         float part = term(over);
-#pragma unroll
-        for (int u = 0; u < V; ++u) {
+        each([&](u32x4 w) {
             float f[kVec];
-            unpack16<T>(v[u], f);
+            unpack16<T>(w, f);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) part += term(f[e]);
-        }
+        });
         return wave_sum(static_cast<double>(part));
     };
     const auto power = [&](float x) { return __builtin_amdgcn_exp2f(fmaf(x, c, -r)); };
     // A sum needs a reference near its largest term, not at it: first one from
     // the first load of each lane, and if the sum then leaves its range, the
     // largest of all.
-    m = wave_max(larger(over, 0));
+    m = wave_max(larger(over, v[0]));
     r = m == -INFINITY || huge_logit(m, c) ? 0.f : rintf(m * c);
     anew();
     double z_wave = sum_of(power);
@@ -552,8 +572,7 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
     reference = r;
     if (!(z_wave >= 0x1p-20 && z_wave <= 0x1p40)) {
         m = over;
-#pragma unroll
-        for (int u = 0; u < V; ++u) m = larger(m, u);
+        each([&](u32x4 w) { m = larger(m, w); });
         m = wave_max(m);
         huge = huge_logit(m, c);
         r = m == -INFINITY || huge ? 0.f : rintf(m * c);
@@ -655,7 +674,7 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
             if (stats) write_stats(stats, out[0], c, f);
         }
     }
-    if (!a.grad) return;
+    if constexpr (GRAD) {
     __syncthreads();
     const float scale = weight * a.inv_t, f = static_cast<float>(out[1]) * scale;
     r = reference == -INFINITY ? 0.f : static_cast<float>(out[0]);
@@ -698,6 +717,7 @@ __global__ __launch_bounds__(B, 4) void distill_held_kernel(DisArgs a) {
 #pragma unroll 1
     for (uint32_t j = tid; j < k; j += B)
         if (col[j] >= 0) g[col[j]] = Row<T>::pattern(sl[j] * scale);
+    }
 }
 
 // How many workgroups share a row: enough that few rows still fill the GPU,
@@ -812,21 +832,21 @@ template <int T> void distill_launch_held(const DisArgs &a, uint32_t rows, const
     TimedLaunch t(4, c);
     const uint32_t lds = HeldLds::bytes(a.k, a.n);
     const uint64_t vecs = a.n / Row<T>::kVec;
-    const auto go = [&](auto kernel, int block) {
-        launch_lds(kernel, dim3(rows), dim3(block), lds, t.L, a);
+    const auto go = [&](auto grad, auto loss, int block) {
+        launch_lds(a.grad ? grad : loss, dim3(rows), dim3(block), lds, t.L, a);
     };
     if (a.rows <= 256) {
-        if (vecs <= 1024 * 2) return go(distill_held_kernel<T, 1024, 2>, 1024);
-        if (vecs <= 1024 * 4) return go(distill_held_kernel<T, 1024, 4>, 1024);
-        if (vecs <= 1024 * 8) return go(distill_held_kernel<T, 1024, 8>, 1024);
-        return go(distill_held_kernel<T, 1024, 16>, 1024);
+        if (vecs <= 1024 * 2) return go(distill_held_kernel<T, 1024, 2, true>, distill_held_kernel<T, 1024, 2, false>, 1024);
+        if (vecs <= 1024 * 4) return go(distill_held_kernel<T, 1024, 4, true>, distill_held_kernel<T, 1024, 4, false>, 1024);
+        if (vecs <= 1024 * 8) return go(distill_held_kernel<T, 1024, 8, true>, distill_held_kernel<T, 1024, 8, false>, 1024);
+        return go(distill_held_kernel<T, 1024, 16, true>, distill_held_kernel<T, 1024, 16, false>, 1024);
     }
-    if (vecs <= 256 * 2) return go(distill_held_kernel<T, 256, 2>, 256);
-    if (vecs <= 256 * 4) return go(distill_held_kernel<T, 256, 4>, 256);
-    if (vecs <= 256 * 8) return go(distill_held_kernel<T, 256, 8>, 256);
-    if (vecs <= 256 * 16) return go(distill_held_kernel<T, 256, 16>, 256);
-    if (vecs <= 512 * 16) return go(distill_held_kernel<T, 512, 16>, 512);
-    go(distill_held_kernel<T, 1024, 16>, 1024);
+    if (vecs <= 256 * 2) return go(distill_held_kernel<T, 256, 2, true>, distill_held_kernel<T, 256, 2, false>, 256);
+    if (vecs <= 256 * 4) return go(distill_held_kernel<T, 256, 4, true>, distill_held_kernel<T, 256, 4, false>, 256);
+    if (vecs <= 256 * 8) return go(distill_held_kernel<T, 256, 8, true>, distill_held_kernel<T, 256, 8, false>, 256);
+    if (vecs <= 256 * 16) return go(distill_held_kernel<T, 256, 16, true>, distill_held_kernel<T, 256, 16, false>, 256);
+    if (vecs <= 512 * 16) return go(distill_held_kernel<T, 512, 16, true>, distill_held_kernel<T, 512, 16, false>, 512);
+    go(distill_held_kernel<T, 1024, 16, true>, distill_held_kernel<T, 1024, 16, false>, 1024);
 }
 
 // The loss and what a gradient needs; with a.grad and held rows the gradient too.

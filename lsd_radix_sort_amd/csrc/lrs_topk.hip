@@ -550,7 +550,7 @@ __global__ __launch_bounds__(kTopBlock) void topk_wave_kernel(TopArgs a) {
 // Bins of images below the largest, 2^shift images a bin; whoever lies lower
 // is not counted.
 constexpr uint32_t kBins = 2048, kCoarse = 64, kFine = kBins / kCoarse;
-constexpr uint32_t kHeldWords = 2048;  // candidates in LDS
+constexpr uint32_t kHeldWords = 2048;  // candidates in LDS; half of them where k is at most 512
 constexpr uint32_t kRankWords = 128;   // so many are ranked by counting all the others
 
 struct Bins {
@@ -700,7 +700,8 @@ template <int W, int B, int V, bool HOLD>
 __global__ __launch_bounds__(B, HOLD ? 4 : 8) void topk_held_kernel(TopArgs a) {
     constexpr int kVec = 16 / W;
     using Stored = typename Row<W == 2 ? kRowF16 : kRowF32>::Stored;
-    __shared__ uint64_t buf[kHeldWords];
+    constexpr uint32_t kWords = HOLD ? kHeldWords : kHeldWords / 2;
+    __shared__ uint64_t buf[kWords];
     __shared__ Bins bins;
     __shared__ int tops[B / kLanes];
     __shared__ uint32_t cells[B / kLanes];
@@ -800,7 +801,7 @@ __global__ __launch_bounds__(B, HOLD ? 4 : 8) void topk_held_kernel(TopArgs a) {
     const auto take = [&](int img, uint32_t at) {
         if (img >= bound) {
             const uint32_t slot = atomicAdd(&count, 1u);
-            if (slot < kHeldWords) buf[slot] = word_of(img, first + at);
+            if (slot < kWords) buf[slot] = word_of(img, first + at);
         }
     };
     if (mine >= bound && some) {
@@ -825,7 +826,7 @@ __global__ __launch_bounds__(B, HOLD ? 4 : 8) void topk_held_kernel(TopArgs a) {
     }
     __syncthreads();
     uint32_t c = count;
-    if (c > kHeldWords) {  // rare: the row is read again
+    if (c > kWords) {  // rare: the row is read again
         const auto again = [&](auto f) {
             for (uint32_t i = tid; i < vecs; i += B) each(load16(x + i * kVec), i * kVec, f);
             if (extra) f(over, rest);
@@ -880,7 +881,7 @@ __global__ __launch_bounds__(B, HOLD ? 4 : 8) void topk_held_kernel(TopArgs a) {
         }
         __syncthreads();
     }
-    write_ranked<W, B, kHeldWords>(a, buf, bins, cells, c, want, top, bound, task, row);
+    write_ranked<W, B, kWords>(a, buf, bins, cells, c, want, top, bound, task, row);
 }
 
 // The k largest of a row's splits * k words.
@@ -972,30 +973,25 @@ uint32_t topk_splits(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
 }
 
 // Threads by the rows there are: workgroups of 1024 where there are no more
-// than CUs, the fewest threads that hold a row where several share a CU.
-template <int W> void launch_held(TopArgs a, uint32_t tasks, const Launch &L) {
+// than CUs, the fewest threads that take a row at 16 loads each where several
+// share a CU.
+template <int W> void launch_held(const TopArgs &a, uint32_t tasks, const Launch &L) {
     const uint64_t vecs = a.split_len / (16 / W);
-    const auto go = [&](auto kernel, int block) { launch_on(kernel, dim3(tasks), dim3(block), L, a); };
+    const uint64_t least = std::min<uint64_t>(a.split_len, a.n - (a.splits - 1) * uint64_t(a.split_len)) / (16 / W);
+    const auto go = [&](auto held, auto again, int block) {
+        launch_on(few_wanted(a.k, block, least) ? again : held, dim3(tasks), dim3(block), L, a);
+    };
     if (a.rows * a.splits <= 256) {
-        if (vecs <= 1024 * 2) return go(topk_held_kernel<W, 1024, 2, true>, 1024);
-        if (vecs <= 1024 * 4) return go(topk_held_kernel<W, 1024, 4, true>, 1024);
-        if (vecs <= 1024 * 8) return go(topk_held_kernel<W, 1024, 8, true>, 1024);
-        return go(topk_held_kernel<W, 1024, 16, true>, 1024);
+        if (vecs <= 1024 * 4) return go(topk_held_kernel<W, 1024, 4, true>, topk_held_kernel<W, 1024, 4, false>, 1024);
+        if (vecs <= 1024 * 8) return go(topk_held_kernel<W, 1024, 8, true>, topk_held_kernel<W, 1024, 8, false>, 1024);
+        return go(topk_held_kernel<W, 1024, 16, true>, topk_held_kernel<W, 1024, 16, false>, 1024);
     }
-    const uint64_t whole = std::min<uint64_t>(a.split_len, a.n - (a.splits - 1) * uint64_t(a.split_len)) / (16 / W);
-    if (vecs <= 256 * 2) return go(topk_held_kernel<W, 256, 2, true>, 256);
-    if (vecs <= 256 * 4) return go(topk_held_kernel<W, 256, 4, true>, 256);
-    if (vecs <= 256 * 8) return go(topk_held_kernel<W, 256, 8, true>, 256);
-    if (vecs <= 256 * 16) {
-        if (few_wanted(a.k, 256, whole)) return go(topk_held_kernel<W, 256, 16, false>, 256);
-        return go(topk_held_kernel<W, 256, 16, true>, 256);
-    }
-    if (vecs <= 512 * 16) {
-        if (few_wanted(a.k, 512, whole)) return go(topk_held_kernel<W, 512, 16, false>, 512);
-        return go(topk_held_kernel<W, 512, 16, true>, 512);
-    }
-    if (few_wanted(a.k, 1024, whole)) return go(topk_held_kernel<W, 1024, 16, false>, 1024);
-    go(topk_held_kernel<W, 1024, 16, true>, 1024);
+    if (vecs <= 256 * 2) return go(topk_held_kernel<W, 256, 2, true>, topk_held_kernel<W, 256, 4, false>, 256);
+    if (vecs <= 256 * 4) return go(topk_held_kernel<W, 256, 4, true>, topk_held_kernel<W, 256, 4, false>, 256);
+    if (vecs <= 256 * 8) return go(topk_held_kernel<W, 256, 8, true>, topk_held_kernel<W, 256, 8, false>, 256);
+    if (vecs <= 256 * 16) return go(topk_held_kernel<W, 256, 16, true>, topk_held_kernel<W, 256, 16, false>, 256);
+    if (vecs <= 512 * 16) return go(topk_held_kernel<W, 512, 16, true>, topk_held_kernel<W, 512, 16, false>, 512);
+    go(topk_held_kernel<W, 1024, 16, true>, topk_held_kernel<W, 1024, 16, false>, 1024);
 }
 
 int check_topk(int64_t rows, int64_t n, int64_t k, int64_t stride, int dtype) {
