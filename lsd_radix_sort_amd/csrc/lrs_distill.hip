@@ -841,8 +841,9 @@ template <int T> void distill_launch_held(const DisArgs &a, uint32_t rows, const
         if (vecs <= 1024 * 8) return go(distill_held_kernel<T, 1024, 8, true>, distill_held_kernel<T, 1024, 8, false>, 1024);
         return go(distill_held_kernel<T, 1024, 16, true>, distill_held_kernel<T, 1024, 16, false>, 1024);
     }
-    if (vecs <= 256 * 2) return go(distill_held_kernel<T, 256, 2, true>, distill_held_kernel<T, 256, 2, false>, 256);
-    if (vecs <= 256 * 4) return go(distill_held_kernel<T, 256, 4, true>, distill_held_kernel<T, 256, 4, false>, 256);
+    if (vecs <= 64 * 4) return go(distill_held_kernel<T, 64, 4, true>, distill_held_kernel<T, 64, 4, false>, 64);
+    if (vecs <= 64 * 8) return go(distill_held_kernel<T, 64, 8, true>, distill_held_kernel<T, 64, 8, false>, 64);
+    if (vecs <= 128 * 8) return go(distill_held_kernel<T, 128, 8, true>, distill_held_kernel<T, 128, 8, false>, 128);
     if (vecs <= 256 * 8) return go(distill_held_kernel<T, 256, 8, true>, distill_held_kernel<T, 256, 8, false>, 256);
     if (vecs <= 256 * 16) return go(distill_held_kernel<T, 256, 16, true>, distill_held_kernel<T, 256, 16, false>, 256);
     if (vecs <= 512 * 16) return go(distill_held_kernel<T, 512, 16, true>, distill_held_kernel<T, 512, 16, false>, 512);

@@ -413,3 +413,15 @@ def test_odd_teachers(dtype, n, k):
     w = torch.tensor([0.5, -0.25, 1.0, 0.0, 2.0, -1.0, 1e-3, 0.125])
     check(s, t, i, 1.0, tlse, w)
     check(s, t, i, 1.0, None, w)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("rows,n,k", [
+    (300, 5, 2), (300, 1023, 8), (270, 1025, 70), (300, 2048, 64), (257, 2051, 3), (300, 4096, 100), (258, 4099, 9),
+    (300, 8192, 20), (260, 8200, 300), (265, 16_385, 33), (300, 33_000, 5)])
+def test_many_rows(dtype, rows, n, k):
+    """More rows than CUs: the edges between the numbers of threads that take a row."""
+    log(f"many rows {dtype} {rows}x{n} k={k}")
+    for tail in (False, True):
+        s, t, i, tlse = make(rows, n, k, dtype, 900 + n, tail)
+        check(s, t, i, 1.0, tlse, None, 1)
