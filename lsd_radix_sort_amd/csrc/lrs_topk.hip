@@ -537,11 +537,19 @@ __global__ __launch_bounds__(kTopBlock) void topk_wave_kernel(TopArgs a) {
         __builtin_amdgcn_wave_barrier();
         const typename Word::T w = lane < static_cast<int>(count) ? held[wave][lane] : 0;
         __builtin_amdgcn_wave_barrier();
+        // 32 bits order the words unless images are equal, which the sum of the
+        // places would show; the words of lanes past the last are 0
+        const uint32_t high = W == 2 ? static_cast<uint32_t>(w) : static_cast<uint32_t>(static_cast<uint64_t>(w) >> 32);
+        const bool on = lane < static_cast<int>(count);
         uint32_t place = 0;
-        for (uint32_t j = 0; j < count; j += 4)  // the words of lanes past the last are 0
+        for (uint32_t j = 0; j < count; j += 4)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) place += Word::lane(w, j + i) > w;
-        if (lane < static_cast<int>(count) && place < k) write_short<W>(a, w, row * k + place);
+            for (int i = 0; i < 4; ++i) place += static_cast<uint32_t>(__builtin_amdgcn_readlane(high, j + i)) > high;
+        if (W == 4 && wave_sum(on ? place : 0) != count * (count - 1) / 2) {
+            place = 0;
+            for (uint32_t j = 0; j < count; ++j) place += Word::lane(w, j) > w;
+        }
+        if (on && place < k) write_short<W>(a, w, row * k + place);
     }
 }
 
