@@ -79,6 +79,13 @@ __device__ inline void join(float &m, float &z, float m2, float z2, float c) {
     m = hi;
 }
 
+// ---- rows over 256 KB ------------------------------------------------------
+//
+// A row's sum, its stats and its gradient are three launches: the row is read
+// twice (1024 x 131072 fp32 step: 353 us, forward with a tail 124 us = 4.3 TB/s).
+// The gradient is also the backward of every length: 515 x 32768 fp32 in 22 us
+// = 6.0 TB/s, the rate of a copy.
+
 // One workgroup: the largest logit and the sum of exponentials of a piece of a row.
 template <int T, bool TAIL>
 __global__ __launch_bounds__(kDisBlock) void distill_sum_kernel(DisArgs a) {
@@ -383,12 +390,22 @@ struct HeldLds {
     __host__ __device__ static uint32_t bytes(uint32_t k, uint32_t n) { return map(k) + (n + 31) / 32 * 4; }
 };
 
-// One workgroup of B threads a row, V loads of 16 bytes a thread held in
-// registers from the one read to the gradient, both past the caches' usual
-// order (nontemporal): nothing of them is read again.  Exponents are in units of
-// log 2 with c = log2(e) / T rounded to 32 bits, everywhere the same c, and
-// references to them are whole numbers R: the sums of 2^(x c - R) of two waves
-// join exactly, and log2 sum 2^(x c) = R + log2(sum).
+// One workgroup of B threads a row, V loads of 16 bytes a thread.  With a
+// gradient the row stays in registers from its one read to its one write, both
+// past the caches' usual order (nontemporal): nothing of it is read again.
+// Without, four loads are on their way at a time and twice the rows are on a CU.
+// Exponents are in units of log 2 with c = log2(e) / T rounded to 32 bits,
+// everywhere the same c, and references to them are whole numbers R: the sums of
+// 2^(x c - R) of two waves join exactly, and log2 sum 2^(x c) = R + log2(sum).
+//
+// Bound by HBM where rows are long and many: 4096 x 131072 bf16 step 418 us = 5.1
+// TB/s, where a copy of the rows in the same form takes 367 us; the rest is the
+// chain from the last load to the first store (joins, the teacher's terms in 64
+// bits by one wave, the factor), which a second row on the CU would hide and two
+// rows of 256 KB do not fit.  1031 x 50021 fp16 step with a tail 49 us, forward
+// 1024 x 65536 fp16 with a tail 27 us = 4.9 TB/s (32 us when it stayed in
+// registers).  Keeping only the first loads with a gradient, too, and reading
+// the rest again costs 0 to 18%.
 template <int T, int B, int V, bool GRAD>
 __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a) {
     constexpr int kVec = Row<T>::kVec;
@@ -841,6 +858,8 @@ template <int T> void distill_launch_held(const DisArgs &a, uint32_t rows, const
         if (vecs <= 1024 * 8) return go(distill_held_kernel<T, 1024, 8, true>, distill_held_kernel<T, 1024, 8, false>, 1024);
         return go(distill_held_kernel<T, 1024, 16, true>, distill_held_kernel<T, 1024, 16, false>, 1024);
     }
+    // a wave for up to 8 KB, so that many short rows' chains run side by side
+    // (8192 x 600 bf16 step: 21 us, 36 us by workgroups of 256)
     if (vecs <= 64 * 4) return go(distill_held_kernel<T, 64, 4, true>, distill_held_kernel<T, 64, 4, false>, 64);
     if (vecs <= 64 * 8) return go(distill_held_kernel<T, 64, 8, true>, distill_held_kernel<T, 64, 8, false>, 64);
     if (vecs <= 128 * 8) return go(distill_held_kernel<T, 128, 8, true>, distill_held_kernel<T, 128, 8, false>, 128);

@@ -3,10 +3,12 @@
 // Each element becomes one 64-bit word, order image above, complemented column
 // below, so the wanted elements are the k largest words, no two words are
 // alike, and ties go to the lowest column whatever order the words arrive in.
-// One workgroup reads its row once, 16 bytes a lane.  The k-th largest of the
-// first chunk's per-load maxima bounds the row's k-th largest from below; only
-// elements at or above the bound enter a buffer in LDS, and when the buffer is
-// nearly full its k largest stay and the least of them becomes the bound.
+// Every form looks for a bound that at least k elements reach and few more,
+// and ranks only those.  A row must be read once; what else a form costs is its
+// chain of dependent steps, so each keeps as many rows on a CU as it can.  By
+// length: a lane network (n <= 64), lanes' sorted heads (n <= 128, k <= 16), a
+// wave (n <= 1024, k <= 64), a workgroup (up to 256 KB), several workgroups and
+// a merge, and streaming where the merge would not fit.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -97,6 +99,12 @@ template <int W> __device__ void write_row(const TopArgs &a, const uint64_t *buf
     }
 }
 
+// Streaming, for rows (or shares of one) over 256 KB.  The k-th largest of the
+// first chunk's per-load maxima bounds the row's k-th largest from below; only
+// elements at or above the bound enter a buffer in LDS, and when the buffer is
+// nearly full its k largest stay and the least of them becomes the bound.  The
+// sorts bound it: 1024 x 65536 fp16, k = 64 took 78 us so, 30 us in the form
+// for shorter rows below.
 template <int W>
 __global__ __launch_bounds__(kTopBlock) void topk_kernel(TopArgs a) {
     constexpr int kVec = 16 / W;
@@ -232,7 +240,9 @@ __global__ __launch_bounds__(kTopBlock) void topk_kernel(TopArgs a) {
 //
 // Rows of at most 64 elements: an element a lane, 64 / P rows a wave (P the
 // power of two at or above n), sorted by a bitonic network across the P lanes.
-// A 16-bit image and the column fit one 32-bit word.
+// A 16-bit image and the column fit one 32-bit word.  65536 x 8 takes as long as
+// an empty launch (7 us); 65536 x 64 fp32 takes 21 us, 21 steps of 64-bit words,
+// so small k goes to the form after next.
 template <int W> struct ShortWord;
 template <> struct ShortWord<2> {
     using T = uint32_t;
@@ -361,7 +371,8 @@ template <int W, int E> __device__ inline void load_images(const typename Row<W 
 // Rows of at most 16 * E elements and small k: 16 lanes a row, E consecutive
 // elements a lane, sorted within the lane.  k times the 16 lanes' heads give
 // the next largest, the lowest lane's where they are equal, and that lane
-// moves on.
+// moves on.  Bound by issue: the network within a lane once for four rows, some
+// 25 instructions a head; 65536 x 64 fp32, k = 6 in 10 us (floor 4 us).
 template <int W, int E>
 __global__ __launch_bounds__(kTopBlock) void topk_heads_kernel(TopArgs a) {
     using Stored = typename Row<W == 2 ? kRowF16 : kRowF32>::Stored;
@@ -429,7 +440,8 @@ __global__ __launch_bounds__(kTopBlock) void topk_heads_kernel(TopArgs a) {
 // 64, a bisection over the images of all finds the bound.  Bound by issue, not
 // memory: scalar steps count as much as vector ones, so the bound is looked
 // for among the lanes (9 scalar instructions a try) and places are summed by
-// lanes.
+// lanes.  32768 x 256 fp32, k = 8: 13.8 us, 172 vector and 140 scalar
+// instructions a row (a bisection in their place: 315 scalar, 21.5 us).
 template <int W, int V>
 __global__ __launch_bounds__(kTopBlock) void topk_wave_kernel(TopArgs a) {
     constexpr int kVec = 16 / W;
@@ -553,7 +565,7 @@ __global__ __launch_bounds__(kTopBlock) void topk_wave_kernel(TopArgs a) {
     }
 }
 
-// ---- a row, or a piece of one, in one workgroup's registers ------------------
+// ---- a row, or a piece of one, by one workgroup -------------------------------
 
 // Bins of images below the largest, 2^shift images a bin; whoever lies lower
 // is not counted.
@@ -699,11 +711,16 @@ __host__ __device__ inline bool few_wanted(uint64_t want, uint64_t threads, uint
 }
 
 // One workgroup of B threads a row (or a split of one), V loads of 16 bytes a
-// thread, all on their way at once.  A histogram below the largest image, of
-// the threads' largest images where k is at most half of them and of all
-// elements otherwise, gives a bound that at least k elements reach; they go to
-// LDS as words.  Where ties leave too many, the k-th image is found exactly and
-// the first of its columns fill up.
+// thread.  A histogram below the largest image, of the threads' largest images
+// where k is at most half of them and of all elements otherwise (HOLD), gives a
+// bound that at least k elements reach; they go to LDS as words.  Where ties
+// leave too many, the k-th image is found exactly and the first of its columns
+// fill up.  With HOLD the row stays in registers.  Without, only the largest
+// image of each load does, and the few loads that reach the bound are read
+// again: half the registers, so twice the rows on a CU, whose chains of barriers
+// hide behind each other's loads (333 x 50021 fp32, k = 129: 16.4 us, 24.6 us
+// held; 1024 x 65536 fp16, k = 64: 30.5 us = 4.4 TB/s, 33.4 us held; 512 x 131072
+// fp32: 5.4 TB/s; 1 x 131072 bf16: 9 us, held 10.4 us).
 template <int W, int B, int V, bool HOLD>
 __global__ __launch_bounds__(B, HOLD ? 4 : 8) void topk_held_kernel(TopArgs a) {
     constexpr int kVec = 16 / W;
@@ -892,7 +909,8 @@ __global__ __launch_bounds__(B, HOLD ? 4 : 8) void topk_held_kernel(TopArgs a) {
     write_ranked<W, B, kWords>(a, buf, bins, cells, c, want, top, bound, task, row);
 }
 
-// The k largest of a row's splits * k words.
+// The k largest of a row's splits * k words, by the same bound: 1 x 131072 fp32
+// in 16 splits takes 9 us with it, 37 us of sorting the words before.
 constexpr int kMergeBlock = 1024;
 template <int W>
 __global__ __launch_bounds__(kMergeBlock) void topk_merge_kernel(TopArgs a) {
@@ -965,12 +983,11 @@ template <int W> void launch_short(const TopArgs &a, const Launch &L) {
     if constexpr (W == 4) launch_on(topk_wave_kernel<W, 4>, waves, block, L, a);
 }
 
-// Rows, or splits of rows, of at most 256 KB are held in registers.
+// Rows, or splits of rows, of at most 256 KB go to one workgroup.
 constexpr uint64_t kHeldBytes = 1024 * 16 * 16;
 
-// How many workgroups share a row: one where it can be held (1 x 131072 bf16 in
-// pieces of 32 KB: 9.8 us on the GPU, 10.9 us whole, but a second launch costs
-// the host 3 us); else as many as leave each 256 KB, or, of few rows, 32 KB
+// How many workgroups share a row: one where one can take it (1 x 131072 bf16:
+// 9 us; in pieces of 32 KB 9.8 us and a second launch); else as many as leave each 256 KB, or, of few rows, 32 KB
 // (1 x 131072 fp32: 9.3 us, 12.9 us in two pieces).  Their words have to fit the
 // merge; rows too long for that are streamed.
 uint32_t topk_splits(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
