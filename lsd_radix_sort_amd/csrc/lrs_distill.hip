@@ -122,12 +122,37 @@ __global__ __launch_bounds__(kDisBlock) void distill_sum_kernel(DisArgs a) {
                     }
                     if (f != -INFINITY) z += exp2f((f - m) * c);
                 };
-                for (uint32_t v = threadIdx.x; v < vecs; v += kDisBlock) {
-                    float f[kVec];
-                    unpack16<T>(load16(x + lo + static_cast<uint64_t>(v) * kVec), f);
-                    const uint32_t bits = TAIL ? map[v * kVec / 32] >> (v * kVec % 32) : 0;
-                    for (int e = 0; e < kVec; ++e)
-                        if (!TAIL || !((bits >> e) & 1)) take(f[e]);
+                // four loads at a time, one largest logit for all of them
+                constexpr int kBatch = 4;
+                for (uint32_t v = threadIdx.x; v < vecs; v += kBatch * kDisBlock) {
+                    u32x4 w[kBatch];
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) {
+                        const uint32_t at = min(v + u * kDisBlock, vecs - 1);
+                        w[u] = load16(x + lo + static_cast<uint64_t>(at) * kVec);
+                    }
+                    float f[kBatch][kVec], top = m;
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) {
+                        const uint32_t at = v + u * kDisBlock;
+                        unpack16<T>(w[u], f[u]);
+                        uint32_t out = at < vecs ? 0 : ~0u;  // elements that do not count
+                        if (TAIL && at < vecs) out = map[at * kVec / 32] >> (at * kVec % 32);
+#pragma unroll
+                        for (int e = 0; e < kVec; ++e) {
+                            if ((out >> e) & 1) f[u][e] = -INFINITY;
+                            top = f[u][e] > top ? f[u][e] : top;
+                        }
+                    }
+                    if (top > m) {
+                        z = m == -INFINITY ? z : z * __builtin_amdgcn_exp2f((m - top) * c);
+                        m = top;
+                    }
+                    const float from = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+                        for (int e = 0; e < kVec; ++e) z += __builtin_amdgcn_exp2f((f[u][e] - from) * c);
                 }
                 const uint32_t t = vecs * kVec + threadIdx.x;
                 if (t < hi - lo && (!TAIL || !((map[t / 32] >> (t % 32)) & 1))) take(Row<T>::value(x[lo + t]));
