@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <limits>
 
 #include "../../include/lsd_radix_sort.h"
 #include "lrs_host.h"
@@ -25,7 +26,6 @@ namespace lrs {
 namespace {
 
 constexpr int kDisBlock = 256;
-constexpr float kLog2e = 1.44269504088896340736f;
 // Columns whose membership in S one workgroup holds as a bitmap at a time.
 constexpr uint32_t kMapColumns = 65536;
 
@@ -43,7 +43,8 @@ struct DisArgs {
     int ti_bytes;
     const float *tlse;    // the teacher's log-sum-exp by row, or null: no tail
     const float *weights; // by row, or null: 1 / rows
-    float inv_t;
+    double inv_t;
+    float c, c_low;       // log2(e) / T, and what its rounding leaves
     uint32_t splits, split_len;
     float2 *partial;      // [rows][splits]: largest logit and sum of exponentials of the tail (of all, without one)
     float *stats;         // [rows][k + kStats]
@@ -92,7 +93,7 @@ __global__ __launch_bounds__(kDisBlock) void distill_sum_kernel(DisArgs a) {
     constexpr int kVec = Row<T>::kVec;
     __shared__ uint32_t map[TAIL ? kMapColumns / 32 : 1];
     __shared__ float wm[kDisBlock / kLanes], wz[kDisBlock / kLanes];
-    const float c = kLog2e * a.inv_t;
+    const float c = a.c;
     using Stored = typename Row<T>::Stored;
     for (uint64_t task = blockIdx.x; task < a.rows * a.splits; task += gridDim.x) {
         const uint64_t row = task / a.splits;
@@ -172,6 +173,25 @@ __global__ __launch_bounds__(kDisBlock) void distill_sum_kernel(DisArgs a) {
     }
 }
 
+// x log2(e) / T less a reference, as an exponent of 2.  In 32-bit rows the
+// rounding of the factor would show, by as much as |x| times its half step.
+template <int T> __device__ inline float exponent(float x, float c, float c_low, float r) {
+    const float e = fmaf(x, c, -r);
+    return T == kRowF32 ? fmaf(x, c_low, e) : e;
+}
+// The factor that exponent() stands for.
+template <int T> __device__ inline double factor_of(const DisArgs &a) {
+    return T == kRowF32 ? static_cast<double>(a.c) + a.c_low : a.c;
+}
+
+// A product rounded by itself, not within a fused difference: where logits are
+// huge, equal ones have to cancel.
+__device__ inline double times(double a, double b) {
+    double p = a * b;
+    asm("" : "+v"(p));
+    return p;
+}
+
 // Whether x c of a row with this largest logit may pass what 32 bits hold.
 __device__ inline bool huge_logit(float m, float c) { return fabsf(m) < INFINITY && !(fabsf(m * c) < 0x1p100f); }
 
@@ -179,7 +199,7 @@ __device__ inline bool huge_logit(float m, float c) { return fabsf(m) < INFINITY
 // the first three stats (r whole and b 0, or b the largest logit and r 0 where
 // that is huge), at slot j's column stats[3 + j], all before weight / T.
 constexpr uint32_t kStats = 3;
-__device__ inline void write_stats(float *stats, double reference, float c, double f) {
+__device__ inline void write_stats(float *stats, double reference, double c, double f) {
     const bool huge = fabs(reference) < INFINITY && !(fabs(reference) < 0x1p100);
     stats[0] = huge ? static_cast<float>(reference / c) : 0.f;
     stats[1] = huge ? 0.f : static_cast<float>(reference);
@@ -290,8 +310,8 @@ __global__ __launch_bounds__(kLanes) void distill_row_kernel(DisArgs a) {
             if (q0 > 0) loss += m == -INFINITY ? INFINITY : q0 * (log(q0) - (lse0 - lse));
             if (a.row_loss) a.row_loss[row] = static_cast<float>(loss);
             // 2^((x - b) c - r) in place of exp((x - m) / T)
-            const float c = kLog2e * a.inv_t;
-            const double exact = static_cast<double>(m) * c;
+            const float c = a.c;
+            const double exact = times(m, factor_of<T>(a));
             const double r = m == -INFINITY ? 0 : huge_logit(m, c) ? exact : rintf(m * c);
             double f = 0;
             if (m != -INFINITY) {
@@ -299,7 +319,7 @@ __global__ __launch_bounds__(kLanes) void distill_row_kernel(DisArgs a) {
                 if (q0 > 0) f -= q0 / z;
                 f *= exp2(r - exact);
             }
-            write_stats(stats, r, c, f);
+            write_stats(stats, r, factor_of<T>(a), f);
         }
     }
 }
@@ -327,7 +347,7 @@ template <int T>
 __global__ __launch_bounds__(kDisBlock) void distill_grad_kernel(DisArgs a) {
     constexpr int kVec = Row<T>::kVec;
     using Stored = typename Row<T>::Stored;
-    const float c = kLog2e * a.inv_t;
+    const float c = a.c;
     const float up = a.loss_grad ? *a.loss_grad : 1.f;
     for (uint64_t task = blockIdx.x; task < a.rows * a.splits; task += gridDim.x) {
         const uint64_t row = task / a.splits;
@@ -344,15 +364,15 @@ __global__ __launch_bounds__(kDisBlock) void distill_grad_kernel(DisArgs a) {
             if (t < len) g[t] = 0;
             continue;
         }
-        const float b = stats[0], r = stats[1], scale = up * w * a.inv_t, f = stats[2] * scale;
+        const float b = stats[0], r = stats[1], scale = up * w * static_cast<float>(a.inv_t), f = stats[2] * scale;
         for (uint32_t v = threadIdx.x; v < vecs; v += kDisBlock) {
             float e[kVec];
             unpack16<T>(load16(x + static_cast<uint64_t>(v) * kVec), e);
-            for (int i = 0; i < kVec; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(e[i] - b, c, -r)) * f;
+            for (int i = 0; i < kVec; ++i) e[i] = __builtin_amdgcn_exp2f(exponent<T>(e[i] - b, c, a.c_low, r)) * f;
             store16(g + static_cast<uint64_t>(v) * kVec, pack16<T>(e));
         }
         const uint32_t t = vecs * kVec + threadIdx.x;
-        if (t < len) g[t] = Row<T>::pattern(__builtin_amdgcn_exp2f(fmaf(Row<T>::value(x[t]) - b, c, -r)) * f);
+        if (t < len) g[t] = Row<T>::pattern(__builtin_amdgcn_exp2f(exponent<T>(Row<T>::value(x[t]) - b, c, a.c_low, r)) * f);
         // the teacher's columns over what was written there
         __syncthreads();
         for (uint32_t j = threadIdx.x; j < a.k; j += kDisBlock) {
@@ -419,8 +439,8 @@ struct HeldLds {
 // gradient the row stays in registers from its one read to its one write, both
 // past the caches' usual order (nontemporal): nothing of it is read again.
 // Without, four loads are on their way at a time and twice the rows are on a CU.
-// Exponents are in units of log 2 with c = log2(e) / T rounded to 32 bits,
-// everywhere the same c, and references to them are whole numbers R: the sums of
+// Exponents are in units of log 2 with c = log2(e) / T, in 16-bit rows rounded
+// to 32 bits, everywhere the same c, and references to them are whole numbers R: the sums of
 // 2^(x c - R) of two waves join exactly, and log2 sum 2^(x c) = R + log2(sum).
 //
 // Bound by HBM where rows are long and many: 4096 x 131072 bf16 step 418 us = 5.1
@@ -452,7 +472,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
     const uint32_t tid = threadIdx.x, vecs = a.n / kVec;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kLanes);
     const uint32_t n = a.n, k = a.k, rest = vecs * kVec + tid;
-    const float c = kLog2e * a.inv_t;
+    const float c = a.c;
     const bool tail = a.tlse != nullptr;
     const uint32_t none = T == kRowF16 ? 0xFC00FC00u : T == kRowBF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
 
@@ -602,7 +622,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
         });
         return wave_sum(static_cast<double>(part));
     };
-    const auto power = [&](float x) { return __builtin_amdgcn_exp2f(fmaf(x, c, -r)); };
+    const auto power = [&](float x) { return __builtin_amdgcn_exp2f(exponent<T>(x, c, a.c_low, r)); };
     // A sum needs a reference near its largest term, not at it: first one from
     // the first load of each lane, and if the sum then leaves its range, the
     // largest of all.
@@ -618,7 +638,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
         m = wave_max(m);
         huge = huge_logit(m, c);
         r = m == -INFINITY || huge ? 0.f : rintf(m * c);
-        reference = m == -INFINITY ? -INFINITY : huge ? static_cast<double>(m) * c : r;
+        reference = m == -INFINITY ? -INFINITY : huge ? times(m, factor_of<T>(a)) : r;
     }
     anew();
     // logits as large as the type's lowest value: all but the largest have no
@@ -635,6 +655,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
         sl[j] = col[j] < 0 ? -INFINITY : Row<T>::value(j == tid ? raw : x[col[j]]);
     __syncthreads();
     if (wave == 0) {
+        const double cd = factor_of<T>(a);
         // the row's sum (off S where there is a tail)
         double R = lane < kWaves ? wr[lane] : -INFINITY;
         double z = lane < kWaves ? wz[lane] : 0;
@@ -659,7 +680,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
 #pragma unroll 1
             for (uint32_t j = lane; j < k; j += kLanes) sm = fmaxf(sm, sl[j]);
             sm = wave_max(sm);
-            if (sm != -INFINITY) whole_r = fmax(empty ? -INFINITY : R, rint(static_cast<double>(sm) * c));
+            if (sm != -INFINITY) whole_r = fmax(empty ? -INFINITY : R, rint(times(sm, cd)));
             double on = 0;
 #pragma unroll 1
             for (uint32_t j = lane; j < k; j += kLanes) {
@@ -667,7 +688,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
                 if (first && *again)
 #pragma unroll 1
                     for (uint32_t i = 0; i < j; ++i) first &= col[i] != col[j];
-                if (first) on += power_of_two(static_cast<double>(sl[j]) * c - whole_r);
+                if (first) on += power_of_two(times(sl[j], cd) - whole_r);
             }
             on = wave_sum(on);
             whole = on + (empty ? z : ldexp(z, static_cast<int>(fmax(R - whole_r, -4000.0))));
@@ -684,7 +705,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
         for (uint32_t j = lane; j < k; j += kLanes) {
             double grad = 0;
             if (col[j] >= 0) {
-                const double qj = q[j] * scale, arg = static_cast<double>(sl[j]) * c - whole_r - lse;
+                const double qj = q[j] * scale, arg = times(sl[j], cd) - whole_r - lse;
                 const bool zero = sl[j] == -INFINITY;
                 if (qj > 0)
                     loss += zero ? INFINITY
@@ -713,12 +734,12 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
             }
             out[0] = empty ? 0.0 : R;
             out[1] = f;
-            if (stats) write_stats(stats, out[0], c, f);
+            if (stats) write_stats(stats, out[0], cd, f);
         }
     }
     if constexpr (GRAD) {
     __syncthreads();
-    const float scale = weight * a.inv_t, f = static_cast<float>(out[1]) * scale;
+    const float scale = weight * static_cast<float>(a.inv_t), f = static_cast<float>(out[1]) * scale;
     r = reference == -INFINITY ? 0.f : static_cast<float>(out[0]);
     if (huge) r = reference == out[0] ? 0.f : INFINITY;
     // 16-bit gradients: the factor joins the exponent, where that keeps it to
@@ -740,7 +761,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
                 for (int i = 0; i < kVec; ++i) e[i] = only(e[i]);
             }
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(e[i], c, -r));
+            for (int i = 0; i < kVec; ++i) e[i] = __builtin_amdgcn_exp2f(exponent<T>(e[i], c, a.c_low, r));
             if (factor != 1.f) {
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) e[i] *= factor;
@@ -751,7 +772,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
         }
     }
     if (rest < n) {
-        const float e = __builtin_amdgcn_exp2f(fmaf(huge ? only(over) : over, c, -r));
+        const float e = __builtin_amdgcn_exp2f(exponent<T>(huge ? only(over) : over, c, a.c_low, r));
         g[rest] = Row<T>::pattern(e * factor) ^ static_cast<Stored>(sign);
     }
     // the teacher's columns over what was written there
@@ -808,7 +829,7 @@ int distill_inputs(const lrs_distill *d, DisArgs &a) {
     if (!row_type_ok(d->teacher_dtype) || (d->index_bytes != 4 && d->index_bytes != 8)) return LRS_ERR_DTYPE;
     if (!stride_ok(d->row_stride, d->rows) || !stride_ok(d->teacher_stride, d->rows) || !stride_ok(d->index_stride, d->rows))
         return LRS_ERR_SIZE;
-    if (!(d->temperature > 0.f) || !std::isfinite(d->temperature) || !std::isfinite(1.f / d->temperature))
+    if (!(d->temperature > 0) || !std::isfinite(d->temperature) || !std::isfinite(static_cast<float>(1.0 / d->temperature)))
         return LRS_ERR_OPTION;
     if (d->rows > 0 && ((d->n > 0 && !d->logits) || !d->teacher_values || !d->teacher_indices))
         return LRS_ERR_NULL_POINTER;
@@ -828,7 +849,12 @@ int distill_inputs(const lrs_distill *d, DisArgs &a) {
     a.ti_bytes = d->index_bytes;
     a.tlse = d->teacher_lse;
     a.weights = d->row_weights;
-    a.inv_t = 1.f / d->temperature;
+    a.inv_t = 1.0 / d->temperature;
+    const double factor = 1.44269504088896340736 * a.inv_t;
+    // rounded down, so that the rest is above 0 and -inf times it is -inf
+    a.c = static_cast<float>(factor);
+    if (a.c > factor) a.c = std::nextafter(a.c, 0.f);
+    a.c_low = std::max(static_cast<float>(factor - a.c), std::numeric_limits<float>::min());
     distill_split(a.rows, a.n, a.splits, a.split_len);
     return LRS_OK;
 }

@@ -132,7 +132,7 @@ struct Distill {
         return take(s, logits) && take(v, values) && take(i, indices) && take(l, lse, true) && take(w, weights, true);
     }
     // False if an argument is not as it should be.
-    bool fill(float temperature) {
+    bool fill(double temperature) {
         int code, teacher, bytes;
         if (!matrix(logits, code) || !matrix(values, teacher) || values.device() != logits.device() ||
             !ids(indices, logits, bytes) || values.size(0) != logits.size(0) || values.size(1) != indices.size(1) ||
@@ -159,7 +159,7 @@ struct Distill {
 py::object distill_step(py::handle logits, py::handle values, py::handle indices, double temperature, py::handle lse,
                         py::handle weights) {
     Distill c;
-    if (!c.take_all(logits, values, indices, lse, weights) || !c.fill(static_cast<float>(temperature))) return py::none();
+    if (!c.take_all(logits, values, indices, lse, weights) || !c.fill(temperature)) return py::none();
     const Tensor ws = c.workspace(), loss = make(c.values, {}, at::kFloat), row_loss = make(c.values, {c.d.rows}, at::kFloat);
     const Tensor grad = like_rows(c.logits);
     if (lib.distill_step(&c.d, pointer<float>(loss), pointer<float>(row_loss), pointer(grad), grad.stride(0), pointer(ws),
@@ -171,7 +171,7 @@ py::object distill_step(py::handle logits, py::handle values, py::handle indices
 py::object distill_forward(py::handle logits, py::handle values, py::handle indices, double temperature, py::handle lse,
                            py::handle weights) {
     Distill c;
-    if (!c.take_all(logits, values, indices, lse, weights) || !c.fill(static_cast<float>(temperature))) return py::none();
+    if (!c.take_all(logits, values, indices, lse, weights) || !c.fill(temperature)) return py::none();
     const Tensor row_loss = make(c.values, {c.d.rows}, at::kFloat);
     Tensor loss, stats;
     if (c.forward(loss, row_loss, stats) != LRS_OK) return py::none();
@@ -193,7 +193,7 @@ struct DistillLoss : torch::autograd::Function<DistillLoss> {
                           double temperature, const Maybe &lse, const Maybe &weights) {
         Distill c{logits, values, indices, given(lse), given(weights)};
         Tensor loss, stats;
-        c.fill(static_cast<float>(temperature));
+        c.fill(temperature);
         const int status = c.forward(loss, Tensor(), stats);
         if (status != LRS_OK) failed("topk_distill_forward", status);
         ctx->save_for_backward({logits, values, indices, stats, c.lse, c.weights});
@@ -204,7 +204,7 @@ struct DistillLoss : torch::autograd::Function<DistillLoss> {
         const auto saved = ctx->get_saved_variables();
         Distill c{saved[0].detach(), saved[1], saved[2], saved[4], saved[5]};
         const Tensor scale = up[0].detach();
-        if (!c.fill(static_cast<float>(ctx->saved_data["temperature"].toDouble())) || scale.scalar_type() != at::kFloat ||
+        if (!c.fill(ctx->saved_data["temperature"].toDouble()) || scale.scalar_type() != at::kFloat ||
             scale.numel() != 1)
             failed("topk_distill_backward", LRS_ERR_SIZE);
         const Tensor grad = like_rows(c.logits);
@@ -218,8 +218,8 @@ struct DistillLoss : torch::autograd::Function<DistillLoss> {
 py::object distill_loss(py::handle logits, py::handle values, py::handle indices, double temperature, py::handle lse,
                         py::handle weights) {
     Distill c;
-    const float t = static_cast<float>(temperature);
-    if (!c.take_all(logits, values, indices, lse, weights) || !c.fill(t) || c.d.k < 1 || c.d.k > LRS_MAX_TOPK || !(t > 0.f) || !std::isfinite(t) || !std::isfinite(1.f / t) ||
+    if (!c.take_all(logits, values, indices, lse, weights) || !c.fill(temperature) || c.d.k < 1 || c.d.k > LRS_MAX_TOPK ||
+        !(temperature > 0) || !std::isfinite(temperature) || !std::isfinite(static_cast<float>(1.0 / temperature)) ||
         c.d.n > LRS_MAX_ROW_LEN)
         return py::none();
     return py::cast(DistillLoss::apply(c.logits, c.values, c.indices, temperature, maybe(c.lse), maybe(c.weights)));

@@ -111,7 +111,7 @@ class _Distill(ctypes.Structure):
                 ("teacher_lse", ctypes.c_void_p), ("row_weights", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
                 ("dtype", ctypes.c_int), ("teacher_dtype", ctypes.c_int), ("index_bytes", ctypes.c_int),
-                ("temperature", ctypes.c_float)]
+                ("temperature", ctypes.c_double)]
 
 
 def _by_row(t, name: str, rows: int, device) -> int | None:
