@@ -46,16 +46,19 @@ __global__ __launch_bounds__(kBalBlock) void count_kernel(CountArgs a) {
     for (uint32_t e = threadIdx.x; e < a.experts; e += kBalBlock) hist[e] = 0;
     if (threadIdx.x == 0) kept = 0;
     __syncthreads();
-    const uint64_t total = a.rows * a.k, step = static_cast<uint64_t>(gridDim.x) * kBalBlock;
-    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kBalBlock + threadIdx.x; i < total; i += step) {
-        const uint64_t row = i / a.k, at = row * a.stride + i % a.k;
+    // rows * k and rows are below 2^31, and 32-bit divisions cost a fifth of 64-bit ones
+    const uint32_t total = static_cast<uint32_t>(a.rows * a.k), step = gridDim.x * kBalBlock;
+    const uint32_t rows = static_cast<uint32_t>(a.rows);
+    for (uint32_t i = blockIdx.x * kBalBlock + threadIdx.x; i < total; i += step) {
+        const uint32_t row = i / a.k;
+        const uint64_t at = row * a.stride + (i - row * a.k);
         if (a.mask && !a.mask[row]) continue;
         const int64_t e = a.idx_bytes == 8 ? static_cast<const int64_t *>(a.idx)[at] : static_cast<const int32_t *>(a.idx)[at];
         if (e >= 0 && e < a.experts) atomicAdd(&hist[e], 1);
     }
     if (a.kept && a.mask) {
         int32_t mine = 0;
-        for (uint64_t r = static_cast<uint64_t>(blockIdx.x) * kBalBlock + threadIdx.x; r < a.rows; r += step)
+        for (uint32_t r = blockIdx.x * kBalBlock + threadIdx.x; r < rows; r += step)
             mine += a.mask[r] != 0;
         mine = wave_sum(mine);
         if (threadIdx.x % kLanes == 0) atomicAdd(&kept, mine);

@@ -738,48 +738,48 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
         }
     }
     if constexpr (GRAD) {
-    __syncthreads();
-    const float scale = weight * static_cast<float>(a.inv_t), f = static_cast<float>(out[1]) * scale;
-    r = reference == -INFINITY ? 0.f : static_cast<float>(out[0]);
-    if (huge) r = reference == out[0] ? 0.f : INFINITY;
-    // 16-bit gradients: the factor joins the exponent, where that keeps it to
-    // 2^-19, and its sign the result
-    const float joint = r - __builtin_amdgcn_logf(fabsf(f));
-    if (T != kRowF32 && fabsf(joint) < 64.f) {
-        r = joint;
-        sign = f < 0.f ? 0x80008000u : 0u;
-    } else {
-        factor = f;
-    }
-    const auto only = [&](float x) { return x == m ? 0.f : x != x ? x : -INFINITY; };
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
-        if (below(vecs, u)) {
-            float e[kVec];
-            unpack16<T>(v[u], e);
-            if (huge) {
-                for (int i = 0; i < kVec; ++i) e[i] = only(e[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) e[i] = __builtin_amdgcn_exp2f(exponent<T>(e[i], c, a.c_low, r));
-            if (factor != 1.f) {
-#pragma unroll
-                for (int i = 0; i < kVec; ++i) e[i] *= factor;
-            }
-            u32x4 w = pack16<T>(e);
-            if (T != kRowF32) w ^= sign;
-            store16_once(reinterpret_cast<uint8_t *>(g + u * B * kVec) + tid * 16, w);
+        __syncthreads();
+        const float scale = weight * static_cast<float>(a.inv_t), f = static_cast<float>(out[1]) * scale;
+        r = reference == -INFINITY ? 0.f : static_cast<float>(out[0]);
+        if (huge) r = reference == out[0] ? 0.f : INFINITY;
+        // 16-bit gradients: the factor joins the exponent, where that keeps it to
+        // 2^-19, and its sign the result
+        const float joint = r - __builtin_amdgcn_logf(fabsf(f));
+        if (T != kRowF32 && fabsf(joint) < 64.f) {
+            r = joint;
+            sign = f < 0.f ? 0x80008000u : 0u;
+        } else {
+            factor = f;
         }
-    }
-    if (rest < n) {
-        const float e = __builtin_amdgcn_exp2f(exponent<T>(huge ? only(over) : over, c, a.c_low, r));
-        g[rest] = Row<T>::pattern(e * factor) ^ static_cast<Stored>(sign);
-    }
-    // the teacher's columns over what was written there
-    __syncthreads();
+        const auto only = [&](float x) { return x == m ? 0.f : x != x ? x : -INFINITY; };
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            if (below(vecs, u)) {
+                float e[kVec];
+                unpack16<T>(v[u], e);
+                if (huge) {
+                    for (int i = 0; i < kVec; ++i) e[i] = only(e[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) e[i] = __builtin_amdgcn_exp2f(exponent<T>(e[i], c, a.c_low, r));
+                if (factor != 1.f) {
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) e[i] *= factor;
+                }
+                u32x4 w = pack16<T>(e);
+                if (T != kRowF32) w ^= sign;
+                store16_once(reinterpret_cast<uint8_t *>(g + u * B * kVec) + tid * 16, w);
+            }
+        }
+        if (rest < n) {
+            const float e = __builtin_amdgcn_exp2f(exponent<T>(huge ? only(over) : over, c, a.c_low, r));
+            g[rest] = Row<T>::pattern(e * factor) ^ static_cast<Stored>(sign);
+        }
+        // the teacher's columns over what was written there
+        __syncthreads();
 #pragma unroll 1
-    for (uint32_t j = tid; j < k; j += B)
-        if (col[j] >= 0) g[col[j]] = Row<T>::pattern(sl[j] * scale);
+        for (uint32_t j = tid; j < k; j += B)
+            if (col[j] >= 0) g[col[j]] = Row<T>::pattern(sl[j] * scale);
     }
 }
 

@@ -269,28 +269,6 @@ def _once(gradient):
     return staticmethod(backward)
 
 
-def _distill_gradient(ctx, loss_grad):
-    logits, values, indices, stats, lse, weights = ctx.saved_tensors
-    d = ctx.inputs
-    # the forward's checked inputs serve again, unless a hook has moved what was saved
-    if (logits.data_ptr() != d.logits or values.data_ptr() != d.teacher_values or indices.data_ptr() != d.teacher_indices
-            or _lrs._ptr(lse) != d.teacher_lse or _lrs._ptr(weights) != d.row_weights):
-        d = _distill_inputs(logits, values, indices, d.temperature, lse, weights)
-    return _distill_backward(d, logits, stats, loss_grad, None, None), None, None, None, None, None
-
-
-class _DistillLoss(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, logits, values, indices, temperature, lse, weights):
-        d = _distill_inputs(logits, values, indices, temperature, lse, weights)
-        loss, stats = _distill_forward(d, logits, None, None, None)
-        ctx.save_for_backward(logits, values, indices, stats, lse, weights)
-        ctx.inputs = d
-        return loss
-
-    backward = _once(_distill_gradient)
-
-
 def topk_distill_loss(logits: torch.Tensor, teacher_values: torch.Tensor, teacher_indices: torch.Tensor,
                       temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
                       row_weights: torch.Tensor | None = None) -> torch.Tensor:
@@ -300,9 +278,10 @@ def topk_distill_loss(logits: torch.Tensor, teacher_values: torch.Tensor, teache
     streams of graphs that were built outside it."""
     out = (_fast or _binding()).distill_loss(logits, teacher_values, teacher_indices, float(temperature), teacher_lse,
                                              row_weights)
-    if out is not None:
-        return out
-    return _DistillLoss.apply(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights)
+    if out is None:
+        topk_distill_forward(logits, teacher_values, teacher_indices, temperature, teacher_lse, row_weights)  # says what is wrong
+        _lrs._bad("topk_distill_loss does not take these arguments")
+    return out
 
 
 # ------------------------------------------ expert counts and balance loss
