@@ -192,17 +192,29 @@ __device__ inline double times(double a, double b) {
     return p;
 }
 
-// Whether x c of a row with this largest logit may pass what 32 bits hold.
-__device__ inline bool huge_logit(float m, float c) { return fabsf(m) < INFINITY && !(fabsf(m * c) < 0x1p100f); }
+// A reference of up to 2^20 is a whole number: m c in 32 bits is within 2^-4 of
+// m times the factor there, so exponents of the largest logits stay near 0.
+// Beyond, the rounding of m c grows with it (at 2^32 to 2^7, and 2^127 is past
+// what 32 bits hold), so exponents are (x - m) c, whose difference is exact for
+// all that have a share, and the reference is m times the factor in 64 bits.
+// The half keeps whole references, after their rounding, from passing 2^20.
+constexpr double kWholeReference = 0x1p20;
+__device__ inline bool huge_logit(float m, float c) {
+    return fabsf(m) < INFINITY && !(fabsf(m * c) < static_cast<float>(kWholeReference) + 0.5f);
+}
+// The logit that exponents with this reference are relative to, 0 where they are relative to the reference itself.
+__device__ inline float base_of(double reference, double factor) {
+    const bool huge = fabs(reference) < INFINITY && fabs(reference) > kWholeReference;
+    return huge ? static_cast<float>(reference / factor) : 0.f;
+}
 
 // What a row's gradient needs: off S it is f 2^((x - b) c - r) with b, r and f
 // the first three stats (r whole and b 0, or b the largest logit and r 0 where
 // that is huge), at slot j's column stats[3 + j], all before weight / T.
 constexpr uint32_t kStats = 3;
-__device__ inline void write_stats(float *stats, double reference, double c, double f) {
-    const bool huge = fabs(reference) < INFINITY && !(fabs(reference) < 0x1p100);
-    stats[0] = huge ? static_cast<float>(reference / c) : 0.f;
-    stats[1] = huge ? 0.f : static_cast<float>(reference);
+__device__ inline void write_stats(float *stats, double reference, float base, double f) {
+    stats[0] = base;
+    stats[1] = base != 0.f ? 0.f : static_cast<float>(reference);
     stats[2] = static_cast<float>(f);
 }
 
@@ -319,7 +331,7 @@ __global__ __launch_bounds__(kLanes) void distill_row_kernel(DisArgs a) {
                 if (q0 > 0) f -= q0 / z;
                 f *= exp2(r - exact);
             }
-            write_stats(stats, r, factor_of<T>(a), f);
+            write_stats(stats, r, base_of(r, factor_of<T>(a)), f);
         }
     }
 }
@@ -418,6 +430,11 @@ __device__ inline double exp2_64(double d) {
     p = fma(p, y, 1.0);
     return ldexp(p, static_cast<int>(fmax(fmin(i, 2000.0), -2000.0)));
 }
+// z 2^d of a d of at most 0, exactly where d is whole.
+__device__ inline double scaled(double z, double d) {
+    if (d == rint(d)) return ldexp(z, static_cast<int>(fmax(d, -4000.0)));
+    return z * exp2_64(d);
+}
 // log2 of a number in the range of 32 bits: the hardware's, and the rest from
 // log(1 + e) = e - e^2 / 2 at e = v 2^-that - 1, below 2^-20.
 __device__ inline double log2_64(double v) {
@@ -463,6 +480,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
     double *teacher = reinterpret_cast<double *>(lds + 272);       // its reference, its mass on S
     uint32_t *again = reinterpret_cast<uint32_t *>(lds + 288);     // a column is there more than once
     uint32_t *columns = again + 1;                                 // distinct ones
+    float *base = reinterpret_cast<float *>(columns + 1);          // the logit that the row's exponents are relative to
     const uint32_t slots = HeldLds::slots(a.k);
     double *q = reinterpret_cast<double *>(lds + HeldLds::kFixed);
     int32_t *col = reinterpret_cast<int32_t *>(q + slots);
@@ -641,9 +659,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
         reference = m == -INFINITY ? -INFINITY : huge ? times(m, factor_of<T>(a)) : r;
     }
     anew();
-    // logits as large as the type's lowest value: all but the largest have no
-    // share, and x c need not be finite
-    if (huge) z_wave = sum_of([&](float x) { return x == m ? 1.f : x != x ? x : 0.f; });
+    if (huge) z_wave = sum_of([&](float x) { return __builtin_amdgcn_exp2f(exponent<T>(x - m, c, a.c_low, 0.f)); });
     else if (!(z_wave >= 0x1p-20 && z_wave <= 0x1p40)) z_wave = sum_of(power);
     anew();
     if (lane == 0) {
@@ -662,7 +678,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
         const double mine = R, known = teacher[0], sum = teacher[1];
         R = wave_max(R);
         const bool empty = R == -INFINITY;
-        if (mine != -INFINITY) z = ldexp(z, static_cast<int>(fmax(mine - R, -4000.0)));
+        if (mine != -INFINITY) z = scaled(z, mine - R);
         z = wave_sum(z);
         double scale = 1, q0 = 0, mass = sum;
         if (tail) {
@@ -691,7 +707,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
                 if (first) on += power_of_two(times(sl[j], cd) - whole_r);
             }
             on = wave_sum(on);
-            whole = on + (empty ? z : ldexp(z, static_cast<int>(fmax(R - whole_r, -4000.0))));
+            whole = on + (empty ? z : scaled(z, R - whole_r));
         }
         // the logarithms, a lane each
         const double of = lane == 0 ? whole : lane == 1 ? z : lane == 2 ? q0 : sum;
@@ -729,19 +745,20 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
             a.row_loss[row] = static_cast<float>(loss);
             double f = 0;
             if (!empty) {
-                f = a_mass * ldexp(1.0, static_cast<int>(fmax(R - whole_r, -4000.0))) / whole;
+                f = a_mass * scaled(1.0, R - whole_r) / whole;
                 if (q0 > 0) f -= q0 / z;
             }
             out[0] = empty ? 0.0 : R;
             out[1] = f;
-            if (stats) write_stats(stats, out[0], cd, f);
+            *base = base_of(out[0], cd);
+            if (stats) write_stats(stats, out[0], *base, f);
         }
     }
     if constexpr (GRAD) {
         __syncthreads();
         const float scale = weight * static_cast<float>(a.inv_t), f = static_cast<float>(out[1]) * scale;
-        r = reference == -INFINITY ? 0.f : static_cast<float>(out[0]);
-        if (huge) r = reference == out[0] ? 0.f : INFINITY;
+        const float from = *base;
+        r = from != 0.f || reference == -INFINITY ? 0.f : static_cast<float>(out[0]);
         // 16-bit gradients: the factor joins the exponent, where that keeps it to
         // 2^-19, and its sign the result
         const float joint = r - __builtin_amdgcn_logf(fabsf(f));
@@ -751,14 +768,14 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
         } else {
             factor = f;
         }
-        const auto only = [&](float x) { return x == m ? 0.f : x != x ? x : -INFINITY; };
 #pragma unroll
         for (int u = 0; u < V; ++u) {
             if (below(vecs, u)) {
                 float e[kVec];
                 unpack16<T>(v[u], e);
-                if (huge) {
-                    for (int i = 0; i < kVec; ++i) e[i] = only(e[i]);
+                if (from != 0.f) {
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) e[i] -= from;
                 }
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) e[i] = __builtin_amdgcn_exp2f(exponent<T>(e[i], c, a.c_low, r));
@@ -772,7 +789,7 @@ __global__ __launch_bounds__(B, GRAD ? 4 : 8) void distill_held_kernel(DisArgs a
             }
         }
         if (rest < n) {
-            const float e = __builtin_amdgcn_exp2f(exponent<T>(huge ? only(over) : over, c, a.c_low, r));
+            const float e = __builtin_amdgcn_exp2f(exponent<T>(over - from, c, a.c_low, r));
             g[rest] = Row<T>::pattern(e * factor) ^ static_cast<Stored>(sign);
         }
         // the teacher's columns over what was written there

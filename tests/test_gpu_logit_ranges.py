@@ -1,0 +1,165 @@
+"""Row operators on finite logits of any size: masks of values in common use
+(-1e4 to -1e20), whole rows at such a value, large logits that differ by little,
+and temperatures that put ordinary logits there.  The oracle takes every row in
+64 bits relative to its own largest logit."""
+import sys
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+lrs = pytest.importorskip("lsd_radix_sort_amd")
+
+DTYPES = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}
+ULP = 2.0 ** -24  # half a step of 32-bit numbers
+INF = float("inf")
+
+
+def log(msg):
+    print(msg, flush=True)
+    sys.stdout.flush()
+
+
+@pytest.fixture(scope="module", autouse=True)
+def device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    lrs.load_library()
+
+
+def half_step(dtype, g):
+    """Half a step of the type at g, with the floor of its smallest numbers."""
+    floor = {"fp16": 2.0 ** -25, "bf16": 2.0 ** -126, "fp32": 2.0 ** -126}[dtype]
+    return g.abs() * (torch.finfo(DTYPES[dtype]).eps / 2) + floor
+
+
+# ------------------------------------------------------------- distillation
+
+def log_softmax(s, temperature):
+    """Each row's log softmax of s / temperature, and its largest logit, its log-sum-exp less the largest."""
+    top = s.max(1, keepdim=True)[0]
+    u = torch.where(s == -INF, s, (s - torch.where(top == -INF, 0.0, top)) / temperature)
+    rest = torch.log(torch.exp(u).sum(1, keepdim=True))
+    return u - rest, top, rest
+
+
+def distill_oracle(s, t, i, temperature, tlse):
+    """Row losses, the sum of their terms' sizes, the gradient (weight 1), the sum of its terms' sizes, and how far
+    (in exponents) each column lies below the largest of the rows that it is weighed in."""
+    s, t = s.double(), t.double()
+    rows, n = s.shape
+    ok = (i >= 0) & (i < n) & (t > -INF)
+    at = torch.where(ok, i.long(), n)
+    member = torch.zeros(rows, n + 1, dtype=torch.bool).scatter_(1, at, True)[:, :n]
+    tz = torch.where(ok, t / temperature, -INF)
+    logp, top, rest = log_softmax(s, temperature)
+    if tlse is None:
+        logq, q0 = torch.log_softmax(tz, 1), torch.zeros(rows, dtype=torch.float64)
+    else:
+        logq = tz - tlse.double()[:, None]
+        q0 = (1 - torch.exp(logq).sum(1)).clamp_min(0)
+    q = torch.exp(logq)
+    zt = torch.gather(logp, 1, torch.where(ok, at, 0))
+    part = torch.where(q > 0, q * (logq - zt), 0.0)
+    loss = part.sum(1)
+    size = torch.where(q > 0, q * (logq.abs() + zt.abs()), 0.0).sum(1)
+    logp_tail, top_tail, rest_tail = log_softmax(torch.where(member, -INF, s), temperature)
+    if tlse is not None:
+        q0 = torch.where((top_tail[:, 0] == -INF) & (q0 <= 2.0 ** -20), 0.0, q0)
+        logp0 = ((top_tail - top) / temperature + rest_tail - rest)[:, 0]
+        loss = loss + torch.where(q0 > 0, q0 * (torch.log(q0) - logp0), 0.0)
+        size = size + torch.where(q0 > 0, q0 * (torch.log(q0).abs() + logp0.abs()), 0.0)
+    mass = q.sum(1) + q0
+    target = torch.zeros(rows, n + 1, dtype=torch.float64).scatter_add_(1, at, q)[:, :n]
+    tail = q0[:, None] * torch.exp(logp_tail)
+    own = mass[:, None] * torch.exp(logp)
+    grad = (own - torch.where(member, target, tail)) / temperature
+    terms = (own + torch.where(member, target, tail)) / temperature
+    # a column so far below that it has no share rounds to none
+    below = torch.where(logp > -200, logp.abs(), 0.0)
+    below = torch.maximum(below, torch.where(~member & (logp_tail > -200), logp_tail.abs(), 0.0))
+    return loss, size, grad, terms, below
+
+
+def check_distill(s, t, i, temperature=1.0, tlse=None, copies=1):
+    dtype = {v: k for k, v in DTYPES.items()}[s.dtype]
+    rows = s.shape[0] * copies
+    loss, size, grad, terms, below = distill_oracle(s, t, i, temperature, tlse)
+
+    def tiled(x):
+        return None if x is None else x.cuda().repeat(copies, *[1] * (x.dim() - 1))
+    args = (tiled(s), tiled(t), tiled(i))
+    lse = tiled(tlse)
+    total, row_loss, stats = lrs.topk_distill_forward(*args, temperature, lse)
+    back = lrs.topk_distill_backward(*args, stats, temperature, lse)
+    total2, row_loss2, step = lrs.topk_distill_step(*args, temperature, lse)
+    torch.cuda.synchronize()
+    # a thread adds at most 128 exponentials in 32 bits; one exponential and the products around it round some tens of times
+    tol = (128 + 64) * ULP
+    # log2(e) / temperature has 32 bits in 16-bit rows, rounded down, and a result is rounded once
+    bound = tol + 4 * ULP * size
+    for name, got in (("forward", row_loss), ("step", row_loss2)):
+        off = (got.cpu().double().view(copies, -1) - loss).abs()
+        assert bool((off <= bound).all()), f"{name}: row losses {got[:loss.numel()].tolist()} for {loss.tolist()}"
+    for name, got in (("forward", total), ("step", total2)):
+        assert abs(float(got) - float(loss.mean())) <= float(bound.mean()) + ULP * abs(float(loss.mean())), name
+    # an exponent that far below rounds by its own half step, and by the factor's
+    want = grad / rows
+    lim = (terms / rows) * (tol + 4 * ULP * (below + 1)) + half_step(dtype, want)
+    # what passes the type's largest number is an infinity
+    past = want.abs() - lim > torch.finfo(s.dtype).max
+    for name, got in (("backward", back), ("step", step)):
+        got = got.cpu().double().view(copies, *grad.shape)
+        off = torch.where(past & (got == want.sign() * INF), 0.0, (got - want).abs())
+        assert bool((off <= lim).all()), f"{name}: gradient off by {(off - lim).max()} over its bound"  # NaN fails too
+
+
+def rows_around(value, n, k, dtype, seed, temperature, tail):
+    """Eight students and their teachers; `value` is a mask, or where all of a row lies."""
+    g = torch.Generator().manual_seed(seed)
+    full = torch.randn(8, n, generator=g) * 2.5 * temperature
+    full[0, n // 8:] = -INF  # the teacher may not answer there either
+    t, i = torch.topk(full, k, dim=1)
+    tlse = torch.logsumexp(full.double() / temperature, dim=1).float() if tail else None
+    s = 0.6 * full.clamp_min(-1e4) + 1.5 * temperature * torch.randn(8, n, generator=g)
+    near = (value + 2.5 * temperature * torch.randn(n, generator=g, dtype=torch.float64)).float()
+    s[0, n // 8:] = value                                  # whole waves' columns masked
+    s[1] = value                                           # a row masked
+    s[2] = s[2].scatter(0, i[2], -INF).clamp(max=value)    # all but S
+    s[2, i[2]] = torch.randn(k, generator=g)
+    s[3] = near                                            # little apart, as far as the type tells
+    s[4, n // 2::5] = -value                               # some as far above
+    s[5, ::2] = value                                      # every other one
+    s[6, ::2], s[6, 1::2] = -INF, value
+    s[6, i[6]] = value
+    return s.to(DTYPES[dtype]), t, i, tlse
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("temperature", [0.5, 0.7, 1.0, 3.0])
+@pytest.mark.parametrize("n,k,copies", [(9001, 30, 1), (601, 6, 38), (140_001, 5, 1)])
+def test_distill_masks(dtype, tail, temperature, n, k, copies):
+    for value in (-1e4, -3e6, -1e9, -3e9, -1e10, -1e12, -1e20):
+        log(f"distill masks {dtype} tail={tail} T={temperature} n={n} value={value}")
+        s, t, i, tlse = rows_around(value, n, k, dtype, 10 + n, temperature, tail)
+        check_distill(s, t, i, temperature, tlse, copies)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("n,k,copies", [(5000, 12, 1), (4099, 20, 35), (135_001, 9, 1)])
+def test_distill_large_logits_and_small_temperatures(dtype, n, k, copies):
+    """Logits over a temperature of about 2^19 to 2^33, where neighbours still have shares or no longer do."""
+    g = torch.Generator().manual_seed(20 + n)
+    for tail in (False, True):
+        for power, temperature in ((19, 1.0), (21, 1.0), (24, 0.3), (27, 1.0), (31, 1.0), (14, 1e-3), (10, 1e-5), (3, 1e-9)):
+            if dtype == "fp16" and power > 14:
+                continue
+            log(f"distill large {dtype} tail={tail} 2^{power} T={temperature} n={n}")
+            sign = torch.tensor([1.0, -1.0] * 4, dtype=torch.float64)[:, None]
+            s = sign * 2.0 ** power + 2 * temperature * torch.randn(8, n, generator=g, dtype=torch.float64)
+            s = s.to(DTYPES[dtype])
+            t, i = torch.topk(2 * temperature * torch.randn(8, n, generator=g), k, dim=1)
+            tlse = torch.logsumexp(t.double() / temperature, 1).float() + 0.5 if tail else None
+            check_distill(s, t, i, temperature, tlse, copies)
