@@ -272,8 +272,9 @@ __global__ __launch_bounds__(B) void balance_kernel(BalArgs a) {
 #pragma unroll
         for (int u = 0; u < V; ++u) unpack16<T>(v[u], w[u]);
         if (base + step < a.rows) load_row(row + step);
-        // exponents of 2 relative to `ref`: x log2(e) - ref, x taken from `from`
-        // where a logit is so large that its product is not finite
+        // exponents of 2 relative to `ref`: x log2(e) - ref, x taken from `from`,
+        // the largest logit, in rows where that is so large that the rounding of
+        // ref (2^-4 at 2^20, 2^7 at 2^32) would show as the largest's own exponent
         float m = 0, ref = 0, from = 0;
         if (!SIG) {
             m = w[0][0];
@@ -283,8 +284,8 @@ __global__ __launch_bounds__(B) void balance_kernel(BalArgs a) {
                 for (int e = 0; e < kVec; e += 2) m = max3(m, w[u][e], w[u][e + 1]);
             m = group_max(m, a.lanes);
             if (m == -INFINITY) m = 0.f;
-            if (__any(fabsf(m) > 0x1p120f)) {
-                from = m;
+            if (__any(fabsf(m) > 0x1p20f)) {
+                from = fabsf(m) > 0x1p20f ? m : 0.f;
 #pragma unroll
                 for (int u = 0; u < V; ++u)
 #pragma unroll

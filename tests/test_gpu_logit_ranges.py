@@ -163,3 +163,78 @@ def test_distill_large_logits_and_small_temperatures(dtype, n, k, copies):
             t, i = torch.topk(2 * temperature * torch.randn(8, n, generator=g), k, dim=1)
             tlse = torch.logsumexp(t.double() / temperature, 1).float() + 0.5 if tail else None
             check_distill(s, t, i, temperature, tlse, copies)
+
+
+# ------------------------------------------------------------- balance loss
+
+def balance_oracle(x, counts, alpha, beta, score):
+    """The loss, the sum of its terms' sizes, the gradient, the sum of its terms' sizes, and how far each element lies
+    below its row's largest."""
+    x = x.double()
+    tokens, experts = x.shape
+    load = counts.double() * experts / max(int(counts.sum()), 1)
+    weight = x if score == "softmax" else torch.nn.functional.logsigmoid(x)  # p is the softmax of this
+    logp, top, rest = log_softmax(weight, 1.0)
+    live = top > -INF
+    p = torch.where(live, torch.exp(logp), 0.0)
+    z = torch.where(live, top + rest, 0.0) if score == "softmax" else torch.zeros_like(top)
+    slope = torch.sigmoid(-x) if score == "sigmoid" else torch.ones_like(x)
+    b = (p * load).sum(1, keepdim=True)
+    row = alpha * b + beta * z * z
+    size = abs(alpha) * b + abs(beta) * z * z
+    grad = p * slope * (alpha * (load - b) + 2 * beta * z) / tokens
+    terms = p * slope * (abs(alpha) * (load + b) + 2 * abs(beta) * z.abs()) / tokens
+    below = torch.where(live & (logp > -200), logp.abs(), 0.0)
+    return row.mean(), size.mean(), grad, terms, below
+
+
+def check_balance(x, idx, alpha=0.3, beta=0.0, score="softmax"):
+    dtype = {v: k for k, v in DTYPES.items()}[x.dtype]
+    tokens, experts = x.shape
+    counts = torch.bincount(idx.flatten(), minlength=experts)
+    loss, size, grad, terms, below = balance_oracle(x, counts, alpha, beta, score)
+    gx, gi = x.cuda(), idx.cuda()
+    got, c, kept = lrs.expert_balance_forward(gx, gi, alpha, beta, score)
+    back = lrs.expert_balance_backward(gx, c, kept, alpha, beta, score)
+    total, _, step = lrs.expert_balance_step(gx, gi, alpha, beta, score)
+    torch.cuda.synchronize()
+    # a lane adds at most experts / 4 terms in 32 bits (its share of a row); an exponential and the products around it
+    # round some tens of times, twice over in a sum of p f
+    tol = (experts / 4 + 64) * ULP
+    bound = 2 * tol * float(size) + ULP * abs(float(loss))
+    for name, l in (("forward", got), ("step", total)):
+        assert abs(float(l) - float(loss)) <= bound, f"{name}: loss {float(l)} for {float(loss)}, {bound}"
+    lim = terms * (2 * tol + 4 * ULP * (below + 1)) + half_step(dtype, grad)
+    for name, g in (("backward", back), ("step", step)):
+        off = (g.cpu().double() - grad).abs()
+        assert bool((off <= lim).all()), f"{name}: gradient off by {(off - lim).max()} over its bound"
+
+
+def routed(tokens, experts, k, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(tokens, experts, generator=g, dtype=torch.float64) * 1.5, torch.randint(0, experts, (tokens, k), generator=g)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("tokens,experts", [(40, 24), (700, 256), (30, 700)])
+@pytest.mark.parametrize("beta", [0.0, 1e-3])
+def test_balance_softmax_large_logits(dtype, tokens, experts, beta):
+    for value in (-1e4, 3e6, -3e9, -1e10, 1e10, -1e12, 1e12):
+        log(f"balance {dtype} {tokens}x{experts} beta={beta} value={value}")
+        x, idx = routed(tokens, experts, 4, 30 + experts)
+        x[3::7] = value                       # tokens whose logits are all at it
+        x[1::7] += value                      # around it
+        x[2::7, ::3] = -abs(value)            # masked experts
+        x[4::7, 1] = abs(value)               # one expert far above
+        check_balance(x.to(DTYPES[dtype]), idx, 0.3, beta)
+
+
+def test_balance_rows_do_not_depend_on_their_neighbours():
+    x, idx = routed(64, 16, 2, 40)
+    x = x.float().cuda()
+    counts = torch.arange(1, 17, dtype=torch.int32, device="cuda")
+    alone = lrs.expert_balance_backward(x, counts)
+    x2 = x.clone()
+    x2[::2] = -1e30
+    beside = lrs.expert_balance_backward(x2, counts)
+    assert torch.equal(alone[1::2], beside[1::2])
