@@ -238,3 +238,20 @@ def test_balance_rows_do_not_depend_on_their_neighbours():
     x2[::2] = -1e30
     beside = lrs.expert_balance_backward(x2, counts)
     assert torch.equal(alone[1::2], beside[1::2])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("beta", [0.0, 1e-8])
+def test_balance_square_of_a_large_log_sum(dtype, beta):
+    """The square of a log-sum-exp passes 32 bits long before the logits do."""
+    top = torch.finfo(DTYPES[dtype]).max
+    for value in (-1e20, 3e22, -top, top):
+        log(f"balance square {dtype} beta={beta} value={value}")
+        x, idx = routed(50, 40, 3, 50)
+        x[5] = value
+        if beta and abs(value) > 1e23:  # the loss itself passes 32 bits
+            x = x.to(DTYPES[dtype]).cuda()
+            loss, _, grad = lrs.expert_balance_step(x, idx.cuda(), 0.3, beta)
+            assert float(loss) == INF and not torch.isnan(grad).any()
+        else:
+            check_balance(x.to(DTYPES[dtype]), idx, 0.3, beta)
