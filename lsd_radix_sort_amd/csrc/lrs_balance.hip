@@ -275,22 +275,40 @@ __global__ __launch_bounds__(B) void balance_kernel(BalArgs a) {
         // exponents of 2 relative to `ref`: x log2(e) - ref, x taken from `from`,
         // the largest logit, in rows where that is so large that the rounding of
         // ref (2^-4 at 2^20, 2^7 at 2^32) would show as the largest's own exponent
-        float m = 0, ref = 0, from = 0;
-        if (!SIG) {
-            m = w[0][0];
+        float ref = 0, from = 0, one = 1;
+        const auto largest = [&]() {
+            float m = w[0][0];
 #pragma unroll
             for (int u = 0; u < V; ++u)
 #pragma unroll
                 for (int e = 0; e < kVec; e += 2) m = max3(m, w[u][e], w[u][e + 1]);
             m = group_max(m, a.lanes);
-            if (m == -INFINITY) m = 0.f;
-            if (__any(fabsf(m) > 0x1p20f)) {
-                from = fabsf(m) > 0x1p20f ? m : 0.f;
+            return m == -INFINITY ? 0.f : m;
+        };
+        const auto take_from = [&](float logit) {
+            from = logit;
 #pragma unroll
-                for (int u = 0; u < V; ++u)
+            for (int u = 0; u < V; ++u)
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) w[u][e] -= from;
+                for (int e = 0; e < kVec; ++e) w[u][e] -= from;
+        };
+        if (SIG) {
+            // Sigmoids below 2^-126 are 0, which would empty a row that lies far
+            // below 0.  A row whose largest logit m is below -7 takes them times
+            // e^-m, which p does not show: 1 / (e^m + e^(m - x)), and 1 - sigmoid
+            // is e^(m - x) times that.  Such rows are few: m is looked for only
+            // where a row's first logit in each of its lanes is that low.
+            constexpr float kFar = -7.f;
+            uint64_t low = __ballot(w[0][0] < kFar);
+            for (uint32_t d = 1; d < a.lanes; d *= 2) low &= low >> d;
+            if (low) {
+                const float m = largest();
+                take_from(m < kFar ? m : 0.f);
+                one = __builtin_amdgcn_exp2f(from * kLog2e);
             }
+        } else {
+            const float m = largest();
+            if (__any(fabsf(m) > 0x1p20f)) take_from(fabsf(m) > 0x1p20f ? m : 0.f);
             ref = (m - from) * kLog2e;
         }
         float s = 0, b = 0;
@@ -305,7 +323,7 @@ __global__ __launch_bounds__(B) void balance_kernel(BalArgs a) {
             for (int u = 0; u < V; ++u)
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) {
-                    const float t = __builtin_amdgcn_exp2f(-w[u][e] * kLog2e), g = __builtin_amdgcn_rcpf(1.f + t);
+                    const float t = __builtin_amdgcn_exp2f(-w[u][e] * kLog2e), g = __builtin_amdgcn_rcpf(one + t);
                     slope[SIG ? u : 0][e] = g == 0.f ? 0.f : g * (g * t);
                     add(u, e, g);
                 }

@@ -255,3 +255,39 @@ def test_balance_square_of_a_large_log_sum(dtype, beta):
             assert float(loss) == INF and not torch.isnan(grad).any()
         else:
             check_balance(x.to(DTYPES[dtype]), idx, 0.3, beta)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("tokens,experts", [(40, 24), (700, 160), (64, 256), (30, 700), (5, 4096)])
+def test_balance_sigmoid_of_low_rows(dtype, tokens, experts):
+    """Rows whose logits are all far below 0: sigmoids divided by their sum tend to a softmax."""
+    for value in (-12.0, -60.0, -95.0, -300.0, -1e4, -3e6, -1e10, -1e20, -3e38):
+        if dtype == "fp16" and value < -6e4:
+            continue
+        log(f"balance sigmoid {dtype} {tokens}x{experts} value={value}")
+        x, idx = routed(tokens, experts, 4, 60 + experts)
+        x[3::7] = value                       # tokens whose logits are all at it
+        x[1::7] += value                      # around it
+        x[2::7, ::3] = value                  # low experts
+        x[4::7] = -INF                        # all at it but masked experts
+        x[4::7, 1::2] = value
+        x[0] = -INF                           # no expert at all
+        check_balance(x.to(DTYPES[dtype]), idx, 0.3, 0.0, "sigmoid")
+
+
+def test_balance_sigmoid_low_rows_beside_others():
+    x, idx = routed(64, 16, 2, 70)
+    x = x.float().cuda()
+    counts = torch.arange(1, 17, dtype=torch.int32, device="cuda")
+    alone = lrs.expert_balance_backward(x, counts, score="sigmoid")
+    x2 = x.clone()
+    x2[::2] = -100.0
+    mask = torch.ones(64, dtype=torch.bool, device="cuda")
+    kept = torch.tensor([64], dtype=torch.int32, device="cuda")
+    beside = lrs.expert_balance_backward(x2, counts, score="sigmoid")
+    assert torch.equal(alone[1::2], beside[1::2])
+    # rows that do not count are not looked at
+    x2[::2] = float("nan")
+    mask[::2] = False
+    beside = lrs.expert_balance_backward(x2, counts, kept, score="sigmoid", row_mask=mask)
+    assert torch.equal(alone[1::2], beside[1::2]) and bool((beside[::2] == 0).all())
