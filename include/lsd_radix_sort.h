@@ -278,7 +278,8 @@ int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_
  * programs that know the loss is what they differentiate.  The teacher's
  * tensors are constants: they get no gradient.
  * 1 <= k <= LRS_MAX_TOPK (also more than n); n <= LRS_MAX_ROW_LEN;
- * rows * n < 2^40; temperature above 0, and it and 1 / temperature finite (else LRS_ERR_OPTION);
+ * rows * n < 2^40; temperature above 0 and finite, log2(e) / temperature finite in 32 bits (from 4.3e-39 on; else
+ * LRS_ERR_OPTION);
  * rows == 0 gives loss 0.  Results do not depend on the order in which
  * workgroups run.  Only opts->timer is used (kind 4).
  */
@@ -295,7 +296,7 @@ typedef struct lrs_distill {
     int dtype;                    /* of the logits and the gradient: LRS_DTYPE_* */
     int teacher_dtype;            /* LRS_DTYPE_* */
     int index_bytes;              /* 4 or 8 */
-    double temperature;           /* 1 / temperature finite in 32 bits */
+    double temperature;           /* log2(e) / temperature finite in 32 bits */
 } lrs_distill;
 
 size_t topk_distill_workspace_size(int64_t rows, int64_t n, int64_t k, int dtype, const lrs_options *opts);

@@ -26,6 +26,7 @@ namespace lrs {
 namespace {
 
 constexpr int kDisBlock = 256;
+constexpr double kLog2e = 1.44269504088896340736;
 // Columns whose membership in S one workgroup holds as a bitmap at a time.
 constexpr uint32_t kMapColumns = 65536;
 
@@ -846,7 +847,7 @@ int distill_inputs(const lrs_distill *d, DisArgs &a) {
     if (!row_type_ok(d->teacher_dtype) || (d->index_bytes != 4 && d->index_bytes != 8)) return LRS_ERR_DTYPE;
     if (!stride_ok(d->row_stride, d->rows) || !stride_ok(d->teacher_stride, d->rows) || !stride_ok(d->index_stride, d->rows))
         return LRS_ERR_SIZE;
-    if (!(d->temperature > 0) || !std::isfinite(d->temperature) || !std::isfinite(static_cast<float>(1.0 / d->temperature)))
+    if (!(d->temperature > 0) || !std::isfinite(d->temperature) || !std::isfinite(static_cast<float>(kLog2e / d->temperature)))
         return LRS_ERR_OPTION;
     if (d->rows > 0 && ((d->n > 0 && !d->logits) || !d->teacher_values || !d->teacher_indices))
         return LRS_ERR_NULL_POINTER;
@@ -867,11 +868,14 @@ int distill_inputs(const lrs_distill *d, DisArgs &a) {
     a.tlse = d->teacher_lse;
     a.weights = d->row_weights;
     a.inv_t = 1.0 / d->temperature;
-    const double factor = 1.44269504088896340736 * a.inv_t;
-    // rounded down, so that the rest is above 0 and -inf times it is -inf
+    const double factor = kLog2e * a.inv_t;
+    // both parts above 0, so that -inf times either is -inf: the first is rounded
+    // down, and neither is below the smallest number (times the largest: 2^-21)
+    constexpr float kLeast = std::numeric_limits<float>::denorm_min();
     a.c = static_cast<float>(factor);
     if (a.c > factor) a.c = std::nextafter(a.c, 0.f);
-    a.c_low = std::max(static_cast<float>(factor - a.c), std::numeric_limits<float>::min());
+    a.c = std::max(a.c, kLeast);
+    a.c_low = std::max(static_cast<float>(factor - a.c), kLeast);
     distill_split(a.rows, a.n, a.splits, a.split_len);
     return LRS_OK;
 }

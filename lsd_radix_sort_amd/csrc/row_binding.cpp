@@ -219,7 +219,7 @@ py::object distill_loss(py::handle logits, py::handle values, py::handle indices
                         py::handle weights) {
     Distill c;
     if (!c.take_all(logits, values, indices, lse, weights) || !c.fill(temperature) || c.d.k < 1 || c.d.k > LRS_MAX_TOPK ||
-        !(temperature > 0) || !std::isfinite(temperature) || !std::isfinite(static_cast<float>(1.0 / temperature)) ||
+        !(temperature > 0) || !std::isfinite(temperature) || !std::isfinite(static_cast<float>(1.44269504088896340736 / temperature)) ||
         c.d.n > LRS_MAX_ROW_LEN)
         return py::none();
     return py::cast(DistillLoss::apply(c.logits, c.values, c.indices, temperature, maybe(c.lse), maybe(c.weights)));

@@ -40,7 +40,7 @@ def log_softmax(s, temperature):
     """Each row's log softmax of s / temperature, and its largest logit, its log-sum-exp less the largest."""
     top = s.max(1, keepdim=True)[0]
     u = torch.where(s == -INF, s, (s - torch.where(top == -INF, 0.0, top)) / temperature)
-    rest = torch.log(torch.exp(u).sum(1, keepdim=True))
+    rest = torch.where(top == -INF, 0.0, torch.log(torch.exp(u).sum(1, keepdim=True)))  # a row without mass keeps -inf
     return u - rest, top, rest
 
 
@@ -291,3 +291,34 @@ def test_balance_sigmoid_low_rows_beside_others():
     mask[::2] = False
     beside = lrs.expert_balance_backward(x2, counts, kept, score="sigmoid", row_mask=mask)
     assert torch.equal(alone[1::2], beside[1::2]) and bool((beside[::2] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("n,k,copies", [(700, 6, 1), (9001, 30, 1), (601, 6, 38), (140_001, 5, 1)])
+def test_distill_temperatures_past_32_bits(dtype, n, k, copies):
+    """Temperatures whose inverse is below what 32 bits hold whole, with masks."""
+    for temperature in (1e30, 1e37, 2e38, 1e40, 1e46, 1e300):
+        for tail in (False, True):
+            log(f"distill {dtype} n={n} T={temperature} tail={tail}")
+            g = torch.Generator().manual_seed(80 + n)
+            s = torch.randn(5, n, generator=g).to(DTYPES[dtype])
+            t, i = torch.topk(torch.randn(5, n, generator=g), k, dim=1)
+            s[0, ::3] = -INF
+            s[0, i[0]] = 0.5
+            s[1, ::2] = torch.finfo(s.dtype).min
+            s[2, ::5] = torch.finfo(s.dtype).max
+            s[3] = s[3].scatter(0, i[3], -INF).clamp(max=-INF)   # all the student has is on S
+            s[3, i[3]] = 1.0
+            tlse = torch.full((5,), float(torch.tensor(2.0 * k).log())) if tail else None
+            if tail:
+                s[3, 0] = 0.25
+            check_distill(s, t, i, temperature, tlse, copies)
+
+
+def test_temperature_refusals():
+    s, t, i = torch.zeros(2, 8, device="cuda"), torch.zeros(2, 2, device="cuda"), torch.zeros(2, 2, dtype=torch.int64, device="cuda")
+    for call in (lrs.topk_distill_step, lrs.topk_distill_forward, lrs.topk_distill_loss):
+        for temperature in (0.0, -1.0, INF, float("nan"), 4e-39, 1e-320):
+            with pytest.raises(ValueError):
+                call(s, t, i, temperature)
+        call(s, t, i, 5e-39)
