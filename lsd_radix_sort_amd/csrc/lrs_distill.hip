@@ -8,9 +8,10 @@
 // (A = all the teacher's mass: 1, or 0 in a row without any).  A row needs one
 // pass for its sum of exponentials and, for the gradient, a second one.
 //
-// Sums over a row are in 32 bits a thread (a few hundred terms) and in 64 bits
-// from there on, as is everything there is once a row or a slot: the terms of
-// a loss nearly cancel, and 1 - sum q loses a small tail in 32 bits.
+// Sums over a row are in 32 bits for a thread's terms (at most 128, or one
+// batch of loads where a row is longer) and in 64 bits from there on, as is
+// everything there is once a row or a slot: the terms of a loss nearly cancel,
+// and 1 - sum q loses a small tail in 32 bits.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -30,6 +31,12 @@ constexpr double kLog2e = 1.44269504088896340736;
 // Columns whose membership in S one workgroup holds as a bitmap at a time.
 constexpr uint32_t kMapColumns = 65536;
 
+// Of a piece of a row: its largest logit and the sum of exponentials relative to that.
+struct Partial {
+    double z;
+    float m;
+};
+
 struct DisArgs {
     const void *logits;
     uint64_t stride;
@@ -47,7 +54,7 @@ struct DisArgs {
     double inv_t;
     float c, c_low;       // log2(e) / T, and what its rounding leaves
     uint32_t splits, split_len;
-    float2 *partial;      // [rows][splits]: largest logit and sum of exponentials of the tail (of all, without one)
+    Partial *partial;     // [rows][splits]: of the tail (of all, without one)
     float *stats;         // [rows][k + kStats]
     float *row_loss;
     float *loss;
@@ -70,15 +77,61 @@ __device__ inline float weight_at(const DisArgs &a, uint64_t row) {
     return a.weights ? a.weights[row] : 1.0f / static_cast<float>(a.rows);
 }
 
-// Joins two (largest, sum of exponentials below it) pairs; c = log2(e) / T.
-__device__ inline void join(float &m, float &z, float m2, float z2, float c) {
-    const float hi = fmaxf(m, m2);
-    if (hi == -INFINITY) {
-        z += z2;  // both sums are 0 (or NaN, which stays)
-        return;
-    }
-    z = z * exp2f((m - hi) * c) + z2 * exp2f((m2 - hi) * c);
-    m = hi;
+// x log2(e) / T less a reference, as an exponent of 2.  In 32-bit rows the
+// rounding of the factor would show, by as much as |x| times its half step.
+template <int T> __device__ inline float exponent(float x, float c, float c_low, float r) {
+    const float e = fmaf(x, c, -r);
+    return T == kRowF32 ? fmaf(x, c_low, e) : e;
+}
+// The factor that exponent() stands for.
+template <int T> __device__ inline double factor_of(const DisArgs &a) {
+    return T == kRowF32 ? static_cast<double>(a.c) + a.c_low : a.c;
+}
+
+// 2^d of a 64-bit d, to 32 bits.
+__device__ inline double power_of_two(double d) {
+    const double i = rint(d);
+    return ldexp(static_cast<double>(__builtin_amdgcn_exp2f(static_cast<float>(d - i))),
+                 static_cast<int>(fmax(fmin(i, 2000.0), -2000.0)));
+}
+
+// 2^d to about 44 bits: the series of exp on |y| <= ln 2 / 2, cut after
+// y^11 / 11!.  Its coefficients go through scalar registers, made where they
+// are used: in a loop that holds a row they would otherwise be kept in 22
+// vector registers throughout.
+__device__ inline double scalar(double v) {
+    asm volatile("" : "+s"(v));
+    return v;
+}
+constexpr double kLn2 = 0.693147180559945309417;
+__device__ inline double exp2_64(double d) {
+    d = d < -2000.0 ? -2000.0 : d;
+    const double i = rint(d), y = (d - i) * scalar(kLn2);
+    double p = scalar(1.0 / 39916800);
+    p = fma(p, y, scalar(1.0 / 3628800));
+    p = fma(p, y, scalar(1.0 / 362880));
+    p = fma(p, y, scalar(1.0 / 40320));
+    p = fma(p, y, scalar(1.0 / 5040));
+    p = fma(p, y, scalar(1.0 / 720));
+    p = fma(p, y, scalar(1.0 / 120));
+    p = fma(p, y, scalar(1.0 / 24));
+    p = fma(p, y, scalar(1.0 / 6));
+    p = fma(p, y, 0.5);
+    p = fma(p, y, 1.0);
+    p = fma(p, y, 1.0);
+    return ldexp(p, static_cast<int>(fmax(fmin(i, 2000.0), -2000.0)));
+}
+// z 2^d of a d of at most 0, exactly where d is whole.
+__device__ inline double scaled(double z, double d) {
+    if (d == rint(d)) return ldexp(z, static_cast<int>(fmax(d, -4000.0)));
+    return z * exp2_64(d);
+}
+// log2 of a number in the range of 32 bits: the hardware's, and the rest from
+// log(1 + e) = e - e^2 / 2 at e = v 2^-that - 1, below 2^-20.
+__device__ inline double log2_64(double v) {
+    const double y = __builtin_amdgcn_logf(static_cast<float>(v));
+    const double e = v * exp2_64(-y) - 1.0;
+    return y + fma(e * e, -0.5, e) * scalar(1.0 / kLn2);
 }
 
 // ---- rows over 256 KB ------------------------------------------------------
@@ -93,15 +146,18 @@ template <int T, bool TAIL>
 __global__ __launch_bounds__(kDisBlock) void distill_sum_kernel(DisArgs a) {
     constexpr int kVec = Row<T>::kVec;
     __shared__ uint32_t map[TAIL ? kMapColumns / 32 : 1];
-    __shared__ float wm[kDisBlock / kLanes], wz[kDisBlock / kLanes];
+    __shared__ float wm[kDisBlock / kLanes];
+    __shared__ double wz[kDisBlock / kLanes];
     const float c = a.c;
     using Stored = typename Row<T>::Stored;
+    const auto power = [&](float below) { return __builtin_amdgcn_exp2f(exponent<T>(below, c, a.c_low, 0.f)); };
     for (uint64_t task = blockIdx.x; task < a.rows * a.splits; task += gridDim.x) {
         const uint64_t row = task / a.splits;
         const uint32_t first = static_cast<uint32_t>(task % a.splits) * a.split_len;
         const uint32_t last = min(a.n, first + a.split_len);
         const Stored *x = static_cast<const Stored *>(a.logits) + row * a.stride;
-        float m = -INFINITY, z = 0.f;
+        float m = -INFINITY;
+        double z = 0;
         if (weight_at(a, row) != 0.f) {
             for (uint32_t lo = first; lo < last; lo += kMapColumns) {
                 const uint32_t hi = min(last, lo + kMapColumns);
@@ -117,14 +173,14 @@ __global__ __launch_bounds__(kDisBlock) void distill_sum_kernel(DisArgs a) {
                     __syncthreads();
                 }
                 const uint32_t vecs = (hi - lo) / kVec;
-                auto take = [&](float f) {
-                    if (f > m) {
-                        z = m == -INFINITY ? z : z * exp2f((m - f) * c);
-                        m = f;
+                const auto raise = [&](float top) {
+                    if (top > m) {
+                        if (m != -INFINITY) z *= power(m - top);
+                        m = top;
                     }
-                    if (f != -INFINITY) z += exp2f((f - m) * c);
                 };
-                // four loads at a time, one largest logit for all of them
+                // four loads at a time, one largest logit for all of them; their
+                // sum alone is in 32 bits
                 constexpr int kBatch = 4;
                 for (uint32_t v = threadIdx.x; v < vecs; v += kBatch * kDisBlock) {
                     u32x4 w[kBatch];
@@ -146,43 +202,38 @@ __global__ __launch_bounds__(kDisBlock) void distill_sum_kernel(DisArgs a) {
                             top = f[u][e] > top ? f[u][e] : top;
                         }
                     }
-                    if (top > m) {
-                        z = m == -INFINITY ? z : z * __builtin_amdgcn_exp2f((m - top) * c);
-                        m = top;
-                    }
+                    raise(top);
                     const float from = m == -INFINITY ? 0.f : m;
+                    float part = 0;
 #pragma unroll
                     for (int u = 0; u < kBatch; ++u)
 #pragma unroll
-                        for (int e = 0; e < kVec; ++e) z += __builtin_amdgcn_exp2f((f[u][e] - from) * c);
+                        for (int e = 0; e < kVec; ++e) part += power(f[u][e] - from);
+                    z += part;
                 }
                 const uint32_t t = vecs * kVec + threadIdx.x;
-                if (t < hi - lo && (!TAIL || !((map[t / 32] >> (t % 32)) & 1))) take(Row<T>::value(x[lo + t]));
+                if (t < hi - lo && (!TAIL || !((map[t / 32] >> (t % 32)) & 1))) {
+                    const float f = Row<T>::value(x[lo + t]);
+                    raise(f);
+                    if (f != -INFINITY) z += power(f - m);
+                }
             }
         }
-        for (int d = kLanes / 2; d > 0; d >>= 1) join(m, z, __shfl_xor(m, d), __shfl_xor(z, d), c);
+        // the threads' sums, relative to the largest logit of all
+        float top = wave_max(m);
         __syncthreads();
-        if (threadIdx.x % kLanes == 0) {
-            wm[threadIdx.x / kLanes] = m;
-            wz[threadIdx.x / kLanes] = z;
-        }
+        if (threadIdx.x % kLanes == 0) wm[threadIdx.x / kLanes] = top;
+        __syncthreads();
+        for (int w = 0; w < kDisBlock / kLanes; ++w) top = fmaxf(top, wm[w]);
+        if (m != -INFINITY) z *= exp2_64((static_cast<double>(m) - top) * factor_of<T>(a));
+        z = wave_sum(z);
+        if (threadIdx.x % kLanes == 0) wz[threadIdx.x / kLanes] = z;
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int w = 1; w < kDisBlock / kLanes; ++w) join(m, z, wm[w], wz[w], c);
-            a.partial[task] = make_float2(m, z);
+            for (int w = 1; w < kDisBlock / kLanes; ++w) z += wz[w];
+            a.partial[task] = Partial{z, top};
         }
     }
-}
-
-// x log2(e) / T less a reference, as an exponent of 2.  In 32-bit rows the
-// rounding of the factor would show, by as much as |x| times its half step.
-template <int T> __device__ inline float exponent(float x, float c, float c_low, float r) {
-    const float e = fmaf(x, c, -r);
-    return T == kRowF32 ? fmaf(x, c_low, e) : e;
-}
-// The factor that exponent() stands for.
-template <int T> __device__ inline double factor_of(const DisArgs &a) {
-    return T == kRowF32 ? static_cast<double>(a.c) + a.c_low : a.c;
 }
 
 // A product rounded by itself, not within a fused difference: where logits are
@@ -238,12 +289,12 @@ __global__ __launch_bounds__(kLanes) void distill_row_kernel(DisArgs a) {
         const bool tail = a.tlse != nullptr;
         // the row's sums
         float m = -INFINITY;
-        for (uint32_t s = lane; s < a.splits; s += kLanes) m = fmaxf(m, a.partial[row * a.splits + s].x);
+        for (uint32_t s = lane; s < a.splits; s += kLanes) m = fmaxf(m, a.partial[row * a.splits + s].m);
         m = wave_max(m);
         double z = 0;
         for (uint32_t s = lane; s < a.splits; s += kLanes) {
-            const float2 p = a.partial[row * a.splits + s];
-            z += p.x == -INFINITY ? p.y : p.y * exp((static_cast<double>(p.x) - m) * inv_t);
+            const Partial p = a.partial[row * a.splits + s];
+            z += p.m == -INFINITY ? p.z : p.z * exp((static_cast<double>(p.m) - m) * inv_t);
         }
         z = wave_sum(z);
         // the counted slots
@@ -397,52 +448,6 @@ __global__ __launch_bounds__(kDisBlock) void distill_grad_kernel(DisArgs a) {
 }
 
 // ---- a whole row in one workgroup's registers ------------------------------
-
-// 2^d of a 64-bit d, to 32 bits.
-__device__ inline double power_of_two(double d) {
-    const double i = rint(d);
-    return ldexp(static_cast<double>(__builtin_amdgcn_exp2f(static_cast<float>(d - i))),
-                 static_cast<int>(fmax(fmin(i, 2000.0), -2000.0)));
-}
-
-// 2^d to about 44 bits: the series of exp on |y| <= ln 2 / 2, cut after
-// y^11 / 11!.  Its coefficients go through scalar registers, made where they
-// are used: in a loop that holds a row they would otherwise be kept in 22
-// vector registers throughout.
-__device__ inline double scalar(double v) {
-    asm volatile("" : "+s"(v));
-    return v;
-}
-constexpr double kLn2 = 0.693147180559945309417;
-__device__ inline double exp2_64(double d) {
-    d = d < -2000.0 ? -2000.0 : d;
-    const double i = rint(d), y = (d - i) * scalar(kLn2);
-    double p = scalar(1.0 / 39916800);
-    p = fma(p, y, scalar(1.0 / 3628800));
-    p = fma(p, y, scalar(1.0 / 362880));
-    p = fma(p, y, scalar(1.0 / 40320));
-    p = fma(p, y, scalar(1.0 / 5040));
-    p = fma(p, y, scalar(1.0 / 720));
-    p = fma(p, y, scalar(1.0 / 120));
-    p = fma(p, y, scalar(1.0 / 24));
-    p = fma(p, y, scalar(1.0 / 6));
-    p = fma(p, y, 0.5);
-    p = fma(p, y, 1.0);
-    p = fma(p, y, 1.0);
-    return ldexp(p, static_cast<int>(fmax(fmin(i, 2000.0), -2000.0)));
-}
-// z 2^d of a d of at most 0, exactly where d is whole.
-__device__ inline double scaled(double z, double d) {
-    if (d == rint(d)) return ldexp(z, static_cast<int>(fmax(d, -4000.0)));
-    return z * exp2_64(d);
-}
-// log2 of a number in the range of 32 bits: the hardware's, and the rest from
-// log(1 + e) = e - e^2 / 2 at e = v 2^-that - 1, below 2^-20.
-__device__ inline double log2_64(double v) {
-    const double y = __builtin_amdgcn_logf(static_cast<float>(v));
-    const double e = v * exp2_64(-y) - 1.0;
-    return y + fma(e * e, -0.5, e) * scalar(1.0 / kLn2);
-}
 
 // LDS of a held row: what is known of the k slots, the partial sums and the
 // bitmap of the columns in S (last).
@@ -833,7 +838,7 @@ DisSpace distill_space(uint64_t rows, uint64_t n, uint64_t k) {
         return at;
     };
     // the same whichever form the rows take
-    w.partial = place(rows * splits * sizeof(float2));
+    w.partial = place(rows * splits * sizeof(Partial));
     w.stats = place(rows * (k + kStats) * sizeof(float));
     w.row_loss = place(rows * sizeof(float));
     return w;
@@ -998,7 +1003,7 @@ int distill_run(const lrs_distill *d, float *loss, float *row_loss, float *stats
             if (overlaps(out[i], bytes[i], out[j], bytes[j])) return LRS_ERR_ALIASING;
     }
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    a.partial = reinterpret_cast<float2 *>(ws + w.partial);
+    a.partial = reinterpret_cast<Partial *>(ws + w.partial);
     const bool held = distill_held(a.n, size);
     a.stats = stats || held ? stats : reinterpret_cast<float *>(ws + w.stats);
     a.row_loss = row_loss ? row_loss : reinterpret_cast<float *>(ws + w.row_loss);
