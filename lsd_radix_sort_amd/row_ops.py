@@ -19,6 +19,7 @@ order, and the code here takes the others and names what is wrong with them.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 import torch
 
@@ -52,13 +53,25 @@ _DTYPES = {torch.float16: _lrs.LRS_DTYPE_FP16, torch.bfloat16: _lrs.LRS_DTYPE_BF
 _ID_BYTES = {torch.int32: 4, torch.int64: 8}
 
 
+def _dtype_code(dtype, name: str) -> int:
+    code = _DTYPES.get(dtype)
+    if code is None:
+        _lrs._bad(f"{name} must be float16, bfloat16 or float32, got {dtype}")
+    return code
+
+
+def _whole(n, name: str) -> int:
+    try:
+        return operator.index(n)
+    except TypeError:
+        _lrs._bad(f"{name} must be a whole number, got {n!r}")
+
+
 def _matrix(x, name: str) -> int:
     """Check a float matrix with contiguous rows; returns its LRS_DTYPE code."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         _lrs._bad(f"{name} must be a GPU tensor")
-    code = _DTYPES.get(x.dtype)
-    if code is None:
-        _lrs._bad(f"{name} must be float16, bfloat16 or float32, got {x.dtype}")
+    code = _dtype_code(x.dtype, name)
     if x.dim() != 2:
         _lrs._bad(f"{name} must be a 2-D tensor")
     if x.stride(1) != 1 and x.size(1) > 1:
@@ -70,7 +83,7 @@ def _matrix(x, name: str) -> int:
 
 def segmented_row_topk_workspace_size(rows: int, n: int, k: int, dtype: torch.dtype = torch.float16,
                                       options: "_lrs.SortOptions | None" = None) -> int:
-    return int(_lrs.load_library().segmented_row_topk_workspace_size(rows, n, k, _DTYPES[dtype],
+    return int(_lrs.load_library().segmented_row_topk_workspace_size(rows, n, k, _dtype_code(dtype, "dtype"),
                                                                      _lrs._opt(options)))
 
 
@@ -79,14 +92,14 @@ def segmented_row_topk(x: torch.Tensor, k: int, descending: bool = True, values_
                        options: "_lrs.SortOptions | None" = None):
     """The k largest (or smallest) elements of every row of a 2-D fp16/bf16/fp32 GPU tensor, in order:
     the first k columns of a stable row sort.  Returns (values, int64 column indices)."""
+    k = _whole(k, "k")
     if values_out is None and indices_out is None and workspace is None and options is None:
-        out = (_fast or _binding()).topk(x, int(k), bool(descending))
+        out = (_fast or _binding()).topk(x, k, bool(descending))
         if out is not None:
             return out
     lib = _lrs.load_library()
     dtype = _matrix(x, "x")
     rows, n = x.shape
-    k = int(k)
     if not 0 <= k <= n:
         _lrs._bad(f"k must be between 0 and the row length {n}, got {k}")
     values_out = _lrs._output(values_out, "values_out", x, shape=(rows, k))
@@ -175,7 +188,8 @@ def _scale(t, device) -> int | None:
 
 def topk_distill_workspace_size(rows: int, n: int, k: int, dtype: torch.dtype = torch.bfloat16,
                                 options: "_lrs.SortOptions | None" = None) -> int:
-    return int(_lrs.load_library().topk_distill_workspace_size(rows, n, k, _DTYPES[dtype], _lrs._opt(options)))
+    return int(_lrs.load_library().topk_distill_workspace_size(rows, n, k, _dtype_code(dtype, "dtype"),
+                                                               _lrs._opt(options)))
 
 
 def _distill_workspace(lib, workspace, d: _Distill, opt, device) -> torch.Tensor:
@@ -287,6 +301,7 @@ def topk_distill_loss(logits: torch.Tensor, teacher_values: torch.Tensor, teache
 # ------------------------------------------ expert counts and balance loss
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
+_MAX_EXPERTS = 4096  # LRS_MAX_EXPERTS
 
 
 def _mask(t, rows: int, device) -> int | None:
@@ -307,6 +322,9 @@ def expert_counts(indices: torch.Tensor, experts: int, row_mask: torch.Tensor | 
         _lrs._bad("indices must be a GPU tensor")
     index_bytes = _ids(indices, "indices", indices.shape[0] if indices.dim() else 0, indices.device)
     rows, k = indices.shape
+    experts = _whole(experts, "experts")
+    if not 1 <= experts <= _MAX_EXPERTS:
+        _lrs._bad(f"experts must be between 1 and {_MAX_EXPERTS}, got {experts}")
     both = torch.empty(experts + 1, dtype=torch.int32, device=indices.device)
     at = both.data_ptr()
     _lrs._check(lib.expert_counts(indices.data_ptr(), indices.stride(0), index_bytes,
@@ -328,7 +346,7 @@ def _balance(logits, counts, rows_counted, balance_weight, z_weight, score, row_
     if score not in _SCORES:
         _lrs._bad(f"score must be one of {sorted(_SCORES)}")
     for t, name, size in ((counts, "counts", experts), (rows_counted, "rows_counted", 1)):
-        if t is None and size == 1:
+        if t is None and name == "rows_counted":
             continue
         _lrs._same_device(t, name, device)
         if t.dtype != torch.int32 or t.shape != (size,) or not t.is_contiguous():
