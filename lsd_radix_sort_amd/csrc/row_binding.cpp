@@ -220,7 +220,7 @@ py::object distill_loss(py::handle logits, py::handle values, py::handle indices
     Distill c;
     if (!c.take_all(logits, values, indices, lse, weights) || !c.fill(temperature) || c.d.k < 1 || c.d.k > LRS_MAX_TOPK ||
         !(temperature > 0) || !std::isfinite(temperature) || !std::isfinite(static_cast<float>(1.44269504088896340736 / temperature)) ||
-        c.d.n > LRS_MAX_ROW_LEN)
+        c.d.n > LRS_MAX_ROW_LEN || c.d.rows >= (int64_t(1) << 40) / std::max<int64_t>(1, c.d.n))
         return py::none();
     return py::cast(DistillLoss::apply(c.logits, c.values, c.indices, temperature, maybe(c.lse), maybe(c.weights)));
 }

@@ -35,6 +35,17 @@ def test_k_is_a_whole_number():
     assert lrs.segmented_row_topk(x, torch.tensor(2))[0].shape == (3, 2)
 
 
+def test_too_many_elements():
+    # rows of one element each that all lie at the same place: 2^25 rows of 65536 make 2^41
+    rows, n = 1 << 25, 65_536
+    logits = torch.zeros(1, n, dtype=torch.float16, device="cuda").expand(rows, n)
+    values = torch.zeros(1, 1, device="cuda").expand(rows, 1)
+    ids = torch.zeros(1, 1, dtype=torch.int64, device="cuda").expand(rows, 1)
+    for call in (lrs.topk_distill_loss, lrs.topk_distill_forward):
+        with pytest.raises(lrs.RadixSortArgumentError):
+            call(logits, values, ids)
+
+
 def test_workspace_size_of_an_unknown_type():
     for size in (lrs.segmented_row_topk_workspace_size, lrs.topk_distill_workspace_size):
         with pytest.raises(lrs.RadixSortArgumentError, match="float16"):
