@@ -322,3 +322,25 @@ def test_temperature_refusals():
             with pytest.raises(ValueError):
                 call(s, t, i, temperature)
         call(s, t, i, 5e-39)
+
+
+@pytest.mark.parametrize("n", [300, 70_001])
+@pytest.mark.parametrize("tail", [False, True])
+def test_temperature_has_64_bits(n, tail):
+    """Losses just below 2048, whose rounding is half that of an inverse temperature in 32 bits."""
+    inverse = 1 + 1.02 * 2.0 ** -24  # 32 bits would hold 1 + 2^-23
+    rows = 256
+    g = torch.Generator().manual_seed(90)
+    s = torch.full((rows, n), -3000.0)
+    s[:, 0] = 0.0
+    s[:, 5] = -2047 + 7 * torch.rand(rows, generator=g)
+    t, i = torch.ones(rows, 1), torch.full((rows, 1), 5)
+    tlse = torch.full((rows,), float(inverse)) if tail else None  # what its own rounding leaves over is a tail of 2^-24
+    want, size, _, _, _ = distill_oracle(s, t, i, 1 / inverse, tlse)
+    _, row_loss, _ = lrs.topk_distill_forward(s.cuda(), t.cuda(), i.cuda(), 1 / inverse, None if tlse is None else tlse.cuda())
+    assert bool((want < 2048).all()) and bool((want > 2039).all())
+    # rounded once; half a step below 2048 is 2^-14
+    off = (row_loss.cpu().double() - want).abs()
+    assert bool((off <= 2.0 ** -14 + 8 * ULP).all()), float(off.max())
+    wrong = distill_oracle(s, t, i, 1 / (1 + 2.0 ** -23), tlse)[0]
+    assert bool(((row_loss.cpu().double() - wrong).abs() > 2.0 ** -14 + 8 * ULP).any())
