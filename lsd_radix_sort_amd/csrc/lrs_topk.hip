@@ -920,7 +920,7 @@ __global__ __launch_bounds__(kMergeBlock) void topk_merge_kernel(TopArgs a) {
     __shared__ int tops[B / kLanes];
     __shared__ uint32_t cells[B / kLanes];
     __shared__ uint32_t count;
-    const uint64_t row = blockIdx.x;
+    const uint64_t row = a.first_task + blockIdx.x;
     const uint32_t tid = threadIdx.x, total = a.splits * a.k;  // at most kTopBuffer
     const uint64_t *in = a.words + row * total;
     uint64_t w[V];
@@ -1110,9 +1110,10 @@ int segmented_row_topk(const void *x, int64_t row_stride, void *vals_out, int64_
             launch_on(topk_kernel<4>, grid, dim3(kTopBlock), t.L, a);
         if (hipGetLastError() != hipSuccess) return LRS_ERR_HIP;
     }
-    if (a.splits > 1) {
+    // a launch of 2^32 threads or more would wrap without an error
+    for (a.first_task = 0; a.splits > 1 && a.first_task < R; a.first_task += kMaxGrid) {
         TimedLaunch t(4, c);
-        const dim3 merge(static_cast<uint32_t>(R));
+        const dim3 merge(static_cast<uint32_t>(std::min<uint64_t>(R - a.first_task, kMaxGrid)));
         if (size == 2)
             launch_on(topk_merge_kernel<2>, merge, dim3(kMergeBlock), t.L, a);
         else

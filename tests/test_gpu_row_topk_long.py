@@ -63,3 +63,14 @@ def test_many_rows_of_the_largest_workgroups(dtype, kind, k):
     rows, n = 258, 66_001 if dtype == "bf16" else 33_001
     log(f"topk many {dtype} {kind} {rows}x{n} k={k}")
     check(make_bits(kind, rows, n, dtype, 600), dtype, k, True, pad=1)
+
+
+def test_more_shared_rows_than_one_launch_joins():
+    """2^22 rows and more, each shared: one row of 256 KB and 4 bytes, seen that often."""
+    n, rows = 65_537, (1 << 22) + 3
+    x = torch.randn(n, generator=torch.Generator().manual_seed(7)).cuda()
+    log(f"topk {rows} shared rows")
+    values, indices = lrs.segmented_row_topk(x.expand(rows, n), 1)
+    best = x.argmax()
+    torch.cuda.synchronize()
+    assert bool((indices == best).all()) and bool((values == x[best]).all())
