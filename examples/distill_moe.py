@@ -33,6 +33,7 @@ class Student(torch.nn.Module):
     def forward(self, x):
         scores = self.router(x)
         _, experts = lrs.segmented_row_topk(scores.detach(), CHOSEN)
+        # its values carry no gradient; the scores gathered at the chosen experts do
         share = torch.softmax(torch.gather(scores, 1, experts), dim=1)
         y = x
         for e in range(EXPERTS):

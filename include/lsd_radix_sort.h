@@ -244,7 +244,9 @@ int segmented_row_sort(const uint16_t *vals_in, uint16_t *vals_out, int64_t *idx
  *   rows == 0 or k == 0 is a no-op.
  * Rows of more than 256 KB are shared among workgroups and need
  * segmented_row_topk_workspace_size bytes; others need none (the size is 0 and
- * workspace may be NULL).  Only opts->timer is used (kind 4).
+ * workspace may be NULL).  Only opts->timer is used (kind 4).  The values are
+ * copies of x's patterns; a program that differentiates through them gathers x
+ * at idx_out itself.
  */
 #define LRS_MAX_TOPK 1024
 size_t segmented_row_topk_workspace_size(int64_t rows, int64_t n, int64_t k, int dtype, const lrs_options *opts);

@@ -35,6 +35,10 @@ struct CountArgs {
     uint32_t k, experts;
 };
 
+// The counts alone, for a program that adds them up over ranks: a clearing
+// launch, then histograms in LDS that go out by atomics.  524288 ids of 256
+// experts 10.2 us (floor 0.7), 128 ids of 64 3.6 us: bound by the two launches
+// and a load, a division and an LDS add one after the other for each id.
 __global__ __launch_bounds__(kBalBlock) void count_clear_kernel(CountArgs a) {
     for (uint32_t e = threadIdx.x; e < a.experts; e += kBalBlock) a.counts[e] = 0;
     if (threadIdx.x == 0 && a.kept) *a.kept = 0;

@@ -137,9 +137,11 @@ __device__ inline double log2_64(double v) {
 // ---- rows over 256 KB ------------------------------------------------------
 //
 // A row's sum, its stats and its gradient are three launches: the row is read
-// twice (1024 x 131072 fp32 step: 353 us, forward with a tail 124 us = 4.3 TB/s).
-// The gradient is also the backward of every length: 515 x 32768 fp32 in 22 us
-// = 6.0 TB/s, the rate of a copy.
+// twice (1024 x 131072 fp32 step: 340 us, forward with a tail 112 us = 4.8 TB/s;
+// 400 x 262144 bf16: 145 and 56 us = 3.7 TB/s, as an element takes the
+// instructions of a 32-bit one at half the bytes).  The gradient is also the
+// backward of every length: 515 x 32768 fp32 in 23 us = 5.8 TB/s, near the rate
+// of a copy.
 
 // One workgroup: the largest logit and the sum of exponentials of a piece of a row.
 template <int T, bool TAIL>
@@ -466,11 +468,11 @@ struct HeldLds {
 // to 32 bits, everywhere the same c, and references to them are whole numbers R: the sums of
 // 2^(x c - R) of two waves join exactly, and log2 sum 2^(x c) = R + log2(sum).
 //
-// Bound by HBM where rows are long and many: 4096 x 131072 bf16 step 418 us = 5.1
+// Bound by HBM where rows are long and many: 4096 x 131072 bf16 step 421 us = 5.1
 // TB/s, where a copy of the rows in the same form takes 367 us; the rest is the
 // chain from the last load to the first store (joins, the teacher's terms in 64
 // bits by one wave, the factor), which a second row on the CU would hide and two
-// rows of 256 KB do not fit.  1031 x 50021 fp16 step with a tail 49 us, forward
+// rows of 256 KB do not fit.  1031 x 50021 fp16 step with a tail 50 us, forward
 // 1024 x 65536 fp16 with a tail 27 us = 4.9 TB/s (32 us when it stayed in
 // registers).  Keeping only the first loads with a gradient, too, and reading
 // the rest again costs 0 to 18%.
@@ -936,7 +938,7 @@ template <int T> void distill_launch_held(const DisArgs &a, uint32_t rows, const
         return go(distill_held_kernel<T, 1024, 16, true>, distill_held_kernel<T, 1024, 16, false>, 1024);
     }
     // a wave for up to 8 KB, so that many short rows' chains run side by side
-    // (8192 x 600 bf16 step: 21 us, 36 us by workgroups of 256)
+    // (8192 x 600 bf16 step: 20 us, 36 us by workgroups of 256)
     if (vecs <= 64 * 4) return go(distill_held_kernel<T, 64, 4, true>, distill_held_kernel<T, 64, 4, false>, 64);
     if (vecs <= 64 * 8) return go(distill_held_kernel<T, 64, 8, true>, distill_held_kernel<T, 64, 8, false>, 64);
     if (vecs <= 128 * 8) return go(distill_held_kernel<T, 128, 8, true>, distill_held_kernel<T, 128, 8, false>, 128);

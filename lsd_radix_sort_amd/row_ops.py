@@ -91,7 +91,9 @@ def segmented_row_topk(x: torch.Tensor, k: int, descending: bool = True, values_
                        indices_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                        options: "_lrs.SortOptions | None" = None):
     """The k largest (or smallest) elements of every row of a 2-D fp16/bf16/fp32 GPU tensor, in order:
-    the first k columns of a stable row sort.  Returns (values, int64 column indices)."""
+    the first k columns of a stable row sort.  Returns (values, int64 column indices).
+
+    Under autograd the values carry no gradient: torch.gather(x, 1, indices) are the same values with one."""
     k = _whole(k, "k")
     if values_out is None and indices_out is None and workspace is None and options is None:
         out = (_fast or _binding()).topk(x, k, bool(descending))
