@@ -358,6 +358,101 @@ int expert_balance_step(const void *logits, int64_t row_stride, const void *indi
                         const lrs_options *opts);
 
 /*
+ * Embedding lookup, and the gradient of its table by sorted tokens.
+ *   forward    out[t] = scale * weight[id_t] for token t, 0 where id_t is
+ *              outside [0, vocab) (places that another rank or encoder fills)
+ *   backward   grad_weight[v] = scale * sum of grad[t] over the tokens t with
+ *              id_t = v, rows of no token 0; with accumulate nonzero that sum is
+ *              added to what grad_weight holds, and rows of no token stay as
+ *              they are.  Ids outside [0, vocab) and ids equal to padding_index
+ *              (-1: none) count for nothing.
+ * Sums are in 32 bits or more, in an order that the tokens alone decide (by
+ * radix_sort_pairs of ids and places), so equal calls give equal bits; each
+ * result is rounded to its type once.
+ *   tokens       ids of `lines` lines of `length` tokens, line i at element
+ *                i * stride; token t is number t in that order
+ *   weight       vocab x width, row v at element v * weight_stride
+ *   out, grad    tokens x width, row t at element t * out_stride (grad_stride)
+ *   grad_weight  vocab x width, row v at element v * weight_stride
+ *   dtype        LRS_DTYPE_* of weight (forward), of grad (backward)
+ *   out_dtype    LRS_DTYPE_* of out (forward), of grad_weight (backward)
+ * Strides are at least 0, of outputs with more than one row at least width.
+ * lines * length < 2^31; 0 <= vocab < 2^31; width <= LRS_MAX_ROW_LEN; tokens *
+ * width and vocab * width below 2^40; scale finite (else LRS_ERR_OPTION).
+ * No tokens: the forward does nothing, the backward clears or keeps
+ * grad_weight.  opts goes to the sort as well; the operators' own kernels use
+ * only opts->timer (kind 4).
+ */
+typedef struct lrs_token_ids {
+    const void *ids;  /* int32 or int64 */
+    int64_t lines, length, stride;
+    int id_bytes;     /* 4 or 8 */
+} lrs_token_ids;
+
+int embedding_forward(const void *weight, int64_t weight_stride, const lrs_token_ids *tokens, void *out,
+                      int64_t out_stride, int64_t vocab, int64_t width, int dtype, int out_dtype, float scale,
+                      void *stream, const lrs_options *opts);
+size_t embedding_backward_workspace_size(int64_t tokens, int64_t vocab, int64_t width, const lrs_options *opts);
+int embedding_backward(const void *grad, int64_t grad_stride, const lrs_token_ids *tokens, void *grad_weight,
+                       int64_t weight_stride, int64_t vocab, int64_t width, int dtype, int out_dtype, float scale,
+                       int64_t padding_index, int accumulate, void *workspace, size_t workspace_bytes, void *stream,
+                       const lrs_options *opts);
+
+/*
+ * Log probabilities of given tokens.  With z = logits / temperature and p =
+ * softmax(z) over a row of n logits and t the row's token:
+ *   logprobs  [rows] f32   log p_t; 0 where t is outside [0, n) (no token)
+ *   entropy   [rows] f32   - sum p log p, 0 log 0 = 0
+ *   ranks     [rows] i32   the token's place in the row's descending stable sort
+ *                          (ordered as segmented_row_topk orders); -1 without one
+ *   top_indices   [rows][k] i64  the first k columns of that sort
+ *   top_logprobs  [rows][k] f32  their log p
+ *   row_stats     [rows][3] f32  written by the forward for the backward of the
+ *                          same inputs (its contents are the library's)
+ * and in the backward, for derivatives a = logprob_grad[r] (0 without a token)
+ * and b = entropy_grad[r] of a loss (either array may be NULL: 0; not both),
+ *   grad_j = (a ([j = t] - p_j) - b p_j (log p_j + entropy)) / temperature
+ * in the logits' type, row r at r * grad_stride (grad_stride >= n).
+ * token_logprobs_step is forward and backward in one call, for programs that
+ * know a and b beforehand.
+ * A row whose row_mask byte is 0 is left out: logprob, entropy and gradient 0
+ * whatever it holds (row_mask NULL: every row counts); token_logprobs_topk
+ * takes no mask.  A row with a = b = 0 has gradient 0 whatever it holds.  Rows
+ * that are all -inf have log p = -inf, entropy 0 and gradient 0; in others a
+ * token of logit -inf has log p = -inf.  NaN and +inf logits give NaN (not in
+ * ranks and top_indices, which go by the patterns).
+ * n <= LRS_MAX_ROW_LEN; rows * n < 2^40; 0 <= k <= n, k <= LRS_MAX_TOPK; tokens
+ * are int32 or int64, row r's at element r * token_stride; temperature above 0
+ * and finite, log2(e) / temperature finite in 32 bits (else LRS_ERR_OPTION).
+ * Results do not depend on the order in which workgroups run.  Only
+ * opts->timer is used (kind 4).
+ */
+typedef struct lrs_logprobs {
+    const void *logits;       /* rows x n, row r at element r * row_stride */
+    int64_t row_stride;
+    const void *tokens;       /* [rows], row r's at element r * token_stride */
+    int64_t token_stride;
+    int token_bytes;          /* 4 or 8 */
+    int dtype;                /* of the logits and the gradient: LRS_DTYPE_* */
+    const uint8_t *row_mask;  /* [rows], or NULL */
+    int64_t rows, n;
+    double temperature;
+} lrs_logprobs;
+
+size_t token_logprobs_workspace_size(int64_t rows, int64_t n, int64_t k, int dtype, const lrs_options *opts);
+int token_logprobs_forward(const lrs_logprobs *in, float *logprobs, float *entropy, float *row_stats, void *workspace,
+                           size_t workspace_bytes, void *stream, const lrs_options *opts);
+int token_logprobs_topk(const lrs_logprobs *in, int64_t k, float *logprobs, float *entropy, int32_t *ranks,
+                        float *top_logprobs, int64_t *top_indices, void *workspace, size_t workspace_bytes, void *stream,
+                        const lrs_options *opts);
+int token_logprobs_backward(const lrs_logprobs *in, const float *row_stats, const float *logprob_grad,
+                            const float *entropy_grad, void *grad, int64_t grad_stride, void *stream,
+                            const lrs_options *opts);
+int token_logprobs_step(const lrs_logprobs *in, const float *logprob_grad, const float *entropy_grad, float *logprobs,
+                        float *entropy, void *grad, int64_t grad_stride, void *workspace, size_t workspace_bytes,
+                        void *stream, const lrs_options *opts);
+
+/*
  * The per-pass digit counts of radix_sort_keys' first kernel: all passes'
  * histograms from one read of the keys (FlagTree PR #1084, step 2 "Before":
  * one kernel counts every pass).  hist_out[p * 2^b + d] = number of keys

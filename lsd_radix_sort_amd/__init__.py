@@ -119,6 +119,14 @@ def load_library():
         "expert_balance_step_workspace_size": ([i64, i64, i64, O], szt),
         "expert_balance_step": ([P, i64, P, i64, c_int, P, i64, i64, i64, c_int, c_int, F, F, P, P, P, P, i64, P, szt, P, O],
                                 c_int),
+        "embedding_forward": ([P, i64, P, P, i64, i64, i64, c_int, c_int, F, P, O], c_int),
+        "embedding_backward_workspace_size": ([i64, i64, i64, O], szt),
+        "embedding_backward": ([P, i64, P, P, i64, i64, i64, c_int, c_int, F, i64, c_int, P, szt, P, O], c_int),
+        "token_logprobs_workspace_size": ([i64, i64, i64, c_int, O], szt),
+        "token_logprobs_forward": ([P, P, P, P, P, szt, P, O], c_int),
+        "token_logprobs_topk": ([P, i64, P, P, P, P, P, P, szt, P, O], c_int),
+        "token_logprobs_backward": ([P, P, P, P, P, i64, P, O], c_int),
+        "token_logprobs_step": ([P, P, P, P, P, P, i64, P, szt, P, O], c_int),
         "radix_sort_status_string": ([c_int], ctypes.c_char_p),
     }
     for name, (args, res) in sigs.items():
@@ -556,3 +564,6 @@ from .row_ops import (  # noqa: E402
     expert_balance_backward, expert_balance_forward, expert_balance_loss, expert_balance_step,
     expert_balance_step_workspace_size, expert_balance_workspace_size, expert_counts, segmented_row_topk, segmented_row_topk_workspace_size,
     topk_distill_backward, topk_distill_forward, topk_distill_loss, topk_distill_step, topk_distill_workspace_size)
+from .vocab_ops import (  # noqa: E402
+    embedding_backward, embedding_backward_workspace_size, embedding_forward, embedding_lookup, token_logprobs,
+    token_logprobs_backward, token_logprobs_forward, token_logprobs_step, token_logprobs_topk, token_logprobs_workspace_size)
