@@ -95,16 +95,24 @@ __global__ __launch_bounds__(kEmbBlock) void lookup_kernel(LookupArgs a) {
 
 // ---------------------------------------------------------------- gradient
 //
-// After the sort the tokens of an id are neighbours, so the gradient is three
-// kinds of work, one launch for all: the sums of ids with few tokens, the sums
-// of those with many, and the rows of ids with none, which are cleared.  Text
-// has a few ids that make up a large share of it, so no wave sums more than
-// some 2 kRun rows: an id with a whole aligned run of kRun places is `long`, its
-// whole runs are summed by a wave each beforehand (in 32 bits, by place), and a
-// workgroup adds those and what is left at both ends.
+// After the sort the tokens of an id are neighbours.  Text has a few ids that
+// make up a large share of it, and most ids in none, so the work is cut into
+// even pieces: a wave takes a run of kRun sorted places, and of each id that
+// begins there all places, at most 2 kRun - 2, unless the id has an aligned run
+// to itself.  Such an id is long: every wave adds up what its own run holds of
+// it, and a second launch joins those sums.  The rows of ids without tokens are
+// cleared in the first launch, in turns with the sums, since sums wait for their
+// reads and clearing only writes.
 
-constexpr uint32_t kRun = 32;
-constexpr uint32_t kNoKey = ~0u;
+constexpr uint32_t kRun = 16;
+constexpr int kJoinBlock = 1024;
+
+// A long id: the first of its whole runs, how many there are, and whether the
+// runs before and after them hold places of it.
+struct Long {
+    uint32_t run, runs, key;
+    uint16_t before, after;
+};
 
 struct GradArgs {
     const void *grad;
@@ -118,245 +126,338 @@ struct GradArgs {
     int accumulate;
     uint32_t *keys, *places;              // unsorted
     const uint32_t *sorted, *order;       // the sorted keys and their places
-    uint32_t *present;                    // a bit for every id, set where a token names it
-    uint32_t *longs;                      // how many ids are long, then the first whole run of each
-    float *runs;                          // [tokens / kRun][width]: sums of whole runs
+    uint32_t *long_count;
+    Long *longs;
+    float *parts;                         // [2][runs][pieces][lanes * 8]: see part_of
+    uint32_t runs;                        // of kRun places, the last one maybe fewer
     uint32_t pieces;                      // of a row, a group of lanes each
-    uint32_t chunk;                       // sorted places whose ids one group sums
-    uint32_t long_blocks, few_blocks;     // of the sums' launch; the others clear rows
+    uint32_t sum_blocks, clear_turns;     // blocks that sum, and how many clear after each of them
 };
 
 // The keys of the sort: ids, those that count for nothing behind the last.
 __global__ __launch_bounds__(kEmbBlock) void embed_keys_kernel(GradArgs a) {
     const uint32_t t = blockIdx.x * kEmbBlock + threadIdx.x;
-    if (t == 0) a.longs[0] = 0;
-    if (!a.accumulate)
-        for (uint32_t w = t; w < (a.vocab + 31) / 32; w += gridDim.x * kEmbBlock) a.present[w] = 0;
+    if (t == 0) *a.long_count = 0;
     if (t >= a.tokens) return;
     const int64_t id = a.ids[t];
     a.keys[t] = id >= 0 && id < a.vocab && id != a.padding ? static_cast<uint32_t>(id) : a.vocab;
     a.places[t] = t;
 }
 
-// What a lane holds of a row: eight columns, fewer at the row's end.
-struct Columns {
-    uint32_t first, count;
-    __device__ Columns(uint32_t piece, uint32_t lanes, uint32_t lane, uint32_t width) {
-        first = (piece * lanes + lane) * 8;
-        count = first < width ? min(width - first, 8u) : 0;
+// What a lane holds of a piece of a row: eight neighbouring columns, or, where
+// one of the types has 32 bits, two fours that lie apart, so that the lanes of a
+// store lie side by side in each type (32-byte steps cost 2.8 times as much).
+template <int LANES, bool FOURS> struct Columns {
+    static constexpr int kParts = FOURS ? 2 : 1, kSize = 8 / kParts;
+    uint32_t first[kParts], count[kParts];
+    __device__ Columns(uint32_t piece, uint32_t width) {
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
+            first[p] = piece * LANES * 8 + p * LANES * kSize + threadIdx.x % LANES * kSize;
+            count[p] = first[p] < width ? min(width - first[p], static_cast<uint32_t>(kSize)) : 0;
+        }
     }
 };
-template <int T> __device__ inline void load_columns(const void *rows, uint64_t row, Columns c, float (&f)[8]) {
-    if (c.count == 8) {
-        load8<T>(rows, row + c.first, f);
-    } else {
-        const auto *p = static_cast<const typename Row<T>::Stored *>(rows) + row + c.first;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_align2 __attribute__((aligned(2)));
+
+// Those columns of one row as they are stored.
+template <int T, int LANES, bool FOURS> struct Eight {
+    using At = Columns<LANES, FOURS>;
+    static constexpr int kWords = T == kRowF32 ? 8 : 4, kEach = kWords / At::kParts;
+    uint32_t w[kWords];
+    __device__ void load(const void *rows, uint64_t row, const At &c) {
 #pragma unroll
-        for (uint32_t e = 0; e < 8; ++e) f[e] = e < c.count ? Row<T>::value(p[e]) : 0.f;
+        for (int p = 0; p < At::kParts; ++p) {
+            const auto *x = static_cast<const typename Row<T>::Stored *>(rows) + row + c.first[p];
+            uint32_t *v = w + p * kEach;
+            if (c.count[p] == At::kSize) {
+                if constexpr (kEach == 4) {
+                    const u32x4 q = load16_once(x);
+                    for (int i = 0; i < 4; ++i) v[i] = q[i];
+                } else {
+                    static_assert(kEach == 2);
+                    const u32x2 q = __builtin_nontemporal_load(reinterpret_cast<const u32x2_align2 *>(x));
+                    v[0] = q.x;
+                    v[1] = q.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) v[i] = 0;
+#pragma unroll
+                for (uint32_t e = 0; e < At::kSize; ++e) {
+                    const uint32_t q = e < c.count[p] ? x[e] : 0;
+                    if constexpr (T == kRowF32) v[e] = q;
+                    else v[e / 2] |= q << (16 * (e & 1));
+                }
+            }
+        }
     }
-}
-// A finished sum to the table's gradient.
-template <int O> __device__ inline void put_row(const GradArgs &a, uint32_t id, Columns c, const float (&sum)[8]) {
-    const uint64_t row = id * a.out_stride;
+    __device__ void values(float (&f)[8]) const {
+        if constexpr (T == kRowF32) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __builtin_bit_cast(float, w[e]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) Row<T>::unpack(w[i], f[2 * i], f[2 * i + 1]);
+        }
+    }
+    __device__ void add_to(float (&sum)[8]) const {
+        float f[8];
+        values(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += f[e];
+    }
+    __device__ static void store(void *rows, uint64_t row, const At &c, const float (&f)[8]) {
+#pragma unroll
+        for (int p = 0; p < At::kParts; ++p) {
+            auto *x = static_cast<typename Row<T>::Stored *>(rows) + row + c.first[p];
+            const float *g = f + p * At::kSize;
+            if (c.count[p] == At::kSize) {
+                if constexpr (T == kRowF32) {
+                    store16_once(x, u32x4{__builtin_bit_cast(uint32_t, g[0]), __builtin_bit_cast(uint32_t, g[1]),
+                                          __builtin_bit_cast(uint32_t, g[2]), __builtin_bit_cast(uint32_t, g[3])});
+                } else if constexpr (FOURS) {
+                    __builtin_nontemporal_store(u32x2{Row<T>::pack(g[0], g[1]), Row<T>::pack(g[2], g[3])},
+                                                reinterpret_cast<u32x2_align2 *>(x));
+                } else {
+                    store16_once(x, u32x4{Row<T>::pack(g[0], g[1]), Row<T>::pack(g[2], g[3]), Row<T>::pack(g[4], g[5]),
+                                          Row<T>::pack(g[6], g[7])});
+                }
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < At::kSize; ++e)
+                    if (e < c.count[p]) x[e] = Row<T>::pattern(g[e]);
+            }
+        }
+    }
+};
+
+// A finished sum to the table's gradient, on top of what that holds or not.
+template <int O, int LANES, bool FOURS, bool ADD>
+__device__ inline void put_row(const GradArgs &a, uint32_t id, const Columns<LANES, FOURS> &c, const float (&sum)[8],
+                               const Eight<O, LANES, FOURS> &old) {
     float f[8] = {};
-    if (a.accumulate) load_columns<O>(a.out, row, c, f);
+    if (ADD) old.values(f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = a.accumulate ? fmaf(sum[e], a.scale, f[e]) : sum[e] * a.scale;
-    if (c.count == 8) {
-        store8<O>(a.out, row + c.first, f);
-    } else {
-        auto *p = static_cast<typename Row<O>::Stored *>(a.out) + row + c.first;
-#pragma unroll
-        for (uint32_t e = 0; e < 8; ++e)
-            if (e < c.count) p[e] = Row<O>::pattern(f[e]);
-    }
-}
-template <int LANES> __device__ inline uint32_t uniform(uint32_t v) {
-    return LANES == kLanes ? __builtin_amdgcn_readfirstlane(v) : v;
+    for (int e = 0; e < 8; ++e) f[e] = ADD ? fmaf(sum[e], a.scale, f[e]) : sum[e] * a.scale;
+    Eight<O, LANES, FOURS>::store(a.out, id * a.out_stride, c, f);
 }
 
-// Marks the ids that tokens name, lists the long ones and sums their whole runs.
-template <int T, int LANES>
-__global__ __launch_bounds__(kEmbBlock) void embed_runs_kernel(GradArgs a) {
-    constexpr uint32_t kGroups = kEmbBlock / LANES;
-    const uint32_t marking = (a.tokens + kEmbBlock - 1) / kEmbBlock, runs = a.tokens / kRun;
-    if (blockIdx.x < marking) {
-        const uint32_t i = blockIdx.x * kEmbBlock + threadIdx.x;
-        if (i >= a.tokens) return;
-        const uint32_t key = a.sorted[i];
-        if (key >= a.vocab) return;
-        if (!a.accumulate && (i == 0 || a.sorted[i - 1] != key)) atomicOr(&a.present[key / 32], 1u << (key % 32));
-        if (i % kRun == 0 && i + kRun <= a.tokens && a.sorted[i + kRun - 1] == key && (i == 0 || a.sorted[i - kRun] != key))
-            a.longs[1 + atomicAdd(&a.longs[0], 1u)] = i / kRun;
-        return;
-    }
-    const uint64_t tasks = static_cast<uint64_t>(runs) * a.pieces, groups = static_cast<uint64_t>(gridDim.x - marking) * kGroups;
-    for (uint64_t task = static_cast<uint64_t>(blockIdx.x - marking) * kGroups + threadIdx.x / LANES; task < tasks; task += groups) {
-        const uint32_t run = uniform<LANES>(static_cast<uint32_t>(task / a.pieces)), piece = uniform<LANES>(static_cast<uint32_t>(task % a.pieces));
-        const uint32_t *key = a.sorted + static_cast<uint64_t>(run) * kRun, *order = a.order + static_cast<uint64_t>(run) * kRun;
-        if (key[0] != key[kRun - 1] || key[0] >= a.vocab) continue;
-        const Columns c(piece, LANES, threadIdx.x % LANES, a.width);
-        constexpr uint32_t kAtOnce = T == kRowF32 ? 8 : 16;
-        float sum[8] = {};
-#pragma unroll 1
-        for (uint32_t i = 0; i < kRun; i += kAtOnce) {
-            float f[kAtOnce][8];
-#pragma unroll
-            for (uint32_t j = 0; j < kAtOnce; ++j) load_columns<T>(a.grad, order[i + j] * a.grad_stride, c, f[j]);
-#pragma unroll
-            for (uint32_t j = 0; j < kAtOnce; ++j)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum[e] += f[j][e];
-        }
-        float *out = a.runs + static_cast<uint64_t>(run) * a.width + c.first;
-#pragma unroll
-        for (uint32_t e = 0; e < 8; ++e)
-            if (e < c.count) out[e] = sum[e];
-    }
+// Where a run's sum of a long id is kept: one place for the id that begins in
+// an earlier run or has the whole one, one for the id that begins within.
+template <int LANES> __device__ inline float *part_of(const GradArgs &a, uint32_t begins, uint32_t run, uint32_t piece) {
+    return a.parts + ((static_cast<uint64_t>(begins) * a.runs + run) * a.pieces + piece) * (LANES * 8) + threadIdx.x % LANES * 4;
 }
 
-// The long id `which`: a workgroup, whose groups take the whole runs in equal
-// shares, the first one also the places before them, the last one those after.
-template <int T, int O, int LANES> __device__ void sum_long(const GradArgs &a, uint32_t which, uint32_t piece) {
-    constexpr uint32_t kGroups = kEmbBlock / LANES;
-    __shared__ float parts[kGroups][LANES * 8];
-    const uint32_t lane = threadIdx.x % kLanes, group = threadIdx.x / LANES;
-    const uint32_t first = __builtin_amdgcn_readfirstlane(a.longs[1 + which]), key = a.sorted[first * kRun];
-    const Columns c(piece, LANES, threadIdx.x % LANES, a.width);
-    uint32_t runs = 1;  // whole ones
-    for (;;) {
-        const uint64_t end = (static_cast<uint64_t>(first) + runs + lane + 1) * kRun;
-        const uint64_t same = __ballot(end <= a.tokens && a.sorted[end - 1] == key);
-        const uint32_t more = same == ~uint64_t(0) ? kLanes : __builtin_ctzll(~same);
-        runs += more;
-        if (more < kLanes) break;
-    }
-    const uint32_t from = first * kRun, to = from + runs * kRun;
-    const uint32_t before = __popcll(__ballot(lane < kRun && from > lane && a.sorted[from - 1 - lane] == key));
-    const uint32_t after = __popcll(__ballot(lane < kRun && a.tokens - to > lane && a.sorted[to + lane] == key));
-    float sum[8] = {};
-    const auto add_rows = [&](uint32_t i, uint32_t end) {
-        for (; i < end; i += 4) {
-            float f[4][8];
-#pragma unroll
-            for (uint32_t j = 0; j < 4; ++j)
-                if (i + j < end) load_columns<T>(a.grad, a.order[i + j] * a.grad_stride, c, f[j]);
-#pragma unroll
-            for (uint32_t j = 0; j < 4; ++j)
-                if (i + j < end)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sum[e] += f[j][e];
-        }
+// The ids of a run.  A wave looks at 64 places at once, from the one before the
+// run on; its groups of lanes take an equal share of the beginnings each, the
+// first one also the id that continues.  Rows are on their way several at a
+// time, whatever ids they are of.
+template <int T, int O, int LANES, bool ADD> __device__ void sum_run(const GradArgs &a, uint32_t run, uint32_t piece) {
+    constexpr bool kFours = T == kRowF32 || O == kRowF32;
+    constexpr uint32_t kGroups = kLanes / LANES, kShare = kRun / kGroups, kLast = kRun;  // kLast: the lane of the run's last place
+    static_assert(3 * kRun - 1 < kLanes, "an id that is not long ends among the places looked at");
+    const uint32_t lane = threadIdx.x % kLanes, begin = run * kRun;
+    const uint64_t place = static_cast<uint64_t>(begin) + lane - 1;  // of this lane
+    const bool real = place < a.tokens;                            // not before the first either
+    const uint32_t key = real ? a.sorted[place] : a.vocab, order = real ? a.order[place] : 0;
+    const uint32_t back = run > 0 ? a.sorted[begin - kRun] : a.vocab;
+    const uint32_t left = __builtin_amdgcn_update_dpp(~0u, key, 0x138, 0xF, 0xF, false);  // wave_shr:1
+    // bit l: the place of lane l begins an id; past the last token, and where ids count for nothing, every place does
+    const uint64_t heads = __ballot(lane > 0 && (key != left || key >= a.vocab || (lane == 1 && run == 0)));
+    const uint64_t counts = __ballot(real && key < a.vocab);
+    const auto bits = [](uint32_t from, uint32_t to) { return ((uint64_t(1) << to) - 1) & ~((uint64_t(1) << from) - 1); };  // to < 64
+    const auto end_of = [&](uint32_t l) {  // the place after the id that has lane l's
+        const uint64_t later = heads & ~((uint64_t(2) << l) - 1);
+        return later ? static_cast<uint32_t>(__builtin_ctzll(later)) : static_cast<uint32_t>(kLanes);
     };
-    if (group == 0) add_rows(from - before, from);
-    const uint32_t share = (runs + kGroups - 1) / kGroups, mine = min(group * share, runs), next = min(mine + share, runs);
-    for (uint32_t r = mine; r < next; r += 4) {
-        float f[4][8];
-#pragma unroll
-        for (uint32_t j = 0; j < 4; ++j)
-            if (r + j < next) load_columns<kRowF32>(a.runs, static_cast<uint64_t>(first + r + j) * a.width, c, f[j]);
-#pragma unroll
-        for (uint32_t j = 0; j < 4; ++j)
-            if (r + j < next)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum[e] += f[j][e];
+    // the places that this group sums, and those of them that are of long ids
+    const uint32_t group = LANES == kLanes ? 0 : lane / LANES, from = 1 + group * kShare;
+    uint64_t todo = 0, of_long = 0;
+    for (uint64_t h = heads & counts & bits(from, from + kShare); h; h &= h - 1) {
+        const uint32_t l = __builtin_ctzll(h), end = end_of(l), whole = l == 1 ? 1 : kLast + 1;  // its first aligned run, if it has one
+        if (end < whole + kRun) todo |= bits(l, end);
+        else of_long |= bits(l, kLast + 1);
     }
-    if (group == kGroups - 1) add_rows(to, to + after);
-    __syncthreads();  // the last task's readers are done
-#pragma unroll
-    for (int e = 0; e < 8; ++e) parts[group][e * LANES + threadIdx.x % LANES] = sum[e];
-    __syncthreads();
-    if (group == 0) {
-        for (uint32_t g = 1; g < kGroups; ++g)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += parts[g][e * LANES + threadIdx.x % LANES];
-        put_row<O>(a, key, c, sum);
-    }
-}
-
-// The ids whose first place is among `chunk` sorted ones from `begin` on, but
-// for the long ones: a group of lanes, four rows on their way at a time.
-template <int T, int O, int LANES> __device__ void sum_few(const GradArgs &a, uint32_t begin, uint32_t piece) {
-    const Columns c(piece, LANES, threadIdx.x % LANES, a.width);
-    const uint32_t last = a.tokens - 1, end = min(begin + a.chunk, a.tokens);
-    uint32_t previous = begin == 0 ? kNoKey : a.sorted[begin - 1], id = kNoKey;  // id: of the sum under way
-    float sum[8] = {};
-    for (uint32_t i = begin; i < end || id != kNoKey; i += 4) {
-        // keys at the end of the run that would make an id starting here long
-        const uint32_t next = (i / kRun + 1) * kRun + kRun - 1;
-        const uint32_t far = next <= last ? uniform<LANES>(a.sorted[next]) : kNoKey;
-        const uint32_t near = i % kRun == 0 && i + kRun - 1 <= last ? uniform<LANES>(a.sorted[i + kRun - 1]) : kNoKey;
-        uint32_t owner[4], at[4];
-        bool head[4], done = false;
-        uint32_t now = id;
-#pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) {
-            const uint32_t key = i + j <= last ? uniform<LANES>(a.sorted[i + j]) : kNoKey;
-            at[j] = i + j <= last ? uniform<LANES>(a.order[i + j]) : 0;
-            head[j] = key != previous;
-            previous = key;
-            done |= head[j] && i + j >= end;
-            if (head[j]) now = done || key >= a.vocab || key == (j == 0 && i % kRun == 0 ? near : far) ? kNoKey : key;
-            owner[j] = now;
+    const uint32_t key1 = __builtin_amdgcn_readlane(key, 1);
+    const uint32_t end1 = end_of(1);
+    const bool full = (counts & 2) && end1 > kLast;  // one id has the whole run
+    if (group == 0 && (counts & 2) && !(heads & 2) && (full || back == key1)) of_long |= bits(1, min(end1, kLast + 1));
+    todo |= of_long;
+    if (full && back != key1 && piece == 0) {  // the id's first whole run
+        uint32_t runs = 1;
+        for (;;) {
+            const uint64_t end = (static_cast<uint64_t>(run) + runs + lane + 1) * kRun;
+            const uint64_t same = __ballot(end <= a.tokens && a.sorted[end - 1] == key1);
+            const uint32_t more = same == ~uint64_t(0) ? kLanes : __builtin_ctzll(~same);
+            runs += more;
+            if (more < kLanes) break;
         }
-        float f[4][8];
+        if (lane == 0) {
+            const uint64_t next = (static_cast<uint64_t>(run) + runs) * kRun;
+            a.longs[atomicAdd(a.long_count, 1u)] = Long{run, runs, key1, static_cast<uint16_t>(!(heads & 2)),
+                                                        static_cast<uint16_t>(next < a.tokens && a.sorted[next] == key1)};
+        }
+    }
+    const Columns<LANES, kFours> c(piece, a.width);
+    constexpr int kAtOnce = T == kRowF32 || ADD ? 4 : 8;
+    float sum[8] = {};
+    while (__ballot(todo != 0)) {  // until all groups are done: each reads places that others' lanes hold
+        Eight<T, LANES, kFours> row[kAtOnce];
+        Eight<O, LANES, kFours> old[ADD ? kAtOnce : 1];
+        uint32_t id[kAtOnce];
+        uint32_t on = 0, last = 0, part = 0, begins = 0;
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j)
-            if (owner[j] != kNoKey) load_columns<T>(a.grad, at[j] * a.grad_stride, c, f[j]);
+        for (int j = 0; j < kAtOnce; ++j) {
+            uint32_t l = 0;
+            if (todo) {
+                l = __builtin_ctzll(todo);
+                todo &= todo - 1;
+                on |= 1u << j;
+                const uint32_t of = static_cast<uint32_t>(of_long >> l) & 1;
+                part |= of << j;
+                last |= (static_cast<uint32_t>((heads >> (l + 1)) & 1) | (of & (l == kLast))) << j;
+                begins |= static_cast<uint32_t>((heads & bits(2, l + 1)) != 0) << j;
+            }
+            const uint32_t at = LANES == kLanes ? __builtin_amdgcn_readlane(order, l) : __shfl(order, l);
+            id[j] = LANES == kLanes ? __builtin_amdgcn_readlane(key, l) : __shfl(key, l);
+            if ((on >> j) & 1) row[j].load(a.grad, at * a.grad_stride, c);
+            if (ADD && ((last & ~part) >> j) & 1) old[ADD ? j : 0].load(a.out, id[j] * a.out_stride, c);
+        }
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) {
-            if (head[j]) {
-                if (id != kNoKey) put_row<O>(a, id, c, sum);
-                id = owner[j];
+        for (int j = 0; j < kAtOnce; ++j) {
+            if ((on >> j) & 1) row[j].add_to(sum);
+            if ((last >> j) & 1) {
+                if ((part >> j) & 1) {
+                    float *p = part_of<LANES>(a, (begins >> j) & 1, run, piece);
+                    *reinterpret_cast<float4 *>(p) = float4{sum[0], sum[1], sum[2], sum[3]};
+                    *reinterpret_cast<float4 *>(p + LANES * 4) = float4{sum[4], sum[5], sum[6], sum[7]};
+                } else {
+                    put_row<O, LANES, kFours, ADD>(a, id[j], c, sum, old[ADD ? j : 0]);
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum[e] = 0.f;
             }
-            if (id != kNoKey)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum[e] += f[j][e];
         }
     }
 }
 
-// Clears the rows of 32 ids that no token names.
+// How many keys are below `id`: by a whole wave, 64 places tried at a time.
+__device__ inline uint32_t keys_below(const uint32_t *keys, uint32_t count, uint32_t id) {
+    const uint32_t lane = threadIdx.x % kLanes;
+    uint32_t lo = 0, hi = count;
+    while (hi - lo > kLanes) {
+        const uint32_t step = (hi - lo + kLanes - 1) / kLanes;
+        const uint64_t at = static_cast<uint64_t>(lo) + (lane + 1) * static_cast<uint64_t>(step) - 1;
+        lo += __popcll(__ballot(at < hi && keys[at] < id)) * step;
+        hi = lo > hi ? lo : min(hi, lo + step - 1);
+    }
+    return lo + __popcll(__ballot(lo + lane < hi && keys[lo + lane] < id));
+}
+
+// Clears the rows of 32 ids that no token names, or a piece of each.
+constexpr uint32_t kClearPiece = 512;  // 16-byte stores
 template <int O> __device__ void clear_rows(const GradArgs &a, uint32_t word, uint32_t piece) {
-    constexpr uint32_t kPiece = kEmbBlock;  // eights of columns
-    const uint32_t all = (a.width + 7) / 8, first = piece * kPiece, eights = min(kPiece, all - first);
-    const uint32_t present = a.tokens ? a.present[word] : 0;
-    for (uint32_t u = threadIdx.x; u < 32 * eights; u += kEmbBlock) {
-        const uint32_t r = u / eights, id = word * 32 + r, col = (first + u % eights) * 8;
-        if (id >= a.vocab || ((present >> r) & 1)) continue;
-        auto *p = static_cast<typename Row<O>::Stored *>(a.out) + id * a.out_stride + col;
-        if (col + 8 <= a.width) {
-            store16_once(p, u32x4{0, 0, 0, 0});
-            if (O == kRowF32) store16_once(p + 4, u32x4{0, 0, 0, 0});
-        } else {
-            for (uint32_t e = 0; col + e < a.width; ++e) p[e] = 0;
+    constexpr uint32_t kVec = Row<O>::kVec;
+    __shared__ uint32_t present;
+    const uint32_t id0 = word * 32, ids = min(32u, a.vocab - id0);
+    const uint32_t from = keys_below(a.sorted, a.tokens, id0), to = keys_below(a.sorted, a.tokens, id0 + ids);
+    __syncthreads();
+    if (threadIdx.x == 0) present = 0;
+    __syncthreads();
+    for (uint32_t i = from + threadIdx.x; i < to; i += kEmbBlock) atomicOr(&present, 1u << (a.sorted[i] - id0));
+    __syncthreads();
+    const uint32_t named = present;
+    const uint32_t all = (a.width + kVec - 1) / kVec, first = piece * kClearPiece, stores = min(kClearPiece, all - first);
+    // rows side by side, where one does not take all threads
+    const uint32_t shift = stores > kEmbBlock / 2 ? 8 : 32 - __builtin_clz(stores - 1 | 1), rows = kEmbBlock >> shift;
+    for (uint32_t r = threadIdx.x >> shift; r < ids; r += rows) {
+        if ((named >> r) & 1) continue;
+        auto *p = static_cast<typename Row<O>::Stored *>(a.out) + (id0 + r) * a.out_stride;
+        for (uint32_t u = threadIdx.x & ((1u << shift) - 1); u < stores; u += 1u << shift) {
+            const uint64_t col = static_cast<uint64_t>(first + u) * kVec;
+            if (col + kVec <= a.width) store16_once(p + col, u32x4{0, 0, 0, 0});
+            else
+                for (uint32_t e = 0; col + e < a.width; ++e) p[col + e] = 0;
         }
     }
 }
 
-template <int T, int O, int LANES>
+template <int T, int O, int LANES, bool ADD>
 __global__ __launch_bounds__(kEmbBlock) void embed_sum_kernel(GradArgs a) {
-    constexpr uint32_t kGroups = kEmbBlock / LANES;
-    uint32_t block = blockIdx.x;
-    if (block < a.long_blocks) {
-        const uint64_t tasks = static_cast<uint64_t>(a.longs[0]) * a.pieces;
-        for (uint64_t t = block; t < tasks; t += a.long_blocks)
-            sum_long<T, O, LANES>(a, static_cast<uint32_t>(t / a.pieces), static_cast<uint32_t>(t % a.pieces));
+    constexpr uint32_t kWaves = kEmbBlock / kLanes;
+    const uint32_t turn = a.clear_turns + 1;
+    if (blockIdx.x % turn == 0 && blockIdx.x / turn < a.sum_blocks) {
+        const uint64_t tasks = static_cast<uint64_t>(a.runs) * a.pieces;
+        for (uint64_t t = blockIdx.x / turn * kWaves + threadIdx.x / kLanes; t < tasks; t += static_cast<uint64_t>(a.sum_blocks) * kWaves)
+            sum_run<T, O, LANES, ADD>(a, __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(t / a.pieces)),
+                                      __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(t % a.pieces)));
         return;
     }
-    block -= a.long_blocks;
-    if (block < a.few_blocks) {
-        const uint64_t chunks = (a.tokens + a.chunk - 1) / a.chunk, tasks = chunks * a.pieces;
-        for (uint64_t t = static_cast<uint64_t>(block) * kGroups + threadIdx.x / LANES; t < tasks; t += static_cast<uint64_t>(a.few_blocks) * kGroups)
-            sum_few<T, O, LANES>(a, uniform<LANES>(static_cast<uint32_t>(t / a.pieces)) * a.chunk, uniform<LANES>(static_cast<uint32_t>(t % a.pieces)));
-        return;
+    if constexpr (!ADD) {
+        const uint32_t block = blockIdx.x - min(a.sum_blocks, (blockIdx.x + turn - 1) / turn);
+        const uint32_t pieces = ((a.width + Row<O>::kVec - 1) / Row<O>::kVec + kClearPiece - 1) / kClearPiece, words = (a.vocab + 31) / 32;
+        const uint64_t tasks = static_cast<uint64_t>(words) * pieces;
+        for (uint64_t t = block; t < tasks; t += gridDim.x - a.sum_blocks)
+            clear_rows<O>(a, static_cast<uint32_t>(t / pieces), static_cast<uint32_t>(t % pieces));
     }
-    block -= a.few_blocks;
-    const uint32_t pieces = ((a.width + 7) / 8 + kEmbBlock - 1) / kEmbBlock, words = (a.vocab + 31) / 32;
-    const uint64_t tasks = static_cast<uint64_t>(words) * pieces, blocks = gridDim.x - a.long_blocks - a.few_blocks;
-    for (uint64_t t = block; t < tasks; t += blocks) clear_rows<O>(a, static_cast<uint32_t>(t / pieces), static_cast<uint32_t>(t % pieces));
+}
+
+// The long ids, a workgroup each and piece: its groups take the runs in equal
+// shares, and their sums are added in order.
+template <int O, int LANES, bool FOURS>
+__global__ __launch_bounds__(kJoinBlock) void embed_join_kernel(GradArgs a) {
+    constexpr uint32_t kGroups = kJoinBlock / LANES, kAtOnce = 4;
+    __shared__ float4 shared[kGroups][2][LANES];
+    const uint32_t group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+    const uint64_t tasks = static_cast<uint64_t>(*a.long_count) * a.pieces;
+    for (uint64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+        const Long of = a.longs[task / a.pieces];
+        const uint32_t piece = static_cast<uint32_t>(task % a.pieces);
+        float sum[8] = {};
+        const auto add = [&](float4 p, float4 q) {
+            const float f[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += f[e];
+        };
+        const auto halves = [&](uint32_t begins, uint32_t run, float4 &p, float4 &q) {
+            const float *at = part_of<LANES>(a, begins, run, piece);
+            p = *reinterpret_cast<const float4 *>(at);
+            q = *reinterpret_cast<const float4 *>(at + LANES * 4);
+        };
+        if (group == 0 && of.before) {
+            float4 p, q;
+            halves(1, of.run - 1, p, q);
+            add(p, q);
+        }
+        const uint32_t all = of.runs + of.after, share = (all + kGroups - 1) / kGroups;
+        const uint32_t mine = min(group * share, all), next = min(mine + share, all);
+        for (uint32_t r = mine; r < next; r += kAtOnce) {
+            float4 p[kAtOnce], q[kAtOnce];
+#pragma unroll
+            for (uint32_t j = 0; j < kAtOnce; ++j)
+                if (r + j < next) halves(0, of.run + r + j, p[j], q[j]);
+#pragma unroll
+            for (uint32_t j = 0; j < kAtOnce; ++j)
+                if (r + j < next) add(p[j], q[j]);
+        }
+        __syncthreads();  // the last task's readers are done
+        shared[group][0][lane] = float4{sum[0], sum[1], sum[2], sum[3]};
+        shared[group][1][lane] = float4{sum[4], sum[5], sum[6], sum[7]};
+        __syncthreads();
+        if (group == 0) {
+            for (uint32_t g = 1; g < kGroups; ++g) add(shared[g][0][lane], shared[g][1][lane]);
+            const Columns<LANES, FOURS> c(piece, a.width);
+            Eight<O, LANES, FOURS> old;
+            if (a.accumulate) {
+                old.load(a.out, of.key * a.out_stride, c);
+                put_row<O, LANES, FOURS, true>(a, of.key, c, sum, old);
+            } else {
+                put_row<O, LANES, FOURS, false>(a, of.key, c, sum, old);
+            }
+        }
+    }
 }
 
 // -------------------------------------------------------------------- host
@@ -397,8 +498,11 @@ template <typename F> void by_types(int in, int out, F f) {
     by_type(in, [&](auto t) { by_type(out, [&](auto o) { f(t, o); }); });
 }
 
+// Rows of at most 128 columns take a quarter of a wave.
+uint64_t lanes_of(uint64_t width) { return width <= 16 * 8 ? 16 : kLanes; }
+
 struct GradSpace {
-    uint64_t keys = 0, places = 0, sorted = 0, order = 0, sort = 0, sort_bytes = 0, present = 0, longs = 0, runs = 0, total = 0;
+    uint64_t keys = 0, places = 0, sorted = 0, order = 0, sort = 0, sort_bytes = 0, long_count = 0, longs = 0, parts = 0, total = 0;
 };
 int key_bits(uint64_t vocab) {
     int b = 1;
@@ -419,33 +523,30 @@ GradSpace grad_space(uint64_t tokens, uint64_t vocab, uint64_t width, const lrs_
     w.order = place(4 * tokens);
     w.sort_bytes = radix_sort_workspace_size(tokens, 0, key_bits(vocab), 8, 1, opts);
     w.sort = place(w.sort_bytes);
-    w.present = place((vocab + 31) / 32 * 4);
-    w.longs = place(4 * (1 + tokens / kRun));
-    w.runs = place(tokens / kRun * width * 4);
+    const uint64_t runs = (tokens + kRun - 1) / kRun, lanes = lanes_of(width);
+    w.long_count = place(4);
+    w.longs = place(runs * sizeof(Long));
+    w.parts = place(2 * runs * ((width + lanes * 8 - 1) / (lanes * 8)) * lanes * 8 * sizeof(float));
     return w;
 }
 
-// Rows of at most 128 columns take a quarter of a wave.
-template <int T, int O, int LANES> void launch_sums(GradArgs a, const Ctx &c) {
-    constexpr uint64_t kGroups = kEmbBlock / LANES;
-    const auto blocks = [](uint64_t tasks, uint64_t each) { return (tasks + each - 1) / each; };
-    a.pieces = static_cast<uint32_t>(blocks(a.width, LANES * 8));
-    // few tokens: more groups, with fewer places each
-    a.chunk = static_cast<uint64_t>(a.tokens) * a.pieces < 16384 ? 4 : 16;
-    const uint64_t runs = a.tokens / kRun;
-    if (a.tokens > 0 && (runs > 0 || !a.accumulate)) {
+template <int T, int O, int LANES, bool ADD> void launch_sums(GradArgs a, const Ctx &c) {
+    const auto over = [](uint64_t tasks, uint64_t each) { return (tasks + each - 1) / each; };
+    a.pieces = static_cast<uint32_t>(over(a.width, LANES * 8));
+    a.runs = static_cast<uint32_t>(over(a.tokens, kRun));
+    const uint64_t tasks = static_cast<uint64_t>(a.runs) * a.pieces;
+    const uint64_t clears = ADD ? 0 : std::min(over(a.vocab, 32) * over(over(a.width, Row<O>::kVec), kClearPiece), kMaxGrid);
+    a.sum_blocks = static_cast<uint32_t>(std::min(over(tasks, kEmbBlock / kLanes), kMaxGrid));
+    a.clear_turns = a.sum_blocks ? static_cast<uint32_t>(clears / a.sum_blocks) : 0;
+    if (a.sum_blocks + clears == 0) return;
+    {
         TimedLaunch t(4, c);
-        const uint64_t grid = blocks(a.tokens, kEmbBlock) + std::min(blocks(runs * a.pieces, kGroups), kMaxGrid);
-        launch_on(embed_runs_kernel<T, LANES>, dim3(static_cast<uint32_t>(grid)), dim3(kEmbBlock), t.L, a);
-        if (hipPeekAtLastError() != hipSuccess) return;
+        launch_on(embed_sum_kernel<T, O, LANES, ADD>, dim3(static_cast<uint32_t>(a.sum_blocks + clears)), dim3(kEmbBlock), t.L, a);
     }
-    a.long_blocks = static_cast<uint32_t>(std::min<uint64_t>(runs * a.pieces, 512));
-    a.few_blocks = static_cast<uint32_t>(std::min(blocks(blocks(a.tokens, a.chunk) * a.pieces, kGroups), kMaxGrid));
-    uint64_t grid = a.long_blocks + a.few_blocks;
-    if (!a.accumulate) grid += std::min(blocks(a.vocab, 32) * blocks(a.width, 8 * kEmbBlock), kMaxGrid);
-    if (grid == 0) return;
+    if (a.tokens < kRun || hipPeekAtLastError() != hipSuccess) return;
     TimedLaunch t(4, c);
-    launch_on(embed_sum_kernel<T, O, LANES>, dim3(static_cast<uint32_t>(grid)), dim3(kEmbBlock), t.L, a);
+    launch_on(embed_join_kernel<O, LANES, T == kRowF32 || O == kRowF32>, dim3(static_cast<uint32_t>(std::min<uint64_t>(tasks, 512))),
+              dim3(kJoinBlock), t.L, a);
 }
 
 }  // namespace
@@ -542,9 +643,9 @@ int embedding_backward(const void *grad, int64_t grad_stride, const lrs_token_id
         uint32_t *sorted = reinterpret_cast<uint32_t *>(ws + w.sorted), *order = reinterpret_cast<uint32_t *>(ws + w.order);
         a.sorted = sorted;
         a.order = order;
-        a.present = reinterpret_cast<uint32_t *>(ws + w.present);
-        a.longs = reinterpret_cast<uint32_t *>(ws + w.longs);
-        a.runs = reinterpret_cast<float *>(ws + w.runs);
+        a.long_count = reinterpret_cast<uint32_t *>(ws + w.long_count);
+        a.longs = reinterpret_cast<Long *>(ws + w.longs);
+        a.parts = reinterpret_cast<float *>(ws + w.parts);
         {
             TimedLaunch t(4, c);
             launch_on(embed_keys_kernel, dim3((a.tokens + kEmbBlock - 1) / kEmbBlock), dim3(kEmbBlock), t.L, a);
@@ -555,8 +656,9 @@ int embedding_backward(const void *grad, int64_t grad_stride, const lrs_token_id
         if (st != LRS_OK) return st;
     }
     by_types(dtype, out_dtype, [&](auto i, auto o) {
-        if (width <= 16 * 8) launch_sums<i.value, o.value, 16>(a, c);
-        else launch_sums<i.value, o.value, kLanes>(a, c);
+        const bool narrow = lanes_of(width) == 16;
+        if (a.accumulate) narrow ? launch_sums<i.value, o.value, 16, true>(a, c) : launch_sums<i.value, o.value, kLanes, true>(a, c);
+        else narrow ? launch_sums<i.value, o.value, 16, false>(a, c) : launch_sums<i.value, o.value, kLanes, false>(a, c);
     });
     return hipGetLastError() == hipSuccess ? LRS_OK : LRS_ERR_HIP;
 } catch (...) {
