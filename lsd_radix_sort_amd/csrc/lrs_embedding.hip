@@ -26,7 +26,7 @@ struct Ids {
     uint32_t length;
     int bytes;
     __device__ int64_t operator[](uint32_t t) const {
-        const uint64_t i = t / length * stride + t % length;
+        const uint64_t i = t < length ? t : t / length * stride + t % length;
         return bytes == 8 ? static_cast<const int64_t *>(at)[i] : static_cast<const int32_t *>(at)[i];
     }
 };
@@ -97,14 +97,13 @@ __global__ __launch_bounds__(kEmbBlock) void lookup_kernel(LookupArgs a) {
 //
 // After the sort the tokens of an id are neighbours.  Text has a few ids that
 // make up a large share of it, and most ids in none, so the work is cut into
-// even pieces: a wave takes a run of kRun sorted places, and of each id that
-// begins there all places, at most 2 kRun - 2, unless the id has an aligned run
-// to itself.  Such an id is long: every wave adds up what its own run holds of
-// it, and a second launch joins those sums.  The rows of ids without tokens are
-// cleared in the first launch, in turns with the sums, since sums wait for their
-// reads and clearing only writes.
+// even pieces: a wave takes a run of sorted places, and of each id that begins
+// there all places, less than two runs, unless the id has an aligned run to
+// itself.  Such an id is long: every wave adds up what its own run holds of it,
+// and a second launch joins those sums.  The rows of ids without tokens are
+// cleared in the first launch, too.
 
-constexpr uint32_t kRun = 16;
+constexpr uint32_t kMaxRun = 16;
 constexpr int kJoinBlock = 1024;
 
 // A long id: the first of its whole runs, how many there are, and whether the
@@ -129,9 +128,12 @@ struct GradArgs {
     uint32_t *long_count;
     Long *longs;
     float *parts;                         // [2][runs][pieces][lanes * 8]: see part_of
-    uint32_t runs;                        // of kRun places, the last one maybe fewer
+    uint32_t run;                         // places in a run: 4, 8 or 16
+    uint32_t runs;                        // the last one maybe shorter
     uint32_t pieces;                      // of a row, a group of lanes each
-    uint32_t sum_blocks, clear_turns;     // blocks that sum, and how many clear after each of them
+    uint32_t sum_blocks;                  // blocks that sum; the others clear
+    uint32_t range;                       // ids whose places one workgroup orders
+    uint32_t line_factor;                 // 2^32 over the ids' length, rounded up
 };
 
 // The keys of the sort: ids, those that count for nothing behind the last.
@@ -142,6 +144,87 @@ __global__ __launch_bounds__(kEmbBlock) void embed_keys_kernel(GradArgs a) {
     const int64_t id = a.ids[t];
     a.keys[t] = id >= 0 && id < a.vocab && id != a.padding ? static_cast<uint32_t>(id) : a.vocab;
     a.places[t] = t;
+}
+
+// For few tokens a workgroup finds the places of a range of ids by itself,
+// from a read of all of them: what a sort needs several launches for, one after
+// the other.  A wave takes a share of the tokens, N for each lane, and counts the
+// range's ids among them; the counts, added up by id and then by wave, say where
+// each wave's first token of an id goes, and the wave deals its tokens out in
+// order.  Bound by the instructions for an id that is not in the range, which are
+// 255 of 256: masks of whole waves and scalar counts.
+constexpr int kOrderBlock = 1024;
+constexpr uint32_t kMaxRange = 1024;
+template <int N, typename Id>
+__global__ __launch_bounds__(kOrderBlock) void embed_order_kernel(GradArgs a, uint32_t *sorted, uint32_t *order) {
+    constexpr uint32_t kWaves = kOrderBlock / kLanes;
+    __shared__ uint32_t counter[kWaves][kMaxRange];
+    __shared__ uint32_t cells[2][kWaves];
+    const uint32_t lane = threadIdx.x % kLanes, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+    const uint32_t first = blockIdx.x * a.range, ids = min(a.range, a.vocab - first);
+    const uint32_t from = wave * (N * kLanes) + lane;
+    Id id[N];
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i) {
+        const uint32_t t = from + i * kLanes, line = a.ids.length == 1 ? t : __umulhi(t, a.line_factor);
+        id[i] = t < a.tokens ? static_cast<const Id *>(a.ids.at)[static_cast<uint64_t>(line) * a.ids.stride + (t - line * a.ids.length)] : -1;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.long_count = 0;
+    for (uint32_t i = lane; i < ids; i += kLanes) counter[wave][i] = 0;
+    // within the range: the id's place there
+    uint32_t of[N], below = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i) {
+        const bool counts = id[i] >= 0 && static_cast<int64_t>(id[i]) != a.padding;
+        below += __popcll(__ballot(counts && id[i] < static_cast<Id>(first)));
+        of[i] = counts && id[i] < static_cast<Id>(a.vocab) ? static_cast<uint32_t>(id[i]) - first : ~0u;
+        if (of[i] < ids) atomicAdd(&counter[wave][of[i]], 1u);
+    }
+    if (lane == 0) cells[0][wave] = below;
+    __syncthreads();
+    // a thread an id: its tokens, and where they begin
+    uint32_t mine = 0;
+    if (threadIdx.x < ids)
+        for (uint32_t w = 0; w < kWaves; ++w) mine += counter[w][threadIdx.x];
+    uint32_t upto = mine;
+    upto += moved<0x111>(upto, 0u);
+    upto += moved<0x112>(upto, 0u);
+    upto += moved<0x114>(upto, 0u);
+    upto += moved<0x118>(upto, 0u);
+    upto += moved<0x142, 0xA>(upto, 0u);
+    upto += moved<0x143, 0xC>(upto, 0u);
+    if (lane == kLanes - 1) cells[1][wave] = upto;
+    __syncthreads();
+    uint32_t start = upto - mine, all = 0;
+    for (uint32_t w = 0; w < kWaves; ++w) {
+        all += cells[0][w] + cells[1][w];
+        start += cells[0][w] + (w < wave ? cells[1][w] : 0);
+    }
+    if (threadIdx.x < ids)
+        for (uint32_t w = 0; w < kWaves; ++w) {
+            const uint32_t c = counter[w][threadIdx.x];
+            counter[w][threadIdx.x] = start;
+            start += c;
+        }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i) {
+        for (uint64_t left = __ballot(of[i] < ids); left;) {  // an id at a time
+            const uint32_t one = __builtin_amdgcn_readlane(of[i], __builtin_ctzll(left));
+            const uint64_t same = __ballot(of[i] == one);
+            const uint32_t at = counter[wave][one];
+            if (of[i] == one) {
+                const uint32_t p = at + __builtin_amdgcn_mbcnt_hi(same >> 32, __builtin_amdgcn_mbcnt_lo(same, 0));
+                sorted[p] = first + one;
+                order[p] = from + i * kLanes;
+            }
+            counter[wave][one] = at + __popcll(same);
+            left &= ~same;
+        }
+    }
+    // behind the last id: what counts for nothing
+    if (blockIdx.x == gridDim.x - 1)
+        for (uint32_t i = all + threadIdx.x; i < a.tokens; i += kOrderBlock) sorted[i] = a.vocab;
 }
 
 // What a lane holds of a piece of a row: eight neighbouring columns, or, where
@@ -166,18 +249,20 @@ template <int T, int LANES, bool FOURS> struct Eight {
     using At = Columns<LANES, FOURS>;
     static constexpr int kWords = T == kRowF32 ? 8 : 4, kEach = kWords / At::kParts;
     uint32_t w[kWords];
-    __device__ void load(const void *rows, uint64_t row, const At &c) {
+    // once: not kept in the caches
+    __device__ void load(const void *rows, uint64_t row, const At &c, bool once) {
 #pragma unroll
         for (int p = 0; p < At::kParts; ++p) {
             const auto *x = static_cast<const typename Row<T>::Stored *>(rows) + row + c.first[p];
             uint32_t *v = w + p * kEach;
             if (c.count[p] == At::kSize) {
                 if constexpr (kEach == 4) {
-                    const u32x4 q = load16_once(x);
+                    const u32x4 q = once ? load16_once(x) : load16(x);
                     for (int i = 0; i < 4; ++i) v[i] = q[i];
                 } else {
                     static_assert(kEach == 2);
-                    const u32x2 q = __builtin_nontemporal_load(reinterpret_cast<const u32x2_align2 *>(x));
+                    const auto *y = reinterpret_cast<const u32x2_align2 *>(x);
+                    const u32x2 q = once ? __builtin_nontemporal_load(y) : *y;
                     v[0] = q.x;
                     v[1] = q.y;
                 }
@@ -215,13 +300,12 @@ template <int T, int LANES, bool FOURS> struct Eight {
             const float *g = f + p * At::kSize;
             if (c.count[p] == At::kSize) {
                 if constexpr (T == kRowF32) {
-                    store16_once(x, u32x4{__builtin_bit_cast(uint32_t, g[0]), __builtin_bit_cast(uint32_t, g[1]),
+                    store16(x, u32x4{__builtin_bit_cast(uint32_t, g[0]), __builtin_bit_cast(uint32_t, g[1]),
                                           __builtin_bit_cast(uint32_t, g[2]), __builtin_bit_cast(uint32_t, g[3])});
                 } else if constexpr (FOURS) {
-                    __builtin_nontemporal_store(u32x2{Row<T>::pack(g[0], g[1]), Row<T>::pack(g[2], g[3])},
-                                                reinterpret_cast<u32x2_align2 *>(x));
+                    *reinterpret_cast<u32x2_align2 *>(x) = u32x2{Row<T>::pack(g[0], g[1]), Row<T>::pack(g[2], g[3])};
                 } else {
-                    store16_once(x, u32x4{Row<T>::pack(g[0], g[1]), Row<T>::pack(g[2], g[3]), Row<T>::pack(g[4], g[5]),
+                    store16(x, u32x4{Row<T>::pack(g[0], g[1]), Row<T>::pack(g[2], g[3]), Row<T>::pack(g[4], g[5]),
                                           Row<T>::pack(g[6], g[7])});
                 }
             } else {
@@ -256,13 +340,14 @@ template <int LANES> __device__ inline float *part_of(const GradArgs &a, uint32_
 // time, whatever ids they are of.
 template <int T, int O, int LANES, bool ADD> __device__ void sum_run(const GradArgs &a, uint32_t run, uint32_t piece) {
     constexpr bool kFours = T == kRowF32 || O == kRowF32;
-    constexpr uint32_t kGroups = kLanes / LANES, kShare = kRun / kGroups, kLast = kRun;  // kLast: the lane of the run's last place
-    static_assert(3 * kRun - 1 < kLanes, "an id that is not long ends among the places looked at");
-    const uint32_t lane = threadIdx.x % kLanes, begin = run * kRun;
+    constexpr uint32_t kGroups = kLanes / LANES;
+    static_assert(3 * kMaxRun - 1 < kLanes, "an id that is not long ends among the places looked at");
+    const uint32_t len = a.run, last_lane = len, share = len / kGroups;  // last_lane: of the run's last place
+    const uint32_t lane = threadIdx.x % kLanes, begin = run * len;
     const uint64_t place = static_cast<uint64_t>(begin) + lane - 1;  // of this lane
     const bool real = place < a.tokens;                            // not before the first either
     const uint32_t key = real ? a.sorted[place] : a.vocab, order = real ? a.order[place] : 0;
-    const uint32_t back = run > 0 ? a.sorted[begin - kRun] : a.vocab;
+    const uint32_t back = run > 0 ? a.sorted[begin - len] : a.vocab;
     const uint32_t left = __builtin_amdgcn_update_dpp(~0u, key, 0x138, 0xF, 0xF, false);  // wave_shr:1
     // bit l: the place of lane l begins an id; past the last token, and where ids count for nothing, every place does
     const uint64_t heads = __ballot(lane > 0 && (key != left || key >= a.vocab || (lane == 1 && run == 0)));
@@ -273,29 +358,29 @@ template <int T, int O, int LANES, bool ADD> __device__ void sum_run(const GradA
         return later ? static_cast<uint32_t>(__builtin_ctzll(later)) : static_cast<uint32_t>(kLanes);
     };
     // the places that this group sums, and those of them that are of long ids
-    const uint32_t group = LANES == kLanes ? 0 : lane / LANES, from = 1 + group * kShare;
+    const uint32_t group = LANES == kLanes ? 0 : lane / LANES, from = 1 + group * share;
     uint64_t todo = 0, of_long = 0;
-    for (uint64_t h = heads & counts & bits(from, from + kShare); h; h &= h - 1) {
-        const uint32_t l = __builtin_ctzll(h), end = end_of(l), whole = l == 1 ? 1 : kLast + 1;  // its first aligned run, if it has one
-        if (end < whole + kRun) todo |= bits(l, end);
-        else of_long |= bits(l, kLast + 1);
+    for (uint64_t h = heads & counts & bits(from, from + share); h; h &= h - 1) {
+        const uint32_t l = __builtin_ctzll(h), end = end_of(l), whole = l == 1 ? 1 : last_lane + 1;  // its first aligned run, if it has one
+        if (end < whole + len) todo |= bits(l, end);
+        else of_long |= bits(l, last_lane + 1);
     }
     const uint32_t key1 = __builtin_amdgcn_readlane(key, 1);
     const uint32_t end1 = end_of(1);
-    const bool full = (counts & 2) && end1 > kLast;  // one id has the whole run
-    if (group == 0 && (counts & 2) && !(heads & 2) && (full || back == key1)) of_long |= bits(1, min(end1, kLast + 1));
+    const bool full = (counts & 2) && end1 > last_lane;  // one id has the whole run
+    if (group == 0 && (counts & 2) && !(heads & 2) && (full || back == key1)) of_long |= bits(1, min(end1, last_lane + 1));
     todo |= of_long;
     if (full && back != key1 && piece == 0) {  // the id's first whole run
         uint32_t runs = 1;
         for (;;) {
-            const uint64_t end = (static_cast<uint64_t>(run) + runs + lane + 1) * kRun;
+            const uint64_t end = (static_cast<uint64_t>(run) + runs + lane + 1) * len;
             const uint64_t same = __ballot(end <= a.tokens && a.sorted[end - 1] == key1);
             const uint32_t more = same == ~uint64_t(0) ? kLanes : __builtin_ctzll(~same);
             runs += more;
             if (more < kLanes) break;
         }
         if (lane == 0) {
-            const uint64_t next = (static_cast<uint64_t>(run) + runs) * kRun;
+            const uint64_t next = (static_cast<uint64_t>(run) + runs) * len;
             a.longs[atomicAdd(a.long_count, 1u)] = Long{run, runs, key1, static_cast<uint16_t>(!(heads & 2)),
                                                         static_cast<uint16_t>(next < a.tokens && a.sorted[next] == key1)};
         }
@@ -317,13 +402,13 @@ template <int T, int O, int LANES, bool ADD> __device__ void sum_run(const GradA
                 on |= 1u << j;
                 const uint32_t of = static_cast<uint32_t>(of_long >> l) & 1;
                 part |= of << j;
-                last |= (static_cast<uint32_t>((heads >> (l + 1)) & 1) | (of & (l == kLast))) << j;
+                last |= (static_cast<uint32_t>((heads >> (l + 1)) & 1) | (of & (l == last_lane))) << j;
                 begins |= static_cast<uint32_t>((heads & bits(2, l + 1)) != 0) << j;
             }
             const uint32_t at = LANES == kLanes ? __builtin_amdgcn_readlane(order, l) : __shfl(order, l);
             id[j] = LANES == kLanes ? __builtin_amdgcn_readlane(key, l) : __shfl(key, l);
-            if ((on >> j) & 1) row[j].load(a.grad, at * a.grad_stride, c);
-            if (ADD && ((last & ~part) >> j) & 1) old[ADD ? j : 0].load(a.out, id[j] * a.out_stride, c);
+            if ((on >> j) & 1) row[j].load(a.grad, at * a.grad_stride, c, true);
+            if (ADD && ((last & ~part) >> j) & 1) old[ADD ? j : 0].load(a.out, id[j] * a.out_stride, c, false);
         }
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
@@ -377,7 +462,7 @@ template <int O> __device__ void clear_rows(const GradArgs &a, uint32_t word, ui
         auto *p = static_cast<typename Row<O>::Stored *>(a.out) + (id0 + r) * a.out_stride;
         for (uint32_t u = threadIdx.x & ((1u << shift) - 1); u < stores; u += 1u << shift) {
             const uint64_t col = static_cast<uint64_t>(first + u) * kVec;
-            if (col + kVec <= a.width) store16_once(p + col, u32x4{0, 0, 0, 0});
+            if (col + kVec <= a.width) store16(p + col, u32x4{0, 0, 0, 0});
             else
                 for (uint32_t e = 0; col + e < a.width; ++e) p[col + e] = 0;
         }
@@ -387,19 +472,17 @@ template <int O> __device__ void clear_rows(const GradArgs &a, uint32_t word, ui
 template <int T, int O, int LANES, bool ADD>
 __global__ __launch_bounds__(kEmbBlock) void embed_sum_kernel(GradArgs a) {
     constexpr uint32_t kWaves = kEmbBlock / kLanes;
-    const uint32_t turn = a.clear_turns + 1;
-    if (blockIdx.x % turn == 0 && blockIdx.x / turn < a.sum_blocks) {
+    if (blockIdx.x < a.sum_blocks) {
         const uint64_t tasks = static_cast<uint64_t>(a.runs) * a.pieces;
-        for (uint64_t t = blockIdx.x / turn * kWaves + threadIdx.x / kLanes; t < tasks; t += static_cast<uint64_t>(a.sum_blocks) * kWaves)
+        for (uint64_t t = static_cast<uint64_t>(blockIdx.x) * kWaves + threadIdx.x / kLanes; t < tasks; t += static_cast<uint64_t>(a.sum_blocks) * kWaves)
             sum_run<T, O, LANES, ADD>(a, __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(t / a.pieces)),
                                       __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(t % a.pieces)));
         return;
     }
     if constexpr (!ADD) {
-        const uint32_t block = blockIdx.x - min(a.sum_blocks, (blockIdx.x + turn - 1) / turn);
         const uint32_t pieces = ((a.width + Row<O>::kVec - 1) / Row<O>::kVec + kClearPiece - 1) / kClearPiece, words = (a.vocab + 31) / 32;
         const uint64_t tasks = static_cast<uint64_t>(words) * pieces;
-        for (uint64_t t = block; t < tasks; t += gridDim.x - a.sum_blocks)
+        for (uint64_t t = blockIdx.x - a.sum_blocks; t < tasks; t += gridDim.x - a.sum_blocks)
             clear_rows<O>(a, static_cast<uint32_t>(t / pieces), static_cast<uint32_t>(t % pieces));
     }
 }
@@ -451,7 +534,7 @@ __global__ __launch_bounds__(kJoinBlock) void embed_join_kernel(GradArgs a) {
             const Columns<LANES, FOURS> c(piece, a.width);
             Eight<O, LANES, FOURS> old;
             if (a.accumulate) {
-                old.load(a.out, of.key * a.out_stride, c);
+                old.load(a.out, of.key * a.out_stride, c, false);
                 put_row<O, LANES, FOURS, true>(a, of.key, c, sum, old);
             } else {
                 put_row<O, LANES, FOURS, false>(a, of.key, c, sum, old);
@@ -500,6 +583,18 @@ template <typename F> void by_types(int in, int out, F f) {
 
 // Rows of at most 128 columns take a quarter of a wave.
 uint64_t lanes_of(uint64_t width) { return width <= 16 * 8 ? 16 : kLanes; }
+uint64_t over(uint64_t tasks, uint64_t each) { return (tasks + each - 1) / each; }
+
+// Places in a run: as many as leave enough waves.
+uint64_t run_of(uint64_t tokens, uint64_t width) {
+    const uint64_t groups = tokens * over(width, lanes_of(width) * 8);
+    return groups >= 16 * 8192 ? 16 : groups >= 8 * 2048 ? 8 : 4;
+}
+// Ids a workgroup orders: as few as make a workgroup a CU.
+uint64_t range_of(uint64_t vocab) { return std::min<uint64_t>(over(vocab, 256), kMaxRange); }
+bool ordered_directly(uint64_t tokens, uint64_t vocab) {
+    return tokens <= 32 * kOrderBlock && over(vocab, range_of(vocab)) <= 1024;
+}
 
 struct GradSpace {
     uint64_t keys = 0, places = 0, sorted = 0, order = 0, sort = 0, sort_bytes = 0, long_count = 0, longs = 0, parts = 0, total = 0;
@@ -511,39 +606,40 @@ int key_bits(uint64_t vocab) {
 }
 GradSpace grad_space(uint64_t tokens, uint64_t vocab, uint64_t width, const lrs_options *opts) {
     GradSpace w;
-    if (tokens == 0) return w;
+    if (tokens == 0 || vocab == 0 || width == 0) return w;
     auto place = [&](uint64_t bytes) {
         const uint64_t at = w.total;
         w.total += (bytes + 255) / 256 * 256;
         return at;
     };
-    w.keys = place(4 * tokens);
-    w.places = place(4 * tokens);
     w.sorted = place(4 * tokens);
     w.order = place(4 * tokens);
-    w.sort_bytes = radix_sort_workspace_size(tokens, 0, key_bits(vocab), 8, 1, opts);
-    w.sort = place(w.sort_bytes);
-    const uint64_t runs = (tokens + kRun - 1) / kRun, lanes = lanes_of(width);
+    if (!ordered_directly(tokens, vocab)) {
+        w.keys = place(4 * tokens);
+        w.places = place(4 * tokens);
+        w.sort_bytes = radix_sort_workspace_size(tokens, 0, key_bits(vocab), 8, 1, opts);
+        w.sort = place(w.sort_bytes);
+    }
+    const uint64_t runs = over(tokens, run_of(tokens, width)), lanes = lanes_of(width);
     w.long_count = place(4);
     w.longs = place(runs * sizeof(Long));
-    w.parts = place(2 * runs * ((width + lanes * 8 - 1) / (lanes * 8)) * lanes * 8 * sizeof(float));
+    w.parts = place(2 * runs * over(width, lanes * 8) * lanes * 8 * sizeof(float));
     return w;
 }
 
 template <int T, int O, int LANES, bool ADD> void launch_sums(GradArgs a, const Ctx &c) {
-    const auto over = [](uint64_t tasks, uint64_t each) { return (tasks + each - 1) / each; };
     a.pieces = static_cast<uint32_t>(over(a.width, LANES * 8));
-    a.runs = static_cast<uint32_t>(over(a.tokens, kRun));
+    a.run = static_cast<uint32_t>(run_of(a.tokens, a.width));
+    a.runs = static_cast<uint32_t>(over(a.tokens, a.run));
     const uint64_t tasks = static_cast<uint64_t>(a.runs) * a.pieces;
     const uint64_t clears = ADD ? 0 : std::min(over(a.vocab, 32) * over(over(a.width, Row<O>::kVec), kClearPiece), kMaxGrid);
     a.sum_blocks = static_cast<uint32_t>(std::min(over(tasks, kEmbBlock / kLanes), kMaxGrid));
-    a.clear_turns = a.sum_blocks ? static_cast<uint32_t>(clears / a.sum_blocks) : 0;
     if (a.sum_blocks + clears == 0) return;
     {
         TimedLaunch t(4, c);
         launch_on(embed_sum_kernel<T, O, LANES, ADD>, dim3(static_cast<uint32_t>(a.sum_blocks + clears)), dim3(kEmbBlock), t.L, a);
     }
-    if (a.tokens < kRun || hipPeekAtLastError() != hipSuccess) return;
+    if (a.tokens < a.run || hipPeekAtLastError() != hipSuccess) return;
     TimedLaunch t(4, c);
     launch_on(embed_join_kernel<O, LANES, T == kRowF32 || O == kRowF32>, dim3(static_cast<uint32_t>(std::min<uint64_t>(tasks, 512))),
               dim3(kJoinBlock), t.L, a);
@@ -638,22 +734,40 @@ int embedding_backward(const void *grad, int64_t grad_stride, const lrs_token_id
     c.elems = static_cast<uint64_t>(count) * width;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     if (count > 0) {
-        a.keys = reinterpret_cast<uint32_t *>(ws + w.keys);
-        a.places = reinterpret_cast<uint32_t *>(ws + w.places);
         uint32_t *sorted = reinterpret_cast<uint32_t *>(ws + w.sorted), *order = reinterpret_cast<uint32_t *>(ws + w.order);
         a.sorted = sorted;
         a.order = order;
         a.long_count = reinterpret_cast<uint32_t *>(ws + w.long_count);
         a.longs = reinterpret_cast<Long *>(ws + w.longs);
         a.parts = reinterpret_cast<float *>(ws + w.parts);
+        const bool direct = ordered_directly(count, vocab);
         {
             TimedLaunch t(4, c);
-            launch_on(embed_keys_kernel, dim3((a.tokens + kEmbBlock - 1) / kEmbBlock), dim3(kEmbBlock), t.L, a);
+            if (direct) {
+                a.range = static_cast<uint32_t>(range_of(vocab));
+                // exact for tokens below 2^16, and lengths up to there
+                a.line_factor = static_cast<uint32_t>(over(uint64_t(1) << 32, std::max<uint32_t>(2, a.ids.length)));
+                const dim3 grid(static_cast<uint32_t>(over(vocab, a.range)));
+                const auto go = [&](auto wide, auto narrow) {
+                    a.ids.bytes == 8 ? launch_on(wide, grid, dim3(kOrderBlock), t.L, a, sorted, order)
+                                     : launch_on(narrow, grid, dim3(kOrderBlock), t.L, a, sorted, order);
+                };
+                if (count <= 2 * kOrderBlock) go(embed_order_kernel<2, int64_t>, embed_order_kernel<2, int32_t>);
+                else if (count <= 8 * kOrderBlock) go(embed_order_kernel<8, int64_t>, embed_order_kernel<8, int32_t>);
+                else if (count <= 16 * kOrderBlock) go(embed_order_kernel<16, int64_t>, embed_order_kernel<16, int32_t>);
+                else go(embed_order_kernel<32, int64_t>, embed_order_kernel<32, int32_t>);
+            } else {
+                a.keys = reinterpret_cast<uint32_t *>(ws + w.keys);
+                a.places = reinterpret_cast<uint32_t *>(ws + w.places);
+                launch_on(embed_keys_kernel, dim3((a.tokens + kEmbBlock - 1) / kEmbBlock), dim3(kEmbBlock), t.L, a);
+            }
         }
         if (hipGetLastError() != hipSuccess) return LRS_ERR_HIP;
-        st = radix_sort_pairs(a.keys, a.places, sorted, order, a.tokens, 0, key_bits(vocab), 8, ws + w.sort, w.sort_bytes,
-                              stream, opts);
-        if (st != LRS_OK) return st;
+        if (!direct) {
+            st = radix_sort_pairs(a.keys, a.places, sorted, order, a.tokens, 0, key_bits(vocab), 8, ws + w.sort, w.sort_bytes,
+                                  stream, opts);
+            if (st != LRS_OK) return st;
+        }
     }
     by_types(dtype, out_dtype, [&](auto i, auto o) {
         const bool narrow = lanes_of(width) == 16;

@@ -163,6 +163,20 @@ def test_gradient_widths(width):
         check_gradient(lrs.embedding_backward(grad.cuda(), ids.cuda(), vocab).cpu(), grad, ids, vocab, 1.0)
 
 
+@pytest.mark.parametrize("tokens,vocab,width,kind", [(65536, 3001, 24, "text"), (65537, 3001, 24, "text"), (140003, 40, 136, "text"),
+                                                     (70001, 200_003, 8, "any"), (66000, 65536, 16, "runs"), (90000, 9, 8, "outside"),
+                                                     (500, 300_001, 12, "any"), (3000, 1 << 20, 9, "text"),
+                                                     (3000, (1 << 20) + 1, 9, "any"), (40, 2_000_003, 4, "any")])
+def test_gradient_of_many_tokens_and_large_tables(tokens, vocab, width, kind):
+    g = torch.Generator().manual_seed(tokens + vocab)
+    ids = make_ids(kind, torch.Size((tokens,)), vocab, g)
+    grad = torch.randn(tokens, width, generator=g).to(torch.bfloat16)
+    args = (grad.cuda(), ids.cuda(), vocab, 0.3)
+    got = lrs.embedding_backward(*args, dtype=torch.float32)
+    check_gradient(got.cpu(), grad, ids, vocab, 0.3)
+    assert torch.equal(got, lrs.embedding_backward(*args, dtype=torch.float32))
+
+
 @pytest.mark.parametrize("out", DTYPES)
 def test_gradient_accumulates(out):
     g = torch.Generator().manual_seed(5)
