@@ -17,6 +17,7 @@
 #include "../../include/lsd_radix_sort.h"
 #include "lrs_host.h"
 #include "lrs_rows.h"
+#include "lrs_select.h"
 
 namespace lrs {
 namespace {
@@ -39,30 +40,6 @@ struct TopArgs {
     uint64_t first_task;  // of this launch
     uint64_t *words;      // splits > 1: [rows][splits][k], 0 where a split has fewer
 };
-
-// Order image of a pattern, the wanted elements largest (signed).
-__device__ inline int image16(uint32_t pattern, uint32_t flip) {
-    const int v = static_cast<int16_t>(pattern);
-    return static_cast<int16_t>((v ^ ((v >> 15) & 0x7FFF)) ^ static_cast<int>(flip));
-}
-__device__ inline int image32(uint32_t pattern, uint32_t flip) {
-    const int v = static_cast<int>(pattern);
-    return (v ^ ((v >> 31) & 0x7FFFFFFF)) ^ static_cast<int>(flip);
-}
-template <int W> __device__ inline int image(uint32_t pattern, uint32_t flip) {
-    return W == 2 ? image16(pattern, flip) : image32(pattern, flip);
-}
-// The map is its own inverse.
-template <int W> __device__ inline uint32_t pattern_of(int img, uint32_t flip) {
-    const int v = img ^ static_cast<int>(flip);
-    if (W == 2) return static_cast<uint32_t>(v ^ ((v >> 15) & 0x7FFF)) & 0xFFFFu;
-    return static_cast<uint32_t>(v ^ ((v >> 31) & 0x7FFFFFFF));
-}
-__device__ inline uint64_t word_of(int img, uint32_t column) {
-    return (static_cast<uint64_t>(static_cast<uint32_t>(img) ^ 0x80000000u) << 32) | (0xFFFFFFFFu - column);
-}
-__device__ inline int image_of(uint64_t word) { return static_cast<int>(static_cast<uint32_t>(word >> 32) ^ 0x80000000u); }
-__device__ inline uint32_t column_of(uint64_t word) { return 0xFFFFFFFFu - static_cast<uint32_t>(word); }
 
 // Sorts buf[0, count) descending; the words from count to the next power of
 // two are cleared (a real word is never 0).  Barriers before and after.
@@ -87,15 +64,17 @@ template <int B> __device__ void sort_words(uint64_t *buf, uint32_t count) {
         }
 }
 
+template <int W> __device__ inline void put_word(const TopArgs &a, uint64_t w, uint64_t at) {
+    if (W == 2)
+        static_cast<uint16_t *>(a.values)[at] = static_cast<uint16_t>(pattern_of<2>(image_of(w), a.flip));
+    else
+        static_cast<uint32_t *>(a.values)[at] = pattern_of<4>(image_of(w), a.flip);
+    a.indices[at] = column_of(w);
+}
+
 template <int W> __device__ void write_row(const TopArgs &a, const uint64_t *buf, uint64_t row, uint32_t k) {
     for (uint32_t j = threadIdx.x; j < k; j += kTopBlock) {
-        const uint64_t w = buf[j];
-        const uint64_t at = row * a.k + j;
-        if (W == 2)
-            static_cast<uint16_t *>(a.values)[at] = static_cast<uint16_t>(pattern_of<2>(image_of(w), a.flip));
-        else
-            static_cast<uint32_t *>(a.values)[at] = pattern_of<4>(image_of(w), a.flip);
-        a.indices[at] = column_of(w);
+        put_word<W>(a, buf[j], row * a.k + j);
     }
 }
 
@@ -315,16 +294,6 @@ __global__ __launch_bounds__(kTopBlock) void topk_lanes_kernel(TopArgs a) {
     }
 }
 
-// The largest of the wave's values, in every lane.
-__device__ inline int wave_max_int(int v) {
-    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x111, 0xF, 0xF, false));  // row_shr 1, 2, 4, 8
-    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x112, 0xF, 0xF, false));
-    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x114, 0xF, 0xF, false));
-    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x118, 0xF, 0xF, false));
-    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x142, 0xF, 0xF, false));  // row_bcast 15, 31
-    v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x143, 0xF, 0xF, false));
-    return __builtin_amdgcn_readlane(v, kLanes - 1);
-}
 // The largest of each 16 lanes' values, in all of them.
 __device__ inline int row16_max(int v) {
     v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x128, 0xF, 0xF, false));  // row_ror 8, 4, 2, 1
@@ -332,17 +301,6 @@ __device__ inline int row16_max(int v) {
     v = max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x122, 0xF, 0xF, false));
     return max(v, __builtin_amdgcn_update_dpp(INT32_MIN, v, 0x121, 0xF, 0xF, false));
 }
-// The sum over this lane and those below.
-__device__ inline uint32_t lanes_sum(uint32_t v) {
-    v += moved<0x111>(v, 0u);
-    v += moved<0x112>(v, 0u);
-    v += moved<0x114>(v, 0u);
-    v += moved<0x118>(v, 0u);
-    v += moved<0x142, 0xA>(v, 0u);
-    v += moved<0x143, 0xC>(v, 0u);
-    return v;
-}
-
 // E consecutive elements of a row as images, INT32_MIN past its end.
 template <int W, int E> __device__ inline void load_images(const typename Row<W == 2 ? kRowF16 : kRowF32>::Stored *x,
                                                            uint32_t at, uint32_t n, uint32_t flip, int (&img)[E]) {
@@ -567,148 +525,7 @@ __global__ __launch_bounds__(kTopBlock) void topk_wave_kernel(TopArgs a) {
 
 // ---- a row, or a piece of one, by one workgroup -------------------------------
 
-// Bins of images below the largest, 2^shift images a bin; whoever lies lower
-// is not counted.
-constexpr uint32_t kBins = 2048, kCoarse = 64, kFine = kBins / kCoarse;
 constexpr uint32_t kHeldWords = 2048;  // candidates in LDS; half of them where k is at most 512
-constexpr uint32_t kRankWords = 128;   // so many are ranked by counting all the others
-
-struct Bins {
-    uint32_t coarse[kCoarse];
-    uint32_t fine[kBins];
-};
-template <int B> __device__ inline void clear_bins(Bins &h) {
-    if (threadIdx.x < kCoarse) h.coarse[threadIdx.x] = 0;
-    for (uint32_t i = threadIdx.x; i < kBins; i += B) h.fine[i] = 0;
-}
-__device__ inline void add_to_bins(Bins &h, int img, int top, uint32_t shift) {
-    const uint32_t bin = (static_cast<uint32_t>(top) - static_cast<uint32_t>(img)) >> shift;
-    if (bin < kBins) {
-        atomicAdd(&h.fine[bin], 1u);
-        atomicAdd(&h.coarse[bin / kFine], 1u);
-    }
-}
-// By a whole wave: the first bin up to which `want` were counted, kBins if fewer were.
-__device__ inline uint32_t bin_of(const Bins &h, uint32_t want) {
-    const uint32_t lane = threadIdx.x % kLanes;
-    const uint32_t c = h.coarse[lane], upto = lanes_sum(c);
-    const uint64_t enough = __ballot(upto >= want);
-    if (enough == 0) return kBins;
-    const int q = __builtin_ctzll(enough);
-    const uint32_t before = __builtin_amdgcn_readlane(upto - c, q);
-    const uint32_t f = lane < kFine ? h.fine[q * kFine + lane] : 0;
-    return q * kFine + __builtin_ctzll(__ballot(before + lanes_sum(f) >= want));
-}
-
-// Two images of 16 bits at once, the wanted elements largest.
-typedef short i16x2 __attribute__((ext_vector_type(2)));
-__device__ inline i16x2 image_pair(uint32_t w, uint32_t flip) {
-    const i16x2 v = __builtin_bit_cast(i16x2, w);
-    const uint32_t sign = __builtin_bit_cast(uint32_t, static_cast<i16x2>(v >> 15));
-    return __builtin_bit_cast(i16x2, w ^ (sign & 0x7FFF7FFFu) ^ flip);
-}
-template <int W> __device__ inline int vec_max(u32x4 v, uint32_t flip) {
-    if constexpr (W == 2) {
-        const i16x2 m = __builtin_elementwise_max(
-            __builtin_elementwise_max(image_pair(v[0], flip), image_pair(v[1], flip)),
-            __builtin_elementwise_max(image_pair(v[2], flip), image_pair(v[3], flip)));
-        return max(static_cast<int>(m.x), static_cast<int>(m.y));
-    } else {
-        return max(max(image32(v[0], flip), image32(v[1], flip)), max(image32(v[2], flip), image32(v[3], flip)));
-    }
-}
-
-// The sum over the workgroup of a count (two barriers).
-template <int B> __device__ inline uint32_t block_sum(uint32_t c, uint32_t *cells) {
-    c = wave_sum(c);
-    __syncthreads();
-    if (threadIdx.x % kLanes == 0) cells[threadIdx.x / kLanes] = c;
-    __syncthreads();
-    c = 0;
-    for (int w = 0; w < B / kLanes; ++w) c += cells[w];
-    return c;
-}
-
-// The candidates' places and their output, from buf[0, c), `want` of them wanted
-// (c <= CAP), no image above `top` or below `low`.  Few count the words above
-// theirs; more are dealt to bins in order first and count within their bin
-// (300 of 512 threads: 3 us by counting all).
-template <int W, int B, int CAP>
-__device__ void write_ranked(const TopArgs &a, uint64_t *buf, Bins &bins, uint32_t *cells, uint32_t c, uint32_t want, int top,
-                             int64_t low, uint64_t task, uint64_t row) {
-    const auto put = [&](uint64_t w, uint32_t place) {
-        if (a.splits == 1) {
-            const uint64_t at = row * a.k + place;
-            if (W == 2)
-                static_cast<uint16_t *>(a.values)[at] = static_cast<uint16_t>(pattern_of<2>(image_of(w), a.flip));
-            else
-                static_cast<uint32_t *>(a.values)[at] = pattern_of<4>(image_of(w), a.flip);
-            a.indices[at] = column_of(w);
-        } else {
-            a.words[task * a.k + place] = w;
-        }
-    };
-    const uint32_t tid = threadIdx.x;
-    if (c <= kRankWords) {
-        for (uint32_t i = tid; i < c; i += B) {
-            const uint64_t w = buf[i];
-            uint32_t place = 0;
-#pragma unroll 8
-            for (uint32_t j = 0; j < c; ++j) place += buf[j] > w;
-            if (place < want) put(w, place);
-        }
-    } else {
-        constexpr int kOwn = CAP / B, kShare = kBins / B;
-        clear_bins<B>(bins);
-        const uint32_t range = static_cast<uint32_t>(static_cast<int64_t>(top) - low);
-        const uint32_t shift = range < kBins ? 0 : 21 - __builtin_clz(range);
-        uint64_t w[kOwn];
-        uint32_t at[kOwn];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-            w[i] = i * B + tid < c ? buf[i * B + tid] : 0;
-            if (w[i]) at[i] = atomicAdd(&bins.fine[(static_cast<uint32_t>(top) - static_cast<uint32_t>(image_of(w[i]))) >> shift], 1u);
-        }
-        __syncthreads();
-        uint32_t held[kShare], sum = 0;
-#pragma unroll
-        for (int i = 0; i < kShare; ++i) sum += held[i] = bins.fine[tid * kShare + i];
-        const uint32_t upto = lanes_sum(sum);
-        if (tid % kLanes == kLanes - 1) cells[tid / kLanes] = upto;
-        __syncthreads();
-        uint32_t start = upto - sum;
-        for (uint32_t v = 0; v < tid / kLanes; ++v) start += cells[v];
-#pragma unroll
-        for (int i = 0; i < kShare; ++i) {
-            bins.fine[tid * kShare + i] = start;
-            start += held[i];
-        }
-        __syncthreads();
-        const auto bin_at = [&](uint64_t word) { return (static_cast<uint32_t>(top) - static_cast<uint32_t>(image_of(word))) >> shift; };
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i)
-            if (w[i]) buf[bins.fine[bin_at(w[i])] + at[i]] = w[i];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i)
-            if (w[i]) {
-                const uint32_t bin = bin_at(w[i]), from = bins.fine[bin], to = bin + 1 < kBins ? bins.fine[bin + 1] : c;
-                uint32_t place = from;
-                if (from < want)
-                    for (uint32_t j = from; j < to; ++j) place += buf[j] > w[i];
-                if (place < want) put(w[i], place);
-            }
-    }
-    if (a.splits > 1)
-        for (uint32_t j = want + tid; j < a.k; j += B) a.words[task * a.k + j] = 0;
-}
-
-// Whether the threads' largest elements give the bound: k of them at most half.
-constexpr int kBatch = 4;
-__host__ __device__ inline bool few_wanted(uint64_t want, uint64_t threads, uint64_t vecs) {
-    return 2 * want <= (threads < vecs ? threads : vecs);
-}
 
 // One workgroup of B threads a row (or a split of one), V loads of 16 bytes a
 // thread.  A histogram below the largest image, of the threads' largest images
@@ -725,12 +542,8 @@ template <int W, int B, int V, bool HOLD>
 __global__ __launch_bounds__(B, HOLD ? 4 : 8) void topk_held_kernel(TopArgs a) {
     constexpr int kVec = 16 / W;
     using Stored = typename Row<W == 2 ? kRowF16 : kRowF32>::Stored;
-    constexpr uint32_t kWords = HOLD ? kHeldWords : kHeldWords / 2;
-    __shared__ uint64_t buf[kWords];
-    __shared__ Bins bins;
+    __shared__ SelectLds<B, HOLD ? kHeldWords : kHeldWords / 2> lds;
     __shared__ int tops[B / kLanes];
-    __shared__ uint32_t cells[B / kLanes];
-    __shared__ uint32_t count;
     const uint32_t tid = threadIdx.x;
     const uint64_t task = a.first_task + xcd_chunk(blockIdx.x, gridDim.x);
     const uint64_t row = task / a.splits;
@@ -751,8 +564,8 @@ __global__ __launch_bounds__(B, HOLD ? 4 : 8) void topk_held_kernel(TopArgs a) {
     }
     const bool extra = rest < len;
     const int over = extra ? image<W>(x[rest], a.flip) : INT32_MIN;
-    clear_bins<B>(bins);
-    if (tid == 0) count = 0;
+    clear_bins<B>(lds.bins);
+    if (tid == 0) lds.count = 0;
 
     // the largest of each load (not held: two 16-bit images to a word), of all
     int most[HOLD || W == 4 ? V : V / 2], top = over;
@@ -786,14 +599,6 @@ __global__ __launch_bounds__(B, HOLD ? 4 : 8) void topk_held_kernel(TopArgs a) {
     __syncthreads();
     for (int w = 0; w < B / kLanes; ++w) top = max(top, tops[w]);
 
-    // f for every element of a load
-    const auto each = [&](u32x4 w, uint32_t at, auto f) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            const uint32_t pat = W == 2 ? (w[e / 2] >> (16 * (e & 1))) & 0xFFFFu : w[e % 4];
-            f(image<W>(pat, a.flip), at + e);
-        }
-    };
     const auto place_of = [&](int u) { return (u * B + tid) * kVec; };
     // each pass makes the images anew: kept, they would take twice the registers
     const auto anew = [&]() {
@@ -802,159 +607,59 @@ __global__ __launch_bounds__(B, HOLD ? 4 : 8) void topk_held_kernel(TopArgs a) {
     };
     anew();
     const bool by_thread = !HOLD || few_wanted(want, B, vecs);
-    uint32_t shift = W == 2 ? 0 : 13, bin;
-    for (;; shift += W == 2 ? 5 : 8) {  // at the second shift every image has a bin
+    const auto fill = [&](uint32_t shift) {
         if (by_thread) {
-            if (some) add_to_bins(bins, mine, top, shift);
+            if (some) add_to_bins(lds.bins, mine, top, shift);
         } else {
 #pragma unroll
             for (int u = 0; u < (HOLD ? V : 0); ++u)
-                if (below(u)) each(v[u], 0, [&](int img, uint32_t) { add_to_bins(bins, img, top, shift); });
-            if (extra) add_to_bins(bins, over, top, shift);
+                if (below(u)) each_image<W>(v[u], a.flip, 0, [&](int img, uint32_t) { add_to_bins(lds.bins, img, top, shift); });
+            if (extra) add_to_bins(lds.bins, over, top, shift);
         }
         anew();
-        __syncthreads();
-        bin = bin_of(bins, want);
-        if (bin < kBins) break;
-        __syncthreads();
-        clear_bins<B>(bins);
-        __syncthreads();
-    }
-    const int64_t low = static_cast<int64_t>(top) - ((static_cast<int64_t>(bin + 1) << shift) - 1);
-    int bound = static_cast<int>(max(low, static_cast<int64_t>(W == 2 ? -32768 : INT32_MIN)));
-
-    const auto take = [&](int img, uint32_t at) {
-        if (img >= bound) {
-            const uint32_t slot = atomicAdd(&count, 1u);
-            if (slot < kWords) buf[slot] = word_of(img, first + at);
+    };
+    const auto reach = [&](int bound, auto take) {
+        if (mine >= bound && some) {
+            if constexpr (HOLD) {
+#pragma unroll
+                for (int u = 0; u < V; ++u)
+                    if (most[u] >= bound && below(u)) each_image<W>(v[u], a.flip, place_of(u), take);
+            } else {
+                uint32_t hits = 0;  // loads that are read again: mostly one
+#pragma unroll
+                for (int u = 0; u < V; ++u) {
+                    const int m = W == 4 ? most[u] : u % 2 ? most[u / 2] >> 16 : static_cast<int16_t>(most[u / 2]);
+                    hits |= static_cast<uint32_t>(m >= bound && below(u)) << u;
+                }
+                while (hits) {
+                    const uint32_t at = (__builtin_ctz(hits) * B + tid) * kVec;
+                    hits &= hits - 1;
+                    each_image<W>(load16(x + at), a.flip, at, take);
+                }
+            }
+            if (extra) take(over, rest);
         }
     };
-    if (mine >= bound && some) {
-        if constexpr (HOLD) {
-#pragma unroll
-            for (int u = 0; u < V; ++u)
-                if (most[u] >= bound && below(u)) each(v[u], place_of(u), take);
-        } else {
-            uint32_t hits = 0;  // loads that are read again: mostly one
-#pragma unroll
-            for (int u = 0; u < V; ++u) {
-                const int m = W == 4 ? most[u] : u % 2 ? most[u / 2] >> 16 : static_cast<int16_t>(most[u / 2]);
-                hits |= static_cast<uint32_t>(m >= bound && below(u)) << u;
-            }
-            while (hits) {
-                const uint32_t at = (__builtin_ctz(hits) * B + tid) * kVec;
-                hits &= hits - 1;
-                each(load16(x + at), at, take);
-            }
-        }
-        if (extra) take(over, rest);
-    }
-    __syncthreads();
-    uint32_t c = count;
-    if (c > kWords) {  // rare: the row is read again
-        const auto again = [&](auto f) {
-            for (uint32_t i = tid; i < vecs; i += B) each(load16(x + i * kVec), i * kVec, f);
-            if (extra) f(over, rest);
-        };
-        // the k-th image: at least `want` reach lo, fewer pass hi
-        int lo = bound, hi = by_thread ? top : min(static_cast<int64_t>(top), low + (int64_t(1) << shift) - 1);
-        while (lo < hi) {
-            const int mid = (lo | hi) - ((lo ^ hi) >> 1);
-            uint32_t n = 0;
-            again([&](int img, uint32_t) { n += img >= mid; });
-            if (block_sum<B>(n, cells) >= want) lo = mid;
-            else hi = mid - 1;
-        }
-        __syncthreads();
-        if (tid == 0) count = 0;
-        __syncthreads();
-        if (lo < INT32_MAX) {
-            bound = lo + 1;
-            again(take);
-        }
-        bound = lo;
-        __syncthreads();
-        c = count;  // below `want`
-        // the first columns of image lo: stripe by stripe, in the order of threads
-        for (uint32_t base = 0; base <= vecs && c < want; base += B) {
-            const uint32_t i = base + tid;
-            // the elements after the last whole load are a stripe of their own threads' order
-            const bool in = i < vecs, last = base + B > vecs;
-            const u32x4 w = in ? load16(x + i * kVec) : u32x4{0, 0, 0, 0};
-            const auto fill = [&](bool on, auto elements) {
-                uint32_t here = 0;
-                if (on) elements([&](int img, uint32_t) { here += img == lo; });
-                const uint32_t upto = lanes_sum(here);
-                __syncthreads();
-                if (tid % kLanes == kLanes - 1) cells[tid / kLanes] = upto;
-                __syncthreads();
-                uint32_t at = c + upto - here, all = 0;
-                for (uint32_t w = 0; w < B / kLanes; ++w) {
-                    if (w < tid / kLanes) at += cells[w];
-                    all += cells[w];
-                }
-                if (on) elements([&](int img, uint32_t column) {
-                    if (img == lo) {
-                        if (at < want) buf[at] = word_of(lo, first + column);
-                        ++at;
-                    }
-                });
-                c = min(c + all, want);
-            };
-            fill(in, [&](auto f) { each(w, i * kVec, f); });
-            if (last) fill(extra, [&](auto f) { f(over, rest); });
-        }
-        __syncthreads();
-    }
-    write_ranked<W, B, kWords>(a, buf, bins, cells, c, want, top, bound, task, row);
+    const auto put = [&](uint64_t w, uint32_t place) {
+        if (a.splits == 1) put_word<W>(a, w, row * a.k + place);
+        else a.words[task * a.k + place] = w;
+    };
+    select_largest<W, B>(lds, x, len, first, a.flip, want, top, by_thread, fill, reach, put);
+    if (a.splits > 1)
+        for (uint32_t j = want + tid; j < a.k; j += B) a.words[task * a.k + j] = 0;
 }
 
-// The k largest of a row's splits * k words, by the same bound: 1 x 131072 fp32
-// in 16 splits takes 9 us with it, 37 us of sorting the words before.
+// The k largest of a row's splits * k words.
 constexpr int kMergeBlock = 1024;
 template <int W>
 __global__ __launch_bounds__(kMergeBlock) void topk_merge_kernel(TopArgs a) {
-    constexpr int B = kMergeBlock, V = kTopBuffer / B;
-    __shared__ uint64_t buf[kTopBuffer];
-    __shared__ Bins bins;
+    constexpr int B = kMergeBlock;
+    __shared__ SelectLds<B, kTopBuffer> lds;
     __shared__ int tops[B / kLanes];
-    __shared__ uint32_t cells[B / kLanes];
-    __shared__ uint32_t count;
     const uint64_t row = a.first_task + blockIdx.x;
-    const uint32_t tid = threadIdx.x, total = a.splits * a.k;  // at most kTopBuffer
+    const uint32_t total = a.splits * a.k;  // at most kTopBuffer
     const uint64_t *in = a.words + row * total;
-    uint64_t w[V];
-    int top = INT32_MIN;
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
-        w[u] = u * B + tid < total ? in[u * B + tid] : 0;
-        if (w[u]) top = max(top, image_of(w[u]));
-    }
-    clear_bins<B>(bins);
-    if (tid == 0) count = 0;
-    top = wave_max_int(top);
-    if (tid % kLanes == 0) tops[tid / kLanes] = top;
-    __syncthreads();
-    for (int i = 0; i < B / kLanes; ++i) top = max(top, tops[i]);
-    uint32_t shift = W == 2 ? 0 : 13, bin;
-    for (;; shift += W == 2 ? 5 : 8) {
-#pragma unroll
-        for (int u = 0; u < V; ++u)
-            if (w[u]) add_to_bins(bins, image_of(w[u]), top, shift);
-        __syncthreads();
-        bin = bin_of(bins, a.k);
-        if (bin < kBins) break;
-        __syncthreads();
-        clear_bins<B>(bins);
-        __syncthreads();
-    }
-    const int64_t low = static_cast<int64_t>(top) - ((static_cast<int64_t>(bin + 1) << shift) - 1);
-#pragma unroll
-    for (int u = 0; u < V; ++u)
-        if (w[u] && image_of(w[u]) >= low) buf[atomicAdd(&count, 1u)] = w[u];
-    __syncthreads();
-    a.splits = 1;  // what is written is the row
-    write_ranked<W, B, kTopBuffer>(a, buf, bins, cells, count, a.k, top, low, row, row);
+    merge_words<W, B>(lds, tops, in, total, a.k, [&](uint64_t w, uint32_t place) { put_word<W>(a, w, row * a.k + place); });
 }
 
 // Rows that one wave, or part of one, sorts in registers.
