@@ -23,11 +23,13 @@
 #include "../../include/lsd_radix_sort.h"
 #include "lrs_host.h"
 #include "lrs_rows.h"
+#include "lrs_select.h"
 
 namespace lrs {
 namespace {
 
 constexpr int kLogBlock = 256;
+constexpr uint32_t kPickWords = 1024;  // candidates in LDS, and words of a row's pieces
 constexpr double kLog2e = 1.44269504088896340736;
 constexpr double kLn2 = 0.693147180559945309417;
 constexpr uint32_t kLogStats = 3;
@@ -63,7 +65,10 @@ struct LogArgs {
     uint32_t k;
     const void *top_values;  // patterns of the top k
     float *top_logprobs;
-    double *row_log;      // [rows][2]: m and log2 Z, for the top k
+    double *lows;         // [rows]: log2 Z
+    int64_t *top_indices;
+    uint64_t *words;      // [rows][splits][k]
+    uint64_t first_task;  // of this launch
 };
 
 __device__ inline int64_t token_of(const LogArgs &a, uint64_t row) {
@@ -87,6 +92,16 @@ __device__ inline void rebase(double &z, double &w, float m, float to, float c) 
     z = s * z;
 }
 
+// log2 of a positive number: the hardware's of 32 bits, and the rest from
+// log(1 + e) = e - e^2 / 2 at e = v 2^-that - 1, below 2^-20.
+__device__ inline double log2_64(double v) {
+    int power;
+    const double f = frexp(v, &power);
+    const double y = __builtin_amdgcn_logf(static_cast<float>(f));
+    const double e = f * exp2(-y) - 1.0;
+    return v > 0 && v < INFINITY ? power + (y + fma(e * e, -0.5, e) * (1.0 / kLn2)) : log2(v);
+}
+
 // The row order of a 32-bit pattern as a signed number.
 __device__ inline int image_of_bits(uint32_t bits) {
     const int v = static_cast<int>(bits);
@@ -97,167 +112,395 @@ template <int T> __device__ inline uint32_t high_bits(typename Row<T>::Stored v)
     return T == kRowF32 ? v : static_cast<uint32_t>(v) << 16;
 }
 
-// One workgroup: the sums over a piece of a row.
-template <int T, bool RANK>
-__global__ __launch_bounds__(kLogBlock) void logprob_sum_kernel(LogArgs a) {
-    constexpr int kVec = Row<T>::kVec;
-    constexpr int kBatch = 4;
-    constexpr int kWaves = kLogBlock / kLanes;
-    using Stored = typename Row<T>::Stored;
-    __shared__ double wz[kWaves], ww[kWaves];
-    __shared__ float wm[kWaves];
-    __shared__ uint32_t wb[kWaves];
-    const float c = a.c;
-    for (uint64_t task = blockIdx.x; task < a.rows * a.splits; task += gridDim.x) {
-        const uint64_t row = task / a.splits;
-        const uint32_t first = static_cast<uint32_t>(task % a.splits) * a.split_len;
-        const uint32_t len = min(a.n - first, a.split_len), vecs = len / kVec;
-        const Stored *x = static_cast<const Stored *>(a.logits) + row * a.stride + first;
-        float m = kLowest;
-        double z = 0, w = 0;
-        uint32_t before = 0;
-        if (counted(a, row)) {
-            const int64_t token = RANK ? token_of(a, row) : -1;
-            const bool given = token >= 0 && token < a.n;
-            int mine = 0;
-            if (RANK && given) mine = image_of_bits(high_bits<T>((x - first)[token]));
-            const auto count = [&](Stored v, uint32_t at) {
-                const int img = image_of_bits(high_bits<T>(v));
-                before += img > mine || (img == mine && first + at < token);
-            };
-            const auto sum = [&](const float *f, int n) {
-                float top = m;
-                for (int e = 0; e < n; ++e) top = larger(top, f[e]);
-                rebase(z, w, m, top, c);
-                m = top;
-                float part = 0, part_w = 0;
-                for (int e = 0; e < n; ++e) {
-                    const float d = (f[e] - m) * c, p = __builtin_amdgcn_exp2f(d);
-                    part += p;
-                    part_w = fmaf(p, fmaxf(d, kZeroBelow), part_w);
-                }
-                z += part;
-                w += part_w;
-            };
-            for (uint32_t v = threadIdx.x; v < vecs; v += kBatch * kLogBlock) {
-                u32x4 t[kBatch];
-                float f[kBatch * kVec];
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const uint32_t at = min(v + u * kLogBlock, vecs - 1);
-                    t[u] = load16(x + static_cast<uint64_t>(at) * kVec);
-                }
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const uint32_t at = v + u * kLogBlock;
-                    float g[kVec];
-                    unpack16<T>(t[u], g);
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e) {
-                        f[u * kVec + e] = at < vecs ? g[e] : -INFINITY;
-                        if (RANK && given && at < vecs)
-                            count(T == kRowF32 ? t[u][e % 4] : static_cast<Stored>(t[u][e / 2] >> (16 * (e & 1))), at * kVec + e);
-                    }
-                }
-                sum(f, kBatch * kVec);
-            }
-            const uint32_t rest = vecs * kVec + threadIdx.x;
-            if (rest < len) {
-                const float f = Row<T>::value(x[rest]);
-                if (RANK && given) count(x[rest], rest);
-                sum(&f, 1);
-            }
-        }
-        // the threads' sums, relative to the largest logit of all
-        const auto join = [](float p, float q) { return larger(p, q); };
-        float top = wave_join(m, kLowest, join);
-        __syncthreads();
-        if (threadIdx.x % kLanes == 0) wm[threadIdx.x / kLanes] = top;
-        __syncthreads();
-        for (int i = 0; i < kWaves; ++i) top = larger(top, wm[i]);
-        rebase(z, w, m, top, c);
-        z = wave_sum(z);
-        w = wave_sum(w);
-        before = wave_sum(before);
-        if (threadIdx.x % kLanes == 0) {
-            wz[threadIdx.x / kLanes] = z;
-            ww[threadIdx.x / kLanes] = w;
-            wb[threadIdx.x / kLanes] = before;
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int i = 1; i < kWaves; ++i) {
-                z += wz[i];
-                w += ww[i];
-                before += wb[i];
-            }
-            a.sums[task] = Sums{z, w, top, before};
-        }
-    }
-}
-
-// What a row's sums say: a thread's whole work.
-template <int T> __device__ inline void finish_row(const LogArgs &a, uint64_t row, double z, double w, float m, uint32_t before) {
-    using Stored = typename Row<T>::Stored;
-    const bool on = counted(a, row), empty = z == 0;
-    const int64_t token = token_of(a, row);
-    const bool given = token >= 0 && token < a.n;
-    const double low = log2(z), mean = w / z;
+// What a row's sums say, by one thread: its numbers, and log2 Z for the top k.
+struct RowEnd {
+    double low;    // log2 Z, infinity where the row is all -inf
+    double mean;   // D
+    double share;  // 1 / Z, 0 where the row counts for nothing
+};
+__device__ inline RowEnd finish_row(const LogArgs &a, uint64_t row, bool on, bool given, float x, double z, double w, float m,
+                                    uint32_t before) {
+    const bool empty = z == 0;
+    const double low = log2_64(z), mean = w / z;
     double logprob = 0, entropy = 0;
     if (on) {
         entropy = empty ? 0 : kLn2 * (low - mean);
-        if (given) {
-            const float x = Row<T>::value(static_cast<const Stored *>(a.logits)[row * a.stride + token]);
-            logprob = empty ? -INFINITY : kLn2 * ((static_cast<double>(x) - m) * a.factor - low);
-        }
+        if (given) logprob = empty ? -INFINITY : kLn2 * ((static_cast<double>(x) - m) * a.factor - low);
     }
     a.logprobs[row] = static_cast<float>(logprob);
     a.entropy[row] = static_cast<float>(entropy);
     if (a.ranks) a.ranks[row] = given ? static_cast<int32_t>(before) : -1;
+    const RowEnd end{empty ? INFINITY : low, !on || empty ? 0 : mean, !on || empty ? 0 : 1 / z};
     if (a.stats) {
         float *s = a.stats + row * kLogStats;
         s[0] = m;
-        s[1] = !on || empty ? 0.f : static_cast<float>(1 / z);
-        s[2] = !on || empty ? 0.f : static_cast<float>(mean);
+        s[1] = static_cast<float>(end.share);
+        s[2] = static_cast<float>(end.mean);
     }
-    if (a.row_log) {
-        a.row_log[2 * row] = m;
-        a.row_log[2 * row + 1] = empty ? INFINITY : low;
-    }
+    if (a.lows) a.lows[row] = end.low;
+    return end;
+}
+// log p of a logit.
+__device__ inline float logprob_of(const LogArgs &a, float x, float m, double low) {
+    return static_cast<float>(kLn2 * ((static_cast<double>(x) - m) * a.factor - low));
 }
 
-// One wave a row: the pieces' sums joined.
-template <int T>
-__global__ __launch_bounds__(kLanes) void logprob_row_kernel(LogArgs a) {
-    for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        float m = kLowest;
-        for (uint32_t s = threadIdx.x; s < a.splits; s += kLanes) m = larger(m, a.sums[row * a.splits + s].m);
-        m = wave_join(m, kLowest, [](float p, float q) { return larger(p, q); });
-        double z = 0, w = 0;
-        uint32_t before = 0;
-        for (uint32_t s = threadIdx.x; s < a.splits; s += kLanes) {
-            Sums p = a.sums[row * a.splits + s];
-            rebase(p.z, p.w, p.m, m, a.c);
-            z += p.z;
-            w += p.w;
-            before += p.before;
+template <int T> __device__ inline void put_top(const LogArgs &a, uint64_t word, uint64_t at, float m, double low) {
+    const uint32_t p = pattern_of<T == kRowF32 ? 4 : 2>(image_of(word), 0);
+    a.top_logprobs[at] = logprob_of(a, Row<T>::value(static_cast<typename Row<T>::Stored>(p)), m, low);
+    a.top_indices[at] = column_of(word);
+}
+
+// A thread's sums of 2^(x c - r), r its largest logit times c, over batches of
+// loads.  r is a number of 32 bits, and a product less r is rounded once, so that
+// sums of different references join exactly, whatever the rounding of r.  Past
+// 2^29 that rounding could be more than a power holds: rows with such a largest
+// logit (masks of the type's lowest value that fill a row) are summed anew.
+constexpr float kLeastReference = -0x1p30f;
+constexpr float kHugeReference = 0x1p29f;
+template <typename Acc> struct Running {
+    Acc z = 0, w = 0;
+    float top = -INFINITY, r = kLeastReference;
+    __device__ void move(float to) {
+        const float d = fmaxf(r - to, kZeroBelow), s = __builtin_amdgcn_exp2f(d);
+        w = s * (w + z * static_cast<Acc>(d));
+        z = s * z;
+        r = to;
+    }
+    // elements of which `most` is the largest
+    template <int N> __device__ void add(const float (&f)[N], float most, float c) {
+        top = larger(top, most);
+        move(fmaxf(top * c, kLeastReference));
+        float part = 0, part_w = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float d = fmaf(f[e], c, -r), p = __builtin_amdgcn_exp2f(d);
+            part += p;
+            part_w = fmaf(p, fmaxf(d, kZeroBelow), part_w);
         }
-        z = wave_sum(z);
-        w = wave_sum(w);
-        before = wave_sum(before);
-        if (threadIdx.x == 0) finish_row<T>(a, row, z, w, m, before);
+        z += part;
+        w += part_w;
+    }
+};
+__device__ inline bool huge(float top, float c) { return fabsf(top) < INFINITY && !(fabsf(top * c) < kHugeReference); }
+
+template <int N> __device__ inline float largest(const float (&f)[N]) {
+    float m = f[0];
+#pragma unroll
+    for (int e = 1; e + 1 < N; e += 2) m = larger(larger(m, f[e]), f[e + 1]);
+    return N % 2 == 0 ? larger(m, f[N - 1]) : m;
+}
+
+template <int B> struct JoinLds {
+    double z[B / kLanes], w[B / kLanes];
+    float top[B / kLanes];
+    uint32_t before[B / kLanes];
+};
+// The workgroup's sums relative to its largest logit, in its first thread;
+// anew(m) gives a thread's sums relative to a huge m.
+template <int B, typename Acc, typename Anew>
+__device__ inline Sums join_sums(JoinLds<B> &lds, Running<Acc> &mine, float &top, uint32_t before_of_wave, float c, Anew anew) {
+    constexpr int kWaves = B / kLanes;
+    const int wave = threadIdx.x / kLanes;
+    top = wave_join(mine.top, -INFINITY, [](float p, float q) { return larger(p, q); });
+    if (kWaves > 1) {
+        if (threadIdx.x % kLanes == 0) lds.top[wave] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) top = larger(top, lds.top[i]);
+    }
+    Sums s{};
+    s.m = top == -INFINITY ? kLowest : top;
+    float shift = 0;
+    if (huge(top, c)) {
+        const double2 sum = anew(top);
+        s.z = sum.x;
+        s.w = sum.y;
+    } else {
+        const float r = fmaxf(top * c, kLeastReference);
+        mine.move(r);
+        s.z = mine.z;
+        s.w = mine.w;
+        shift = static_cast<float>(static_cast<double>(top) * c - r);  // of exponents, to be relative to top itself
+    }
+    s.z = wave_sum(s.z);
+    s.w = wave_sum(s.w);
+    s.before = before_of_wave;
+    if (kWaves > 1) {
+        if (threadIdx.x % kLanes == 0) {
+            lds.z[wave] = s.z;
+            lds.w[wave] = s.w;
+            lds.before[wave] = s.before;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int i = 1; i < kWaves; ++i) {
+                s.z += lds.z[i];
+                s.w += lds.w[i];
+                s.before += lds.before[i];
+            }
+    }
+    if (fabsf(shift) < INFINITY && shift != 0) {
+        const double p = __builtin_amdgcn_exp2f(-shift);
+        s.w = p * (s.w - s.z * shift);
+        s.z = p * s.z;
+    }
+    return s;
+}
+
+// What a row, or a piece of one, holds of the row order around its token.
+template <int T> struct Token {
+    using Stored = typename Row<T>::Stored;
+    int64_t at;
+    bool given, exact;   // exact: its order takes the patterns
+    float x, from, least;  // its logit; what later columns are above, and earlier ones
+    Stored pattern;
+    __device__ Token(const LogArgs &a, uint64_t row) {
+        at = token_of(a, row);
+        given = at >= 0 && at < a.n;
+        pattern = given ? static_cast<const Stored *>(a.logits)[row * a.stride + at] : 0;
+        x = Row<T>::value(pattern);
+        // a number of 32 bits is at least x where it is above the one before x
+        const uint32_t bits = __builtin_bit_cast(uint32_t, x);
+        from = x;
+        least = __builtin_bit_cast(float, x > 0 ? bits - 1 : bits + 1);
+        exact = given && !(fabsf(x) > 0 && x > -INFINITY);
+    }
+    // Whether an element comes before it.
+    __device__ bool after(Stored v, uint32_t column) const {
+        const int i = image_of_bits(high_bits<T>(v)), mine = image_of_bits(high_bits<T>(pattern));
+        return i > mine || (i == mine && column < at);
+    }
+};
+
+// One workgroup of B threads a row, or a piece of one.  PICK: V loads a thread
+// at most, whose largest elements are kept, and the alternatives are selected
+// from them as segmented_row_topk does; loads that reach the bound are read
+// again.  Else a row may have any length.
+template <int T, int B, int V, bool RANK>
+__global__ __launch_bounds__(B, B == 64 && V > 0 ? 3 : 8) void logprob_kernel(LogArgs a) {
+    constexpr int kVec = Row<T>::kVec, kLoads = 4, kWidth = T == kRowF32 ? 4 : 2;
+    constexpr bool kPick = V > 0;
+    using Stored = typename Row<T>::Stored;
+    __shared__ JoinLds<B> join;
+    __shared__ SelectLds<B, kPick ? kPickWords : B> lds;
+    __shared__ RowEnd end;
+    const uint32_t tid = threadIdx.x;
+    const uint64_t task = a.first_task + xcd_chunk(blockIdx.x, gridDim.x);
+    const uint64_t row = task / a.splits;
+    const uint32_t first = static_cast<uint32_t>(task % a.splits) * a.split_len;
+    const bool on = counted(a, row);
+    const uint32_t len = on ? min(a.n - first, a.split_len) : 0, vecs = len / kVec, rest = vecs * kVec + tid;
+    const Stored *x = static_cast<const Stored *>(a.logits) + row * a.stride + first;
+    const uint32_t none = T == kRowF16 ? 0xFC00FC00u : T == kRowBF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+    const auto load = [&](uint32_t v) {
+        u32x4 t{none, none, none, none};
+        if (v < vecs) t = kPick ? load16(x + static_cast<uint64_t>(v) * kVec) : load16_once(x + static_cast<uint64_t>(v) * kVec);
+        return t;
+    };
+    const Token<T> token(a, row);
+    const bool ranked = RANK && token.given && !token.exact;
+    const float c = a.c;
+    uint32_t before = 0;  // of the wave
+    int most[kPick ? (kWidth == 4 ? V : V / 2) : 1];
+    Running<std::conditional_t<kPick, float, double>> mine;
+    const auto batch = [&](uint32_t base, int keep) {
+        u32x4 t[kLoads];
+        float f[kLoads * kVec], top[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) t[u] = load(base + u * B + tid);
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            float g[kVec];
+            unpack16<T>(t[u], g);
+            top[u] = largest(g);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) f[u * kVec + e] = g[e];
+            if constexpr (kPick) {
+                const uint32_t p = Row<T>::pattern(top[u]);
+                const int m = image<kWidth>(p, 0);
+                if (kWidth == 4) most[keep + u] = m;
+                else if (u % 2 == 0) most[(keep + u) / 2] = m & 0xFFFF;
+                else most[(keep + u) / 2] |= m << 16;
+            }
+        }
+        const float all = largest(top);
+        if (RANK && ranked && __ballot(!(all < token.x))) {
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                const int64_t last = static_cast<int64_t>(first) + static_cast<int64_t>(base + u * B + tid + 1) * kVec;
+                const float bound = last <= token.at ? token.least : token.from;
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) before += __popcll(__ballot(f[u * kVec + e] > bound));
+            }
+        }
+        mine.add(f, all, c);
+    };
+    if constexpr (kPick) {
+#pragma unroll
+        for (int b = 0; b < V; b += kLoads) {
+            if (b * B < static_cast<int>(vecs)) {
+                batch(b * B, b);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    if (kWidth == 4) most[b + u] = INT32_MIN;
+                    else most[(b + u) / 2] = static_cast<int>(0x80008000u);
+                }
+            }
+        }
+    } else {
+#pragma unroll 1
+        for (uint32_t b = 0; b < vecs; b += kLoads * B) batch(b, 0);
+    }
+    const bool extra = rest < len;
+    float over = -INFINITY;
+    if (len > vecs * kVec) {  // the elements after the last whole load
+        Stored v = 0;
+        if (extra) {
+            v = x[rest];
+            over = Row<T>::value(v);
+        }
+        if (RANK && ranked) before += __popcll(__ballot(extra && token.after(v, first + rest)));
+        const float f[1] = {over};
+        mine.add(f, over, c);
+    }
+    if (RANK && token.given) {
+        const int64_t at = token.at - first;
+        if (token.exact || __ballot(__builtin_isnan(mine.top))) {  // by their patterns, from a second read
+            before = 0;
+            for (uint32_t v = tid; v - tid < vecs; v += B) {
+                uint32_t n = 0;
+                if (v < vecs)
+                    for (int e = 0; e < kVec; ++e) n += token.after(x[static_cast<uint64_t>(v) * kVec + e], first + v * kVec + e);
+                before += wave_sum(n);
+            }
+            before += __popcll(__ballot(extra && token.after(extra ? x[rest] : Stored(0), first + rest)));
+        } else if (at >= 0 && at < static_cast<int64_t>(vecs) * kVec && at / kVec % B / kLanes == tid / kLanes) {
+            // equal ones of the token's own load, before it: the wave that has that
+            const bool here = tid % kLanes < at % kVec;
+            before += __popcll(__ballot(here && x[here ? at - at % kVec + tid % kLanes : 0] == token.pattern));
+        }
+    }
+    float top;  // of the workgroup
+    const Sums s = join_sums<B>(join, mine, top, before, c, [&](float m) {
+        double z = 0, w = 0;
+        const auto add = [&](float f) {
+            const float d = (f - m) * c, p = __builtin_amdgcn_exp2f(d);
+            z += p;
+            w += p * fmaxf(d, kZeroBelow);
+        };
+        for (uint32_t v = tid; v < vecs; v += B) {
+            float f[kVec];
+            unpack16<T>(load(v), f);
+            for (int e = 0; e < kVec; ++e) add(f[e]);
+        }
+        if (extra) add(over);
+        return double2{z, w};
+    });
+    if (tid == 0) {
+        if (a.splits == 1) end = finish_row(a, row, on, token.given, token.x, s.z, s.w, s.m, s.before);
+        else a.sums[task] = s;
+    }
+    if constexpr (kPick) {
+        __shared__ int tops[B / kLanes];
+        int mine_image = image<kWidth>(Row<T>::pattern(mine.top), 0), top_image = image<kWidth>(Row<T>::pattern(top), 0);
+        const int over_image = extra ? image<kWidth>(x[rest], 0) : INT32_MIN;
+        const bool some = extra || tid < vecs;
+        if (__builtin_isnan(top)) {  // NaNs have an order among themselves, by their patterns
+            mine_image = over_image;
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                const bool in = u * B + tid < vecs;
+                const int m = in ? vec_max<kWidth>(load(u * B + tid), 0) : kWidth == 2 ? -32768 : INT32_MIN;
+                if (in) mine_image = max(mine_image, m);
+                if (kWidth == 4) most[u] = m;
+                else if (u % 2 == 0) most[u / 2] = m & 0xFFFF;
+                else most[u / 2] |= m << 16;
+            }
+            top_image = wave_max_int(mine_image);
+            if (tid % kLanes == 0) tops[tid / kLanes] = top_image;
+            __syncthreads();
+            for (int i = 0; i < B / kLanes; ++i) top_image = max(top_image, tops[i]);
+        }
+        clear_bins<B>(lds.bins);
+        if (tid == 0) lds.count = 0;
+        __syncthreads();
+        const auto fill = [&](uint32_t shift) {
+            if (some) add_to_bins(lds.bins, mine_image, top_image, shift);
+        };
+        const auto reach = [&](int bound, auto take) {
+            if (mine_image >= bound && some) {
+                uint32_t hits = 0;  // loads that are read again: mostly one
+#pragma unroll
+                for (int u = 0; u < V; ++u) {
+                    const int m = kWidth == 4 ? most[u] : u % 2 ? most[u / 2] >> 16 : static_cast<int16_t>(most[u / 2]);
+                    hits |= static_cast<uint32_t>(m >= bound && u * B + tid < vecs) << u;
+                }
+                while (hits) {
+                    const uint32_t at = (__builtin_ctz(hits) * B + tid) * kVec;
+                    hits &= hits - 1;
+                    each_image<kWidth>(load16(x + at), 0, at, take);
+                }
+                if (extra) take(over_image, rest);
+            }
+        };
+        const auto put = [&](uint64_t w, uint32_t place) {
+            if (a.splits == 1) put_top<T>(a, w, row * a.k + place, s.m, end.low);
+            else a.words[task * a.k + place] = w;
+        };
+        select_largest<kWidth, B>(lds, x, len, first, 0, a.k, top_image, true, fill, reach, put);
     }
 }
 
-// Patterns of the top logits to log probabilities.
+// The rows' pieces joined, a workgroup each: their sums, and of their words the
+// first k.
+template <int T, bool PICK>
+__global__ __launch_bounds__(PICK ? kLogBlock : kLanes) void logprob_join_kernel(LogArgs a) {
+    constexpr int B = PICK ? kLogBlock : kLanes, kWidth = T == kRowF32 ? 4 : 2;
+    __shared__ SelectLds<B, PICK ? kPickWords : B> lds;
+    __shared__ int tops[B / kLanes];
+    __shared__ RowEnd end;
+    __shared__ float most;
+    for (uint64_t row = a.first_task + blockIdx.x; row < a.rows; row += gridDim.x) {
+        if (threadIdx.x < kLanes) {
+            const Token<T> token(a, row);
+            float m = kLowest;
+            for (uint32_t s = threadIdx.x; s < a.splits; s += kLanes) m = larger(m, a.sums[row * a.splits + s].m);
+            m = wave_join(m, kLowest, [](float p, float q) { return larger(p, q); });
+            double z = 0, w = 0;
+            uint32_t before = 0;
+            for (uint32_t s = threadIdx.x; s < a.splits; s += kLanes) {
+                Sums p = a.sums[row * a.splits + s];
+                rebase(p.z, p.w, p.m, m, a.c);
+                z += p.z;
+                w += p.w;
+                before += p.before;
+            }
+            z = wave_sum(z);
+            w = wave_sum(w);
+            before = wave_sum(before);
+            if (threadIdx.x == 0) {
+                end = finish_row(a, row, counted(a, row), token.given, token.x, z, w, m, before);
+                most = m;
+            }
+        }
+        if constexpr (PICK)
+            merge_words<kWidth, B>(lds, tops, a.words + row * a.splits * a.k, a.splits * a.k, a.k,
+                                   [&](uint64_t w, uint32_t place) { put_top<T>(a, w, row * a.k + place, most, end.low); });
+        __syncthreads();
+    }
+}
+
+// The first k of a row sort, as segmented_row_topk gave them, to log probabilities.
 template <int T>
 __global__ __launch_bounds__(kLogBlock) void logprob_top_kernel(LogArgs a) {
     const uint64_t all = a.rows * a.k;
     for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kLogBlock + threadIdx.x; i < all;
          i += static_cast<uint64_t>(gridDim.x) * kLogBlock) {
-        const double *of = a.row_log + 2 * (i / a.k);
-        const double x = Row<T>::value(static_cast<const typename Row<T>::Stored *>(a.top_values)[i]);
-        a.top_logprobs[i] = static_cast<float>(kLn2 * ((x - of[0]) * a.factor - of[1]));
+        const float *s = a.stats + i / a.k * kLogStats;
+        const float x = Row<T>::value(static_cast<const typename Row<T>::Stored *>(a.top_values)[i]);
+        a.top_logprobs[i] = logprob_of(a, x, s[0], a.lows[i / a.k]);
     }
 }
 
@@ -305,9 +548,46 @@ __global__ __launch_bounds__(kLogBlock) void logprob_grad_kernel(LogArgs a) {
 
 constexpr uint64_t kMaxGrid = 1u << 20;
 
-// How many workgroups share a row: enough that few rows still fill the GPU,
-// each with a piece worth a workgroup.
-void logprob_split(uint64_t rows, uint64_t n, uint32_t &splits, uint32_t &len) {
+// How the rows are laid out on workgroups: as many threads a row as it has loads
+// for, and several workgroups where rows are fewer than would fill the GPU.
+// With alternatives (k > 0) a workgroup holds at most 16 loads a thread, k is at
+// most half of its threads, and the pieces' words fit one workgroup; where that
+// cannot be (fused false) segmented_row_topk selects them.
+struct LogPlan {
+    int block = kLogBlock, loads = 0;  // loads: of a thread, with alternatives
+    uint32_t splits = 1, len = 8;
+    bool fused = true;
+};
+LogPlan logprob_plan(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
+    LogPlan p;
+    const uint64_t vec = 16 / size, vecs = n / vec;
+    const auto pieces = [&](uint64_t s) {
+        p.len = static_cast<uint32_t>(std::max<uint64_t>(8, ((n + s - 1) / s + 7) / 8 * 8));
+        p.splits = static_cast<uint32_t>(std::max<uint64_t>(1, (n + p.len - 1) / p.len));
+    };
+    if (rows >= 512) {
+        // a wave for up to 4 KB; 1024 threads for more than 64 KB
+        p.block = vecs <= 64 * 4 ? 64 : vecs <= 256 * 16 ? 256 : 1024;
+        pieces(k > 0 ? std::max<uint64_t>(1, (vecs + 16 * 1024 - 1) / (16 * 1024)) : std::max<uint64_t>(1, n >> 20));
+    } else {
+        // pieces of 4 loads a thread, or more of them where there would be more than some 1024
+        uint64_t s = std::max<uint64_t>(1, (vecs + 4 * 256 - 1) / (4 * 256));
+        s = std::min<uint64_t>(s, std::max<uint64_t>(1, 1024 / std::max<uint64_t>(1, rows)));
+        if (k > 0) s = std::min<uint64_t>(s, std::max<uint64_t>(1, kPickWords / k));
+        pieces(s);
+        if (k > 0 && p.len / vec > 16 * 256) p.block = 1024;
+    }
+    if (k > 0) {
+        const uint64_t most = p.len / vec, least = (n - (p.splits - 1) * uint64_t(p.len)) / vec;
+        p.loads = most <= 4 * uint64_t(p.block) && p.block != 1024 ? 4 : 16;
+        p.fused = most <= 16 * uint64_t(p.block) && few_wanted(k, p.block, least) && (p.splits == 1 || p.splits * k <= kPickWords) &&
+                  (p.block != 64 || p.loads == 4);
+    }
+    return p;
+}
+
+// How many workgroups share a row of the gradient, whose elements are independent.
+void gradient_split(uint64_t rows, uint64_t n, uint32_t &splits, uint32_t &len) {
     uint64_t s = 1;
     if (rows < 2048) s = std::min<uint64_t>((2048 + rows - 1) / std::max<uint64_t>(rows, 1), n / 8192);
     s = std::max<uint64_t>(1, s);
@@ -323,26 +603,30 @@ int check_sizes(int64_t rows, int64_t n, int64_t k, int dtype) {
     return LRS_OK;
 }
 struct LogSpace {
-    uint64_t sums = 0, stats = 0, row_log = 0, values = 0, sort = 0, sort_bytes = 0, total = 0;
+    uint64_t sums = 0, stats = 0, lows = 0, words = 0, values = 0, sort = 0, sort_bytes = 0, total = 0;
 };
 LogSpace logprob_space(uint64_t rows, uint64_t n, uint64_t k, int dtype) {
     LogSpace w;
     if (rows == 0) return w;
-    uint32_t splits, len;
-    logprob_split(rows, n, splits, len);
     auto place = [&](uint64_t bytes) {
         const uint64_t at = w.total;
         w.total += (bytes + 255) / 256 * 256;
         return at;
     };
-    w.sums = place(rows * splits * sizeof(Sums));
-    w.stats = place(rows * kLogStats * sizeof(float));
-    if (k > 0) {
-        w.row_log = place(rows * 2 * sizeof(double));
-        w.values = place(rows * k * row_type_size(dtype));
+    const uint64_t size = row_type_size(dtype);
+    const LogPlan p = logprob_plan(rows, n, k, size);
+    if (p.fused) {
+        if (p.splits > 1) w.sums = place(rows * p.splits * sizeof(Sums));
+        if (p.splits > 1) w.words = place(rows * p.splits * k * sizeof(uint64_t));
+    } else {
+        const LogPlan q = logprob_plan(rows, n, 0, size);
+        if (q.splits > 1) w.sums = place(rows * q.splits * sizeof(Sums));
+        w.lows = place(rows * sizeof(double));
+        w.values = place(rows * k * size);
         w.sort_bytes = segmented_row_topk_workspace_size(rows, n, k, dtype, nullptr);
         w.sort = place(w.sort_bytes);
     }
+    if (k == 0 || !p.fused) w.stats = place(rows * kLogStats * sizeof(float));
     return w;
 }
 
@@ -370,7 +654,6 @@ int logprob_inputs(const lrs_logprobs *d, int64_t k, LogArgs &a) {
     // above 0, so that -inf times it is -inf
     a.c = std::max(static_cast<float>(a.factor), std::numeric_limits<float>::denorm_min());
     a.k = static_cast<uint32_t>(k);
-    logprob_split(a.rows, a.n, a.splits, a.split_len);
     return LRS_OK;
 }
 
@@ -400,22 +683,47 @@ template <typename F> void by_type(int type, F f) {
 bool launched() { return hipGetLastError() == hipSuccess; }
 dim3 grid_of(uint64_t tasks) { return dim3(static_cast<uint32_t>(std::min<uint64_t>(tasks, kMaxGrid))); }
 
-int logprob_sums(const LogArgs &a, int dtype, const Ctx &c) {
-    if (a.rows == 0) return LRS_OK;
-    {
-        TimedLaunch t(4, c);
-        by_type(dtype, [&](auto i) {
-            launch_on(a.ranks ? logprob_sum_kernel<i.value, true> : logprob_sum_kernel<i.value, false>, grid_of(a.rows * a.splits),
-                      dim3(kLogBlock), t.L, a);
-        });
+template <int T, bool PICK, bool RANK> void launch_plan(const LogPlan &p, const LogArgs &a, uint32_t tasks, const Launch &L) {
+    const auto go = [&](auto kernel, int block) { launch_on(kernel, dim3(tasks), dim3(block), L, a); };
+    if constexpr (PICK) {
+        if (p.block == 64) go(logprob_kernel<T, 64, 4, true>, 64);
+        else if (p.block == 256 && p.loads == 4) go(logprob_kernel<T, 256, 4, true>, 256);
+        else if (p.block == 256) go(logprob_kernel<T, 256, 16, true>, 256);
+        else go(logprob_kernel<T, 1024, 16, true>, 1024);
+    } else {
+        if (p.block == 64) go(logprob_kernel<T, 64, 0, RANK>, 64);
+        else if (p.block == 256) go(logprob_kernel<T, 256, 0, RANK>, 256);
+        else go(logprob_kernel<T, 1024, 0, RANK>, 1024);
     }
-    if (!launched()) return LRS_ERR_HIP;
+}
+
+// The rows' numbers, and with a plan that has room for them the alternatives.
+int logprob_values(LogArgs a, const LogPlan &p, int dtype, const Ctx &c) {
+    a.splits = p.splits;
+    a.split_len = p.len;
+    const uint64_t tasks = a.rows * a.splits;
+    for (a.first_task = 0; a.first_task < tasks; a.first_task += kMaxGrid) {
+        TimedLaunch t(4, c);
+        const uint32_t now = static_cast<uint32_t>(std::min<uint64_t>(tasks - a.first_task, kMaxGrid));
+        by_type(dtype, [&](auto i) {
+            if (p.loads > 0) launch_plan<i.value, true, true>(p, a, now, t.L);
+            else if (a.ranks) launch_plan<i.value, false, true>(p, a, now, t.L);
+            else launch_plan<i.value, false, false>(p, a, now, t.L);
+        });
+        if (!launched()) return LRS_ERR_HIP;
+    }
+    if (a.splits == 1) return LRS_OK;
+    a.first_task = 0;
     TimedLaunch t(4, c);
-    by_type(dtype, [&](auto i) { launch_on(logprob_row_kernel<i.value>, grid_of(a.rows), dim3(kLanes), t.L, a); });
+    by_type(dtype, [&](auto i) {
+        if (p.loads > 0) launch_on(logprob_join_kernel<i.value, true>, grid_of(a.rows), dim3(kLogBlock), t.L, a);
+        else launch_on(logprob_join_kernel<i.value, false>, grid_of(a.rows), dim3(kLanes), t.L, a);
+    });
     return launched() ? LRS_OK : LRS_ERR_HIP;
 }
-int logprob_gradient(const LogArgs &a, int dtype, const Ctx &c) {
+int logprob_gradient(LogArgs a, int dtype, const Ctx &c) {
     if (a.rows == 0 || a.n == 0) return LRS_OK;
+    gradient_split(a.rows, a.n, a.splits, a.split_len);
     TimedLaunch t(4, c);
     by_type(dtype, [&](auto i) { launch_on(logprob_grad_kernel<i.value>, grid_of(a.rows * a.splits), dim3(kLogBlock), t.L, a); });
     return launched() ? LRS_OK : LRS_ERR_HIP;
@@ -454,7 +762,7 @@ int token_logprobs_forward(const lrs_logprobs *in, float *logprobs, float *entro
     a.entropy = entropy;
     a.stats = row_stats;
     c.elems = a.rows * a.n;
-    return logprob_sums(a, in->dtype, c);
+    return logprob_values(a, logprob_plan(a.rows, a.n, 0, row_type_size(in->dtype)), in->dtype, c);
 } catch (...) {
     return LRS_ERR_HIP;
 }
@@ -479,19 +787,25 @@ int token_logprobs_topk(const lrs_logprobs *in, int64_t k, float *logprobs, floa
     const uint64_t bytes[] = {4 * a.rows, 4 * a.rows, 4 * a.rows, 4 * a.rows * a.k, 8 * a.rows * a.k, w.total};
     if (aliased(in, out, bytes)) return LRS_ERR_ALIASING;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const uint64_t size = row_type_size(in->dtype);
+    const LogPlan p = logprob_plan(a.rows, a.n, a.k, size);
     a.sums = reinterpret_cast<Sums *>(ws + w.sums);
+    a.words = reinterpret_cast<uint64_t *>(ws + w.words);
     a.logprobs = logprobs;
     a.entropy = entropy;
     a.ranks = ranks;
-    a.row_log = k > 0 ? reinterpret_cast<double *>(ws + w.row_log) : nullptr;
+    a.top_logprobs = top_logprobs;
+    a.top_indices = top_indices;
     c.elems = a.rows * a.n;
-    int fs = logprob_sums(a, in->dtype, c);
-    if (fs != LRS_OK || k == 0) return fs;
+    if (p.fused) return logprob_values(a, p, in->dtype, c);
+    a.stats = reinterpret_cast<float *>(ws + w.stats);
+    a.lows = reinterpret_cast<double *>(ws + w.lows);
+    int fs = logprob_values(a, logprob_plan(a.rows, a.n, 0, size), in->dtype, c);
+    if (fs != LRS_OK) return fs;
     fs = segmented_row_topk(a.logits, in->row_stride, ws + w.values, top_indices, in->rows, in->n, k, in->dtype, 1, ws + w.sort,
                             w.sort_bytes, stream, opts);
     if (fs != LRS_OK) return fs;
     a.top_values = ws + w.values;
-    a.top_logprobs = top_logprobs;
     TimedLaunch t(4, c);
     by_type(in->dtype, [&](auto i) {
         launch_on(logprob_top_kernel<i.value>, grid_of((a.rows * a.k + kLogBlock - 1) / kLogBlock), dim3(kLogBlock), t.L, a);
@@ -562,7 +876,7 @@ int token_logprobs_step(const lrs_logprobs *in, const float *logprob_grad, const
     a.grad = grad;
     a.grad_stride = grad_stride;
     c.elems = a.rows * a.n;
-    const int fs = logprob_sums(a, in->dtype, c);
+    const int fs = logprob_values(a, logprob_plan(a.rows, a.n, 0, size), in->dtype, c);
     return fs != LRS_OK ? fs : logprob_gradient(a, in->dtype, c);
 } catch (...) {
     return LRS_ERR_HIP;
