@@ -29,7 +29,10 @@ namespace lrs {
 namespace {
 
 constexpr int kLogBlock = 256;
-constexpr uint32_t kPickWords = 1024;  // candidates in LDS, and words of a row's pieces
+constexpr int kLoads = 4;              // of a batch
+constexpr int kKept = 16;              // batches whose largest elements are kept
+constexpr uint32_t kPickWords = 512;   // candidates in LDS
+constexpr uint32_t kJoinWords = 1024;  // of a row's pieces
 constexpr double kLog2e = 1.44269504088896340736;
 constexpr double kLn2 = 0.693147180559945309417;
 constexpr uint32_t kLogStats = 3;
@@ -114,14 +117,15 @@ template <int T> __device__ inline uint32_t high_bits(typename Row<T>::Stored v)
 
 // What a row's sums say, by one thread: its numbers, and log2 Z for the top k.
 struct RowEnd {
-    double low;    // log2 Z, infinity where the row is all -inf
     double mean;   // D
     double share;  // 1 / Z, 0 where the row counts for nothing
 };
+// log2 Z, infinity where the row is all -inf: log p is -inf there
+__device__ inline double low_of(double z) { return z == 0 ? INFINITY : log2_64(z); }
 __device__ inline RowEnd finish_row(const LogArgs &a, uint64_t row, bool on, bool given, float x, double z, double w, float m,
                                     uint32_t before) {
     const bool empty = z == 0;
-    const double low = log2_64(z), mean = w / z;
+    const double low = low_of(z), mean = w / z;
     double logprob = 0, entropy = 0;
     if (on) {
         entropy = empty ? 0 : kLn2 * (low - mean);
@@ -130,14 +134,14 @@ __device__ inline RowEnd finish_row(const LogArgs &a, uint64_t row, bool on, boo
     a.logprobs[row] = static_cast<float>(logprob);
     a.entropy[row] = static_cast<float>(entropy);
     if (a.ranks) a.ranks[row] = given ? static_cast<int32_t>(before) : -1;
-    const RowEnd end{empty ? INFINITY : low, !on || empty ? 0 : mean, !on || empty ? 0 : 1 / z};
+    const RowEnd end{!on || empty ? 0 : mean, !on || empty ? 0 : 1 / z};
     if (a.stats) {
         float *s = a.stats + row * kLogStats;
         s[0] = m;
         s[1] = static_cast<float>(end.share);
         s[2] = static_cast<float>(end.mean);
     }
-    if (a.lows) a.lows[row] = end.low;
+    if (a.lows) a.lows[row] = low;
     return end;
 }
 // log p of a logit.
@@ -199,7 +203,7 @@ template <int B> struct JoinLds {
 // The workgroup's sums relative to its largest logit, in its first thread;
 // anew(m) gives a thread's sums relative to a huge m.
 template <int B, typename Acc, typename Anew>
-__device__ inline Sums join_sums(JoinLds<B> &lds, Running<Acc> &mine, float &top, uint32_t before_of_wave, float c, Anew anew) {
+__device__ inline Sums join_sums(JoinLds<B> &lds, Running<Acc> &mine, float &top, uint32_t before, float c, Anew anew) {
     constexpr int kWaves = B / kLanes;
     const int wave = threadIdx.x / kLanes;
     top = wave_join(mine.top, -INFINITY, [](float p, float q) { return larger(p, q); });
@@ -225,7 +229,7 @@ __device__ inline Sums join_sums(JoinLds<B> &lds, Running<Acc> &mine, float &top
     }
     s.z = wave_sum(s.z);
     s.w = wave_sum(s.w);
-    s.before = before_of_wave;
+    s.before = wave_sum(before);
     if (kWaves > 1) {
         if (threadIdx.x % kLanes == 0) {
             lds.z[wave] = s.z;
@@ -273,18 +277,18 @@ template <int T> struct Token {
     }
 };
 
-// One workgroup of B threads a row, or a piece of one.  PICK: V loads a thread
-// at most, whose largest elements are kept, and the alternatives are selected
-// from them as segmented_row_topk does; loads that reach the bound are read
-// again.  Else a row may have any length.
-template <int T, int B, int V, bool RANK>
-__global__ __launch_bounds__(B, B == 64 && V > 0 ? 3 : 8) void logprob_kernel(LogArgs a) {
-    constexpr int kVec = Row<T>::kVec, kLoads = 4, kWidth = T == kRowF32 ? 4 : 2;
-    constexpr bool kPick = V > 0;
+// One workgroup of B threads a row, or a piece of one.  PICK: at most kKept
+// batches of loads a thread, whose largest elements are kept in LDS; the
+// alternatives are selected from them as segmented_row_topk does, and batches
+// that reach the bound are read again.  Else a row may have any length.
+template <int T, int B, bool RANK, bool PICK>
+__global__ __launch_bounds__(B, B == 64 && PICK ? 3 : T == kRowF32 && PICK ? 5 : 7) void logprob_kernel(LogArgs a) {
+    constexpr int kVec = Row<T>::kVec, kWidth = T == kRowF32 ? 4 : 2;
     using Stored = typename Row<T>::Stored;
     __shared__ JoinLds<B> join;
-    __shared__ SelectLds<B, kPick ? kPickWords : B> lds;
-    __shared__ RowEnd end;
+    __shared__ SelectLds<B, PICK ? kPickWords : B> lds;
+    __shared__ Stored kept[PICK ? kKept : 1][B];
+    __shared__ double whole;
     const uint32_t tid = threadIdx.x;
     const uint64_t task = a.first_task + xcd_chunk(blockIdx.x, gridDim.x);
     const uint64_t row = task / a.splits;
@@ -295,16 +299,16 @@ __global__ __launch_bounds__(B, B == 64 && V > 0 ? 3 : 8) void logprob_kernel(Lo
     const uint32_t none = T == kRowF16 ? 0xFC00FC00u : T == kRowBF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
     const auto load = [&](uint32_t v) {
         u32x4 t{none, none, none, none};
-        if (v < vecs) t = kPick ? load16(x + static_cast<uint64_t>(v) * kVec) : load16_once(x + static_cast<uint64_t>(v) * kVec);
+        if (v < vecs) t = PICK ? load16(x + static_cast<uint64_t>(v) * kVec) : load16_once(x + static_cast<uint64_t>(v) * kVec);
         return t;
     };
     const Token<T> token(a, row);
     const bool ranked = RANK && token.given && !token.exact;
     const float c = a.c;
-    uint32_t before = 0;  // of the wave
-    int most[kPick ? (kWidth == 4 ? V : V / 2) : 1];
-    Running<std::conditional_t<kPick, float, double>> mine;
-    const auto batch = [&](uint32_t base, int keep) {
+    uint32_t before = 0;  // of this thread
+    Running<std::conditional_t<PICK, float, double>> mine;
+#pragma unroll 1
+    for (uint32_t base = 0; base < vecs; base += kLoads * B) {
         u32x4 t[kLoads];
         float f[kLoads * kVec], top[kLoads];
 #pragma unroll
@@ -316,70 +320,36 @@ __global__ __launch_bounds__(B, B == 64 && V > 0 ? 3 : 8) void logprob_kernel(Lo
             top[u] = largest(g);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) f[u * kVec + e] = g[e];
-            if constexpr (kPick) {
-                const uint32_t p = Row<T>::pattern(top[u]);
-                const int m = image<kWidth>(p, 0);
-                if (kWidth == 4) most[keep + u] = m;
-                else if (u % 2 == 0) most[(keep + u) / 2] = m & 0xFFFF;
-                else most[(keep + u) / 2] |= m << 16;
-            }
         }
         const float all = largest(top);
+        if (PICK) kept[base / (kLoads * B)][tid] = Row<T>::pattern(all);
         if (RANK && ranked && __ballot(!(all < token.x))) {
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
                 const int64_t last = static_cast<int64_t>(first) + static_cast<int64_t>(base + u * B + tid + 1) * kVec;
                 const float bound = last <= token.at ? token.least : token.from;
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) before += __popcll(__ballot(f[u * kVec + e] > bound));
+                for (int e = 0; e < kVec; ++e) before += f[u * kVec + e] > bound;
             }
         }
         mine.add(f, all, c);
-    };
-    if constexpr (kPick) {
-#pragma unroll
-        for (int b = 0; b < V; b += kLoads) {
-            if (b * B < static_cast<int>(vecs)) {
-                batch(b * B, b);
-            } else {
-#pragma unroll
-                for (int u = 0; u < kLoads; ++u) {
-                    if (kWidth == 4) most[b + u] = INT32_MIN;
-                    else most[(b + u) / 2] = static_cast<int>(0x80008000u);
-                }
-            }
-        }
-    } else {
-#pragma unroll 1
-        for (uint32_t b = 0; b < vecs; b += kLoads * B) batch(b, 0);
     }
     const bool extra = rest < len;
-    float over = -INFINITY;
     if (len > vecs * kVec) {  // the elements after the last whole load
-        Stored v = 0;
-        if (extra) {
-            v = x[rest];
-            over = Row<T>::value(v);
-        }
-        if (RANK && ranked) before += __popcll(__ballot(extra && token.after(v, first + rest)));
-        const float f[1] = {over};
-        mine.add(f, over, c);
+        const Stored v = extra ? x[rest] : Stored(0);
+        const float f[1] = {extra ? Row<T>::value(v) : -INFINITY};
+        if (RANK && ranked) before += extra && token.after(v, first + rest);
+        mine.add(f, f[0], c);
     }
     if (RANK && token.given) {
         const int64_t at = token.at - first;
         if (token.exact || __ballot(__builtin_isnan(mine.top))) {  // by their patterns, from a second read
-            before = 0;
-            for (uint32_t v = tid; v - tid < vecs; v += B) {
-                uint32_t n = 0;
-                if (v < vecs)
-                    for (int e = 0; e < kVec; ++e) n += token.after(x[static_cast<uint64_t>(v) * kVec + e], first + v * kVec + e);
-                before += wave_sum(n);
-            }
-            before += __popcll(__ballot(extra && token.after(extra ? x[rest] : Stored(0), first + rest)));
-        } else if (at >= 0 && at < static_cast<int64_t>(vecs) * kVec && at / kVec % B / kLanes == tid / kLanes) {
-            // equal ones of the token's own load, before it: the wave that has that
-            const bool here = tid % kLanes < at % kVec;
-            before += __popcll(__ballot(here && x[here ? at - at % kVec + tid % kLanes : 0] == token.pattern));
+            before = extra && token.after(x[rest], first + rest);
+            for (uint32_t v = tid; v < vecs; v += B)
+                for (int e = 0; e < kVec; ++e) before += token.after(x[static_cast<uint64_t>(v) * kVec + e], first + v * kVec + e);
+        } else if (at >= 0 && at < static_cast<int64_t>(vecs) * kVec && at / kVec % B == tid) {
+            // equal ones of the token's own load, before it: the thread that has that
+            for (int64_t i = at - at % kVec; i < at; ++i) before += x[i] == token.pattern;
         }
     }
     float top;  // of the workgroup
@@ -395,61 +365,65 @@ __global__ __launch_bounds__(B, B == 64 && V > 0 ? 3 : 8) void logprob_kernel(Lo
             unpack16<T>(load(v), f);
             for (int e = 0; e < kVec; ++e) add(f[e]);
         }
-        if (extra) add(over);
+        if (extra) add(Row<T>::value(x[rest]));
         return double2{z, w};
     });
-    if (tid == 0) {
-        if (a.splits == 1) end = finish_row(a, row, on, token.given, token.x, s.z, s.w, s.m, s.before);
-        else a.sums[task] = s;
-    }
-    if constexpr (kPick) {
+    if constexpr (PICK) {
         __shared__ int tops[B / kLanes];
-        int mine_image = image<kWidth>(Row<T>::pattern(mine.top), 0), top_image = image<kWidth>(Row<T>::pattern(top), 0);
-        const int over_image = extra ? image<kWidth>(x[rest], 0) : INT32_MIN;
+        const int over = extra ? image<kWidth>(x[rest], 0) : INT32_MIN;
         const bool some = extra || tid < vecs;
+        const uint32_t batches = (vecs + kLoads * B - 1) / (kLoads * B);
+        int own = image<kWidth>(Row<T>::pattern(mine.top), 0), top_image = image<kWidth>(Row<T>::pattern(top), 0);
         if (__builtin_isnan(top)) {  // NaNs have an order among themselves, by their patterns
-            mine_image = over_image;
-#pragma unroll
-            for (int u = 0; u < V; ++u) {
-                const bool in = u * B + tid < vecs;
-                const int m = in ? vec_max<kWidth>(load(u * B + tid), 0) : kWidth == 2 ? -32768 : INT32_MIN;
-                if (in) mine_image = max(mine_image, m);
-                if (kWidth == 4) most[u] = m;
-                else if (u % 2 == 0) most[u / 2] = m & 0xFFFF;
-                else most[u / 2] |= m << 16;
+            own = over;
+            for (uint32_t b = 0; b < batches; ++b) {
+                int m = kWidth == 2 ? -32768 : INT32_MIN;
+                for (int u = 0; u < kLoads; ++u) {
+                    const uint32_t v = (b * kLoads + u) * B + tid;
+                    if (v < vecs) m = max(m, vec_max<kWidth>(load(v), 0));
+                }
+                kept[b][tid] = static_cast<Stored>(pattern_of<kWidth>(m, 0));
+                if (b * kLoads * B + tid < vecs) own = max(own, m);
             }
-            top_image = wave_max_int(mine_image);
+            top_image = wave_max_int(own);
             if (tid % kLanes == 0) tops[tid / kLanes] = top_image;
             __syncthreads();
             for (int i = 0; i < B / kLanes; ++i) top_image = max(top_image, tops[i]);
         }
+        if (tid == 0) whole = s.z;
         clear_bins<B>(lds.bins);
         if (tid == 0) lds.count = 0;
         __syncthreads();
         const auto fill = [&](uint32_t shift) {
-            if (some) add_to_bins(lds.bins, mine_image, top_image, shift);
+            if (some) add_to_bins(lds.bins, own, top_image, shift);
         };
         const auto reach = [&](int bound, auto take) {
-            if (mine_image >= bound && some) {
-                uint32_t hits = 0;  // loads that are read again: mostly one
-#pragma unroll
-                for (int u = 0; u < V; ++u) {
-                    const int m = kWidth == 4 ? most[u] : u % 2 ? most[u / 2] >> 16 : static_cast<int16_t>(most[u / 2]);
-                    hits |= static_cast<uint32_t>(m >= bound && u * B + tid < vecs) << u;
-                }
+            if (own >= bound && some) {
+                uint32_t hits = 0;  // batches that are read again: mostly one
+                for (uint32_t b = 0; b < batches; ++b) hits |= static_cast<uint32_t>(image<kWidth>(kept[b][tid], 0) >= bound) << b;
                 while (hits) {
-                    const uint32_t at = (__builtin_ctz(hits) * B + tid) * kVec;
+                    const uint32_t v = __builtin_ctz(hits) * (kLoads * B) + tid;
                     hits &= hits - 1;
-                    each_image<kWidth>(load16(x + at), 0, at, take);
+                    u32x4 t[kLoads];
+#pragma unroll
+                    for (int u = 0; u < kLoads; ++u)
+                        if (v + u * B < vecs) t[u] = load16(x + static_cast<uint64_t>(v + u * B) * kVec);
+#pragma unroll
+                    for (int u = 0; u < kLoads; ++u)
+                        if (v + u * B < vecs) each_image<kWidth>(t[u], 0, (v + u * B) * kVec, take);
                 }
-                if (extra) take(over_image, rest);
+                if (extra) take(over, rest);
             }
         };
         const auto put = [&](uint64_t w, uint32_t place) {
-            if (a.splits == 1) put_top<T>(a, w, row * a.k + place, s.m, end.low);
+            if (a.splits == 1) put_top<T>(a, w, row * a.k + place, s.m, low_of(whole));
             else a.words[task * a.k + place] = w;
         };
         select_largest<kWidth, B>(lds, x, len, first, 0, a.k, top_image, true, fill, reach, put);
+    }
+    if (tid == 0) {
+        if (a.splits == 1) finish_row(a, row, on, token.given, token.x, s.z, s.w, s.m, s.before);
+        else a.sums[task] = s;
     }
 }
 
@@ -458,9 +432,9 @@ __global__ __launch_bounds__(B, B == 64 && V > 0 ? 3 : 8) void logprob_kernel(Lo
 template <int T, bool PICK>
 __global__ __launch_bounds__(PICK ? kLogBlock : kLanes) void logprob_join_kernel(LogArgs a) {
     constexpr int B = PICK ? kLogBlock : kLanes, kWidth = T == kRowF32 ? 4 : 2;
-    __shared__ SelectLds<B, PICK ? kPickWords : B> lds;
+    __shared__ SelectLds<B, PICK ? kJoinWords : B> lds;
     __shared__ int tops[B / kLanes];
-    __shared__ RowEnd end;
+    __shared__ double low;
     __shared__ float most;
     for (uint64_t row = a.first_task + blockIdx.x; row < a.rows; row += gridDim.x) {
         if (threadIdx.x < kLanes) {
@@ -481,13 +455,14 @@ __global__ __launch_bounds__(PICK ? kLogBlock : kLanes) void logprob_join_kernel
             w = wave_sum(w);
             before = wave_sum(before);
             if (threadIdx.x == 0) {
-                end = finish_row(a, row, counted(a, row), token.given, token.x, z, w, m, before);
+                finish_row(a, row, counted(a, row), token.given, token.x, z, w, m, before);
+                low = low_of(z);
                 most = m;
             }
         }
         if constexpr (PICK)
             merge_words<kWidth, B>(lds, tops, a.words + row * a.splits * a.k, a.splits * a.k, a.k,
-                                   [&](uint64_t w, uint32_t place) { put_top<T>(a, w, row * a.k + place, most, end.low); });
+                                   [&](uint64_t w, uint32_t place) { put_top<T>(a, w, row * a.k + place, most, low); });
         __syncthreads();
     }
 }
@@ -534,13 +509,133 @@ __global__ __launch_bounds__(kLogBlock) void logprob_grad_kernel(LogArgs a) {
             const float v = __builtin_amdgcn_exp2f(d) * share * fmaf(slope, fmaxf(d, kZeroBelow) - mean, up);
             return at == own ? fmaf(up, inv_t, v) : v;
         };
-        for (uint32_t v = threadIdx.x; v < vecs; v += kLogBlock) {
-            float e[kVec];
-            unpack16<T>(load16(x + static_cast<uint64_t>(v) * kVec), e);
-            for (int i = 0; i < kVec; ++i) e[i] = of(e[i], v * kVec + i);
-            store16(g + static_cast<uint64_t>(v) * kVec, pack16<T>(e));
+        for (uint32_t base = threadIdx.x; base < vecs; base += kLoads * kLogBlock) {
+            u32x4 t[kLoads];
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u)
+                if (base + u * kLogBlock < vecs) t[u] = load16_once(x + static_cast<uint64_t>(base + u * kLogBlock) * kVec);
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                const uint32_t v = base + u * kLogBlock;
+                float e[kVec];
+                unpack16<T>(t[u], e);
+                for (int i = 0; i < kVec; ++i) e[i] = of(e[i], v * kVec + i);
+                if (v < vecs) store16_once(g + static_cast<uint64_t>(v) * kVec, pack16<T>(e));
+            }
         }
         if (rest < len) g[rest] = Row<T>::pattern(of(Row<T>::value(x[rest]), rest));
+    }
+}
+
+// A row's numbers and its gradient by one workgroup of B threads that holds it,
+// V loads a thread, from its one read to its one write.
+template <int T, int B, int V>
+__global__ __launch_bounds__(B, 4) void logprob_step_kernel(LogArgs a) {
+    constexpr int kVec = Row<T>::kVec;
+    using Stored = typename Row<T>::Stored;
+    __shared__ JoinLds<B> join;
+    __shared__ float shared[2];
+    const uint32_t tid = threadIdx.x, vecs = a.n / kVec, rest = vecs * kVec + tid;
+    const uint64_t row = a.first_task + xcd_chunk(blockIdx.x, gridDim.x);
+    const Stored *x = static_cast<const Stored *>(a.logits) + row * a.stride;
+    Stored *g = static_cast<Stored *>(a.grad) + row * a.grad_stride;
+    const uint32_t none = T == kRowF16 ? 0xFC00FC00u : T == kRowBF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+    const bool on = counted(a, row), extra = rest < a.n;
+    const auto below = [&](int u) { return static_cast<int>(tid) < static_cast<int>(vecs) - u * B; };
+    u32x4 v[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        v[u] = u32x4{none, none, none, none};
+        if (on && below(u)) v[u] = load16_once(reinterpret_cast<const uint8_t *>(x + u * B * kVec) + tid * 16);
+    }
+    const float over = on && extra ? Row<T>::value(x[rest]) : -INFINITY;
+    const Token<T> token(a, row);
+    const float up = a.up && token.given ? a.up[row] : 0.f, down = a.up_entropy ? a.up_entropy[row] : 0.f;
+    const float c = a.c;
+    // each pass unpacks the held words anew: their floats would take twice the registers
+    const auto anew = [&]() {
+#pragma unroll
+        for (int u = 0; u < V; ++u) asm volatile("" : "+v"(v[u]));
+    };
+    Running<float> mine;
+    constexpr int kBatch = V < kLoads ? V : kLoads;
+#pragma unroll
+    for (int b = 0; b < V; b += kBatch) {
+        float f[kBatch * kVec];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            float e[kVec];
+            unpack16<T>(v[b + u], e);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) f[u * kVec + i] = e[i];
+        }
+        mine.add(f, largest(f), c);
+    }
+    if (a.n > vecs * kVec) {
+        const float f[1] = {over};
+        mine.add(f, over, c);
+    }
+    anew();
+    float top;
+    const Sums s = join_sums<B>(join, mine, top, 0, c, [&](float m) {
+        double z = 0, w = 0;
+        const auto add = [&](float f) {
+            const float d = (f - m) * c, p = __builtin_amdgcn_exp2f(d);
+            z += p;
+            w += p * fmaxf(d, kZeroBelow);
+        };
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            float f[kVec];
+            unpack16<T>(v[u], f);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) add(f[e]);
+        }
+        add(over);
+        return double2{z, w};
+    });
+    anew();
+    if (tid == 0) {
+        const RowEnd end = finish_row(a, row, on, token.given, token.x, s.z, s.w, s.m, 0);
+        shared[0] = -static_cast<float>(end.share * a.inv_t);
+        shared[1] = static_cast<float>(end.mean);
+    }
+    __syncthreads();
+    // p (a + b ln2 (d - D)): nothing where nothing is asked, whatever the logits hold.
+    // Exponents are relative to r, which is not quite the largest logit's.
+    const float m = s.m, r = fmaxf(top * c, kLeastReference);
+    const float shift = huge(top, c) ? 0.f : static_cast<float>(static_cast<double>(top) * c - r);
+    const float share = shared[0], scaled = share * __builtin_amdgcn_exp2f(-shift);
+    const float flat = scaled * up, slope = scaled * down * static_cast<float>(kLn2), mean = shared[1] + shift;
+    const bool none_asked = !on || share == 0.f || (up == 0.f && down == 0.f);
+    const auto pass = [&](auto of) {
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            float e[kVec];
+            unpack16<T>(v[u], e);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) e[i] = of(e[i]);
+            if (below(u)) store16_once(reinterpret_cast<uint8_t *>(g + u * B * kVec) + tid * 16, pack16<T>(e));
+        }
+        if (extra) g[rest] = Row<T>::pattern(of(over));
+    };
+    if (none_asked) pass([&](float) { return 0.f; });
+    else if (huge(top, c)) pass([&](float f) {
+        const float d = (f - m) * c;
+        return __builtin_amdgcn_exp2f(d) * fmaf(slope, fmaxf(d, kZeroBelow) - mean, flat);
+    });
+    else if (slope == 0.f) pass([&](float f) { return __builtin_amdgcn_exp2f(fmaf(f, c, -r)) * flat; });
+    else pass([&](float f) {
+        const float d = fmaf(f, c, -r);
+        return __builtin_amdgcn_exp2f(d) * fmaf(slope, fmaxf(d, kZeroBelow) - mean, flat);
+    });
+    if (!none_asked && token.given) {
+        // the token's column over what was written there
+        __syncthreads();
+        if (tid == 0) {
+            const float d = huge(top, c) ? (token.x - m) * c : fmaf(token.x, c, -r), p = __builtin_amdgcn_exp2f(d);
+            g[token.at] = Row<T>::pattern(fmaf(up, static_cast<float>(a.inv_t), p * fmaf(slope, fmaxf(d, kZeroBelow) - mean, flat)));
+        }
     }
 }
 
@@ -548,40 +643,32 @@ __global__ __launch_bounds__(kLogBlock) void logprob_grad_kernel(LogArgs a) {
 
 constexpr uint64_t kMaxGrid = 1u << 20;
 
-// How the rows are laid out on workgroups: as many threads a row as it has loads
-// for, and several workgroups where rows are fewer than would fill the GPU.
-// With alternatives (k > 0) a workgroup holds at most 16 loads a thread, k is at
-// most half of its threads, and the pieces' words fit one workgroup; where that
-// cannot be (fused false) segmented_row_topk selects them.
+// How the rows are laid out on workgroups: a wave a row for up to 4 KB of many
+// rows, else 256 threads, and several workgroups a row where rows are fewer than
+// fill the GPU, down to a batch of loads a thread each.  With alternatives (k > 0)
+// a workgroup holds at most kKept batches, k is at most half of its threads, and
+// the pieces' words fit one workgroup; where that cannot be (fused false)
+// segmented_row_topk selects them.
 struct LogPlan {
-    int block = kLogBlock, loads = 0;  // loads: of a thread, with alternatives
+    int block = kLogBlock;
     uint32_t splits = 1, len = 8;
-    bool fused = true;
+    bool pick = false, fused = true;
 };
 LogPlan logprob_plan(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
     LogPlan p;
     const uint64_t vec = 16 / size, vecs = n / vec;
-    const auto pieces = [&](uint64_t s) {
-        p.len = static_cast<uint32_t>(std::max<uint64_t>(8, ((n + s - 1) / s + 7) / 8 * 8));
-        p.splits = static_cast<uint32_t>(std::max<uint64_t>(1, (n + p.len - 1) / p.len));
-    };
-    if (rows >= 512) {
-        // a wave for up to 4 KB; 1024 threads for more than 64 KB
-        p.block = vecs <= 64 * 4 ? 64 : vecs <= 256 * 16 ? 256 : 1024;
-        pieces(k > 0 ? std::max<uint64_t>(1, (vecs + 16 * 1024 - 1) / (16 * 1024)) : std::max<uint64_t>(1, n >> 20));
-    } else {
-        // pieces of 4 loads a thread, or more of them where there would be more than some 1024
-        uint64_t s = std::max<uint64_t>(1, (vecs + 4 * 256 - 1) / (4 * 256));
-        s = std::min<uint64_t>(s, std::max<uint64_t>(1, 1024 / std::max<uint64_t>(1, rows)));
-        if (k > 0) s = std::min<uint64_t>(s, std::max<uint64_t>(1, kPickWords / k));
-        pieces(s);
-        if (k > 0 && p.len / vec > 16 * 256) p.block = 1024;
-    }
+    if (rows >= 512 && vecs <= 64 * kLoads) p.block = 64;
+    const uint64_t batch = static_cast<uint64_t>(kLoads) * p.block;
+    uint64_t s = rows >= 1024 ? 1 : std::min<uint64_t>((vecs + batch - 1) / batch, 1024 / std::max<uint64_t>(1, rows));
+    if (k > 0) s = std::min<uint64_t>(s, kJoinWords / k);
+    s = std::max<uint64_t>(s, k > 0 ? (vecs + kKept * batch - 1) / (kKept * batch) : n >> 20);
+    s = std::max<uint64_t>(s, 1);
+    p.len = static_cast<uint32_t>(std::max<uint64_t>(8, ((n + s - 1) / s + 7) / 8 * 8));
+    p.splits = static_cast<uint32_t>(std::max<uint64_t>(1, (n + p.len - 1) / p.len));
     if (k > 0) {
         const uint64_t most = p.len / vec, least = (n - (p.splits - 1) * uint64_t(p.len)) / vec;
-        p.loads = most <= 4 * uint64_t(p.block) && p.block != 1024 ? 4 : 16;
-        p.fused = most <= 16 * uint64_t(p.block) && few_wanted(k, p.block, least) && (p.splits == 1 || p.splits * k <= kPickWords) &&
-                  (p.block != 64 || p.loads == 4);
+        p.pick = true;
+        p.fused = most <= kKept * batch && few_wanted(k, p.block, least) && (p.splits == 1 || p.splits * k <= kJoinWords);
     }
     return p;
 }
@@ -683,18 +770,9 @@ template <typename F> void by_type(int type, F f) {
 bool launched() { return hipGetLastError() == hipSuccess; }
 dim3 grid_of(uint64_t tasks) { return dim3(static_cast<uint32_t>(std::min<uint64_t>(tasks, kMaxGrid))); }
 
-template <int T, bool PICK, bool RANK> void launch_plan(const LogPlan &p, const LogArgs &a, uint32_t tasks, const Launch &L) {
-    const auto go = [&](auto kernel, int block) { launch_on(kernel, dim3(tasks), dim3(block), L, a); };
-    if constexpr (PICK) {
-        if (p.block == 64) go(logprob_kernel<T, 64, 4, true>, 64);
-        else if (p.block == 256 && p.loads == 4) go(logprob_kernel<T, 256, 4, true>, 256);
-        else if (p.block == 256) go(logprob_kernel<T, 256, 16, true>, 256);
-        else go(logprob_kernel<T, 1024, 16, true>, 1024);
-    } else {
-        if (p.block == 64) go(logprob_kernel<T, 64, 0, RANK>, 64);
-        else if (p.block == 256) go(logprob_kernel<T, 256, 0, RANK>, 256);
-        else go(logprob_kernel<T, 1024, 0, RANK>, 1024);
-    }
+template <int T, bool RANK, bool PICK> void launch_plan(const LogPlan &p, const LogArgs &a, uint32_t tasks, const Launch &L) {
+    if (p.block == 64) launch_on(logprob_kernel<T, 64, RANK, PICK>, dim3(tasks), dim3(64), L, a);
+    else launch_on(logprob_kernel<T, kLogBlock, RANK, PICK>, dim3(tasks), dim3(kLogBlock), L, a);
 }
 
 // The rows' numbers, and with a plan that has room for them the alternatives.
@@ -706,8 +784,8 @@ int logprob_values(LogArgs a, const LogPlan &p, int dtype, const Ctx &c) {
         TimedLaunch t(4, c);
         const uint32_t now = static_cast<uint32_t>(std::min<uint64_t>(tasks - a.first_task, kMaxGrid));
         by_type(dtype, [&](auto i) {
-            if (p.loads > 0) launch_plan<i.value, true, true>(p, a, now, t.L);
-            else if (a.ranks) launch_plan<i.value, false, true>(p, a, now, t.L);
+            if (p.pick) launch_plan<i.value, true, true>(p, a, now, t.L);
+            else if (a.ranks) launch_plan<i.value, true, false>(p, a, now, t.L);
             else launch_plan<i.value, false, false>(p, a, now, t.L);
         });
         if (!launched()) return LRS_ERR_HIP;
@@ -716,10 +794,40 @@ int logprob_values(LogArgs a, const LogPlan &p, int dtype, const Ctx &c) {
     a.first_task = 0;
     TimedLaunch t(4, c);
     by_type(dtype, [&](auto i) {
-        if (p.loads > 0) launch_on(logprob_join_kernel<i.value, true>, grid_of(a.rows), dim3(kLogBlock), t.L, a);
+        if (p.pick) launch_on(logprob_join_kernel<i.value, true>, grid_of(a.rows), dim3(kLogBlock), t.L, a);
         else launch_on(logprob_join_kernel<i.value, false>, grid_of(a.rows), dim3(kLanes), t.L, a);
     });
     return launched() ? LRS_OK : LRS_ERR_HIP;
+}
+// Rows of at most 256 KB are held: by 1024 threads where there are no more rows
+// than CUs, by the fewest that hold one where several workgroups share a CU.
+constexpr uint64_t kHeldBytes = 1024 * 16 * 16;
+bool logprob_held(uint64_t n, uint64_t size) { return n * size <= kHeldBytes; }
+template <int T> void launch_step(const LogArgs &a, uint32_t rows, const Launch &L) {
+    const uint64_t vecs = a.n / Row<T>::kVec;
+    const auto go = [&](auto kernel, int block) { launch_on(kernel, dim3(rows), dim3(block), L, a); };
+    if (a.rows <= 256) {
+        if (vecs <= 1024 * 2) return go(logprob_step_kernel<T, 1024, 2>, 1024);
+        if (vecs <= 1024 * 4) return go(logprob_step_kernel<T, 1024, 4>, 1024);
+        if (vecs <= 1024 * 8) return go(logprob_step_kernel<T, 1024, 8>, 1024);
+        return go(logprob_step_kernel<T, 1024, 16>, 1024);
+    }
+    if (vecs <= 64 * 4) return go(logprob_step_kernel<T, 64, 4>, 64);
+    if (vecs <= 64 * 8) return go(logprob_step_kernel<T, 64, 8>, 64);
+    if (vecs <= 128 * 8) return go(logprob_step_kernel<T, 128, 8>, 128);
+    if (vecs <= 256 * 8) return go(logprob_step_kernel<T, 256, 8>, 256);
+    if (vecs <= 256 * 16) return go(logprob_step_kernel<T, 256, 16>, 256);
+    if (vecs <= 512 * 16) return go(logprob_step_kernel<T, 512, 16>, 512);
+    go(logprob_step_kernel<T, 1024, 16>, 1024);
+}
+int logprob_step(LogArgs a, int dtype, const Ctx &c) {
+    for (a.first_task = 0; a.first_task < a.rows; a.first_task += kMaxGrid) {
+        TimedLaunch t(4, c);
+        const uint32_t now = static_cast<uint32_t>(std::min<uint64_t>(a.rows - a.first_task, kMaxGrid));
+        by_type(dtype, [&](auto i) { launch_step<i.value>(a, now, t.L); });
+        if (!launched()) return LRS_ERR_HIP;
+    }
+    return LRS_OK;
 }
 int logprob_gradient(LogArgs a, int dtype, const Ctx &c) {
     if (a.rows == 0 || a.n == 0) return LRS_OK;
@@ -868,7 +976,6 @@ int token_logprobs_step(const lrs_logprobs *in, const float *logprob_grad, const
             return LRS_ERR_ALIASING;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.sums = reinterpret_cast<Sums *>(ws + w.sums);
-    a.stats = reinterpret_cast<float *>(ws + w.stats);
     a.logprobs = logprobs;
     a.entropy = entropy;
     a.up = logprob_grad;
@@ -876,6 +983,8 @@ int token_logprobs_step(const lrs_logprobs *in, const float *logprob_grad, const
     a.grad = grad;
     a.grad_stride = grad_stride;
     c.elems = a.rows * a.n;
+    if (logprob_held(a.n, size)) return logprob_step(a, in->dtype, c);
+    a.stats = reinterpret_cast<float *>(ws + w.stats);
     const int fs = logprob_values(a, logprob_plan(a.rows, a.n, 0, size), in->dtype, c);
     return fs != LRS_OK ? fs : logprob_gradient(a, in->dtype, c);
 } catch (...) {

@@ -40,7 +40,9 @@ def _binding():
                               "`python -m lsd_radix_sort_amd.build`") from e
         names = ("segmented_row_topk_workspace_size", "segmented_row_topk", "topk_distill_workspace_size",
                  "topk_distill_forward", "topk_distill_backward", "topk_distill_step",
-                 "expert_balance_step_workspace_size", "expert_balance_step", "expert_balance")
+                 "expert_balance_step_workspace_size", "expert_balance_step", "expert_balance", "embedding_forward",
+                 "embedding_backward_workspace_size", "embedding_backward", "token_logprobs_workspace_size",
+                 "token_logprobs_forward", "token_logprobs_topk", "token_logprobs_backward", "token_logprobs_step")
         fast.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names})
         _fast = fast
     return _fast

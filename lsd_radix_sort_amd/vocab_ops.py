@@ -5,7 +5,8 @@
     token_logprobs_topk(logits, tokens, k, ...)
 
 The entry points of the C ABI (include/lsd_radix_sort.h), with the checks,
-streams, outputs and errors of the package's sorts.  The table's gradient is a
+streams, outputs and errors of the package's sorts.  Regular calls go through
+the compiled binding, as in row_ops.  The table's gradient is a
 stable sort of the tokens' ids (radix_sort_pairs) and a sum over equal ones; a
 token's rank and the top alternatives are places in the descending row sort.
 embedding_lookup and token_logprobs differentiate through torch autograd; the
@@ -19,7 +20,8 @@ import math
 import torch
 
 import lsd_radix_sort_amd as _lrs
-from .row_ops import _ID_BYTES, _dtype_code, _grad_out, _mask, _matrix, _once, _whole
+from . import row_ops as _rows
+from .row_ops import _ID_BYTES, _dtype_code, _grad_out, _mask, _matrix, _whole
 
 
 class _TokenIds(ctypes.Structure):
@@ -71,8 +73,15 @@ def _rows_of(t, name: str, tokens, width: int, device) -> int:
     return rows.stride(0)
 
 
+def _number(v, name: str) -> float:
+    try:
+        return float(v)
+    except (TypeError, ValueError, OverflowError):
+        _lrs._bad(f"{name} must be a number, got {v!r}")
+
+
 def _finite(scale) -> float:
-    scale = float(scale)
+    scale = _number(scale, "scale")
     if not math.isfinite(ctypes.c_float(scale).value):
         _lrs._bad(f"scale must be finite in 32 bits, got {scale}")
     return scale
@@ -82,6 +91,10 @@ def embedding_forward(weight: torch.Tensor, tokens: torch.Tensor, scale: float =
                       out: torch.Tensor | None = None, options: "_lrs.SortOptions | None" = None) -> torch.Tensor:
     """Rows of a [vocab, width] table times scale: [*tokens.shape, width] of `dtype` (the table's), 0 for tokens
     outside [0, vocab)."""
+    if out is None and options is None:
+        fast = (_rows._fast or _rows._binding()).embedding_forward(weight, tokens, _finite(scale), dtype)
+        if fast is not None:
+            return fast
     lib = _lrs.load_library()
     code = _matrix(weight, "weight")
     vocab, width = weight.shape
@@ -116,12 +129,19 @@ def embedding_backward(grad: torch.Tensor, tokens: torch.Tensor, vocab: int, sca
     grad: [*tokens.shape, width] or [tokens.numel(), width].  Tokens outside [0, vocab) and those equal to
     padding_index count for nothing.  accumulate: the gradient is added to grad_out, whose rows without a token
     stay as they are.  The sums are in 32 bits and their order is the tokens' own: equal calls give equal bits."""
+    vocab = _whole(vocab, "vocab")
+    if not 0 <= vocab < 2 ** 31 - 1:
+        _lrs._bad(f"vocab must be in [0, 2^31 - 1), got {vocab}")
+    if workspace is None and options is None:
+        fast = (_rows._fast or _rows._binding()).embedding_backward(grad, tokens, vocab, _finite(scale), padding_index, dtype,
+                                                                    grad_out, bool(accumulate))
+        if fast is not None:
+            return fast
     lib = _lrs.load_library()
     if not isinstance(grad, torch.Tensor) or not grad.is_cuda:
         _lrs._bad("grad must be a GPU tensor")
     device = grad.device
     ids = _token_ids(tokens, device)
-    vocab = _whole(vocab, "vocab")
     if grad.dim() == 0:
         _lrs._bad("grad must have a last dimension, the table's width")
     width = grad.size(-1)
@@ -133,8 +153,6 @@ def embedding_backward(grad: torch.Tensor, tokens: torch.Tensor, vocab: int, sca
         padding = _whole(padding_index, "padding_index")
         if not 0 <= padding < vocab:
             _lrs._bad(f"padding_index must be in [0, {vocab}), got {padding}")
-    if not 0 <= vocab < 2 ** 31 - 1:
-        _lrs._bad(f"vocab must be in [0, 2^31 - 1), got {vocab}")
     if grad_out is None:
         if accumulate:
             _lrs._bad("accumulate needs the grad_out to add to")
@@ -158,28 +176,6 @@ def embedding_backward(grad: torch.Tensor, tokens: torch.Tensor, vocab: int, sca
     return grad_out
 
 
-def _embedding_gradient(ctx, grad):
-    tokens, = ctx.saved_tensors
-    vocab, dtype, scale, padding = ctx.how
-    # an upstream gradient may be expanded from one number
-    try:
-        _rows_of(grad, "grad", tokens, grad.size(-1), grad.device)
-    except _lrs.RadixSortArgumentError:
-        grad = grad.contiguous()
-    return embedding_backward(grad, tokens, vocab, scale, padding, dtype), None, None, None, None
-
-
-class _Lookup(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, weight, tokens, scale, padding_index, dtype):
-        out = embedding_forward(weight, tokens, scale, dtype)
-        ctx.save_for_backward(tokens)
-        ctx.how = (weight.size(0), weight.dtype, scale, padding_index)
-        return out
-
-    backward = _once(_embedding_gradient)
-
-
 def embedding_lookup(weight: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0, padding_index: int | None = None,
                      dtype: torch.dtype | None = None) -> torch.Tensor:
     """embedding_forward, differentiable in the table; rows of padding_index get no gradient.
@@ -190,7 +186,11 @@ def embedding_lookup(weight: torch.Tensor, tokens: torch.Tensor, scale: float = 
         padding_index = _whole(padding_index, "padding_index")
         if isinstance(weight, torch.Tensor) and weight.dim() == 2 and not 0 <= padding_index < weight.size(0):
             _lrs._bad(f"padding_index must be in [0, {weight.size(0)}), got {padding_index}")
-    return _Lookup.apply(weight, tokens, scale, padding_index, dtype)
+    out = (_rows._fast or _rows._binding()).embedding_lookup(weight, tokens, _finite(scale), padding_index, dtype)
+    if out is None:
+        embedding_forward(weight, tokens, scale, dtype)  # says what is wrong
+        _lrs._bad("embedding_lookup does not take these arguments")
+    return out
 
 
 # --------------------------------------- log probabilities of given tokens
@@ -205,7 +205,7 @@ def _logprob_inputs(logits, tokens, temperature, row_mask=None) -> _Logprobs:
     if tokens.dim() != 1 or tokens.size(0) != rows:
         _lrs._bad(f"tokens must be a 1-D tensor of {rows} tokens, got {tuple(tokens.shape)}")
     return _Logprobs(logits.data_ptr(), logits.stride(0), tokens.data_ptr(), tokens.stride(0), size, dtype,
-                     _mask(row_mask, rows, logits.device), rows, n, temperature)
+                     _mask(row_mask, rows, logits.device), rows, n, _number(temperature, "temperature"))
 
 
 def _by_row(t, name: str, rows: int, device) -> int | None:
@@ -233,13 +233,17 @@ def token_logprobs_forward(logits: torch.Tensor, tokens: torch.Tensor, temperatu
 
     A token outside [0, n), such as -1, has log probability 0; rows whose row_mask is not set have entropy 0, too.
     Returns (logprobs [rows] float32, entropy [rows] float32, row_stats for the backward)."""
+    if workspace is None and options is None:
+        fast = (_rows._fast or _rows._binding()).logprobs_forward(logits, tokens, _number(temperature, "temperature"), row_mask)
+        if fast is not None:
+            return fast
     lib = _lrs.load_library()
     d = _logprob_inputs(logits, tokens, temperature, row_mask)
     opt = _lrs._opt(options)
     device = logits.device
     with torch.cuda.device(device):
         workspace = _logprob_workspace(lib, workspace, d, 0, opt, device)
-        logprobs, entropy = torch.empty((2, d.rows), dtype=torch.float32, device=device)
+        logprobs, entropy = (torch.empty(d.rows, dtype=torch.float32, device=device) for _ in range(2))
         stats = torch.empty((d.rows, 3), dtype=torch.float32, device=device)
         _lrs._check(lib.token_logprobs_forward(ctypes.byref(d), logprobs.data_ptr(), entropy.data_ptr(), stats.data_ptr(),
                                                workspace.data_ptr(), workspace.numel(), _lrs._stream(logits), opt),
@@ -254,8 +258,12 @@ def token_logprobs_topk(logits: torch.Tensor, tokens: torch.Tensor, k: int, temp
     Ranks and alternatives are places in the row's descending stable sort, so top_indices[r, ranks[r]] is the
     token where ranks[r] < k; a token outside [0, n) has rank -1.
     Returns (logprobs, entropy, ranks [rows] int32, top_logprobs [rows, k] float32, top_indices [rows, k] int64)."""
-    lib = _lrs.load_library()
     k = _whole(k, "k")
+    if workspace is None and options is None:
+        fast = (_rows._fast or _rows._binding()).logprobs_topk(logits, tokens, k, _number(temperature, "temperature"))
+        if fast is not None:
+            return fast
+    lib = _lrs.load_library()
     d = _logprob_inputs(logits, tokens, temperature)
     if not 0 <= k <= d.n:
         _lrs._bad(f"k must be between 0 and the row length {d.n}, got {k}")
@@ -263,7 +271,7 @@ def token_logprobs_topk(logits: torch.Tensor, tokens: torch.Tensor, k: int, temp
     device = logits.device
     with torch.cuda.device(device):
         workspace = _logprob_workspace(lib, workspace, d, k, opt, device)
-        logprobs, entropy = torch.empty((2, d.rows), dtype=torch.float32, device=device)
+        logprobs, entropy = (torch.empty(d.rows, dtype=torch.float32, device=device) for _ in range(2))
         ranks = torch.empty(d.rows, dtype=torch.int32, device=device)
         top = torch.empty((d.rows, k), dtype=torch.float32, device=device)
         indices = torch.empty((d.rows, k), dtype=torch.int64, device=device)
@@ -286,6 +294,11 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, row_stat
     """The gradient in the logits of a loss whose derivatives in token_logprobs_forward's log probabilities and
     entropies are logprob_grad and entropy_grad ([rows] float32, None: 0), from the same inputs and the row_stats
     that the forward returned."""
+    if grad_out is None and options is None:
+        fast = (_rows._fast or _rows._binding()).logprobs_backward(logits, tokens, row_stats, logprob_grad, entropy_grad,
+                                                                   _number(temperature, "temperature"), row_mask)
+        if fast is not None:
+            return fast
     lib = _lrs.load_library()
     d = _logprob_inputs(logits, tokens, temperature, row_mask)
     device = logits.device
@@ -305,6 +318,11 @@ def token_logprobs_step(logits: torch.Tensor, tokens: torch.Tensor, logprob_grad
                         workspace: torch.Tensor | None = None, options: "_lrs.SortOptions | None" = None):
     """token_logprobs_forward and _backward in one call, for derivatives that are known beforehand (such as those of
     a weighted sum of log probabilities): returns (logprobs, entropy, grad)."""
+    if grad_out is None and workspace is None and options is None:
+        fast = (_rows._fast or _rows._binding()).logprobs_step(logits, tokens, logprob_grad, entropy_grad, _number(temperature, "temperature"),
+                                                               row_mask)
+        if fast is not None:
+            return fast
     lib = _lrs.load_library()
     d = _logprob_inputs(logits, tokens, temperature, row_mask)
     opt = _lrs._opt(options)
@@ -312,7 +330,7 @@ def token_logprobs_step(logits: torch.Tensor, tokens: torch.Tensor, logprob_grad
     up, up_entropy = _derivatives(logprob_grad, entropy_grad, d, device)
     with torch.cuda.device(device):
         workspace = _logprob_workspace(lib, workspace, d, 0, opt, device)
-        logprobs, entropy = torch.empty((2, d.rows), dtype=torch.float32, device=device)
+        logprobs, entropy = (torch.empty(d.rows, dtype=torch.float32, device=device) for _ in range(2))
         grad_out = _grad_out(grad_out, logits)
         _lrs._check(lib.token_logprobs_step(ctypes.byref(d), up, up_entropy, logprobs.data_ptr(), entropy.data_ptr(),
                                             grad_out.data_ptr(), grad_out.stride(0), workspace.data_ptr(), workspace.numel(),
@@ -320,28 +338,12 @@ def token_logprobs_step(logits: torch.Tensor, tokens: torch.Tensor, logprob_grad
     return logprobs, entropy, grad_out
 
 
-def _logprob_gradient(ctx, logprob_grad, entropy_grad):
-    logits, tokens, stats, row_mask = ctx.saved_tensors
-    if logprob_grad is None and entropy_grad is None:
-        return None, None, None, None
-    up = [None if g is None else g.contiguous() for g in (logprob_grad, entropy_grad)]
-    return token_logprobs_backward(logits.detach(), tokens, stats, *up, *ctx.how, row_mask), None, None, None
-
-
-class _TokenLogprobs(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, logits, tokens, temperature, row_mask):
-        logprobs, entropy, stats = token_logprobs_forward(logits, tokens, temperature, row_mask)
-        ctx.save_for_backward(logits, tokens, stats, row_mask)
-        ctx.how = (temperature,)
-        ctx.set_materialize_grads(False)
-        return logprobs, entropy
-
-    backward = _once(_logprob_gradient)
-
-
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.0, row_mask: torch.Tensor | None = None):
     """token_logprobs_forward's (logprobs, entropy), differentiable in the logits.
 
     Inside a graph capture use token_logprobs_forward and _backward, or _step, as with embedding_lookup."""
-    return _TokenLogprobs.apply(logits, tokens, temperature, row_mask)
+    out = (_rows._fast or _rows._binding()).logprobs_autograd(logits, tokens, _number(temperature, "temperature"), row_mask)
+    if out is None:
+        token_logprobs_forward(logits, tokens, temperature, row_mask)  # says what is wrong
+        _lrs._bad("token_logprobs does not take these arguments")
+    return out
