@@ -281,7 +281,8 @@ template <int T> struct Token {
 // batches of loads a thread, whose largest elements are kept in LDS; the
 // alternatives are selected from them as segmented_row_topk does, and batches
 // that reach the bound are read again.  Else a row may have any length.
-template <int T, int B, bool RANK, bool PICK>
+// ONCE: the logits are read past the caches (see read_once).
+template <int T, int B, bool RANK, bool PICK, bool ONCE>
 __global__ __launch_bounds__(B, B == 64 && PICK ? 3 : T == kRowF32 && PICK ? 5 : 7) void logprob_kernel(LogArgs a) {
     constexpr int kVec = Row<T>::kVec, kWidth = T == kRowF32 ? 4 : 2;
     using Stored = typename Row<T>::Stored;
@@ -299,7 +300,7 @@ __global__ __launch_bounds__(B, B == 64 && PICK ? 3 : T == kRowF32 && PICK ? 5 :
     const uint32_t none = T == kRowF16 ? 0xFC00FC00u : T == kRowBF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
     const auto load = [&](uint32_t v) {
         u32x4 t{none, none, none, none};
-        if (v < vecs) t = PICK ? load16(x + static_cast<uint64_t>(v) * kVec) : load16_once(x + static_cast<uint64_t>(v) * kVec);
+        if (v < vecs) t = ONCE ? load16_once(x + static_cast<uint64_t>(v) * kVec) : load16(x + static_cast<uint64_t>(v) * kVec);
         return t;
     };
     const Token<T> token(a, row);
@@ -307,14 +308,12 @@ __global__ __launch_bounds__(B, B == 64 && PICK ? 3 : T == kRowF32 && PICK ? 5 :
     const float c = a.c;
     uint32_t before = 0;  // of this thread
     Running<std::conditional_t<PICK, float, double>> mine;
-#pragma unroll 1
-    for (uint32_t base = 0; base < vecs; base += kLoads * B) {
-        u32x4 t[kLoads];
-        float f[kLoads * kVec], top[kLoads];
+    // N loads of a thread, from load `v` on
+    const auto take = [&](auto loads, const u32x4 *t, uint32_t v) {
+        constexpr int N = decltype(loads)::value;
+        float f[N * kVec], top[N];
 #pragma unroll
-        for (int u = 0; u < kLoads; ++u) t[u] = load(base + u * B + tid);
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
+        for (int u = 0; u < N; ++u) {
             float g[kVec];
             unpack16<T>(t[u], g);
             top[u] = largest(g);
@@ -322,17 +321,44 @@ __global__ __launch_bounds__(B, B == 64 && PICK ? 3 : T == kRowF32 && PICK ? 5 :
             for (int e = 0; e < kVec; ++e) f[u * kVec + e] = g[e];
         }
         const float all = largest(top);
-        if (PICK) kept[base / (kLoads * B)][tid] = Row<T>::pattern(all);
         if (RANK && ranked && __ballot(!(all < token.x))) {
 #pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                const int64_t last = static_cast<int64_t>(first) + static_cast<int64_t>(base + u * B + tid + 1) * kVec;
+            for (int u = 0; u < N; ++u) {
+                const int64_t last = static_cast<int64_t>(first) + static_cast<int64_t>(v + u * B + 1) * kVec;
                 const float bound = last <= token.at ? token.least : token.from;
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) before += f[u * kVec + e] > bound;
             }
         }
         mine.add(f, all, c);
+        return all;
+    };
+    // whole batches, the next one's loads on their way; then the loads that are left, one at a time
+    const uint32_t whole_batches = vecs / (kLoads * B);
+    u32x4 t[kLoads], next[kLoads];
+    if (whole_batches > 0) {
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) next[u] = load(u * B + tid);
+    }
+#pragma unroll 1
+    for (uint32_t b = 0; b < whole_batches; ++b) {
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) t[u] = next[u];
+        if (b + 1 < whole_batches) {
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) next[u] = load(((b + 1) * kLoads + u) * B + tid);
+        }
+        const float all = take(std::integral_constant<int, kLoads>(), t, b * kLoads * B + tid);
+        if (PICK) kept[b][tid] = Row<T>::pattern(all);
+    }
+    if (whole_batches * kLoads * B < vecs) {
+        float all = -INFINITY;
+#pragma unroll 1
+        for (uint32_t v = whole_batches * kLoads * B + tid; v - tid < vecs; v += B) {
+            t[0] = load(v);
+            all = larger(all, take(std::integral_constant<int, 1>(), t, v));
+        }
+        if (PICK) kept[whole_batches][tid] = Row<T>::pattern(all);
     }
     const bool extra = rest < len;
     if (len > vecs * kVec) {  // the elements after the last whole load
@@ -480,7 +506,7 @@ __global__ __launch_bounds__(kLogBlock) void logprob_top_kernel(LogArgs a) {
 }
 
 // One workgroup: the gradient of a piece of a row.
-template <int T>
+template <int T, bool ONCE>
 __global__ __launch_bounds__(kLogBlock) void logprob_grad_kernel(LogArgs a) {
     constexpr int kVec = Row<T>::kVec;
     using Stored = typename Row<T>::Stored;
@@ -513,7 +539,10 @@ __global__ __launch_bounds__(kLogBlock) void logprob_grad_kernel(LogArgs a) {
             u32x4 t[kLoads];
 #pragma unroll
             for (int u = 0; u < kLoads; ++u)
-                if (base + u * kLogBlock < vecs) t[u] = load16_once(x + static_cast<uint64_t>(base + u * kLogBlock) * kVec);
+                if (base + u * kLogBlock < vecs) {
+                    const Stored *from = x + static_cast<uint64_t>(base + u * kLogBlock) * kVec;
+                    t[u] = ONCE ? load16_once(from) : load16(from);
+                }
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
                 const uint32_t v = base + u * kLogBlock;
@@ -546,7 +575,7 @@ __global__ __launch_bounds__(B, 4) void logprob_step_kernel(LogArgs a) {
 #pragma unroll
     for (int u = 0; u < V; ++u) {
         v[u] = u32x4{none, none, none, none};
-        if (on && below(u)) v[u] = load16_once(reinterpret_cast<const uint8_t *>(x + u * B * kVec) + tid * 16);
+        if (on && below(u)) v[u] = load16(reinterpret_cast<const uint8_t *>(x + u * B * kVec) + tid * 16);
     }
     const float over = on && extra ? Row<T>::value(x[rest]) : -INFINITY;
     const Token<T> token(a, row);
@@ -644,7 +673,7 @@ __global__ __launch_bounds__(B, 4) void logprob_step_kernel(LogArgs a) {
 constexpr uint64_t kMaxGrid = 1u << 20;
 
 // How the rows are laid out on workgroups: a wave a row for up to 4 KB of many
-// rows, else 256 threads, and several workgroups a row where rows are fewer than
+// rows (32 KB of very many: 8192 x 4096 bf16 17 us against 24), else 256 threads, and several workgroups a row where rows are fewer than
 // fill the GPU, down to a batch of loads a thread each.  With alternatives (k > 0)
 // a workgroup holds at most kKept batches, k is at most half of its threads, and
 // the pieces' words fit one workgroup; where that cannot be (fused false)
@@ -658,6 +687,7 @@ LogPlan logprob_plan(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
     LogPlan p;
     const uint64_t vec = 16 / size, vecs = n / vec;
     if (rows >= 512 && vecs <= 64 * kLoads) p.block = 64;
+    if (rows >= 2048 && vecs <= 2048 && k == 0) p.block = 64;
     const uint64_t batch = static_cast<uint64_t>(kLoads) * p.block;
     uint64_t s = rows >= 1024 ? 1 : std::min<uint64_t>((vecs + batch - 1) / batch, 1024 / std::max<uint64_t>(1, rows));
     if (k > 0) s = std::min<uint64_t>(s, kJoinWords / k);
@@ -668,7 +698,9 @@ LogPlan logprob_plan(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
     if (k > 0) {
         const uint64_t most = p.len / vec, least = (n - (p.splits - 1) * uint64_t(p.len)) / vec;
         p.pick = true;
-        p.fused = most <= kKept * batch && few_wanted(k, p.block, least) && (p.splits == 1 || p.splits * k <= kJoinWords);
+        // short rows' alternatives are a wave's own work there
+        const bool brief = n <= kLanes || (k <= kLanes && n <= 1024);
+        p.fused = !brief && most <= kKept * batch && few_wanted(k, p.block, least) && (p.splits == 1 || p.splits * k <= kJoinWords);
     }
     return p;
 }
@@ -770,9 +802,21 @@ template <typename F> void by_type(int type, F f) {
 bool launched() { return hipGetLastError() == hipSuccess; }
 dim3 grid_of(uint64_t tasks) { return dim3(static_cast<uint32_t>(std::min<uint64_t>(tasks, kMaxGrid))); }
 
+// Logits that the 256 MB behind the L2s cannot hold are read past the caches:
+// forward of 4096 x 131072 bf16 172 us against 191, gradient 403 against 413.
+// Smaller ones may be there from the product that made them, and are for the
+// gradient that follows: 1027 x 32768 fp32 24 us against 26, gradient 42 against 49.
+bool read_once(uint64_t rows, uint64_t n, uint64_t size) { return rows * n * size > (uint64_t(256) << 20); }
+
 template <int T, bool RANK, bool PICK> void launch_plan(const LogPlan &p, const LogArgs &a, uint32_t tasks, const Launch &L) {
-    if (p.block == 64) launch_on(logprob_kernel<T, 64, RANK, PICK>, dim3(tasks), dim3(64), L, a);
-    else launch_on(logprob_kernel<T, kLogBlock, RANK, PICK>, dim3(tasks), dim3(kLogBlock), L, a);
+    const auto go = [&](auto once) {
+        constexpr bool kOnce = decltype(once)::value;
+        if (p.block == 64) launch_on(logprob_kernel<T, 64, RANK, PICK, kOnce>, dim3(tasks), dim3(64), L, a);
+        else launch_on(logprob_kernel<T, kLogBlock, RANK, PICK, kOnce>, dim3(tasks), dim3(kLogBlock), L, a);
+    };
+    if constexpr (PICK) go(std::false_type());  // batches are read again
+    else if (read_once(a.rows, a.n, row_type_size(T))) go(std::true_type());
+    else go(std::false_type());
 }
 
 // The rows' numbers, and with a plan that has room for them the alternatives.
@@ -802,7 +846,10 @@ int logprob_values(LogArgs a, const LogPlan &p, int dtype, const Ctx &c) {
 // Rows of at most 256 KB are held: by 1024 threads where there are no more rows
 // than CUs, by the fewest that hold one where several workgroups share a CU.
 constexpr uint64_t kHeldBytes = 1024 * 16 * 16;
-bool logprob_held(uint64_t n, uint64_t size) { return n * size <= kHeldBytes; }
+bool logprob_held(uint64_t rows, uint64_t n, uint64_t size) {
+    // of few long rows, forward and gradient by many workgroups (1 x 131072 bf16: 14 us, 19 us held)
+    return n * size <= kHeldBytes && (rows > 32 || n * size <= kHeldBytes / 2);
+}
 template <int T> void launch_step(const LogArgs &a, uint32_t rows, const Launch &L) {
     const uint64_t vecs = a.n / Row<T>::kVec;
     const auto go = [&](auto kernel, int block) { launch_on(kernel, dim3(rows), dim3(block), L, a); };
@@ -833,7 +880,11 @@ int logprob_gradient(LogArgs a, int dtype, const Ctx &c) {
     if (a.rows == 0 || a.n == 0) return LRS_OK;
     gradient_split(a.rows, a.n, a.splits, a.split_len);
     TimedLaunch t(4, c);
-    by_type(dtype, [&](auto i) { launch_on(logprob_grad_kernel<i.value>, grid_of(a.rows * a.splits), dim3(kLogBlock), t.L, a); });
+    const bool once = read_once(a.rows, a.n, row_type_size(dtype));
+    by_type(dtype, [&](auto i) {
+        launch_on(once ? logprob_grad_kernel<i.value, true> : logprob_grad_kernel<i.value, false>, grid_of(a.rows * a.splits),
+                  dim3(kLogBlock), t.L, a);
+    });
     return launched() ? LRS_OK : LRS_ERR_HIP;
 }
 
@@ -983,7 +1034,7 @@ int token_logprobs_step(const lrs_logprobs *in, const float *logprob_grad, const
     a.grad = grad;
     a.grad_stride = grad_stride;
     c.elems = a.rows * a.n;
-    if (logprob_held(a.n, size)) return logprob_step(a, in->dtype, c);
+    if (logprob_held(a.rows, a.n, size)) return logprob_step(a, in->dtype, c);
     a.stats = reinterpret_cast<float *>(ws + w.stats);
     const int fs = logprob_values(a, logprob_plan(a.rows, a.n, 0, size), in->dtype, c);
     return fs != LRS_OK ? fs : logprob_gradient(a, in->dtype, c);
