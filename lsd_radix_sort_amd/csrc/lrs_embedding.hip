@@ -31,30 +31,99 @@ struct Ids {
     }
 };
 
-// Eight elements as floats, and back, at any element alignment.
-template <int T> __device__ inline void load8(const void *rows, uint64_t at, float (&f)[8]) {
-    const auto *p = static_cast<const typename Row<T>::Stored *>(rows) + at;
-    if constexpr (T == kRowF32) {
-        const u32x4 a = load16(p), b = load16(p + 4);
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t u = a[i], v = b[i];
-            f[i] = __builtin_bit_cast(float, u);
-            f[4 + i] = __builtin_bit_cast(float, v);
+// What a lane holds of a piece of a row: eight neighbouring columns, or, where
+// one of the types has 32 bits, two fours that lie apart, so that the lanes of a
+// store lie side by side in each type (32-byte steps cost 2.8 times as much).
+template <int LANES, bool FOURS> struct Columns {
+    static constexpr int kParts = FOURS ? 2 : 1, kSize = 8 / kParts;
+    uint32_t first[kParts], count[kParts];
+    __device__ Columns(uint32_t piece, uint32_t width) {
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
+            first[p] = piece * LANES * 8 + p * LANES * kSize + threadIdx.x % LANES * kSize;
+            count[p] = first[p] < width ? min(width - first[p], static_cast<uint32_t>(kSize)) : 0;
         }
-    } else {
-        unpack16<T>(load16(p), f);
     }
-}
-template <int T> __device__ inline void store8(void *rows, uint64_t at, const float (&f)[8]) {
-    auto *p = static_cast<typename Row<T>::Stored *>(rows) + at;
-    if constexpr (T == kRowF32) {
-        const float a[4] = {f[0], f[1], f[2], f[3]}, b[4] = {f[4], f[5], f[6], f[7]};
-        store16(p, pack16<kRowF32>(a));
-        store16(p + 4, pack16<kRowF32>(b));
-    } else {
-        store16(p, pack16<T>(f));
+};
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_align2 __attribute__((aligned(2)));
+
+// Those columns of one row as they are stored.
+template <int T, int LANES, bool FOURS> struct Eight {
+    using At = Columns<LANES, FOURS>;
+    static constexpr int kWords = T == kRowF32 ? 8 : 4, kEach = kWords / At::kParts;
+    uint32_t w[kWords];
+    // ONCE: not kept in the caches (a template argument: of two branches alike but for that, one is made)
+    template <bool ONCE> __device__ void load(const void *rows, uint64_t row, const At &c) {
+#pragma unroll
+        for (int p = 0; p < At::kParts; ++p) {
+            const auto *x = static_cast<const typename Row<T>::Stored *>(rows) + row + c.first[p];
+            uint32_t *v = w + p * kEach;
+            if (c.count[p] == At::kSize) {
+                if constexpr (kEach == 4) {
+                    const u32x4 q = ONCE ? load16_once(x) : load16(x);
+                    for (int i = 0; i < 4; ++i) v[i] = q[i];
+                } else {
+                    static_assert(kEach == 2);
+                    const auto *y = reinterpret_cast<const u32x2_align2 *>(x);
+                    const u32x2 q = ONCE ? __builtin_nontemporal_load(y) : *y;
+                    v[0] = q.x;
+                    v[1] = q.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) v[i] = 0;
+#pragma unroll
+                for (uint32_t e = 0; e < At::kSize; ++e) {
+                    const uint32_t q = e < c.count[p] ? x[e] : 0;
+                    if constexpr (T == kRowF32) v[e] = q;
+                    else v[e / 2] |= q << (16 * (e & 1));
+                }
+            }
+        }
     }
-}
+    __device__ void values(float (&f)[8]) const {
+        if constexpr (T == kRowF32) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __builtin_bit_cast(float, w[e]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) Row<T>::unpack(w[i], f[2 * i], f[2 * i + 1]);
+        }
+    }
+    __device__ void add_to(float (&sum)[8]) const {
+        float f[8];
+        values(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += f[e];
+    }
+    template <bool ONCE> __device__ static void store(void *rows, uint64_t row, const At &c, const float (&f)[8]) {
+        const auto put = [&](void *x, u32x4 v) { ONCE ? store16_once(x, v) : store16(x, v); };
+#pragma unroll
+        for (int p = 0; p < At::kParts; ++p) {
+            auto *x = static_cast<typename Row<T>::Stored *>(rows) + row + c.first[p];
+            const float *g = f + p * At::kSize;
+            if (c.count[p] == At::kSize) {
+                if constexpr (T == kRowF32) {
+                    put(x, u32x4{__builtin_bit_cast(uint32_t, g[0]), __builtin_bit_cast(uint32_t, g[1]),
+                                 __builtin_bit_cast(uint32_t, g[2]), __builtin_bit_cast(uint32_t, g[3])});
+                } else if constexpr (FOURS) {
+                    const u32x2 v{Row<T>::pack(g[0], g[1]), Row<T>::pack(g[2], g[3])};
+                    auto *y = reinterpret_cast<u32x2_align2 *>(x);
+                    if constexpr (ONCE) __builtin_nontemporal_store(v, y);
+                    else *y = v;
+                } else {
+                    put(x, u32x4{Row<T>::pack(g[0], g[1]), Row<T>::pack(g[2], g[3]), Row<T>::pack(g[4], g[5]),
+                                 Row<T>::pack(g[6], g[7])});
+                }
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < At::kSize; ++e)
+                    if (e < c.count[p]) x[e] = Row<T>::pattern(g[e]);
+            }
+        }
+    }
+};
 
 // ------------------------------------------------------------------ lookup
 
@@ -65,30 +134,53 @@ struct LookupArgs {
     void *out;
     uint64_t out_stride;
     uint32_t tokens, vocab, width;
+    uint32_t tasks;  // of a token
     float scale;
 };
 
-template <int T, int O>
+template <int LANES> __device__ inline uint32_t uniform(uint32_t v) {
+    return LANES == kLanes ? __builtin_amdgcn_readfirstlane(v) : v;
+}
+
+// A group of lanes has kSlots loads on their way: pieces of one token's row, or,
+// where a piece is a row, tokens.  Written past the caches: 32768 x 4096 bf16 of
+// text 63 us = 5.3 TB/s of what it has to move, 81 us through them, which the
+// rows' repeated reads need more.
+constexpr uint32_t kSlots = 4;
+template <int T, int O, int LANES>
 __global__ __launch_bounds__(kEmbBlock) void lookup_kernel(LookupArgs a) {
-    const uint32_t pieces = (a.width + 7) / 8;
-    const uint64_t all = static_cast<uint64_t>(a.tokens) * pieces;
-    for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * kEmbBlock + threadIdx.x; u < all;
-         u += static_cast<uint64_t>(gridDim.x) * kEmbBlock) {
-        const uint32_t t = static_cast<uint32_t>(u / pieces), first = static_cast<uint32_t>(u % pieces) * 8;
-        const int64_t id = a.ids[t];
-        const bool inside = id >= 0 && id < a.vocab;
-        const uint64_t from = inside ? id * a.weight_stride + first : 0, to = t * a.out_stride + first;
-        if (first + 8 <= a.width) {
-            float f[8] = {};
-            if (inside) load8<T>(a.weight, from, f);
-            for (int i = 0; i < 8; ++i) f[i] = inside ? f[i] * a.scale : 0.f;
-            store8<O>(a.out, to, f);
-        } else {
-            for (uint32_t i = 0; first + i < a.width; ++i) {
-                float f = 0.f;
-                if (inside) f = Row<T>::value(static_cast<const typename Row<T>::Stored *>(a.weight)[from + i]) * a.scale;
-                static_cast<typename Row<O>::Stored *>(a.out)[to + i] = Row<O>::pattern(f);
-            }
+    constexpr bool kFours = T == kRowF32 || O == kRowF32, kNarrow = LANES < kLanes;
+    constexpr uint32_t kGroups = kEmbBlock / LANES;
+    const uint64_t tasks = kNarrow ? (static_cast<uint64_t>(a.tokens) + kSlots - 1) / kSlots : static_cast<uint64_t>(a.tokens) * a.tasks;
+    for (uint64_t task = static_cast<uint64_t>(blockIdx.x) * kGroups + threadIdx.x / LANES; task < tasks;
+         task += static_cast<uint64_t>(gridDim.x) * kGroups) {
+        // a.tasks is 1 unless rows are long
+        const uint64_t first = kNarrow ? task * kSlots : a.tasks == 1 ? task : task / a.tasks;
+        const uint32_t piece = kNarrow ? 0 : uniform<LANES>(static_cast<uint32_t>(task - first * a.tasks)) * kSlots;
+        uint32_t token[kSlots];
+        int64_t id[kSlots];
+        bool on[kSlots], inside[kSlots];
+#pragma unroll
+        for (uint32_t j = 0; j < kSlots; ++j) {
+            token[j] = uniform<LANES>(static_cast<uint32_t>(kNarrow ? first + j : first));
+            on[j] = kNarrow ? first + j < a.tokens : (piece + j) * LANES * 8 < a.width;
+            id[j] = kNarrow ? (on[j] ? a.ids[token[j]] : -1) : j == 0 ? a.ids[token[0]] : id[0];
+            inside[j] = id[j] >= 0 && id[j] < a.vocab;
+        }
+        Eight<T, LANES, kFours> row[kSlots];
+#pragma unroll
+        for (uint32_t j = 0; j < kSlots; ++j)
+            if (on[j] && inside[j])
+                row[j].template load<false>(a.weight, id[j] * a.weight_stride, Columns<LANES, kFours>(kNarrow ? 0 : piece + j, a.width));
+#pragma unroll
+        for (uint32_t j = 0; j < kSlots; ++j) {
+            if (!on[j]) continue;
+            float f[8];
+            row[j].values(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = inside[j] ? f[e] * a.scale : 0.f;
+            Eight<O, LANES, kFours>::template store<true>(a.out, token[j] * a.out_stride,
+                                                          Columns<LANES, kFours>(kNarrow ? 0 : piece + j, a.width), f);
         }
     }
 }
@@ -104,6 +196,11 @@ __global__ __launch_bounds__(kEmbBlock) void lookup_kernel(LookupArgs a) {
 // cleared in the first launch, too.
 
 constexpr uint32_t kMaxRun = 16;
+
+// What the sums do with the gradient: write it, the sums past the caches or the
+// cleared rows past them (see launch_sums), or add to it.
+enum Mode : int { kSumsOnce, kClearOnce, kAdd };
+
 constexpr int kJoinBlock = 1024;
 
 // A long id: the first of its whole runs, how many there are, and whether the
@@ -132,7 +229,8 @@ struct GradArgs {
     uint32_t runs;                        // the last one maybe shorter
     uint32_t pieces;                      // of a row, a group of lanes each
     uint32_t sum_blocks;                  // blocks that sum; the others clear
-    uint32_t range;                       // ids whose places one workgroup orders
+    uint32_t *present;                    // a bit for every id that a token names
+    uint32_t range;                       // ids whose places one workgroup orders, a multiple of 32
     uint32_t line_factor;                 // 2^32 over the ids' length, rounded up
 };
 
@@ -140,10 +238,20 @@ struct GradArgs {
 __global__ __launch_bounds__(kEmbBlock) void embed_keys_kernel(GradArgs a) {
     const uint32_t t = blockIdx.x * kEmbBlock + threadIdx.x;
     if (t == 0) *a.long_count = 0;
+    if (!a.accumulate)
+        for (uint32_t w = t; w < (a.vocab + 31) / 32; w += gridDim.x * kEmbBlock) a.present[w] = 0;
     if (t >= a.tokens) return;
     const int64_t id = a.ids[t];
     a.keys[t] = id >= 0 && id < a.vocab && id != a.padding ? static_cast<uint32_t>(id) : a.vocab;
     a.places[t] = t;
+}
+
+// The bits of the ids that tokens name.
+__global__ __launch_bounds__(kEmbBlock) void embed_present_kernel(GradArgs a) {
+    const uint32_t i = blockIdx.x * kEmbBlock + threadIdx.x;
+    if (i >= a.tokens) return;
+    const uint32_t key = a.sorted[i];
+    if (key < a.vocab && (i == 0 || a.sorted[i - 1] != key)) atomicOr(&a.present[key / 32], 1u << (key % 32));
 }
 
 // For few tokens a workgroup finds the places of a range of ids by itself,
@@ -186,6 +294,8 @@ __global__ __launch_bounds__(kOrderBlock) void embed_order_kernel(GradArgs a, ui
     uint32_t mine = 0;
     if (threadIdx.x < ids)
         for (uint32_t w = 0; w < kWaves; ++w) mine += counter[w][threadIdx.x];
+    const uint64_t named = __ballot(mine > 0);
+    if (lane % 32 == 0 && threadIdx.x < ids) a.present[(first + threadIdx.x) / 32] = static_cast<uint32_t>(named >> lane);
     uint32_t upto = mine;
     upto += moved<0x111>(upto, 0u);
     upto += moved<0x112>(upto, 0u);
@@ -227,105 +337,15 @@ __global__ __launch_bounds__(kOrderBlock) void embed_order_kernel(GradArgs a, ui
         for (uint32_t i = all + threadIdx.x; i < a.tokens; i += kOrderBlock) sorted[i] = a.vocab;
 }
 
-// What a lane holds of a piece of a row: eight neighbouring columns, or, where
-// one of the types has 32 bits, two fours that lie apart, so that the lanes of a
-// store lie side by side in each type (32-byte steps cost 2.8 times as much).
-template <int LANES, bool FOURS> struct Columns {
-    static constexpr int kParts = FOURS ? 2 : 1, kSize = 8 / kParts;
-    uint32_t first[kParts], count[kParts];
-    __device__ Columns(uint32_t piece, uint32_t width) {
-#pragma unroll
-        for (int p = 0; p < kParts; ++p) {
-            first[p] = piece * LANES * 8 + p * LANES * kSize + threadIdx.x % LANES * kSize;
-            count[p] = first[p] < width ? min(width - first[p], static_cast<uint32_t>(kSize)) : 0;
-        }
-    }
-};
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x2 u32x2_align2 __attribute__((aligned(2)));
-
-// Those columns of one row as they are stored.
-template <int T, int LANES, bool FOURS> struct Eight {
-    using At = Columns<LANES, FOURS>;
-    static constexpr int kWords = T == kRowF32 ? 8 : 4, kEach = kWords / At::kParts;
-    uint32_t w[kWords];
-    // once: not kept in the caches
-    __device__ void load(const void *rows, uint64_t row, const At &c, bool once) {
-#pragma unroll
-        for (int p = 0; p < At::kParts; ++p) {
-            const auto *x = static_cast<const typename Row<T>::Stored *>(rows) + row + c.first[p];
-            uint32_t *v = w + p * kEach;
-            if (c.count[p] == At::kSize) {
-                if constexpr (kEach == 4) {
-                    const u32x4 q = once ? load16_once(x) : load16(x);
-                    for (int i = 0; i < 4; ++i) v[i] = q[i];
-                } else {
-                    static_assert(kEach == 2);
-                    const auto *y = reinterpret_cast<const u32x2_align2 *>(x);
-                    const u32x2 q = once ? __builtin_nontemporal_load(y) : *y;
-                    v[0] = q.x;
-                    v[1] = q.y;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kEach; ++i) v[i] = 0;
-#pragma unroll
-                for (uint32_t e = 0; e < At::kSize; ++e) {
-                    const uint32_t q = e < c.count[p] ? x[e] : 0;
-                    if constexpr (T == kRowF32) v[e] = q;
-                    else v[e / 2] |= q << (16 * (e & 1));
-                }
-            }
-        }
-    }
-    __device__ void values(float (&f)[8]) const {
-        if constexpr (T == kRowF32) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __builtin_bit_cast(float, w[e]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) Row<T>::unpack(w[i], f[2 * i], f[2 * i + 1]);
-        }
-    }
-    __device__ void add_to(float (&sum)[8]) const {
-        float f[8];
-        values(f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += f[e];
-    }
-    __device__ static void store(void *rows, uint64_t row, const At &c, const float (&f)[8]) {
-#pragma unroll
-        for (int p = 0; p < At::kParts; ++p) {
-            auto *x = static_cast<typename Row<T>::Stored *>(rows) + row + c.first[p];
-            const float *g = f + p * At::kSize;
-            if (c.count[p] == At::kSize) {
-                if constexpr (T == kRowF32) {
-                    store16(x, u32x4{__builtin_bit_cast(uint32_t, g[0]), __builtin_bit_cast(uint32_t, g[1]),
-                                          __builtin_bit_cast(uint32_t, g[2]), __builtin_bit_cast(uint32_t, g[3])});
-                } else if constexpr (FOURS) {
-                    *reinterpret_cast<u32x2_align2 *>(x) = u32x2{Row<T>::pack(g[0], g[1]), Row<T>::pack(g[2], g[3])};
-                } else {
-                    store16(x, u32x4{Row<T>::pack(g[0], g[1]), Row<T>::pack(g[2], g[3]), Row<T>::pack(g[4], g[5]),
-                                          Row<T>::pack(g[6], g[7])});
-                }
-            } else {
-#pragma unroll
-                for (uint32_t e = 0; e < At::kSize; ++e)
-                    if (e < c.count[p]) x[e] = Row<T>::pattern(g[e]);
-            }
-        }
-    }
-};
-
 // A finished sum to the table's gradient, on top of what that holds or not.
-template <int O, int LANES, bool FOURS, bool ADD>
+template <int O, int LANES, bool FOURS, int MODE>
 __device__ inline void put_row(const GradArgs &a, uint32_t id, const Columns<LANES, FOURS> &c, const float (&sum)[8],
                                const Eight<O, LANES, FOURS> &old) {
     float f[8] = {};
-    if (ADD) old.values(f);
+    if (MODE == kAdd) old.values(f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = ADD ? fmaf(sum[e], a.scale, f[e]) : sum[e] * a.scale;
-    Eight<O, LANES, FOURS>::store(a.out, id * a.out_stride, c, f);
+    for (int e = 0; e < 8; ++e) f[e] = MODE == kAdd ? fmaf(sum[e], a.scale, f[e]) : sum[e] * a.scale;
+    Eight<O, LANES, FOURS>::template store<MODE == kSumsOnce>(a.out, id * a.out_stride, c, f);
 }
 
 // Where a run's sum of a long id is kept: one place for the id that begins in
@@ -334,12 +354,26 @@ template <int LANES> __device__ inline float *part_of(const GradArgs &a, uint32_
     return a.parts + ((static_cast<uint64_t>(begins) * a.runs + run) * a.pieces + piece) * (LANES * 8) + threadIdx.x % LANES * 4;
 }
 
+// How many keys are below `id`, as `from` are at least: by a whole wave, 64
+// places tried at a time.
+__device__ inline uint32_t keys_below(const uint32_t *keys, uint32_t from, uint32_t count, uint32_t id) {
+    const uint32_t lane = threadIdx.x % kLanes;
+    uint32_t lo = from, hi = count;
+    while (hi - lo > kLanes) {
+        const uint32_t step = (hi - lo + kLanes - 1) / kLanes;
+        const uint64_t at = static_cast<uint64_t>(lo) + (lane + 1) * static_cast<uint64_t>(step) - 1;
+        lo += __popcll(__ballot(at < hi && keys[at] < id)) * step;
+        hi = lo > hi ? lo : min(hi, lo + step - 1);
+    }
+    return lo + __popcll(__ballot(lo + lane < hi && keys[lo + lane] < id));
+}
+
 // The ids of a run.  A wave looks at 64 places at once, from the one before the
 // run on; its groups of lanes take an equal share of the beginnings each, the
 // first one also the id that continues.  Rows are on their way several at a
 // time, whatever ids they are of.
-template <int T, int O, int LANES, bool ADD> __device__ void sum_run(const GradArgs &a, uint32_t run, uint32_t piece) {
-    constexpr bool kFours = T == kRowF32 || O == kRowF32;
+template <int T, int O, int LANES, int MODE> __device__ void sum_run(const GradArgs &a, uint32_t run, uint32_t piece) {
+    constexpr bool kFours = T == kRowF32 || O == kRowF32, ADD = MODE == kAdd;
     constexpr uint32_t kGroups = kLanes / LANES;
     static_assert(3 * kMaxRun - 1 < kLanes, "an id that is not long ends among the places looked at");
     const uint32_t len = a.run, last_lane = len, share = len / kGroups;  // last_lane: of the run's last place
@@ -371,22 +405,14 @@ template <int T, int O, int LANES, bool ADD> __device__ void sum_run(const GradA
     if (group == 0 && (counts & 2) && !(heads & 2) && (full || back == key1)) of_long |= bits(1, min(end1, last_lane + 1));
     todo |= of_long;
     if (full && back != key1 && piece == 0) {  // the id's first whole run
-        uint32_t runs = 1;
-        for (;;) {
-            const uint64_t end = (static_cast<uint64_t>(run) + runs + lane + 1) * len;
-            const uint64_t same = __ballot(end <= a.tokens && a.sorted[end - 1] == key1);
-            const uint32_t more = same == ~uint64_t(0) ? kLanes : __builtin_ctzll(~same);
-            runs += more;
-            if (more < kLanes) break;
-        }
+        const uint32_t end = keys_below(a.sorted, begin + len, a.tokens, key1 + 1), runs = end / len - run;
         if (lane == 0) {
-            const uint64_t next = (static_cast<uint64_t>(run) + runs) * len;
             a.longs[atomicAdd(a.long_count, 1u)] = Long{run, runs, key1, static_cast<uint16_t>(!(heads & 2)),
-                                                        static_cast<uint16_t>(next < a.tokens && a.sorted[next] == key1)};
+                                                        static_cast<uint16_t>(end % len != 0)};
         }
     }
     const Columns<LANES, kFours> c(piece, a.width);
-    constexpr int kAtOnce = T == kRowF32 || ADD ? 4 : 8;
+    constexpr int kAtOnce = T == kRowF32 || ADD ? 4 : MODE == kClearOnce ? 16 : 8;
     float sum[8] = {};
     while (__ballot(todo != 0)) {  // until all groups are done: each reads places that others' lanes hold
         Eight<T, LANES, kFours> row[kAtOnce];
@@ -407,8 +433,8 @@ template <int T, int O, int LANES, bool ADD> __device__ void sum_run(const GradA
             }
             const uint32_t at = LANES == kLanes ? __builtin_amdgcn_readlane(order, l) : __shfl(order, l);
             id[j] = LANES == kLanes ? __builtin_amdgcn_readlane(key, l) : __shfl(key, l);
-            if ((on >> j) & 1) row[j].load(a.grad, at * a.grad_stride, c, true);
-            if (ADD && ((last & ~part) >> j) & 1) old[ADD ? j : 0].load(a.out, id[j] * a.out_stride, c, false);
+            if ((on >> j) & 1) row[j].template load<true>(a.grad, at * a.grad_stride, c);
+            if (ADD && ((last & ~part) >> j) & 1) old[ADD ? j : 0].template load<false>(a.out, id[j] * a.out_stride, c);
         }
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
@@ -419,7 +445,7 @@ template <int T, int O, int LANES, bool ADD> __device__ void sum_run(const GradA
                     *reinterpret_cast<float4 *>(p) = float4{sum[0], sum[1], sum[2], sum[3]};
                     *reinterpret_cast<float4 *>(p + LANES * 4) = float4{sum[4], sum[5], sum[6], sum[7]};
                 } else {
-                    put_row<O, LANES, kFours, ADD>(a, id[j], c, sum, old[ADD ? j : 0]);
+                    put_row<O, LANES, kFours, MODE>(a, id[j], c, sum, old[ADD ? j : 0]);
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum[e] = 0.f;
@@ -428,32 +454,13 @@ template <int T, int O, int LANES, bool ADD> __device__ void sum_run(const GradA
     }
 }
 
-// How many keys are below `id`: by a whole wave, 64 places tried at a time.
-__device__ inline uint32_t keys_below(const uint32_t *keys, uint32_t count, uint32_t id) {
-    const uint32_t lane = threadIdx.x % kLanes;
-    uint32_t lo = 0, hi = count;
-    while (hi - lo > kLanes) {
-        const uint32_t step = (hi - lo + kLanes - 1) / kLanes;
-        const uint64_t at = static_cast<uint64_t>(lo) + (lane + 1) * static_cast<uint64_t>(step) - 1;
-        lo += __popcll(__ballot(at < hi && keys[at] < id)) * step;
-        hi = lo > hi ? lo : min(hi, lo + step - 1);
-    }
-    return lo + __popcll(__ballot(lo + lane < hi && keys[lo + lane] < id));
-}
-
-// Clears the rows of 32 ids that no token names, or a piece of each.
-constexpr uint32_t kClearPiece = 512;  // 16-byte stores
-template <int O> __device__ void clear_rows(const GradArgs &a, uint32_t word, uint32_t piece) {
+// Clears the rows of 32 ids that no token names, or a piece of each: 32 KB, so
+// that the last pieces do not leave most of the GPU idle.
+constexpr uint32_t kClearPiece = 64;  // 16-byte stores
+template <int O, bool ONCE> __device__ void clear_rows(const GradArgs &a, uint32_t word, uint32_t piece) {
     constexpr uint32_t kVec = Row<O>::kVec;
-    __shared__ uint32_t present;
     const uint32_t id0 = word * 32, ids = min(32u, a.vocab - id0);
-    const uint32_t from = keys_below(a.sorted, a.tokens, id0), to = keys_below(a.sorted, a.tokens, id0 + ids);
-    __syncthreads();
-    if (threadIdx.x == 0) present = 0;
-    __syncthreads();
-    for (uint32_t i = from + threadIdx.x; i < to; i += kEmbBlock) atomicOr(&present, 1u << (a.sorted[i] - id0));
-    __syncthreads();
-    const uint32_t named = present;
+    const uint32_t named = a.tokens ? a.present[word] : 0;
     const uint32_t all = (a.width + kVec - 1) / kVec, first = piece * kClearPiece, stores = min(kClearPiece, all - first);
     // rows side by side, where one does not take all threads
     const uint32_t shift = stores > kEmbBlock / 2 ? 8 : 32 - __builtin_clz(stores - 1 | 1), rows = kEmbBlock >> shift;
@@ -462,28 +469,28 @@ template <int O> __device__ void clear_rows(const GradArgs &a, uint32_t word, ui
         auto *p = static_cast<typename Row<O>::Stored *>(a.out) + (id0 + r) * a.out_stride;
         for (uint32_t u = threadIdx.x & ((1u << shift) - 1); u < stores; u += 1u << shift) {
             const uint64_t col = static_cast<uint64_t>(first + u) * kVec;
-            if (col + kVec <= a.width) store16(p + col, u32x4{0, 0, 0, 0});
+            if (col + kVec <= a.width) (ONCE ? store16_once : store16)(p + col, u32x4{0, 0, 0, 0});
             else
                 for (uint32_t e = 0; col + e < a.width; ++e) p[col + e] = 0;
         }
     }
 }
 
-template <int T, int O, int LANES, bool ADD>
+template <int T, int O, int LANES, int MODE>
 __global__ __launch_bounds__(kEmbBlock) void embed_sum_kernel(GradArgs a) {
     constexpr uint32_t kWaves = kEmbBlock / kLanes;
     if (blockIdx.x < a.sum_blocks) {
         const uint64_t tasks = static_cast<uint64_t>(a.runs) * a.pieces;
         for (uint64_t t = static_cast<uint64_t>(blockIdx.x) * kWaves + threadIdx.x / kLanes; t < tasks; t += static_cast<uint64_t>(a.sum_blocks) * kWaves)
-            sum_run<T, O, LANES, ADD>(a, __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(t / a.pieces)),
+            sum_run<T, O, LANES, MODE>(a, __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(t / a.pieces)),
                                       __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(t % a.pieces)));
         return;
     }
-    if constexpr (!ADD) {
+    if constexpr (MODE != kAdd) {
         const uint32_t pieces = ((a.width + Row<O>::kVec - 1) / Row<O>::kVec + kClearPiece - 1) / kClearPiece, words = (a.vocab + 31) / 32;
         const uint64_t tasks = static_cast<uint64_t>(words) * pieces;
         for (uint64_t t = blockIdx.x - a.sum_blocks; t < tasks; t += gridDim.x - a.sum_blocks)
-            clear_rows<O>(a, static_cast<uint32_t>(t / pieces), static_cast<uint32_t>(t % pieces));
+            clear_rows<O, MODE == kClearOnce>(a, static_cast<uint32_t>(t / pieces), static_cast<uint32_t>(t % pieces));
     }
 }
 
@@ -534,10 +541,10 @@ __global__ __launch_bounds__(kJoinBlock) void embed_join_kernel(GradArgs a) {
             const Columns<LANES, FOURS> c(piece, a.width);
             Eight<O, LANES, FOURS> old;
             if (a.accumulate) {
-                old.load(a.out, of.key * a.out_stride, c, false);
-                put_row<O, LANES, FOURS, true>(a, of.key, c, sum, old);
+                old.template load<false>(a.out, of.key * a.out_stride, c);
+                put_row<O, LANES, FOURS, kAdd>(a, of.key, c, sum, old);
             } else {
-                put_row<O, LANES, FOURS, false>(a, of.key, c, sum, old);
+                put_row<O, LANES, FOURS, kClearOnce>(a, of.key, c, sum, old);
             }
         }
     }
@@ -591,13 +598,13 @@ uint64_t run_of(uint64_t tokens, uint64_t width) {
     return groups >= 16 * 8192 ? 16 : groups >= 8 * 2048 ? 8 : 4;
 }
 // Ids a workgroup orders: as few as make a workgroup a CU.
-uint64_t range_of(uint64_t vocab) { return std::min<uint64_t>(over(vocab, 256), kMaxRange); }
+uint64_t range_of(uint64_t vocab) { return std::min<uint64_t>(over(vocab, 256 * 32) * 32, kMaxRange); }
 bool ordered_directly(uint64_t tokens, uint64_t vocab) {
     return tokens <= 32 * kOrderBlock && over(vocab, range_of(vocab)) <= 1024;
 }
 
 struct GradSpace {
-    uint64_t keys = 0, places = 0, sorted = 0, order = 0, sort = 0, sort_bytes = 0, long_count = 0, longs = 0, parts = 0, total = 0;
+    uint64_t keys = 0, places = 0, sorted = 0, order = 0, sort = 0, sort_bytes = 0, present = 0, long_count = 0, longs = 0, parts = 0, total = 0;
 };
 int key_bits(uint64_t vocab) {
     int b = 1;
@@ -614,6 +621,7 @@ GradSpace grad_space(uint64_t tokens, uint64_t vocab, uint64_t width, const lrs_
     };
     w.sorted = place(4 * tokens);
     w.order = place(4 * tokens);
+    w.present = place(over(vocab, 32) * 4);
     if (!ordered_directly(tokens, vocab)) {
         w.keys = place(4 * tokens);
         w.places = place(4 * tokens);
@@ -627,17 +635,17 @@ GradSpace grad_space(uint64_t tokens, uint64_t vocab, uint64_t width, const lrs_
     return w;
 }
 
-template <int T, int O, int LANES, bool ADD> void launch_sums(GradArgs a, const Ctx &c) {
+template <int T, int O, int LANES, int MODE> void launch_sums(GradArgs a, const Ctx &c) {
     a.pieces = static_cast<uint32_t>(over(a.width, LANES * 8));
     a.run = static_cast<uint32_t>(run_of(a.tokens, a.width));
     a.runs = static_cast<uint32_t>(over(a.tokens, a.run));
     const uint64_t tasks = static_cast<uint64_t>(a.runs) * a.pieces;
-    const uint64_t clears = ADD ? 0 : std::min(over(a.vocab, 32) * over(over(a.width, Row<O>::kVec), kClearPiece), kMaxGrid);
+    const uint64_t clears = MODE == kAdd ? 0 : std::min(over(a.vocab, 32) * over(over(a.width, Row<O>::kVec), kClearPiece), kMaxGrid);
     a.sum_blocks = static_cast<uint32_t>(std::min(over(tasks, kEmbBlock / kLanes), kMaxGrid));
     if (a.sum_blocks + clears == 0) return;
     {
         TimedLaunch t(4, c);
-        launch_on(embed_sum_kernel<T, O, LANES, ADD>, dim3(static_cast<uint32_t>(a.sum_blocks + clears)), dim3(kEmbBlock), t.L, a);
+        launch_on(embed_sum_kernel<T, O, LANES, MODE>, dim3(static_cast<uint32_t>(a.sum_blocks + clears)), dim3(kEmbBlock), t.L, a);
     }
     if (a.tokens < a.run || hipPeekAtLastError() != hipSuccess) return;
     TimedLaunch t(4, c);
@@ -681,10 +689,17 @@ int embedding_forward(const void *weight, int64_t weight_stride, const lrs_token
     a.width = static_cast<uint32_t>(width);
     a.scale = scale;
     c.elems = static_cast<uint64_t>(count) * width;
-    const uint64_t pieces = static_cast<uint64_t>(count) * ((width + 7) / 8);
-    const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>((pieces + kEmbBlock - 1) / kEmbBlock, kMaxGrid)));
+    const uint64_t lanes = width <= 16 * 8 ? 16 : width <= 32 * 8 ? 32 : kLanes;
+    a.tasks = static_cast<uint32_t>(over(width, lanes * 8 * kSlots));
+    const uint64_t tasks = lanes < kLanes ? over(count, kSlots) : static_cast<uint64_t>(count) * a.tasks;
+    const dim3 grid(static_cast<uint32_t>(std::min(over(tasks, kEmbBlock / lanes), kMaxGrid)));
     TimedLaunch t(4, c);
-    by_types(dtype, out_dtype, [&](auto i, auto o) { launch_on(lookup_kernel<i.value, o.value>, grid, dim3(kEmbBlock), t.L, a); });
+    by_types(dtype, out_dtype, [&](auto i, auto o) {
+        const auto go = [&](auto kernel) { launch_on(kernel, grid, dim3(kEmbBlock), t.L, a); };
+        if (lanes == 16) go(lookup_kernel<i.value, o.value, 16>);
+        else if (lanes == 32) go(lookup_kernel<i.value, o.value, 32>);
+        else go(lookup_kernel<i.value, o.value, kLanes>);
+    });
     return hipGetLastError() == hipSuccess ? LRS_OK : LRS_ERR_HIP;
 } catch (...) {
     return LRS_ERR_HIP;
@@ -739,6 +754,7 @@ int embedding_backward(const void *grad, int64_t grad_stride, const lrs_token_id
         a.order = order;
         a.long_count = reinterpret_cast<uint32_t *>(ws + w.long_count);
         a.longs = reinterpret_cast<Long *>(ws + w.longs);
+        a.present = reinterpret_cast<uint32_t *>(ws + w.present);
         a.parts = reinterpret_cast<float *>(ws + w.parts);
         const bool direct = ordered_directly(count, vocab);
         {
@@ -767,12 +783,25 @@ int embedding_backward(const void *grad, int64_t grad_stride, const lrs_token_id
             st = radix_sort_pairs(a.keys, a.places, sorted, order, a.tokens, 0, key_bits(vocab), 8, ws + w.sort, w.sort_bytes,
                                   stream, opts);
             if (st != LRS_OK) return st;
+            if (!a.accumulate) {
+                TimedLaunch t(4, c);
+                launch_on(embed_present_kernel, dim3((a.tokens + kEmbBlock - 1) / kEmbBlock), dim3(kEmbBlock), t.L, a);
+                if (hipGetLastError() != hipSuccess) return LRS_ERR_HIP;
+            }
         }
     }
     by_types(dtype, out_dtype, [&](auto i, auto o) {
-        const bool narrow = lanes_of(width) == 16;
-        if (a.accumulate) narrow ? launch_sums<i.value, o.value, 16, true>(a, c) : launch_sums<i.value, o.value, kLanes, true>(a, c);
-        else narrow ? launch_sums<i.value, o.value, 16, false>(a, c) : launch_sums<i.value, o.value, kLanes, false>(a, c);
+        const auto go = [&](auto mode) {
+            constexpr int kMode = decltype(mode)::value;
+            lanes_of(width) == 16 ? launch_sums<i.value, o.value, 16, kMode>(a, c) : launch_sums<i.value, o.value, kLanes, kMode>(a, c);
+        };
+        // Beside reads past the caches: a gradient far larger than the 256 MB
+        // behind the L2s is cleared past them, and its sums are not (1.07 GB from
+        // 32768 tokens: 228 us, 252 with both and 269 with neither); of a smaller one the
+        // sums are (320 MB from 8188 tokens: 63 us, 76 with both, 71 with neither).
+        if (a.accumulate) go(std::integral_constant<int, kAdd>());
+        else if (wb > (uint64_t(512) << 20)) go(std::integral_constant<int, kClearOnce>());
+        else go(std::integral_constant<int, kSumsOnce>());
     });
     return hipGetLastError() == hipSuccess ? LRS_OK : LRS_ERR_HIP;
 } catch (...) {
