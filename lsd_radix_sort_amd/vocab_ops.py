@@ -24,6 +24,9 @@ from . import row_ops as _rows
 from .row_ops import _ID_BYTES, _dtype_code, _grad_out, _mask, _matrix, _whole
 
 
+_MAX_TOPK = 1024  # LRS_MAX_TOPK
+
+
 class _TokenIds(ctypes.Structure):
     # mirrors struct lrs_token_ids
     _fields_ = [("ids", ctypes.c_void_p), ("lines", ctypes.c_int64), ("length", ctypes.c_int64),
@@ -259,6 +262,8 @@ def token_logprobs_topk(logits: torch.Tensor, tokens: torch.Tensor, k: int, temp
     token where ranks[r] < k; a token outside [0, n) has rank -1.
     Returns (logprobs, entropy, ranks [rows] int32, top_logprobs [rows, k] float32, top_indices [rows, k] int64)."""
     k = _whole(k, "k")
+    if not 0 <= k <= _MAX_TOPK:
+        _lrs._bad(f"k must be between 0 and {_MAX_TOPK}, got {k}")
     if workspace is None and options is None:
         fast = (_rows._fast or _rows._binding()).logprobs_topk(logits, tokens, k, _number(temperature, "temperature"))
         if fast is not None:
@@ -303,6 +308,8 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, row_stat
     d = _logprob_inputs(logits, tokens, temperature, row_mask)
     device = logits.device
     _lrs.check_output(row_stats, "row_stats", device, 4, (d.rows, 3))
+    if row_stats.dtype != torch.float32:
+        _lrs._bad("row_stats must be float32, as token_logprobs_forward returned them")
     up, up_entropy = _derivatives(logprob_grad, entropy_grad, d, device)
     with torch.cuda.device(device):
         grad_out = _grad_out(grad_out, logits)
@@ -319,8 +326,8 @@ def token_logprobs_step(logits: torch.Tensor, tokens: torch.Tensor, logprob_grad
     """token_logprobs_forward and _backward in one call, for derivatives that are known beforehand (such as those of
     a weighted sum of log probabilities): returns (logprobs, entropy, grad)."""
     if grad_out is None and workspace is None and options is None:
-        fast = (_rows._fast or _rows._binding()).logprobs_step(logits, tokens, logprob_grad, entropy_grad, _number(temperature, "temperature"),
-                                                               row_mask)
+        fast = (_rows._fast or _rows._binding()).logprobs_step(logits, tokens, logprob_grad, entropy_grad,
+                                                               _number(temperature, "temperature"), row_mask)
         if fast is not None:
             return fast
     lib = _lrs.load_library()
