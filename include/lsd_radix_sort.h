@@ -377,7 +377,7 @@ int expert_balance_step(const void *logits, int64_t row_stride, const void *indi
  *   dtype        LRS_DTYPE_* of weight (forward), of grad (backward)
  *   out_dtype    LRS_DTYPE_* of out (forward), of grad_weight (backward)
  * Strides are at least 0, of outputs with more than one row at least width.
- * lines * length < 2^31; 0 <= vocab < 2^31; width <= LRS_MAX_ROW_LEN; tokens *
+ * lines * length < 2^31; 0 <= vocab < 2^31 - 1; width <= LRS_MAX_ROW_LEN; tokens *
  * width and vocab * width below 2^40; scale finite (else LRS_ERR_OPTION).
  * No tokens: the forward does nothing, the backward clears or keeps
  * grad_weight.  opts goes to the sort as well; the operators' own kernels use

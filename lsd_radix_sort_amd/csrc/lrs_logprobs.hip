@@ -673,11 +673,12 @@ __global__ __launch_bounds__(B, 4) void logprob_step_kernel(LogArgs a) {
 constexpr uint64_t kMaxGrid = 1u << 20;
 
 // How the rows are laid out on workgroups: a wave a row for up to 4 KB of many
-// rows (32 KB of very many: 8192 x 4096 bf16 17 us against 24), else 256 threads, and several workgroups a row where rows are fewer than
-// fill the GPU, down to a batch of loads a thread each.  With alternatives (k > 0)
-// a workgroup holds at most kKept batches, k is at most half of its threads, and
-// the pieces' words fit one workgroup; where that cannot be (fused false)
-// segmented_row_topk selects them.
+// rows (32 KB of very many: 8192 x 4096 bf16 17 us against 24), else 256 threads,
+// and several workgroups a row where rows are fewer than fill the GPU, down to a
+// batch of loads a thread each.  With alternatives (k > 0) a workgroup holds at
+// most kKept batches, k is at most half of its threads, and the pieces' words fit
+// one workgroup; where that cannot be (fused false) segmented_row_topk selects
+// them.
 struct LogPlan {
     int block = kLogBlock;
     uint32_t splits = 1, len = 8;
@@ -937,9 +938,10 @@ int token_logprobs_topk(const lrs_logprobs *in, int64_t k, float *logprobs, floa
     if (a.mask != nullptr) return LRS_ERR_OPTION;
     if (a.rows == 0) return LRS_OK;
     const LogSpace w = logprob_space(a.rows, a.n, a.k, in->dtype);
-    if (!logprobs || !entropy || !ranks || (k > 0 && (!top_logprobs || !top_indices)) || !workspace) return LRS_ERR_NULL_POINTER;
+    if (!logprobs || !entropy || !ranks || (k > 0 && (!top_logprobs || !top_indices)) || (w.total && !workspace))
+        return LRS_ERR_NULL_POINTER;
     if (misaligned(logprobs, 4) || misaligned(entropy, 4) || misaligned(ranks, 4) || misaligned(top_logprobs, 4) ||
-        misaligned(top_indices, 8) || misaligned(workspace, 256))
+        misaligned(top_indices, 8) || (w.total && misaligned(workspace, 256)))
         return LRS_ERR_ALIGNMENT;
     if (workspace_bytes < w.total) return LRS_ERR_WORKSPACE_TOO_SMALL;
     const void *const out[] = {logprobs, entropy, ranks, top_logprobs, top_indices, workspace};

@@ -104,6 +104,26 @@ def test_refusals():
             pytest.fail(f"call {i} was taken")
 
 
+def test_no_workspace_needed():
+    """Where the query says 0 bytes, the workspace may be NULL."""
+    from lsd_radix_sort_amd.vocab_ops import _logprob_inputs, _token_ids
+    import ctypes
+    lib, P = lrs.load_library(), ctypes.c_void_p
+    logits, tokens = torch.randn(2, 3000, device="cuda"), torch.tensor([7, 2999], device="cuda")
+    want = lrs.token_logprobs_topk(logits, tokens, 5)
+    assert lrs.token_logprobs_workspace_size(2, 3000, 5, torch.float32) == 0
+    out = [torch.empty_like(t) for t in want]
+    d = _logprob_inputs(logits, tokens, 1.0)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.token_logprobs_topk(ctypes.byref(d), 5, *(P(t.data_ptr()) for t in out), None, 0, P(stream), None) == 0
+    same(tuple(out), want)
+    table, none = torch.ones(40, 8, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda")
+    assert lrs.embedding_backward_workspace_size(0, 40, 8) == 0
+    assert lib.embedding_backward(None, 8, ctypes.byref(_token_ids(none, none.device)), P(table.data_ptr()), 8, 40, 8, 2, 2, 1.0, -1, 0,
+                                  None, 0, P(stream), None) == 0
+    assert not table.any()
+
+
 def test_too_many_elements():
     rows, n = 1 << 25, 65_536  # rows that all lie at the same place
     logits = torch.zeros(1, n, dtype=torch.float16, device="cuda").expand(rows, n)
