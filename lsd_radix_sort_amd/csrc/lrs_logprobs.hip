@@ -31,7 +31,7 @@ namespace {
 constexpr int kLogBlock = 256;
 constexpr int kLoads = 4;              // of a batch
 constexpr int kKept = 16;              // batches whose largest elements are kept
-constexpr uint32_t kPickWords = 512;   // candidates in LDS
+constexpr uint32_t kPickWords = 512;   // candidates in LDS, by fewer threads than that
 constexpr uint32_t kJoinWords = 1024;  // of a row's pieces
 constexpr double kLog2e = 1.44269504088896340736;
 constexpr double kLn2 = 0.693147180559945309417;
@@ -283,11 +283,11 @@ template <int T> struct Token {
 // that reach the bound are read again.  Else a row may have any length.
 // ONCE: the logits are read past the caches (see read_once).
 template <int T, int B, bool RANK, bool PICK, bool ONCE>
-__global__ __launch_bounds__(B, B == 64 && PICK ? 3 : T == kRowF32 && PICK ? 5 : 7) void logprob_kernel(LogArgs a) {
+__global__ __launch_bounds__(B, B == 1024 ? 4 : B == 64 && PICK ? 3 : T == kRowF32 && PICK ? 5 : 7) void logprob_kernel(LogArgs a) {
     constexpr int kVec = Row<T>::kVec, kWidth = T == kRowF32 ? 4 : 2;
     using Stored = typename Row<T>::Stored;
     __shared__ JoinLds<B> join;
-    __shared__ SelectLds<B, PICK ? kPickWords : B> lds;
+    __shared__ SelectLds<B, PICK && B < kPickWords ? kPickWords : B> lds;
     __shared__ Stored kept[PICK ? kKept : 1][B];
     __shared__ double whole;
     const uint32_t tid = threadIdx.x;
@@ -672,13 +672,18 @@ __global__ __launch_bounds__(B, 4) void logprob_step_kernel(LogArgs a) {
 
 constexpr uint64_t kMaxGrid = 1u << 20;
 
-// How the rows are laid out on workgroups: a wave a row for up to 4 KB of many
-// rows (32 KB of very many: 8192 x 4096 bf16 17 us against 24), else 256 threads,
-// and several workgroups a row where rows are fewer than fill the GPU, down to a
-// batch of loads a thread each.  With alternatives (k > 0) a workgroup holds at
-// most kKept batches, k is at most half of its threads, and the pieces' words fit
-// one workgroup; where that cannot be (fused false) segmented_row_topk selects
-// them.
+// How the rows are laid out on workgroups.  A row that several share costs a
+// second launch, 3 to 4 us, so that most have one:
+//  - a wave for up to 4 KB of many rows (32 KB of very many: 8192 x 4096 bf16 17 us
+//    against 24), else 256 threads (400 x 16000 bf16 top 5 11 us, shared by two 15);
+//  - 1024 threads where there are no more rows than CUs and a row is more than a
+//    load a thread (48 x 32000 bf16 top 5 11.1 us, shared 12.6; 256 x 9000 fp16
+//    8.4 against 12.0).
+// Shared are long rows of too few to fill the GPU, down to a batch of loads a thread
+// (1 x 131072 bf16 top 5 11.4 us, 17.3 by 1024 threads; 200 of them 24.5 against
+// 20.8).  With alternatives (k > 0) a workgroup holds at most kKept batches, k is at
+// most half of its threads, and the pieces' words fit one workgroup; where that
+// cannot be (fused false) segmented_row_topk selects them.
 struct LogPlan {
     int block = kLogBlock;
     uint32_t splits = 1, len = 8;
@@ -689,8 +694,11 @@ LogPlan logprob_plan(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
     const uint64_t vec = 16 / size, vecs = n / vec;
     if (rows >= 512 && vecs <= 64 * kLoads) p.block = 64;
     if (rows >= 2048 && vecs <= 2048 && k == 0) p.block = 64;
+    const uint64_t bytes = n * size;
+    if (rows <= 256 && vecs > 1024 && bytes <= (rows < 128 ? 64 : 512) * 1024) p.block = 1024;
+    const bool alone = p.block == 1024 || rows >= 1024 || (rows > 256 && bytes <= 256 * 1024);
     const uint64_t batch = static_cast<uint64_t>(kLoads) * p.block;
-    uint64_t s = rows >= 1024 ? 1 : std::min<uint64_t>((vecs + batch - 1) / batch, 1024 / std::max<uint64_t>(1, rows));
+    uint64_t s = alone ? 1 : std::min<uint64_t>((vecs + batch - 1) / batch, 1024 / std::max<uint64_t>(1, rows));
     if (k > 0) s = std::min<uint64_t>(s, kJoinWords / k);
     s = std::max<uint64_t>(s, k > 0 ? (vecs + kKept * batch - 1) / (kKept * batch) : n >> 20);
     s = std::max<uint64_t>(s, 1);
@@ -813,6 +821,7 @@ template <int T, bool RANK, bool PICK> void launch_plan(const LogPlan &p, const 
     const auto go = [&](auto once) {
         constexpr bool kOnce = decltype(once)::value;
         if (p.block == 64) launch_on(logprob_kernel<T, 64, RANK, PICK, kOnce>, dim3(tasks), dim3(64), L, a);
+        else if (p.block == 1024) launch_on(logprob_kernel<T, 1024, RANK, PICK, kOnce>, dim3(tasks), dim3(1024), L, a);
         else launch_on(logprob_kernel<T, kLogBlock, RANK, PICK, kOnce>, dim3(tasks), dim3(kLogBlock), L, a);
     };
     if constexpr (PICK) go(std::false_type());  // batches are read again

@@ -212,6 +212,24 @@ def test_many_rows(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kind", ["any", "lowest", "levels", "equal", "zeros"])
+@pytest.mark.parametrize("shape", [(3, 32003, 3), (130, 60001, 0), (256, 9007, 1), (257, 9007, 0)], ids=lambda s: f"{s[0]}x{s[1]}")
+def test_alternatives_of_rows_alone(dtype, kind, shape):
+    """Rows that one workgroup holds: its most alternatives, and more than one batch of loads a thread."""
+    rows, n, pad = shape
+    log(f"{dtype} {kind} {shape}")
+    x, tokens, logits = make(kind, rows, n, DTYPES[dtype], rows + n, pad)
+    ref = Reference(x, tokens, 0.8)
+    for k in (3, 300, 512, 513):
+        lp, h, ranks, top, indices = (t.cpu() for t in lrs.token_logprobs_topk(logits, tokens.cuda(), k, 0.8))
+        ref.values(lp, h)
+        check_places(x, tokens, k, ranks, indices)
+        want = in_32_bits(torch.where(ref.empty[:, None], -INF, torch.gather(ref.logp, 1, indices)))
+        off = (top.double() - want).abs()
+        assert bool(torch.where(torch.isinf(want), top.double() == want, off <= ref.lse_off[:, None] + 2 * ULP * want.abs()).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_masked_rows_hold_anything(dtype):
     x, tokens, logits = make("any", 6, 2003, DTYPES[dtype], 3)
     for r, v in ((0, float("nan")), (1, INF), (2, -INF)):
