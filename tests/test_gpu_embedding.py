@@ -154,6 +154,31 @@ def test_gradient(dtype, out, tokens):
         assert torch.equal(got, lrs.embedding_backward(*args, dtype=DTYPES[out]))  # bit for bit
 
 
+@pytest.mark.parametrize("dtype,out", [("fp16", "fp16"), ("bf16", "fp32"), ("fp32", "bf16"), ("fp32", "fp32")])
+@pytest.mark.parametrize("tokens,vocab,width,pad", [(2048, 700, 128, 0), (2047, 33, 121, 5), (1000, 5003, 261, 0), (130, 40, 2015, 1),
+                                                    (60, 9, 4096, 0), (2049, 500, 40, 0), (2048, 700, 129, 0), (100, 40_000, 420, 0),
+                                                    (1025, 513, 250, 2), (17, 100_003, 130, 0)])
+def test_gradient_of_few_tokens(dtype, out, tokens, vocab, width, pad):
+    """One launch's work and what is just too much for that, added and not."""
+    g = torch.Generator().manual_seed(tokens + width)
+    for kind in ("any", "text", "same", "runs", "outside"):
+        log(f"few {dtype} -> {out} {tokens} {vocab} {width} {kind}")
+        ids = make_ids(kind, torch.Size((tokens,)), vocab, g)
+        grad = torch.randn(tokens, width, generator=g).to(DTYPES[dtype])
+        lines = torch.full((tokens, 3), vocab // 2)
+        lines[:, 1] = ids
+        ours = lines.int().cuda()[:, 1] if kind == "runs" else ids.cuda()
+        args = (padded(grad.cuda(), pad), ours, vocab, 0.9)
+        got = lrs.embedding_backward(*args, padding_index=vocab // 3, dtype=DTYPES[out])
+        check_gradient(got.cpu(), grad, ids, vocab, 0.9, vocab // 3)
+        old = torch.randn(vocab, width, generator=g).to(DTYPES[out])
+        sums = [padded(old.cuda(), pad) for _ in range(2)]
+        for s in sums:
+            lrs.embedding_backward(*args, grad_out=s, accumulate=True)
+        assert torch.equal(*sums)
+        check_gradient(sums[0].cpu(), grad, ids, vocab, 0.9, old=old)
+
+
 @pytest.mark.parametrize("width", WIDTHS)
 def test_gradient_widths(width):
     g = torch.Generator().manual_seed(width)
