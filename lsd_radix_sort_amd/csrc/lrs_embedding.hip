@@ -203,6 +203,7 @@ constexpr uint32_t kMaxRun = 16;
 enum Mode : int { kSumsOnce, kClearOnce, kAdd };
 
 constexpr int kJoinBlock = 1024;
+constexpr uint32_t kShort = 16;  // runs of a long id that a group of lanes joins alone
 
 // A long id: the first of its whole runs, how many there are, and whether the
 // runs before and after them hold places of it.
@@ -223,8 +224,8 @@ struct GradArgs {
     int accumulate;
     uint32_t *keys, *places;              // unsorted
     const uint32_t *sorted, *order;       // the sorted keys and their places
-    uint32_t *long_count;
-    Long *longs;
+    uint32_t *long_count;                 // of more than kShort runs, of fewer
+    Long *longs;                          // [runs]: the former from the front, the latter from the back
     float *parts;                         // [2][runs][pieces][lanes * 8]: see part_of
     uint32_t run;                         // places in a run: 4, 8 or 16
     uint32_t runs;                        // the last one maybe shorter
@@ -238,7 +239,7 @@ struct GradArgs {
 // The keys of the sort: ids, those that count for nothing behind the last.
 __global__ __launch_bounds__(kEmbBlock) void embed_keys_kernel(GradArgs a) {
     const uint32_t t = blockIdx.x * kEmbBlock + threadIdx.x;
-    if (t == 0) *a.long_count = 0;
+    if (t < 2) a.long_count[t] = 0;
     if (!a.accumulate)
         for (uint32_t w = t; w < (a.vocab + 31) / 32; w += gridDim.x * kEmbBlock) a.present[w] = 0;
     if (t >= a.tokens) return;
@@ -278,7 +279,7 @@ __global__ __launch_bounds__(kOrderBlock) void embed_order_kernel(GradArgs a, ui
         const uint32_t t = from + i * kLanes, line = a.ids.length == 1 ? t : __umulhi(t, a.line_factor);
         id[i] = t < a.tokens ? static_cast<const Id *>(a.ids.at)[static_cast<uint64_t>(line) * a.ids.stride + (t - line * a.ids.length)] : -1;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.long_count = 0;
+    if (blockIdx.x == 0 && threadIdx.x < 2) a.long_count[threadIdx.x] = 0;
     for (uint32_t i = lane; i < ids; i += kLanes) counter[wave][i] = 0;
     // within the range: the id's place there
     uint32_t of[N], below = 0;
@@ -402,8 +403,10 @@ template <int T, int O, int LANES, int MODE> __device__ void sum_run(const GradA
     if (full && back != key1 && piece == 0) {  // the id's first whole run
         const uint32_t end = keys_below(a.sorted, begin + len, a.tokens, key1 + 1), runs = end / len - run;
         if (lane == 0) {
-            a.longs[atomicAdd(a.long_count, 1u)] = Long{run, runs, key1, static_cast<uint16_t>(!(heads & 2)),
-                                                        static_cast<uint16_t>(end % len != 0)};
+            const bool few = runs <= kShort;
+            const uint32_t at = atomicAdd(&a.long_count[few], 1u);
+            a.longs[few ? a.runs - 1 - at : at] = Long{run, runs, key1, static_cast<uint16_t>(!(heads & 2)),
+                                                       static_cast<uint16_t>(end % len != 0)};
         }
     }
     const Columns<LANES, kFours> c(piece, a.width);
@@ -624,59 +627,76 @@ __global__ __launch_bounds__(kOrderBlock) void embed_few_kernel(GradArgs a) {
     }
 }
 
-// The long ids, a workgroup each and piece: its groups take the runs in equal
-// shares, and their sums are added in order.
+// The long ids: those of many runs by a workgroup each and piece, whose groups take
+// the runs in equal shares and whose sums are added in order; the others by a
+// group each (65536 tokens, each id 13 times, 64 columns: 31 us by a workgroup each
+// XXX).
 template <int O, int LANES, bool FOURS>
 __global__ __launch_bounds__(kJoinBlock) void embed_join_kernel(GradArgs a) {
     constexpr uint32_t kGroups = kJoinBlock / LANES, kAtOnce = 4;
     __shared__ float4 shared[kGroups][2][LANES];
     const uint32_t group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-    const uint64_t tasks = static_cast<uint64_t>(*a.long_count) * a.pieces;
-    for (uint64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
-        const Long of = a.longs[task / a.pieces];
-        const uint32_t piece = static_cast<uint32_t>(task % a.pieces);
-        float sum[8] = {};
-        const auto add = [&](float4 p, float4 q) {
-            const float f[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+    float sum[8] = {};
+    const auto add = [&](float4 p, float4 q) {
+        const float f[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += f[e];
-        };
+        for (int e = 0; e < 8; ++e) sum[e] += f[e];
+    };
+    // the sum of runs [from, to), from the part of the run before them on if that is wanted
+    const auto sum_runs = [&](const Long &of, uint32_t piece, bool before, uint32_t from, uint32_t to) {
         const auto halves = [&](uint32_t begins, uint32_t run, float4 &p, float4 &q) {
             const float *at = part_of<LANES>(a, begins, run, piece);
             p = *reinterpret_cast<const float4 *>(at);
             q = *reinterpret_cast<const float4 *>(at + LANES * 4);
         };
-        if (group == 0 && of.before) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+        if (before) {
             float4 p, q;
             halves(1, of.run - 1, p, q);
             add(p, q);
         }
-        const uint32_t all = of.runs + of.after, share = (all + kGroups - 1) / kGroups;
-        const uint32_t mine = min(group * share, all), next = min(mine + share, all);
-        for (uint32_t r = mine; r < next; r += kAtOnce) {
+        for (uint32_t r = from; r < to; r += kAtOnce) {
             float4 p[kAtOnce], q[kAtOnce];
 #pragma unroll
             for (uint32_t j = 0; j < kAtOnce; ++j)
-                if (r + j < next) halves(0, of.run + r + j, p[j], q[j]);
+                if (r + j < to) halves(0, of.run + r + j, p[j], q[j]);
 #pragma unroll
             for (uint32_t j = 0; j < kAtOnce; ++j)
-                if (r + j < next) add(p[j], q[j]);
+                if (r + j < to) add(p[j], q[j]);
         }
+    };
+    const auto put = [&](uint32_t key, uint32_t piece) {
+        const Columns<LANES, FOURS> c(piece, a.width);
+        Eight<O, LANES, FOURS> old;
+        if (a.accumulate) {
+            old.template load<false>(a.out, key * a.out_stride, c);
+            put_row<O, LANES, FOURS, kAdd>(a, key, c, sum, old);
+        } else {
+            put_row<O, LANES, FOURS, kClearOnce>(a, key, c, sum, old);
+        }
+    };
+    const uint64_t many = static_cast<uint64_t>(a.long_count[0]) * a.pieces, few = static_cast<uint64_t>(a.long_count[1]) * a.pieces;
+    for (uint64_t task = blockIdx.x; task < many; task += gridDim.x) {
+        const Long of = a.longs[task / a.pieces];
+        const uint32_t piece = static_cast<uint32_t>(task % a.pieces);
+        const uint32_t all = of.runs + of.after, share = (all + kGroups - 1) / kGroups, from = min(group * share, all);
+        sum_runs(of, piece, group == 0 && of.before, from, min(from + share, all));
         __syncthreads();  // the last task's readers are done
         shared[group][0][lane] = float4{sum[0], sum[1], sum[2], sum[3]};
         shared[group][1][lane] = float4{sum[4], sum[5], sum[6], sum[7]};
         __syncthreads();
         if (group == 0) {
             for (uint32_t g = 1; g < kGroups; ++g) add(shared[g][0][lane], shared[g][1][lane]);
-            const Columns<LANES, FOURS> c(piece, a.width);
-            Eight<O, LANES, FOURS> old;
-            if (a.accumulate) {
-                old.template load<false>(a.out, of.key * a.out_stride, c);
-                put_row<O, LANES, FOURS, kAdd>(a, of.key, c, sum, old);
-            } else {
-                put_row<O, LANES, FOURS, kClearOnce>(a, of.key, c, sum, old);
-            }
+            put(of.key, piece);
         }
+    }
+    for (uint64_t task = static_cast<uint64_t>(gridDim.x - 1 - blockIdx.x) * kGroups + group; task < few;
+         task += static_cast<uint64_t>(gridDim.x) * kGroups) {
+        const Long of = a.longs[a.runs - 1 - task / a.pieces];
+        const uint32_t piece = static_cast<uint32_t>(task % a.pieces);
+        sum_runs(of, piece, of.before, 0, of.runs + of.after);
+        put(of.key, piece);
     }
 }
 
@@ -773,7 +793,7 @@ GradSpace grad_space(uint64_t tokens, uint64_t vocab, uint64_t width, const lrs_
         w.sort = place(w.sort_bytes);
     }
     const uint64_t runs = over(tokens, run_of(tokens, width)), lanes = lanes_of(width);
-    w.long_count = place(4);
+    w.long_count = place(8);
     w.longs = place(runs * sizeof(Long));
     w.parts = place(2 * runs * over(width, lanes * 8) * lanes * 8 * sizeof(float));
     return w;
