@@ -38,10 +38,11 @@ struct Ids {
 template <int LANES, bool FOURS> struct Columns {
     static constexpr int kParts = FOURS ? 2 : 1, kSize = 8 / kParts;
     uint32_t first[kParts], count[kParts];
-    __device__ Columns(uint32_t piece, uint32_t width) {
+    __device__ Columns(uint32_t piece, uint32_t width) : Columns(piece, width, threadIdx.x % LANES) {}
+    __device__ Columns(uint32_t piece, uint32_t width, uint32_t lane) {
 #pragma unroll
         for (int p = 0; p < kParts; ++p) {
-            first[p] = piece * LANES * 8 + p * LANES * kSize + threadIdx.x % LANES * kSize;
+            first[p] = piece * LANES * 8 + p * LANES * kSize + lane * kSize;
             count[p] = first[p] < width ? min(width - first[p], static_cast<uint32_t>(kSize)) : 0;
         }
     }
@@ -203,7 +204,7 @@ constexpr uint32_t kMaxRun = 16;
 enum Mode : int { kSumsOnce, kClearOnce, kAdd };
 
 constexpr int kJoinBlock = 1024;
-constexpr uint32_t kShort = 16;  // runs of a long id that a group of lanes joins alone
+constexpr uint32_t kShort = 8;  // runs of a long id that a group of lanes joins alone
 
 // A long id: the first of its whole runs, how many there are, and whether the
 // runs before and after them hold places of it.
@@ -346,8 +347,8 @@ __device__ inline void put_row(const GradArgs &a, uint32_t id, const Columns<LAN
 
 // Where a run's sum of a long id is kept: one place for the id that begins in
 // an earlier run or has the whole one, one for the id that begins within.
-template <int LANES> __device__ inline float *part_of(const GradArgs &a, uint32_t begins, uint32_t run, uint32_t piece) {
-    return a.parts + ((static_cast<uint64_t>(begins) * a.runs + run) * a.pieces + piece) * (LANES * 8) + threadIdx.x % LANES * 4;
+template <int LANES> __device__ inline float *part_of(const GradArgs &a, uint32_t begins, uint32_t run, uint32_t piece, uint32_t lane) {
+    return a.parts + ((static_cast<uint64_t>(begins) * a.runs + run) * a.pieces + piece) * (LANES * 8) + lane * 4;
 }
 
 // How many keys are below `id`, as `from` are at least: by a whole wave, 64
@@ -439,7 +440,7 @@ template <int T, int O, int LANES, int MODE> __device__ void sum_run(const GradA
             if ((on >> j) & 1) row[j].add_to(sum);
             if ((last >> j) & 1) {
                 if ((part >> j) & 1) {
-                    float *p = part_of<LANES>(a, (begins >> j) & 1, run, piece);
+                    float *p = part_of<LANES>(a, (begins >> j) & 1, run, piece, threadIdx.x % LANES);
                     *reinterpret_cast<float4 *>(p) = float4{sum[0], sum[1], sum[2], sum[3]};
                     *reinterpret_cast<float4 *>(p + LANES * 4) = float4{sum[4], sum[5], sum[6], sum[7]};
                 } else {
@@ -627,15 +628,16 @@ __global__ __launch_bounds__(kOrderBlock) void embed_few_kernel(GradArgs a) {
     }
 }
 
-// The long ids: those of many runs by a workgroup each and piece, whose groups take
-// the runs in equal shares and whose sums are added in order; the others by a
-// group each (65536 tokens, each id 13 times, 64 columns: 31 us by a workgroup each
-// XXX).
+// The long ids.  Those of few runs take a group of lanes each and piece (65536
+// tokens, each id 13 times, 64 columns: 83 us in all, 126 by a workgroup each);
+// those of many a workgroup for 16 lanes of a piece, whose groups of 16 take the
+// runs in equal shares, joined in an order of their own (32768 tokens of one id,
+// 4096 columns: 107 us in all, 134 by a workgroup for the piece, and 102 by 8 lanes,
+// which cost text 3 us).
 template <int O, int LANES, bool FOURS>
 __global__ __launch_bounds__(kJoinBlock) void embed_join_kernel(GradArgs a) {
-    constexpr uint32_t kGroups = kJoinBlock / LANES, kAtOnce = 4;
-    __shared__ float4 shared[kGroups][2][LANES];
-    const uint32_t group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+    constexpr uint32_t kAtOnce = 4, kNarrow = 16, kShares = kJoinBlock / kNarrow, kSubs = LANES / kNarrow;
+    __shared__ float4 shared[kJoinBlock / kLanes][2][kNarrow];
     float sum[8] = {};
     const auto add = [&](float4 p, float4 q) {
         const float f[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
@@ -643,9 +645,9 @@ __global__ __launch_bounds__(kJoinBlock) void embed_join_kernel(GradArgs a) {
         for (int e = 0; e < 8; ++e) sum[e] += f[e];
     };
     // the sum of runs [from, to), from the part of the run before them on if that is wanted
-    const auto sum_runs = [&](const Long &of, uint32_t piece, bool before, uint32_t from, uint32_t to) {
+    const auto sum_runs = [&](const Long &of, uint32_t piece, uint32_t lane, bool before, uint32_t from, uint32_t to) {
         const auto halves = [&](uint32_t begins, uint32_t run, float4 &p, float4 &q) {
-            const float *at = part_of<LANES>(a, begins, run, piece);
+            const float *at = part_of<LANES>(a, begins, run, piece, lane);
             p = *reinterpret_cast<const float4 *>(at);
             q = *reinterpret_cast<const float4 *>(at + LANES * 4);
         };
@@ -666,8 +668,8 @@ __global__ __launch_bounds__(kJoinBlock) void embed_join_kernel(GradArgs a) {
                 if (r + j < to) add(p[j], q[j]);
         }
     };
-    const auto put = [&](uint32_t key, uint32_t piece) {
-        const Columns<LANES, FOURS> c(piece, a.width);
+    const auto put = [&](uint32_t key, uint32_t piece, uint32_t lane) {
+        const Columns<LANES, FOURS> c(piece, a.width, lane);
         Eight<O, LANES, FOURS> old;
         if (a.accumulate) {
             old.template load<false>(a.out, key * a.out_stride, c);
@@ -676,27 +678,38 @@ __global__ __launch_bounds__(kJoinBlock) void embed_join_kernel(GradArgs a) {
             put_row<O, LANES, FOURS, kClearOnce>(a, key, c, sum, old);
         }
     };
-    const uint64_t many = static_cast<uint64_t>(a.long_count[0]) * a.pieces, few = static_cast<uint64_t>(a.long_count[1]) * a.pieces;
+    const uint32_t here = threadIdx.x % kNarrow, slot = threadIdx.x / kNarrow;
+    const uint64_t many = static_cast<uint64_t>(a.long_count[0]) * a.pieces * kSubs;
     for (uint64_t task = blockIdx.x; task < many; task += gridDim.x) {
-        const Long of = a.longs[task / a.pieces];
-        const uint32_t piece = static_cast<uint32_t>(task % a.pieces);
-        const uint32_t all = of.runs + of.after, share = (all + kGroups - 1) / kGroups, from = min(group * share, all);
-        sum_runs(of, piece, group == 0 && of.before, from, min(from + share, all));
+        const Long of = a.longs[task / (a.pieces * kSubs)];
+        const uint32_t sub = static_cast<uint32_t>(task % (a.pieces * kSubs)), piece = sub / kSubs, lane = sub % kSubs * kNarrow + here;
+        const uint32_t all = of.runs + of.after, share = (all + kShares - 1) / kShares, from = min(slot * share, all);
+        sum_runs(of, piece, lane, slot == 0 && of.before, from, min(from + share, all));
+        // over a wave's groups, then over the waves
+#pragma unroll
+        for (uint32_t d = kNarrow; d < kLanes; d *= 2)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor(sum[e], d);
         __syncthreads();  // the last task's readers are done
-        shared[group][0][lane] = float4{sum[0], sum[1], sum[2], sum[3]};
-        shared[group][1][lane] = float4{sum[4], sum[5], sum[6], sum[7]};
+        if (threadIdx.x % kLanes < kNarrow) {
+            shared[threadIdx.x / kLanes][0][here] = float4{sum[0], sum[1], sum[2], sum[3]};
+            shared[threadIdx.x / kLanes][1][here] = float4{sum[4], sum[5], sum[6], sum[7]};
+        }
         __syncthreads();
-        if (group == 0) {
-            for (uint32_t g = 1; g < kGroups; ++g) add(shared[g][0][lane], shared[g][1][lane]);
-            put(of.key, piece);
+        if (threadIdx.x < kNarrow) {
+            for (uint32_t w = 1; w < kJoinBlock / kLanes; ++w) add(shared[w][0][here], shared[w][1][here]);
+            put(of.key, piece, lane);
         }
     }
+    constexpr uint32_t kGroups = kJoinBlock / LANES;
+    const uint32_t group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+    const uint64_t few = static_cast<uint64_t>(a.long_count[1]) * a.pieces;
     for (uint64_t task = static_cast<uint64_t>(gridDim.x - 1 - blockIdx.x) * kGroups + group; task < few;
          task += static_cast<uint64_t>(gridDim.x) * kGroups) {
         const Long of = a.longs[a.runs - 1 - task / a.pieces];
         const uint32_t piece = static_cast<uint32_t>(task % a.pieces);
-        sum_runs(of, piece, of.before, 0, of.runs + of.after);
-        put(of.key, piece);
+        sum_runs(of, piece, lane, of.before, 0, of.runs + of.after);
+        put(of.key, piece, lane);
     }
 }
 
@@ -813,7 +826,7 @@ template <int T, int O, int LANES, int MODE> void launch_sums(GradArgs a, const 
     }
     if (a.tokens < a.run || hipPeekAtLastError() != hipSuccess) return;
     TimedLaunch t(4, c);
-    launch_on(embed_join_kernel<O, LANES, T == kRowF32 || O == kRowF32>, dim3(static_cast<uint32_t>(std::min<uint64_t>(tasks, 512))),
+    launch_on(embed_join_kernel<O, LANES, T == kRowF32 || O == kRowF32>, dim3(static_cast<uint32_t>(std::min<uint64_t>(tasks * (LANES / 16), 512))),
               dim3(kJoinBlock), t.L, a);
 }
 
