@@ -195,7 +195,8 @@ __global__ __launch_bounds__(kEmbBlock) void lookup_kernel(LookupArgs a) {
 // there all places, less than two runs, unless the id has an aligned run to
 // itself.  Such an id is long: every wave adds up what its own run holds of it,
 // and a second launch joins those sums.  The rows of ids without tokens are
-// cleared in the first launch, too.
+// cleared in the first launch, too.  Bound by HBM: 32768 tokens of text, 131072 x
+// 4096 bf16 217 us = 6.2 TB/s.
 
 constexpr uint32_t kMaxRun = 16;
 
@@ -263,7 +264,8 @@ __global__ __launch_bounds__(kEmbBlock) void embed_present_kernel(GradArgs a) {
 // range's ids among them; the counts, added up by id and then by wave, say where
 // each wave's first token of an id goes, and the wave deals its tokens out in
 // order.  Bound by the instructions for an id that is not in the range, which are
-// 255 of 256: masks of whole waves and scalar counts.
+// 255 of 256: masks of whole waves and scalar counts.  8192 tokens 7 us, 32768 18 us
+// (the sort takes 35 to 45); twice as many a lane spill.
 constexpr int kOrderBlock = 1024;
 constexpr uint32_t kMaxRange = 1024;
 template <int N, typename Id>
