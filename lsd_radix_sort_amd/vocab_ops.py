@@ -93,7 +93,7 @@ def _finite(scale) -> float:
 def embedding_forward(weight: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0, dtype: torch.dtype | None = None,
                       out: torch.Tensor | None = None, options: "_lrs.SortOptions | None" = None) -> torch.Tensor:
     """Rows of a [vocab, width] table times scale: [*tokens.shape, width] of `dtype` (the table's), 0 for tokens
-    outside [0, vocab)."""
+    outside [0, vocab).  tokens: int32 or int64, contiguous, 1-D with any stride, or 2-D with contiguous rows."""
     if out is None and options is None:
         fast = (_rows._fast or _rows._binding()).embedding_forward(weight, tokens, _finite(scale), dtype)
         if fast is not None:

@@ -235,3 +235,52 @@ def test_together():
         _, indices = lrs.segmented_row_topk(logits, 5)
         lp, _, ranks, top, alternatives = lrs.token_logprobs_topk(logits, indices[:, 2].contiguous(), 5)
         assert torch.equal(alternatives, indices) and ranks.tolist() == [2] * 5 and torch.equal(lp, top[:, 2])
+
+
+@pytest.mark.parametrize("tokens,width", [(200, 40), (5000, 264), (40_000, 16)])
+def test_ids_that_do_not_fit(tokens, width):
+    """Ids whose low 32 bits name a row are outside all the same; so is such a padding index."""
+    from lsd_radix_sort_amd.vocab_ops import _token_ids
+    import ctypes
+    g = torch.Generator().manual_seed(tokens)
+    vocab = 50
+    inside = torch.randint(0, vocab, (tokens,), generator=g)
+    far = torch.tensor([1 << 32, -(1 << 32), 1 << 31, -(1 << 63), (1 << 63) - vocab, 1 << 62])[torch.randint(0, 6, (tokens,), generator=g)]
+    out = torch.rand(tokens, generator=g) < 0.5
+    ids, only = torch.where(out, inside + far, inside).cuda(), torch.where(out, -1, inside).cuda()
+    weight, grad = torch.randn(vocab, width, generator=g).cuda(), torch.randn(tokens, width, generator=g).cuda()
+    same(lrs.embedding_forward(weight, ids), lrs.embedding_forward(weight, only))
+    want = lrs.embedding_backward(grad, only, vocab)
+    same(lrs.embedding_backward(grad, ids, vocab), want)
+    lib, P = lrs.load_library(), ctypes.c_void_p
+    got = torch.empty_like(want)
+    ws = torch.empty(lrs.embedding_backward_workspace_size(tokens, vocab, width), dtype=torch.uint8, device="cuda")
+    assert lib.embedding_backward(P(grad.data_ptr()), width, ctypes.byref(_token_ids(only, only.device)), P(got.data_ptr()), width, vocab,
+                                  width, 2, 2, 1.0, (1 << 32) + 7, 0, P(ws.data_ptr()), ws.numel(),
+                                  P(torch.cuda.current_stream().cuda_stream), None) == 0
+    same(got, want)
+    logits = torch.randn(tokens, vocab, generator=g).cuda()
+    same(lrs.token_logprobs_topk(logits, ids, 3), lrs.token_logprobs_topk(logits, only, 3))
+    up = torch.randn(tokens, generator=g).cuda()
+    same(lrs.token_logprobs_step(logits, ids, up, up), lrs.token_logprobs_step(logits, only, up, up))
+
+
+def test_backward_in_a_graph_with_its_forward():
+    """Forward and backward of the autograd forms captured together, where no graph of the leaves is alive."""
+    g = torch.Generator().manual_seed(8)
+    weight = torch.randn(300, 40, generator=g).cuda().requires_grad_(True)
+    ids = torch.randint(0, 300, (64,), generator=g).cuda()
+
+    def step():
+        logprobs, entropy = lrs.token_logprobs(lrs.embedding_lookup(weight, ids, 2.0), ids % 40)
+        return torch.autograd.grad((logprobs, entropy), weight, (torch.ones_like(logprobs), torch.ones_like(entropy)))[0]
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(3):
+        ids.copy_(torch.randint(0, 300, (64,), generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        same(out, step())
