@@ -680,7 +680,8 @@ constexpr uint64_t kMaxGrid = 1u << 20;
 // How the rows are laid out on workgroups.  A row that several share costs a
 // second launch, 3 to 4 us, so that most have one:
 //  - a wave for up to 4 KB of many rows (32 KB of very many: 8192 x 4096 bf16 17 us
-//    against 24), else 256 threads (400 x 16000 bf16 top 5 11 us, shared by two 15);
+//    against 24; with up to 16 alternatives 12 KB: 8192 x 2048 fp32 top 5 33 us against
+//    42), else 256 threads (400 x 16000 bf16 top 5 11 us, shared by two 15);
 //  - 1024 threads where there are no more rows than CUs and a row is more than a
 //    load a thread (48 x 32000 bf16 top 5 11.1 us, shared 12.6; 256 x 9000 fp16
 //    8.4 against 12.0).
@@ -698,7 +699,7 @@ LogPlan logprob_plan(uint64_t rows, uint64_t n, uint64_t k, uint64_t size) {
     LogPlan p;
     const uint64_t vec = 16 / size, vecs = n / vec;
     if (rows >= 512 && vecs <= 64 * kLoads) p.block = 64;
-    if (rows >= 2048 && vecs <= 2048 && k == 0) p.block = 64;
+    if (rows >= 2048 && (k == 0 ? vecs <= 2048 : k <= 16 && vecs <= 768)) p.block = 64;
     const uint64_t bytes = n * size;
     if (rows <= 256 && vecs > 1024 && bytes <= (rows < 128 ? 64 : 512) * 1024) p.block = 1024;
     const bool alone = p.block == 1024 || rows >= 1024 || (rows > 256 && bytes <= 256 * 1024);

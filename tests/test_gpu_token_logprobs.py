@@ -230,6 +230,32 @@ def test_alternatives_of_rows_alone(dtype, kind, shape):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kind", ["any", "masked", "levels", "zeros"])
+def test_alternatives_of_many_short_rows(dtype, kind):
+    """A wave a row, several batches of loads."""
+    for rows, n, pad in ((2050, 2995, 1), (2048, 1027, 0)):
+        x, tokens, logits = make(kind, rows, n, DTYPES[dtype], rows + n, pad)
+        if kind == "any":
+            x[7, 900] = x[9, n - 1] = float("nan")
+            x[8, 5:1000] = INF
+            logits.copy_(x)
+        ref = Reference(x, tokens)
+        sound = torch.ones(rows, dtype=torch.bool)
+        sound[7:10] = kind != "any"
+        ref.on &= sound  # the others have no values to compare
+        for k in (1, 16, 17):
+            lp, h, ranks, top, indices = (t.cpu() for t in lrs.token_logprobs_topk(logits, tokens.cuda(), k))
+            for t in (lp, h):
+                t[~sound] = 0
+            ref.values(lp, h)
+            check_places(x, tokens, k, ranks, indices)
+            want = in_32_bits(torch.where(ref.empty[:, None], -INF, torch.gather(ref.logp, 1, indices)))[sound]
+            off = (top[sound].double() - want).abs()
+            allowed = ref.lse_off[sound][:, None] + 2 * ULP * want.abs()
+            assert bool(torch.where(torch.isinf(want), top[sound].double() == want, off <= allowed).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_masked_rows_hold_anything(dtype):
     x, tokens, logits = make("any", 6, 2003, DTYPES[dtype], 3)
     for r, v in ((0, float("nan")), (1, INF), (2, -INF)):
