@@ -366,8 +366,8 @@ int expert_balance_step(const void *logits, int64_t row_stride, const void *indi
  *              added to what grad_weight holds, and rows of no token stay as
  *              they are.  Ids outside [0, vocab) and ids equal to padding_index
  *              (-1: none) count for nothing.
- * Sums are in 32 bits or more, in an order that the tokens alone decide (by
- * radix_sort_pairs of ids and places), so equal calls give equal bits; each
+ * Sums are in 32 bits or more, in an order that the ids and sizes alone decide
+ * (a stable sort of ids and places), so equal calls give equal bits; each
  * result is rounded to its type once.
  *   tokens       ids of `lines` lines of `length` tokens, line i at element
  *                i * stride; token t is number t in that order

@@ -3,8 +3,9 @@
 //
 // out[t] = scale W[id_t]; dW[v] = scale * sum of g[t] over the tokens with id_t =
 // v.  The sum over the tokens of one id is a segmented sum once the pairs (id,
-// place) are sorted, which the library's stable sort does; within an id the
-// places then stand in order, so the sum has one order however the GPU runs it.
+// place) are sorted, by the library's stable sort or, for fewer tokens, by a
+// counting sort of the ids in one launch; within an id the places then stand in
+// order, so the sum has one order however the GPU runs it.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -7,7 +7,7 @@
 The entry points of the C ABI (include/lsd_radix_sort.h), with the checks,
 streams, outputs and errors of the package's sorts.  Regular calls go through
 the compiled binding, as in row_ops.  The table's gradient is a
-stable sort of the tokens' ids (radix_sort_pairs) and a sum over equal ones; a
+stable sort of the tokens' ids and a sum over equal ones; a
 token's rank and the top alternatives are places in the descending row sort.
 embedding_lookup and token_logprobs differentiate through torch autograd; the
 other calls do not record a graph.
