@@ -420,7 +420,8 @@ int embedding_backward(const void *grad, int64_t grad_stride, const lrs_token_id
  * takes no mask.  A row with a = b = 0 has gradient 0 whatever it holds.  Rows
  * that are all -inf have log p = -inf, entropy 0 and gradient 0; in others a
  * token of logit -inf has log p = -inf.  NaN and +inf logits give NaN (not in
- * ranks and top_indices, which go by the patterns).
+ * ranks and top_indices, which go by the patterns); else no log p is above 0
+ * and no entropy below.
  * n <= LRS_MAX_ROW_LEN; rows * n < 2^40; 0 <= k <= n, k <= LRS_MAX_TOPK; tokens
  * are int32 or int64, row r's at element r * token_stride; temperature above 0
  * and finite, log2(e) / temperature finite in 32 bits (else LRS_ERR_OPTION).

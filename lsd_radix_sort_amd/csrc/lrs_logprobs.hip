@@ -245,9 +245,12 @@ __device__ inline Sums join_sums(JoinLds<B> &lds, Running<Acc> &mine, float &top
             }
     }
     if (fabsf(shift) < INFINITY && shift != 0) {
-        const double p = __builtin_amdgcn_exp2f(-shift);
-        s.w = p * (s.w - s.z * shift);
-        s.z = p * s.z;
+        // over the very power that the largest logit's own term is: that becomes exactly 1, so that Z >= 1, and no
+        // log p above 0 comes of a sure token (a product with 2^-shift gave up to 9e-8); no exponent is above 0 either
+        const double p = __builtin_amdgcn_exp2f(shift);
+        s.w = (s.w - s.z * shift) / p;
+        s.w = s.w > 0 ? 0 : s.w;  // NaN stays
+        s.z = s.z / p;
     }
     return s;
 }
