@@ -57,7 +57,9 @@ struct LogArgs {
     const uint8_t *mask;
     float c;              // log2(e) / T
     double factor;        // the same in 64 bits
-    double inv_t;
+    // 1 / T in two factors, of derivatives and of shares: either of them alone can leave the range of 32 bits
+    double soft;          // at most 1
+    float sharp;          // at least 1
     uint32_t splits, split_len;
     Sums *sums;           // [rows][splits]
     float *logprobs, *entropy, *stats;
@@ -526,21 +528,22 @@ __global__ __launch_bounds__(kLogBlock) void logprob_grad_kernel(LogArgs a) {
         Stored *g = static_cast<Stored *>(a.grad) + row * a.grad_stride + first;
         const int64_t token = token_of(a, row);
         const bool given = token >= 0 && token < a.n;
-        const float up = a.up && given ? a.up[row] : 0.f, down = a.up_entropy ? a.up_entropy[row] : 0.f;
+        const float up = a.up && given ? static_cast<float>(a.up[row] * a.soft) : 0.f;
+        const float down = a.up_entropy ? static_cast<float>(a.up_entropy[row] * a.soft) : 0.f;
         const float *s = a.stats + row * kLogStats;
         if (!counted(a, row) || s[1] == 0.f || (up == 0.f && down == 0.f)) {  // whatever its logits hold
             for (uint32_t v = threadIdx.x; v < vecs; v += kLogBlock) store16(g + static_cast<uint64_t>(v) * kVec, u32x4{0, 0, 0, 0});
             if (rest < len) g[rest] = 0;
             continue;
         }
-        const float inv_t = static_cast<float>(a.inv_t), m = s[0], share = -s[1] * inv_t, mean = s[2];
+        const float m = s[0], share = -s[1] * a.sharp, mean = s[2];
         const float slope = down * static_cast<float>(kLn2);
         // p (a + b ln2 (d - D)), and what the given token has besides
         const uint32_t own = given && token >= first && token < first + len ? static_cast<uint32_t>(token - first) : ~0u;
         const auto of = [&](float f, uint32_t at) {
             const float d = (f - m) * c;
             const float v = __builtin_amdgcn_exp2f(d) * share * fmaf(slope, fmaxf(d, kZeroBelow) - mean, up);
-            return at == own ? fmaf(up, inv_t, v) : v;
+            return at == own ? fmaf(up, a.sharp, v) : v;
         };
         for (uint32_t base = threadIdx.x; base < vecs; base += kLoads * kLogBlock) {
             u32x4 t[kLoads];
@@ -587,7 +590,8 @@ __global__ __launch_bounds__(B, 4) void logprob_step_kernel(LogArgs a) {
     }
     const float over = on && extra ? Row<T>::value(x[rest]) : -INFINITY;
     const Token<T> token(a, row);
-    const float up = a.up && token.given ? a.up[row] : 0.f, down = a.up_entropy ? a.up_entropy[row] : 0.f;
+    const float up = a.up && token.given ? static_cast<float>(a.up[row] * a.soft) : 0.f;
+    const float down = a.up_entropy ? static_cast<float>(a.up_entropy[row] * a.soft) : 0.f;
     const float c = a.c;
     // each pass unpacks the held words anew: their floats would take twice the registers
     const auto anew = [&]() {
@@ -634,7 +638,7 @@ __global__ __launch_bounds__(B, 4) void logprob_step_kernel(LogArgs a) {
     anew();
     if (tid == 0) {
         const RowEnd end = finish_row(a, row, on, token.given, token.x, s.z, s.w, s.m, 0);
-        shared[0] = -static_cast<float>(end.share * a.inv_t);
+        shared[0] = -static_cast<float>(end.share * a.sharp);
         shared[1] = static_cast<float>(end.mean);
     }
     __syncthreads();
@@ -671,7 +675,7 @@ __global__ __launch_bounds__(B, 4) void logprob_step_kernel(LogArgs a) {
         __syncthreads();
         if (tid == 0) {
             const float d = huge(top, c) ? (token.x - m) * c : fmaf(token.x, c, -r), p = __builtin_amdgcn_exp2f(d);
-            g[token.at] = Row<T>::pattern(fmaf(up, static_cast<float>(a.inv_t), p * fmaf(slope, fmaxf(d, kZeroBelow) - mean, flat)));
+            g[token.at] = Row<T>::pattern(fmaf(up, a.sharp, p * fmaf(slope, fmaxf(d, kZeroBelow) - mean, flat)));
         }
     }
 }
@@ -786,8 +790,10 @@ int logprob_inputs(const lrs_logprobs *d, int64_t k, LogArgs &a) {
     a.token_stride = d->token_stride;
     a.token_bytes = d->token_bytes;
     a.mask = d->row_mask;
-    a.inv_t = 1.0 / d->temperature;
-    a.factor = kLog2e * a.inv_t;
+    const double inv_t = 1.0 / d->temperature;
+    a.soft = std::min(inv_t, 1.0);
+    a.sharp = static_cast<float>(std::max(inv_t, 1.0));
+    a.factor = kLog2e * inv_t;
     // above 0, so that -inf times it is -inf
     a.c = std::max(static_cast<float>(a.factor), std::numeric_limits<float>::denorm_min());
     a.k = static_cast<uint32_t>(k);
