@@ -247,12 +247,14 @@ __device__ inline Sums join_sums(JoinLds<B> &lds, Running<Acc> &mine, float &top
             }
     }
     if (fabsf(shift) < INFINITY && shift != 0) {
-        // over the very power that the largest logit's own term is: that becomes exactly 1, so that Z >= 1, and no
-        // log p above 0 comes of a sure token (a product with 2^-shift gave up to 9e-8); no exponent is above 0 either
-        const double p = __builtin_amdgcn_exp2f(shift);
-        s.w = (s.w - s.z * shift) / p;
-        s.w = s.w > 0 ? 0 : s.w;  // NaN stays
-        s.z = s.z / p;
+        // Over the very power that the largest logit's own term is, to 2^-46 by one step of Newton's method from the
+        // opposite power (that alone left log p of up to 9e-8 above 0).  The term itself is 1 and every exponent at
+        // most 0: what rounding left beyond is cut off, so that log p <= 0 and the entropy >= 0.  NaN stays.
+        const double p = __builtin_amdgcn_exp2f(shift), q = __builtin_amdgcn_exp2f(-shift), inverse = q * fma(-p, q, 2.0);
+        s.w = (s.w - s.z * shift) * inverse;
+        s.z = s.z * inverse;
+        s.w = s.w > 0 ? 0 : s.w;
+        s.z = s.z < 1 ? 1 : s.z;
     }
     return s;
 }
