@@ -58,7 +58,8 @@ struct LogArgs {
     float c;              // log2(e) / T
     double factor;        // the same in 64 bits
     // 1 / T in two factors, of derivatives and of shares: either of them alone can leave the range of 32 bits
-    double soft;          // at most 1
+    float soft;           // at most 1, times a power of two
+    int soft_power;
     float sharp;          // at least 1
     uint32_t splits, split_len;
     Sums *sums;           // [rows][splits]
@@ -80,6 +81,7 @@ __device__ inline int64_t token_of(const LogArgs &a, uint64_t row) {
     const uint64_t at = row * a.token_stride;
     return a.token_bytes == 8 ? static_cast<const int64_t *>(a.tokens)[at] : static_cast<const int32_t *>(a.tokens)[at];
 }
+__device__ inline float softened(const LogArgs &a, float derivative) { return __builtin_amdgcn_ldexpf(derivative * a.soft, a.soft_power); }
 __device__ inline bool counted(const LogArgs &a, uint64_t row) { return a.mask == nullptr || a.mask[row] != 0; }
 
 // The larger of two, NaN if either is.
@@ -530,16 +532,15 @@ __global__ __launch_bounds__(kLogBlock) void logprob_grad_kernel(LogArgs a) {
         Stored *g = static_cast<Stored *>(a.grad) + row * a.grad_stride + first;
         const int64_t token = token_of(a, row);
         const bool given = token >= 0 && token < a.n;
-        const float up = a.up && given ? static_cast<float>(a.up[row] * a.soft) : 0.f;
-        const float down = a.up_entropy ? static_cast<float>(a.up_entropy[row] * a.soft) : 0.f;
+        const float asked = a.up && given ? a.up[row] : 0.f, asked_entropy = a.up_entropy ? a.up_entropy[row] : 0.f;
         const float *s = a.stats + row * kLogStats;
-        if (!counted(a, row) || s[1] == 0.f || (up == 0.f && down == 0.f)) {  // whatever its logits hold
+        if (!counted(a, row) || s[1] == 0.f || (asked == 0.f && asked_entropy == 0.f)) {  // whatever its logits hold
             for (uint32_t v = threadIdx.x; v < vecs; v += kLogBlock) store16(g + static_cast<uint64_t>(v) * kVec, u32x4{0, 0, 0, 0});
             if (rest < len) g[rest] = 0;
             continue;
         }
         const float m = s[0], share = -s[1] * a.sharp, mean = s[2];
-        const float slope = down * static_cast<float>(kLn2);
+        const float up = softened(a, asked), slope = softened(a, asked_entropy) * static_cast<float>(kLn2);
         // p (a + b ln2 (d - D)), and what the given token has besides
         const uint32_t own = given && token >= first && token < first + len ? static_cast<uint32_t>(token - first) : ~0u;
         const auto of = [&](float f, uint32_t at) {
@@ -592,8 +593,7 @@ __global__ __launch_bounds__(B, 4) void logprob_step_kernel(LogArgs a) {
     }
     const float over = on && extra ? Row<T>::value(x[rest]) : -INFINITY;
     const Token<T> token(a, row);
-    const float up = a.up && token.given ? static_cast<float>(a.up[row] * a.soft) : 0.f;
-    const float down = a.up_entropy ? static_cast<float>(a.up_entropy[row] * a.soft) : 0.f;
+    const float asked = a.up && token.given ? a.up[row] : 0.f, asked_entropy = a.up_entropy ? a.up_entropy[row] : 0.f;
     const float c = a.c;
     // each pass unpacks the held words anew: their floats would take twice the registers
     const auto anew = [&]() {
@@ -648,9 +648,10 @@ __global__ __launch_bounds__(B, 4) void logprob_step_kernel(LogArgs a) {
     // Exponents are relative to r, which is not quite the largest logit's.
     const float m = s.m, r = fmaxf(top * c, kLeastReference);
     const float shift = huge(top, c) ? 0.f : static_cast<float>(static_cast<double>(top) * c - r);
+    const float up = softened(a, asked), down = softened(a, asked_entropy);
     const float share = shared[0], scaled = share * __builtin_amdgcn_exp2f(-shift);
     const float flat = scaled * up, slope = scaled * down * static_cast<float>(kLn2), mean = shared[1] + shift;
-    const bool none_asked = !on || share == 0.f || (up == 0.f && down == 0.f);
+    const bool none_asked = !on || share == 0.f || (asked == 0.f && asked_entropy == 0.f);
     const auto pass = [&](auto of) {
 #pragma unroll
         for (int u = 0; u < V; ++u) {
@@ -793,7 +794,7 @@ int logprob_inputs(const lrs_logprobs *d, int64_t k, LogArgs &a) {
     a.token_bytes = d->token_bytes;
     a.mask = d->row_mask;
     const double inv_t = 1.0 / d->temperature;
-    a.soft = std::min(inv_t, 1.0);
+    a.soft = static_cast<float>(std::frexp(std::min(inv_t, 1.0), &a.soft_power));
     a.sharp = static_cast<float>(std::max(inv_t, 1.0));
     a.factor = kLog2e * inv_t;
     // above 0, so that -inf times it is -inf
