@@ -464,17 +464,16 @@ template <int O, bool ONCE> __device__ void clear_rows(const GradArgs &a, uint32
     const uint32_t id0 = word * 32, ids = min(32u, a.vocab - id0);
     const uint32_t named = a.tokens ? a.present[word] : 0;
     const uint32_t all = (a.width + kVec - 1) / kVec, first = piece * kClearPiece, stores = min(kClearPiece, all - first);
-    // rows side by side, where one does not take all threads
-    const uint32_t shift = stores > kEmbBlock / 2 ? 8 : 32 - __builtin_clz(stores - 1 | 1), rows = kEmbBlock >> shift;
+    // rows side by side: a piece of one takes at most a quarter of the threads
+    const uint32_t shift = 32 - __builtin_clz((stores - 1) | 1), rows = kEmbBlock >> shift, u = threadIdx.x & ((1u << shift) - 1);
+    if (u >= stores) return;
+    const uint64_t col = static_cast<uint64_t>(first + u) * kVec;
     for (uint32_t r = threadIdx.x >> shift; r < ids; r += rows) {
         if ((named >> r) & 1) continue;
         auto *p = static_cast<typename Row<O>::Stored *>(a.out) + (id0 + r) * a.out_stride;
-        for (uint32_t u = threadIdx.x & ((1u << shift) - 1); u < stores; u += 1u << shift) {
-            const uint64_t col = static_cast<uint64_t>(first + u) * kVec;
-            if (col + kVec <= a.width) (ONCE ? store16_once : store16)(p + col, u32x4{0, 0, 0, 0});
-            else
-                for (uint32_t e = 0; col + e < a.width; ++e) p[col + e] = 0;
-        }
+        if (col + kVec <= a.width) (ONCE ? store16_once : store16)(p + col, u32x4{0, 0, 0, 0});
+        else
+            for (uint32_t e = 0; col + e < a.width; ++e) p[col + e] = 0;
     }
 }
 
