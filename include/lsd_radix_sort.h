@@ -425,7 +425,9 @@ int embedding_backward(const void *grad, int64_t grad_stride, const lrs_token_id
  * n <= LRS_MAX_ROW_LEN; rows * n < 2^40; 0 <= k <= n, k <= LRS_MAX_TOPK; tokens
  * are int32 or int64, row r's at element r * token_stride; temperature above 0
  * and finite, log2(e) / temperature finite in 32 bits (else LRS_ERR_OPTION).
- * Results do not depend on the order in which workgroups run.  Only
+ * Results do not depend on the order in which workgroups run: equal calls give
+ * equal bits.  The forward, token_logprobs_topk and the step take a row's sums in
+ * orders of their own, so their values can differ in the last bits.  Only
  * opts->timer is used (kind 4).
  */
 typedef struct lrs_logprobs {

@@ -145,10 +145,12 @@ template <int LANES> __device__ inline uint32_t uniform(uint32_t v) {
     return LANES == kLanes ? __builtin_amdgcn_readfirstlane(v) : v;
 }
 
-// A group of lanes has kSlots loads on their way: pieces of one token's row, or,
-// where a piece is a row, tokens.  Written past the caches: 32768 x 4096 bf16 of
-// text 63 us = 5.3 TB/s of what it has to move, 81 us through them, which the
-// rows' repeated reads need more.
+// A group of lanes has up to kSlots loads on their way: pieces of one token's row,
+// or, where a piece is a row, tokens.  (Pieces past a row's end are idle slots: two
+// of four at 1024 columns, one at 1031, which has another for 7 columns.)  Always
+// written past the caches: 32768 x 4096 bf16 of text, calls in a row, whose 97 MB of
+// table rows stay behind the L2s, 63 us, 81 us through the caches, which the rows'
+// repeated reads need more; of a table that is not there 84 us = 4.4 TB/s.
 constexpr uint32_t kSlots = 4;
 template <int T, int O, int LANES>
 __global__ __launch_bounds__(kEmbBlock) void lookup_kernel(LookupArgs a) {
@@ -197,7 +199,7 @@ __global__ __launch_bounds__(kEmbBlock) void lookup_kernel(LookupArgs a) {
 // itself.  Such an id is long: every wave adds up what its own run holds of it,
 // and a second launch joins those sums.  The rows of ids without tokens are
 // cleared in the first launch, too.  Bound by HBM: 32768 tokens of text, 131072 x
-// 4096 bf16 217 us = 6.2 TB/s.
+// 4096 bf16 206 to 217 us = 6.2 TB/s and more.
 
 constexpr uint32_t kMaxRun = 16;
 

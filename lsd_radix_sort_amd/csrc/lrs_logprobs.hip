@@ -10,9 +10,12 @@
 // A difference x - m is exact or rounded by its own last bit, so however large
 // the logits are, exponents near 0 are right.
 //
-// A thread's terms are summed in 32 bits within one batch of loads and in 64
-// bits from there on, as is everything there is once a row: an entropy is the
-// difference of two numbers that nearly cancel.
+// A thread's terms are summed in 32 bits within one batch of loads.  Its batches
+// are added in 64 bits where a row may have any number of them (forward, ranks
+// alone), in 32 where it has at most 16 (a row whose alternatives are selected, a
+// row that the step holds); what there is once a row, from the threads' sums on,
+// is in 64 bits: an entropy is the difference of two numbers that nearly cancel.
+// So the calls can differ in their last bits over the same row.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -689,17 +692,22 @@ constexpr uint64_t kMaxGrid = 1u << 20;
 
 // How the rows are laid out on workgroups.  A row that several share costs a
 // second launch, 3 to 4 us, so that most have one:
-//  - a wave for up to 4 KB of many rows (32 KB of very many: 8192 x 4096 bf16 17 us
-//    against 24; with up to 16 alternatives 12 KB: 8192 x 2048 fp32 top 5 33 us against
-//    42), else 256 threads (400 x 16000 bf16 top 5 11 us, shared by two 15);
-//  - 1024 threads where there are no more rows than CUs and a row is more than a
-//    load a thread (48 x 32000 bf16 top 5 11.1 us, shared 12.6; 256 x 9000 fp16
-//    8.4 against 12.0).
+//  - a wave for up to 4 KB of many rows (2000 x 2048 bf16 top 5 10.4 us, by 256
+//    threads 12.4; of 1000 rows 9.7 and 8.0, of 2000 x 2056 10.9 and 12.9: the border
+//    lies between them), for up to 32 KB of very many (2048 x 16384 bf16 13.8 against
+//    15.7, 8192 of them 47.4 and 44.2), with up to 16 alternatives 12 KB (8192 x 6144 bf16
+//    top 5 44.1 against 46.0, 8192 x 8192 53.2 and 47.5);
+//  - else 256 threads (300 x 16384 bf16 top 5 11.0 us, shared 13.6), and 1024 where there
+//    are no more rows than CUs and a row is more than a load a thread: 256 x 65536 bf16
+//    top 5 13.0 us, by 256 threads 15.4, shared 18.0; 300 of them 24.0, 19.6 and 21.8; up to
+//    64 KB of under 128 rows (48 x 32768 10.4, shared 11.9; 48 x 65536 12.8 and 12.5), up to
+//    512 KB of more (128 x 131072 18.0, shared 18.3; of 256 x 262152 31.4 and 37.0).
 // Shared are long rows of too few to fill the GPU, down to a batch of loads a thread
-// (1 x 131072 bf16 top 5 11.4 us, 17.3 by 1024 threads; 200 of them 24.5 against
-// 20.8).  With alternatives (k > 0) a workgroup holds at most kKept batches, k is at
+// (1 x 131072 bf16 top 5 11.0 us, 17.0 by 1024 threads; 300 x 262144 43.2, alone 45.0;
+// 512 of them 56.4 and 56.2, but 47.6 and 41.9 without alternatives).  With alternatives (k > 0) a workgroup holds at most kKept batches, k is at
 // most half of its threads, and the pieces' words fit one workgroup; where that
-// cannot be (fused false) segmented_row_topk selects them.
+// cannot be (fused false) segmented_row_topk selects them from a second read
+// (4096 x 131072 bf16 top 128 242 us, top 129 377, top 500 420).
 struct LogPlan {
     int block = kLogBlock;
     uint32_t splits = 1, len = 8;

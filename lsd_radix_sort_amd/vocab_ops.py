@@ -131,7 +131,8 @@ def embedding_backward(grad: torch.Tensor, tokens: torch.Tensor, vocab: int, sca
 
     grad: [*tokens.shape, width] or [tokens.numel(), width].  Tokens outside [0, vocab) and those equal to
     padding_index count for nothing.  accumulate: the gradient is added to grad_out, whose rows without a token
-    stay as they are.  The sums are in 32 bits and their order is the tokens' own: equal calls give equal bits."""
+    stay as they are.  The sums are in 32 bits, in an order that the ids and sizes alone decide: equal calls
+    give equal bits."""
     vocab = _whole(vocab, "vocab")
     if not 0 <= vocab < 2 ** 31 - 1:
         _lrs._bad(f"vocab must be in [0, 2^31 - 1), got {vocab}")
@@ -256,7 +257,8 @@ def token_logprobs_forward(logits: torch.Tensor, tokens: torch.Tensor, temperatu
 
 def token_logprobs_topk(logits: torch.Tensor, tokens: torch.Tensor, k: int, temperature: float = 1.0,
                         workspace: torch.Tensor | None = None, options: "_lrs.SortOptions | None" = None):
-    """token_logprobs_forward's values with the tokens' ranks (0: the likeliest) and the k likeliest alternatives.
+    """token_logprobs_forward's values, up to their last bits (the sums are taken in another order), with the tokens'
+    ranks (0: the likeliest) and the k likeliest alternatives.
 
     Ranks and alternatives are places in the row's descending stable sort, so top_indices[r, ranks[r]] is the
     token where ranks[r] < k; a token outside [0, n) has rank -1.
@@ -324,7 +326,7 @@ def token_logprobs_step(logits: torch.Tensor, tokens: torch.Tensor, logprob_grad
                         row_mask: torch.Tensor | None = None, grad_out: torch.Tensor | None = None,
                         workspace: torch.Tensor | None = None, options: "_lrs.SortOptions | None" = None):
     """token_logprobs_forward and _backward in one call, for derivatives that are known beforehand (such as those of
-    a weighted sum of log probabilities): returns (logprobs, entropy, grad)."""
+    a weighted sum of log probabilities): returns (logprobs, entropy, grad), the first two up to their last bits."""
     if grad_out is None and workspace is None and options is None:
         fast = (_rows._fast or _rows._binding()).logprobs_step(logits, tokens, logprob_grad, entropy_grad,
                                                                _number(temperature, "temperature"), row_mask)
